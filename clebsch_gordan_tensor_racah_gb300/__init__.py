@@ -5,8 +5,9 @@ kernels of ``libcgtp.so`` (built in-tree by ``_build.build()``).  PyTorch is use
 for device memory and streams.  There is no CPU fallback: if the library is
 missing or no GPU is present the calls raise.
 
-Names follow the C ABI in ``include/cgtp.h`` (and ``include/cgtp_measure.h`` for the
-measurement kernels ``measure_fma`` / ``measure_read``):
+Names follow the C ABI in ``include/cgtp.h`` (``include/cgtp_train.h`` for the operators of a
+training step, which ``train.py`` binds, and ``include/cgtp_measure.h`` for the measurement
+kernels ``measure_fma`` / ``measure_read``):
 
 * ``Plan(irreps_in1, irreps_in2, irreps_out, mode, dtype, radial_k)`` --
   ``cgtp_plan_create``; ``plan.d1, d2, d_out, w_numel, n_paths``;
@@ -16,6 +17,9 @@ measurement kernels ``measure_fma`` / ``measure_read``):
 * ``cgtp_conv_forward(plan, graph, x, Y, W_or_R, M=None)`` and
   ``cgtp_conv_backward(plan, graph, gout, x, Y, W_or_R, M=None)``.
 * ``cgtp_real_cg_block(l1, l2, l3)`` -- host-only query of the planner's block.
+* ``ResNormPlan(irreps, ...)`` with ``cgtp_resnorm_forward`` / ``cgtp_resnorm_backward`` -- the
+  norms, gate and residual around a block.
+* ``AdamW(numel, ...)`` with ``cgtp_grad_norm``, ``cgtp_adamw_step``, ``cgtp_adamw_state_values``.
 """
 
 import ctypes
@@ -42,7 +46,11 @@ EXPORTS = ["cgtp_plan_create", "cgtp_plan_destroy", "cgtp_plan_info", "cgtp_plan
            "cgtp_mixed_conv_workspace", "cgtp_mixed_conv_forward", "cgtp_mixed_conv_backward",
            "cgtp_mixed_conv_double_backward", "cgtp_measure_fma", "cgtp_measure_read",
            "cgtp_plan_device_bytes", "cgtp_graph_device_bytes", "cgtp_plan_set_wait_limit",
-           "cgtp_plan_set_node_chunk", "cgtp_plan_node_chunk"]
+           "cgtp_plan_set_node_chunk", "cgtp_plan_node_chunk",
+           "cgtp_resnorm_create", "cgtp_resnorm_destroy", "cgtp_resnorm_info", "cgtp_resnorm_device_bytes",
+           "cgtp_resnorm_forward", "cgtp_resnorm_backward", "cgtp_adamw_create", "cgtp_adamw_destroy",
+           "cgtp_adamw_info", "cgtp_adamw_device_bytes", "cgtp_adamw_step", "cgtp_grad_norm",
+           "cgtp_adamw_state_values"]
 
 
 class CgtpError(RuntimeError):
@@ -106,9 +114,22 @@ def lib():
         L.cgtp_graph_device_bytes.argtypes = [vp, ctypes.POINTER(i64)]
         L.cgtp_measure_fma.argtypes = [i32, i32, i32, vp, ctypes.POINTER(ctypes.c_double), vp]
         L.cgtp_measure_read.argtypes = [vp, i64, i32, i32, vp, ctypes.POINTER(ctypes.c_double), vp]
+        L.cgtp_resnorm_create.argtypes = [ctypes.POINTER(vp), ctypes.c_char_p, i32, i32, i32, dbl, dbl]
+        L.cgtp_resnorm_info.argtypes = [vp, ctypes.POINTER(i64), ctypes.POINTER(i64), ctypes.POINTER(i32)]
+        L.cgtp_resnorm_forward.argtypes = [vp, i64] + [vp, i64] * 3 + [vp] * 3 + [vp, i64] * 2 + [vp]
+        L.cgtp_resnorm_backward.argtypes = [vp, i64] + [vp, i64] * 5 + [vp] * 3 + [vp, i64] * 3 + [vp] * 4
+        L.cgtp_adamw_create.argtypes = [ctypes.POINTER(vp), i32, vp, vp, i32, i32, i32]
+        L.cgtp_adamw_info.argtypes = [vp, ctypes.POINTER(i64)]
+        L.cgtp_adamw_step.argtypes = [vp] * 8 + [dbl] * 5 + [i64, ctypes.c_uint64, vp, vp]
+        L.cgtp_grad_norm.argtypes = [vp, vp, dbl, vp, vp]
+        L.cgtp_adamw_state_values.argtypes = [vp] * 8
+        for fn in (L.cgtp_resnorm_device_bytes, L.cgtp_adamw_device_bytes):
+            fn.argtypes = [vp, ctypes.POINTER(i64)]
+        for fn in (L.cgtp_resnorm_destroy, L.cgtp_adamw_destroy):
+            fn.argtypes, fn.restype = [vp], None
         for name in EXPORTS:
             if name not in ("cgtp_last_error", "cgtp_plan_destroy", "cgtp_graph_destroy",
-                            "cgtp_mixed_plan_destroy"):
+                            "cgtp_mixed_plan_destroy", "cgtp_resnorm_destroy", "cgtp_adamw_destroy"):
                 getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -543,3 +564,7 @@ def cgtp_mixed_conv_double_backward(plan, graph, gout, x, Y, Wu, Ww, ggx, ggY, g
         _ptr(ggWw, "ggWw", dt), _ptr(d_g, "d_gout"), _ptr(d_x, "d_x"), _ptr(d_Y, "d_Y"), _ptr(d_Wu, "d_Wu"),
         _ptr(d_Ww, "d_Ww"), _ptr(ws, "workspace"), nb, _stream(stream)))
     return d_g, d_x, d_Y, d_Wu, d_Ww
+
+
+from .train import (AdamW, ResNormPlan, cgtp_adamw_state_values, cgtp_adamw_step, cgtp_grad_norm,  # noqa: E402
+                    cgtp_resnorm_backward, cgtp_resnorm_forward)

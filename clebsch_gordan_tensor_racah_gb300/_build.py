@@ -22,7 +22,8 @@ CU_SOURCES = ["api.cu", "graph.cu", "uvu.cu", "uvu_f32.cu", "uvu_f32_l7.cu", "uv
               "uvu3_f64_2.cu", "uvu3_f64_8.cu", "uvu3_f64_32.cu", "uvw.cu", "bt.cu", "dbl.cu",
               "uvu3_bf16_2.cu", "uvu3_bf16_8.cu", "uvu3_bf16_32.cu", "sh.cu",
               "uvu3_sh_f32_2.cu", "uvu3_sh_f32_8.cu", "uvu3_sh_f32_32.cu", "uvu3_sh_f64_2.cu",
-              "uvu3_sh_f64_8.cu", "uvu3_sh_f64_32.cu", "uvwe.cu", "mixed.cu", "measure.cu"]
+              "uvu3_sh_f64_8.cu", "uvu3_sh_f64_32.cu", "uvwe.cu", "mixed.cu", "measure.cu",
+              "resnorm.cu", "resnorm_f32.cu", "resnorm_f64.cu", "resnorm_bf16.cu", "resnorm_bf16s.cu", "adamw.cu"]
 CPP_SOURCES = ["planner.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
