@@ -32,11 +32,6 @@ cgtp_status param(const void* ptr, int es, const char* name) {
   return CGTP_OK;
 }
 
-int ctas_for(const cgtp_resnorm_s* p, int64_t N) {
-  const int teams = kRnThreads / p->team;
-  return static_cast<int>(std::min<int64_t>((N + teams - 1) / teams, p->teams_max / teams));
-}
-
 RnArgs base_args(const cgtp_resnorm_s* p, int64_t N) {
   RnArgs a;
   a.N = N;
@@ -45,7 +40,6 @@ RnArgs base_args(const cgtp_resnorm_s* p, int64_t N) {
   a.dim = static_cast<int>(p->dim);
   a.chan = static_cast<int>(p->chan);
   a.act = p->act;
-  a.team = p->team;
   a.pre_norm = p->flags & CGTP_RESNORM_PRE;
   a.post_norm = p->flags & CGTP_RESNORM_POST;
   a.alpha = p->alpha;
@@ -54,11 +48,121 @@ RnArgs base_args(const cgtp_resnorm_s* p, int64_t N) {
   return a;
 }
 
-cgtp_status launch(const cgtp_resnorm_s* p, const RnArgs& a, bool backward, int ctas, cudaStream_t st) {
-  const cudaError_t e = p->dtype == CGTP_F64                          ? rn_launch_f64(a, backward, ctas, st)
-                        : p->dtype == CGTP_F32                        ? rn_launch_f32(a, backward, ctas, st)
-                        : (p->flags & CGTP_RESNORM_STORAGE)           ? rn_launch_bf16s(a, backward, ctas, st)
-                                                                      : rn_launch_bf16(a, backward, ctas, st);
+void set(RnRows* r, const void* ptr, int64_t ld, int64_t width, int es) {
+  r->ptr = const_cast<char*>(static_cast<const char*>(ptr));
+  r->ld = ld;
+  r->width = static_cast<int>(width);
+  r->es = es;
+}
+
+// widest copy (16, 8, 4 or 2 bytes) that divides every offset in `bits`
+int widest_copy(uint64_t bits) { return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2; }
+
+int round16(int64_t v) { return static_cast<int>((v + 15) / 16 * 16); }
+
+// Regions of a stage for tiles of `rows` rows.  An input whose rows lie side by side keeps that
+// layout (one run of bytes a tile); other rows start at multiples of 16 bytes.  A result takes
+// the region of an operand that is dead, element by element, when it is written (see the kernels).
+int lay_out(RnArgs* a, bool backward, int rows) {
+  int at = 0;
+  const auto own = [&](RnRows* r) {
+    const int dense = r->width * r->es;
+    r->linear = r->ld == r->width;
+    r->pitch = r->linear ? dense : round16(dense);
+    r->at = at;
+    at = round16(at + int64_t(rows) * r->pitch);
+  };
+  const auto over = [&](RnRows* r, const RnRows& in) {
+    r->at = in.at;
+    r->pitch = in.pitch;
+    r->linear = r->ld == r->width && r->pitch == r->width * r->es;
+  };
+  RnRows* t = a->t;
+  for (int i = 0; i < kRnInputs[backward]; ++i)
+    if (t[i].ptr) own(&t[i]);
+  if (!backward) {
+    if (t[kRnOut].ptr) over(&t[kRnOut], t[kRnH].ptr ? t[kRnH] : t[kRnZ]);
+    if (t[kRnY].ptr) {
+      if (t[kRnZ].ptr && t[kRnH].ptr) over(&t[kRnY], t[kRnZ]);
+      else if (!t[kRnZ].ptr && t[kRnY].es == t[kRnH].es) over(&t[kRnY], t[kRnH]);
+      else own(&t[kRnY]);
+    }
+  } else {
+    if (t[kRnGh].ptr) {
+      if (t[kRnGout].ptr) over(&t[kRnGh], t[kRnGout]);
+      else own(&t[kRnGh]);
+    }
+    if (t[kRnGz].ptr) {
+      if (t[kRnGy].ptr && t[kRnGz].es == t[kRnGy].es) over(&t[kRnGz], t[kRnGy]);
+      else own(&t[kRnGz]);
+    }
+    if (t[kRnGq].ptr) own(&t[kRnGq]);
+  }
+  for (int i = 0; i < (backward ? kRnBackward : kRnForward); ++i) {
+    RnRows& r = t[i];
+    if (!r.ptr) continue;
+    uint64_t bits = reinterpret_cast<uintptr_t>(r.ptr) | uint64_t(r.ld) * r.es * (r.linear ? rows : 1);
+    if (!r.linear) bits |= r.pitch;
+    r.vec = widest_copy(bits);
+  }
+  return at;
+}
+
+// How rows are dealt out (see resnorm_impl.cuh).
+void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
+  const int n_rows = backward ? kRnBackward : kRnForward, ep = es_param(p);
+  int lanes = 1;
+  while (lanes < 32 && lanes < p->widest) lanes *= 2;
+  const int abreast = 32 / lanes;
+  // Rows of a tile: as many as run side by side, and enough that a tile of every contiguous tensor
+  // starts at a multiple of 16 bytes.
+  int rows = abreast;
+  const auto aligned = [&] {
+    for (int i = 0; i < n_rows; ++i)
+      if (a->t[i].ptr && a->t[i].ld == a->t[i].width && (int64_t(rows) * a->t[i].width * a->t[i].es) % 16) return false;
+    return true;
+  };
+  while (!aligned()) rows *= 2;
+  // The fewest warps a row that still fill the CTA: more warps a row need fewer tiles in
+  // shared memory, but exchange their sums through it.  Shares that stay in registers go first.
+  const int factors = round16(2 * p->chan * ep);
+  int best = 0;
+  for (int warps = 1; warps <= kRnWarps; warps *= 2) {
+    if (warps > 1 && (lanes < 32 || warps * 32 >= 2 * p->widest)) break;
+    const int r = warps == 1 ? rows : std::max(1, rows / abreast);
+    const int stage = lay_out(a, backward, r);
+    const int64_t group = int64_t(kRnStages) * stage +
+                          round16(8 * kRnWarps * ep + (backward ? int64_t(warps == 1 ? abreast : 1) * 2 * p->chan * ep : 0));
+    const int groups = static_cast<int>(std::min<int64_t>((p->smem_cap - factors) / group, kRnWarps / warps));
+    int held = 1;
+    for (const RnBlock& b : p->blocks) held &= rn_share(b.D, b.mul, warps == 1 ? lanes : 32 * warps) > 0;
+    const int score = groups <= 0 ? 0 : held * 64 + groups * warps;
+    if (score > best) {
+      best = score;
+      a->staged = true;
+      a->warps = warps;
+      a->lanes = warps == 1 ? lanes : 32 * warps;
+      a->groups = groups;
+      a->rows = r;
+      a->group_bytes = static_cast<int>(group);
+    }
+  }
+  if (!a->staged) {
+    a->ctas = static_cast<int>(std::min<int64_t>(a->N, int64_t(p->num_sms) * kRnCtasPerSm));
+    return;
+  }
+  a->stage_bytes = lay_out(a, backward, a->rows);
+  a->smem = a->groups * a->group_bytes + factors;
+  a->tiles = (a->N + a->rows - 1) / a->rows;
+  a->ctas = static_cast<int>(std::min<int64_t>(a->tiles, p->num_sms));
+}
+
+cgtp_status launch(const cgtp_resnorm_s* p, RnArgs& a, bool backward, cudaStream_t st) {
+  deal(p, &a, backward);
+  const cudaError_t e = p->dtype == CGTP_F64                ? rn_launch_f64(a, backward, st)
+                        : p->dtype == CGTP_F32              ? rn_launch_f32(a, backward, st)
+                        : (p->flags & CGTP_RESNORM_STORAGE) ? rn_launch_bf16s(a, backward, st)
+                                                            : rn_launch_bf16(a, backward, st);
   return e == cudaSuccess ? CGTP_OK : fail(CGTP_ECUDA, std::string("resnorm: ") + cudaGetErrorString(e));
 }
 
@@ -66,27 +170,24 @@ cgtp_status create(cgtp_resnorm_s* p, const char* irreps) {
   std::vector<Irrep> ir;
   std::string err;
   if (!parse_irreps(irreps, &ir, &err)) return fail(CGTP_EINVAL, err);
-  int widest = 1;
   for (const Irrep& i : ir) {
     if (i.mul < 1) return fail(CGTP_EINVAL, "irreps blocks of a norm must have a channel");
     p->blocks.push_back({static_cast<int>(p->dim), static_cast<int>(p->chan), i.mul, 2 * i.l + 1});
     p->dim += int64_t(i.mul) * (2 * i.l + 1);
     p->chan += i.mul;
-    widest = std::max(widest, i.mul);
+    p->widest = std::max(p->widest, i.mul);
     if (p->dim > (1 << 20)) return fail(CGTP_EUNSUPPORTED, "rows of more than 1048576 elements");
   }
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&p->smem_cap, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) {
     cudaGetLastError();
     return fail(CGTP_ECUDA, "no CUDA device");
   }
-  p->team = 1;
-  while (p->team < 32 && p->team < widest) p->team *= 2;
-  if (p->dim > 4096) p->team = kRnThreads;
-  p->teams_max = p->num_sms * 8 * (kRnThreads / p->team);
+  p->smem_cap -= 512;   // the kernels' static shared memory
   const size_t tab = p->blocks.size() * sizeof(RnBlock);
-  const size_t part = size_t(p->teams_max) * 2 * p->chan * es_param(p);
+  const size_t part = size_t(p->num_sms) * kRnCtasPerSm * 2 * p->chan * es_param(p);
   if (cudaMalloc(reinterpret_cast<void**>(&p->blocks_dev), tab) != cudaSuccess || cudaMalloc(&p->part, part) != cudaSuccess) {
     cudaGetLastError();
     return fail(CGTP_ENOMEM, "norm table allocation failed");
@@ -183,13 +284,13 @@ cgtp_status cgtp_resnorm_forward(cgtp_resnorm p, int64_t N, const void* h, int64
       (s = param(pre, ep, "pre")))
     return s;
   if (N == 0) return CGTP_OK;
-  a.h = h, a.ld_h = ld_h;
-  a.z = z, a.ld_z = ld_z;
-  a.q = z && p->act != CGTP_ACT_NONE ? q : nullptr, a.ld_q = ld_q;
+  set(&a.t[kRnH], h, ld_h, p->dim, es);
+  set(&a.t[kRnZ], z, ld_z, p->dim, es);
+  set(&a.t[kRnQ], z && p->act != CGTP_ACT_NONE ? q : nullptr, ld_q, p->chan, es);
+  set(&a.t[kRnOut], out, ld_out, p->dim, es);
+  set(&a.t[kRnY], y, ld_y, p->dim, go);
   a.post = post, a.scale = scale, a.pre = pre;
-  a.out = out, a.ld_out = ld_out;
-  a.y = y, a.ld_y = ld_y;
-  return launch(p, a, false, ctas_for(p, N), static_cast<cudaStream_t>(stream));
+  return launch(p, a, false, static_cast<cudaStream_t>(stream));
 }
 
 cgtp_status cgtp_resnorm_backward(cgtp_resnorm p, int64_t N, const void* gout, int64_t ld_gout, const void* gy,
@@ -228,17 +329,17 @@ cgtp_status cgtp_resnorm_backward(cgtp_resnorm p, int64_t N, const void* gout, i
       }
     return CGTP_OK;
   }
-  a.gout = gout, a.ld_gout = ld_gout;
-  a.gy = gy, a.ld_gy = ld_gy;
-  a.x = x, a.ld_x = ld_x;
-  a.z = z, a.ld_z = ld_z;
-  a.q = gated ? q : nullptr, a.ld_q = ld_q;
+  set(&a.t[kRnGout], gout, ld_gout, p->dim, es);
+  set(&a.t[kRnGy], gy, ld_gy, p->dim, es);
+  set(&a.t[kRnX], a.pre_norm ? x : nullptr, ld_x, p->dim, es);
+  set(&a.t[kRnBz], z, ld_z, p->dim, es);
+  set(&a.t[kRnBq], gated ? q : nullptr, ld_q, p->chan, es);
+  set(&a.t[kRnGh], gh, ld_gh, p->dim, es);
+  set(&a.t[kRnGz], gz, ld_gz, p->dim, go);
+  set(&a.t[kRnGq], gq, ld_gq, p->chan, go);
   a.post = post, a.scale = scale, a.pre = pre;
-  a.gh = gh, a.ld_gh = ld_gh;
-  a.gz = gz, a.ld_gz = ld_gz;
-  a.gq = gated ? gq : nullptr, a.ld_gq = ld_gq;
   a.gpost = gpost, a.gscale = gscale, a.gpre = gpre;
-  return launch(p, a, true, ctas_for(p, N), st);
+  return launch(p, a, true, st);
 }
 
 }  // extern "C"

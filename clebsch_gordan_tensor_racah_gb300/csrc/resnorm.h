@@ -13,21 +13,39 @@ struct RnBlock {
   int off, coff, mul, D;
 };
 
-// Arguments of one launch.  Row distances are in elements.
+// A row tensor of a launch (distances in elements) and its place in a staged tile.
+struct RnRows {
+  char* ptr = nullptr;
+  int64_t ld = 0;
+  int width = 0, es = 0;    // elements of a row, bytes of an element
+  int at = -1, pitch = 0;   // first byte and row distance in bytes of its region of a stage; -1: no region
+  int vec = 0;              // bytes of a copy between the region and memory
+  bool linear = false;      // the rows of a tile are one run of bytes on both sides
+};
+
+enum { kRnH, kRnZ, kRnQ, kRnOut, kRnY, kRnForward };                                    // forward
+enum { kRnGout, kRnGy, kRnX, kRnBz, kRnBq, kRnGh, kRnGz, kRnGq, kRnBackward };          // backward
+constexpr int kRnInputs[2] = {3, 5};
+constexpr int kRnMaxRows = kRnBackward;
+
+// Arguments of one launch.
 struct RnArgs {
-  int64_t N = 0;
-  const void *h = nullptr, *z = nullptr, *q = nullptr, *gout = nullptr, *gy = nullptr, *x = nullptr;
-  int64_t ld_h = 0, ld_z = 0, ld_q = 0, ld_gout = 0, ld_gy = 0, ld_x = 0;
+  int64_t N = 0, tiles = 0;
+  RnRows t[kRnMaxRows];
   const void *post = nullptr, *scale = nullptr, *pre = nullptr;
-  void *out = nullptr, *y = nullptr, *gh = nullptr, *gz = nullptr, *gq = nullptr;
-  int64_t ld_out = 0, ld_y = 0, ld_gh = 0, ld_gz = 0, ld_gq = 0;
   void *gpost = nullptr, *gscale = nullptr, *gpre = nullptr;
   const RnBlock* blocks = nullptr;
-  void* part = nullptr;   // per team: [2][C] partial sums (see resnorm_impl.cuh)
+  void* part = nullptr;       // [CTAs][2][C] partial sums: of a(q) P, of gpre
   int n_blocks = 0, dim = 0, chan = 0, act = 0;
-  int team = 32;          // threads of a row: a power of two up to 32, or the whole CTA
   bool post_norm = false, pre_norm = false;
   double alpha = 1.0, eps = 0.0;
+  // how rows are dealt out
+  bool staged = false;
+  int lanes = 32;             // threads of a row: a power of two below a warp, or 32 * warps
+  int warps = 1;              // warps of a group
+  int groups = 1;             // groups of a CTA
+  int rows = 1;               // rows of a tile
+  int stage_bytes = 0, group_bytes = 0, smem = 0, ctas = 1;
 };
 
 }  // namespace cgtp
@@ -36,21 +54,36 @@ struct cgtp_resnorm_s {
   int dtype = 0, flags = 0, act = 0;
   double alpha = 1.0, eps = 0.0;
   int64_t dim = 0, chan = 0;
+  int widest = 1;             // channels of the widest block
   std::vector<cgtp::RnBlock> blocks;
   cgtp::RnBlock* blocks_dev = nullptr;
   void* part = nullptr;
-  int num_sms = 0, team = 32, teams_max = 0;
+  int num_sms = 0, smem_cap = 0;
   size_t device_bytes = 0;
 };
 
 namespace cgtp {
 
 // resnorm_*.cu: one translation unit per set of element types
-cudaError_t rn_launch_f32(const RnArgs& a, bool backward, int ctas, cudaStream_t st);
-cudaError_t rn_launch_f64(const RnArgs& a, bool backward, int ctas, cudaStream_t st);
-cudaError_t rn_launch_bf16(const RnArgs& a, bool backward, int ctas, cudaStream_t st);
-cudaError_t rn_launch_bf16s(const RnArgs& a, bool backward, int ctas, cudaStream_t st);
+cudaError_t rn_launch_f32(const RnArgs& a, bool backward, cudaStream_t st);
+cudaError_t rn_launch_f64(const RnArgs& a, bool backward, cudaStream_t st);
+cudaError_t rn_launch_bf16(const RnArgs& a, bool backward, cudaStream_t st);
+cudaError_t rn_launch_bf16s(const RnArgs& a, bool backward, cudaStream_t st);
 
-constexpr int kRnThreads = 256;
+// Channels of a block that a thread keeps in registers: mul / lanes rounded up to a share that the
+// kernels have code for, or 0.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int rn_share(int D, int mul, int lanes) {
+  const int k = (mul + lanes - 1) / lanes;
+  const int share = k <= 2 ? k : k <= 4 ? 4 : 0;
+  return D >= 9 ? (share == 1 ? 1 : 0) : D >= 5 ? (share <= 2 ? share : 0) : share;
+}
+
+constexpr int kRnStages = 2;        // tiles of a group in shared memory
+constexpr int kRnWarps = 16;        // warps of a CTA at most
+constexpr int kRnDirectWarps = 8;   // warps of a row that is too long for shared memory
+constexpr int kRnCtasPerSm = 4;     // of the unstaged kernels
 
 }  // namespace cgtp

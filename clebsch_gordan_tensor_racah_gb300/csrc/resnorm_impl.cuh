@@ -9,10 +9,17 @@
 //   gq_c = scale post a'(q) P_c,   A_c = sum_n a(q) P_c,   gpost = scale A,   gscale = post A,
 //   gpre_c = sum_n p sum_m gy out.
 //
-// A team of threads owns a row; a thread owns channels u, u + team, ... of every block, so the
-// sums over m (gates, parameter gradients) stay inside a thread and the only exchange is the
-// block sum of an rms.  Rows are dealt to teams by index and a channel's partial sums belong to
-// one thread of a team, so every sum has a fixed order.
+// A thread owns whole channels of a row (u, u + lanes, ... of every block), so the sums over m
+// (gates, parameter gradients) stay inside a thread and the only exchange is the block sum of an
+// rms.  A channel's 2l+1 components lie side by side, so reading channel by channel would
+// touch 2l+1 times the cache lines of a row; rows therefore pass through shared memory (odd
+// distances between the channels of neighbouring lanes: no bank conflicts), where each value is read
+// once from memory and once written.  A group of warps owns a ring of tiles: while it computes one,
+// the copies of the next are in flight.  Results go over the operands that they replace and
+// leave in wide runs.
+//
+// Rows are dealt to groups by index and a channel's partial sums belong to one thread of a
+// group, so every sum has a fixed order.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -23,17 +30,10 @@
 namespace cgtp {
 namespace {
 
-template <typename A>
-__device__ __forceinline__ A rn_get(const float* p) {
-  return static_cast<A>(*p);
-}
-template <typename A>
-__device__ __forceinline__ A rn_get(const double* p) {
-  return static_cast<A>(*p);
-}
-template <typename A>
-__device__ __forceinline__ A rn_get(const __nv_bfloat16* p) {
-  return static_cast<A>(__bfloat162float(*p));
+template <typename A, typename T>
+__device__ __forceinline__ A rn_get(const T* p) {
+  if constexpr (sizeof(T) == 2) return static_cast<A>(__bfloat162float(*p));
+  else return static_cast<A>(*p);
 }
 // stores v rounded once and returns what is stored
 __device__ __forceinline__ float rn_put(float* p, float v) { return *p = v; }
@@ -45,8 +45,9 @@ __device__ __forceinline__ float rn_put(__nv_bfloat16* p, float v) {
 
 __device__ __forceinline__ float rn_rsqrt(float v) { return rsqrtf(v); }
 __device__ __forceinline__ double rn_rsqrt(double v) { return rsqrt(v); }
-__device__ __forceinline__ float rn_exp(float v) { return expf(v); }
-__device__ __forceinline__ double rn_exp(double v) { return exp(v); }
+// 1 / (1 + e^-q): exponential and quotient to a few units in the last place, 0 and 1 far out
+__device__ __forceinline__ float rn_sigmoid(float q) { return __fdividef(1.0f, 1.0f + __expf(-q)); }
+__device__ __forceinline__ double rn_sigmoid(double q) { return 1.0 / (1.0 + exp(-q)); }
 
 // a(q) and, when asked for, a'(q)
 template <typename A>
@@ -55,261 +56,689 @@ __device__ __forceinline__ A rn_gate(int act, A q, A* derivative) {
     if (derivative) *derivative = A(1);
     return q;
   }
-  const A s = A(1) / (A(1) + rn_exp(-q));
-  if (act == CGTP_ACT_SIGMOID) {
-    if (derivative) *derivative = s * (A(1) - s);
-    return s;
+  const A s = rn_sigmoid(q);
+  const bool silu = act == CGTP_ACT_SILU;
+  if (derivative) *derivative = silu ? s + s * (q * (A(1) - s)) : s * (A(1) - s);
+  return silu ? q * s : s;
+}
+
+// Per-channel factors: post * scale and pre, in shared memory or read in place.
+template <bool STAGED, typename A>
+struct RnFactors {
+  const A *post, *scale, *pre;   // STAGED: post holds the product, and no pointer is null
+  __device__ __forceinline__ A base_at(int c) const {
+    if constexpr (STAGED) return post[c];
+    return (post ? __ldg(post + c) : A(1)) * (scale ? __ldg(scale + c) : A(1));
   }
-  if (derivative) *derivative = s * (A(1) + q * (A(1) - s));
-  return q * s;
-}
+  __device__ __forceinline__ A pre_at(int c) const {
+    if constexpr (STAGED) return pre[c];
+    return pre ? __ldg(pre + c) : A(1);
+  }
+};
 
-// Sum over the team.  Every thread of the CTA calls it the same number of times.
+// The threads of a row.  Groups of several warps exchange sums through `scratch`
+// (two banks in turn, so that one barrier separates the uses of a bank).
 template <typename A>
-__device__ __forceinline__ A rn_team_sum(A v, int team, A* scratch) {
-  const int wide = team < 32 ? team : 32;
-  for (int o = wide >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (team <= 32) return v;
-  __syncthreads();   // the previous sum has been read
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  A t = A(0);
-  for (int w = 0; w < kRnThreads / 32; ++w) t += scratch[w];
-  return t;
-}
+struct RnTeam {
+  int t, lanes, warps, barrier;   // place in the row, threads of a row, warps of the group, its named barrier
+  A* scratch;
+  int bank;
 
-template <typename A, typename P>
-__device__ __forceinline__ A rn_param(const void* p, int c) {
-  return p ? rn_get<A>(static_cast<const P*>(p) + c) : A(1);
-}
+  __device__ __forceinline__ void sync() const {
+    if (warps == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(warps * 32) : "memory");
+  }
+  // sums of K values over the row's threads; collective over the group
+  template <int K>
+  __device__ __forceinline__ void sum(A (&v)[K]) {
+    if (lanes >= 32) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < K; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    } else {
+      for (int o = lanes >> 1; o; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < K; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    }
+    if (warps == 1) {
+      __syncwarp();
+      return;
+    }
+    A* s = scratch + bank * 4 * kRnWarps;
+    bank ^= 1;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int i = 0; i < K; ++i) s[i * kRnWarps + (t >> 5)] = v[i];
+    sync();
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      v[i] = s[i * kRnWarps];
+      for (int w = 1; w < warps; ++w) v[i] += s[i * kRnWarps + w];
+    }
+  }
+};
+
+// Pointers to one row, in shared memory or in global memory.
+template <typename S, typename I, typename O>
+struct RnForwardRow {
+  const S* h;
+  const I *z, *q;
+  S* out;
+  O* y;
+};
+template <typename S, typename I, typename O, typename A>
+struct RnBackwardRow {
+  const S *g, *x;
+  const I *gy, *z, *q;
+  S* gh;
+  O *gz, *gq;
+  A* part;
+  bool live;   // false: a place without a row (its results stay in its place of the tile)
+};
 
 // S: residual stream, I: what comes from a product, O: what goes to one, A: arithmetic and parameters.
-template <typename S, typename I, typename O, typename A, int D>
-__device__ __forceinline__ void rn_forward_block(const RnArgs& a, const RnBlock b, int64_t n, bool live, int t,
-                                                 A* scratch) {
+// Results may lie over operands: an element is written by the thread that read it, after its last read.
+//
+// A block's values stay in registers where a thread's share, K channels of D components, is small
+// (every operand is then read once from shared memory); larger shares are read again for each pass.
+template <int D, int K, typename S, typename I, typename O, typename A, bool STAGED>
+__device__ __forceinline__ void rn_forward_held(const RnArgs& a, const RnBlock b, const RnForwardRow<S, I, O>& row,
+                                                const RnFactors<STAGED, A>& f, RnTeam<A>& team) {
   const A inv_n = A(1) / static_cast<A>(b.mul * D), eps = static_cast<A>(a.eps);
-  const S* h = a.h ? static_cast<const S*>(a.h) + n * a.ld_h + b.off : nullptr;
-  const I* z = a.z ? static_cast<const I*>(a.z) + n * a.ld_z + b.off : nullptr;
-  const I* q = a.q ? static_cast<const I*>(a.q) + n * a.ld_q + b.coff : nullptr;
-  S* out = a.out ? static_cast<S*>(a.out) + n * a.ld_out + b.off : nullptr;
-  const int step = a.team;
-  A r = A(1);
-  if (z && a.post_norm) {
-    A ss = A(0);
-    for (int u = t; u < b.mul; u += step)
+  const bool has_h = a.t[kRnH].ptr, has_z = a.t[kRnZ].ptr, gated = a.t[kRnQ].ptr;
+  A v[K][D], w[K];
+  A s[1] = {A(0)};
+  const I* z = row.z + b.off;
+  const S* h = row.h + b.off;
+  if (has_z) {
 #pragma unroll
-      for (int m = 0; m < D; ++m) {
-        const A v = rn_get<A>(z + u * D + m);
-        ss += v * v;
+    for (int k = 0; k < K; ++k) {
+      const int u = team.t + k * team.lanes;
+      w[k] = A(0);
+#pragma unroll
+      for (int m = 0; m < D; ++m) v[k][m] = A(0);
+      if (u < b.mul) {
+        w[k] = f.base_at(b.coff + u);
+        if (gated) w[k] *= rn_gate<A>(a.act, rn_get<A>(row.q + b.coff + u), nullptr);
+#pragma unroll
+        for (int m = 0; m < D; ++m) {
+          v[k][m] = rn_get<A>(z + u * D + m);
+          s[0] += v[k][m] * v[k][m];
+        }
       }
-    r = rn_rsqrt(rn_team_sum(ss, a.team, scratch) * inv_n + eps);
-  }
-  A ss = A(0);
-  for (int u = t; u < b.mul; u += step) {
-    if (z) {
-      const int c = b.coff + u;
-      A w = r * rn_param<A, A>(a.post, c) * rn_param<A, A>(a.scale, c);
-      if (q) w *= rn_gate<A>(a.act, rn_get<A>(q + u), nullptr);
+    }
+    if (a.post_norm) {
+      team.sum(s);
+      const A r = rn_rsqrt(s[0] * inv_n + eps);
 #pragma unroll
-      for (int m = 0; m < D; ++m) {
-        A v = w * rn_get<A>(z + u * D + m);
-        if (h) v += static_cast<A>(a.alpha) * rn_get<A>(h + u * D + m);
-        if (live) v = rn_put(out + u * D + m, v);
-        ss += v * v;
+      for (int k = 0; k < K; ++k) w[k] *= r;
+    }
+    s[0] = A(0);
+    S* out = row.out + b.off;
+    const A alpha = static_cast<A>(a.alpha);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int u = team.t + k * team.lanes;
+      if (u < b.mul) {
+        if (has_h) {
+#pragma unroll
+          for (int m = 0; m < D; ++m) v[k][m] = w[k] * v[k][m] + alpha * rn_get<A>(h + u * D + m);
+        } else {
+#pragma unroll
+          for (int m = 0; m < D; ++m) v[k][m] *= w[k];
+        }
+#pragma unroll
+        for (int m = 0; m < D; ++m) {
+          v[k][m] = rn_put(out + u * D + m, v[k][m]);
+          s[0] += v[k][m] * v[k][m];
+        }
       }
-    } else {
+    }
+  } else {
 #pragma unroll
-      for (int m = 0; m < D; ++m) {
-        const A v = rn_get<A>(h + u * D + m);
-        ss += v * v;
+    for (int k = 0; k < K; ++k) {
+      const int u = team.t + k * team.lanes;
+#pragma unroll
+      for (int m = 0; m < D; ++m) v[k][m] = A(0);
+      if (u < b.mul) {
+#pragma unroll
+        for (int m = 0; m < D; ++m) {
+          v[k][m] = rn_get<A>(h + u * D + m);
+          s[0] += v[k][m] * v[k][m];
+        }
       }
     }
   }
   if (!a.pre_norm) return;
-  const A p = rn_rsqrt(rn_team_sum(ss, a.team, scratch) * inv_n + eps);
-  if (!live) return;
-  const S* x = z ? out : h;
-  O* y = static_cast<O*>(a.y) + n * a.ld_y + b.off;
-  for (int u = t; u < b.mul; u += step) {
-    const A w = p * rn_param<A, A>(a.pre, b.coff + u);
+  team.sum(s);
+  const A p = rn_rsqrt(s[0] * inv_n + eps);
+  O* y = row.y + b.off;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int u = team.t + k * team.lanes;
+    if (u < b.mul) {
+      const A g = p * f.pre_at(b.coff + u);
+#pragma unroll
+      for (int m = 0; m < D; ++m) rn_put(y + u * D + m, g * v[k][m]);
+    }
+  }
+}
+
+template <int D, typename S, typename I, typename O, typename A, bool STAGED>
+__device__ __forceinline__ void rn_forward_block(const RnArgs& a, const RnBlock b, const RnForwardRow<S, I, O>& row,
+                                                 const RnFactors<STAGED, A>& f, RnTeam<A>& team) {
+  const A inv_n = A(1) / static_cast<A>(b.mul * D), eps = static_cast<A>(a.eps), alpha = static_cast<A>(a.alpha);
+  const bool has_h = a.t[kRnH].ptr, has_z = a.t[kRnZ].ptr, gated = a.t[kRnQ].ptr;
+  const S* h = row.h + b.off;
+  const I *z = row.z + b.off, *q = row.q + b.coff;
+  S* out = row.out + b.off;
+  O* y = row.y + b.off;
+  A r = A(1);
+  if (has_z && a.post_norm) {
+    A ss[1] = {A(0)};
+    for (int u = team.t; u < b.mul; u += team.lanes)
+#pragma unroll
+      for (int m = 0; m < D; ++m) {
+        const A v = rn_get<A>(z + u * D + m);
+        ss[0] += v * v;
+      }
+    team.sum(ss);
+    r = rn_rsqrt(ss[0] * inv_n + eps);
+  }
+  A ss[1] = {A(0)};
+  if (has_z) {
+    for (int u = team.t; u < b.mul; u += team.lanes) {
+      A w = r * f.base_at(b.coff + u);
+      if (gated) w *= rn_gate<A>(a.act, rn_get<A>(q + u), nullptr);
+#pragma unroll
+      for (int m = 0; m < D; ++m) {
+        A v = w * rn_get<A>(z + u * D + m);
+        if (has_h) v += alpha * rn_get<A>(h + u * D + m);
+        v = rn_put(out + u * D + m, v);
+        ss[0] += v * v;
+      }
+    }
+  } else {
+    for (int u = team.t; u < b.mul; u += team.lanes)
+#pragma unroll
+      for (int m = 0; m < D; ++m) {
+        const A v = rn_get<A>(h + u * D + m);
+        ss[0] += v * v;
+      }
+  }
+  if (!a.pre_norm) return;
+  team.sum(ss);
+  const A p = rn_rsqrt(ss[0] * inv_n + eps);
+  const S* x = has_z ? out : h;
+  for (int u = team.t; u < b.mul; u += team.lanes) {
+    const A w = p * f.pre_at(b.coff + u);
 #pragma unroll
     for (int m = 0; m < D; ++m) rn_put(y + u * D + m, w * rn_get<A>(x + u * D + m));
   }
 }
 
-template <typename S, typename I, typename O, typename A, int D>
-__device__ __forceinline__ void rn_backward_block(const RnArgs& a, const RnBlock b, int64_t n, bool live, int t,
-                                                  A* scratch, A* part) {
-  const A inv_n = A(1) / static_cast<A>(b.mul * D), eps = static_cast<A>(a.eps);
-  const S* g = a.gout ? static_cast<const S*>(a.gout) + n * a.ld_gout + b.off : nullptr;
-  const I* gy = a.pre_norm ? static_cast<const I*>(a.gy) + n * a.ld_gy + b.off : nullptr;
-  const S* x = a.pre_norm ? static_cast<const S*>(a.x) + n * a.ld_x + b.off : nullptr;
-  const I* z = a.z ? static_cast<const I*>(a.z) + n * a.ld_z + b.off : nullptr;
-  const I* q = a.q ? static_cast<const I*>(a.q) + n * a.ld_q + b.coff : nullptr;
-  S* gh = a.gh ? static_cast<S*>(a.gh) + n * a.ld_gh + b.off : nullptr;
-  O* gz = a.z ? static_cast<O*>(a.gz) + n * a.ld_gz + b.off : nullptr;
-  O* gq = a.q ? static_cast<O*>(a.gq) + n * a.ld_gq + b.coff : nullptr;
-  const int step = a.team;
-  A p = A(0), k = A(0), r = A(1);
-  if (a.pre_norm) {
-    A sx = A(0), sxy = A(0);
-    for (int u = t; u < b.mul; u += step) {
-      const A pre = rn_param<A, A>(a.pre, b.coff + u);
-      A xy = A(0);
+template <int D, int K, typename S, typename I, typename O, typename A, bool STAGED>
+__device__ __forceinline__ void rn_backward_held(const RnArgs& a, const RnBlock b,
+                                                 const RnBackwardRow<S, I, O, A>& row, const RnFactors<STAGED, A>& f,
+                                                 RnTeam<A>& team) {
+  const A inv_n = A(1) / static_cast<A>(b.mul * D), eps = static_cast<A>(a.eps), alpha = static_cast<A>(a.alpha);
+  const bool has_g = a.t[kRnGout].ptr, has_gh = a.t[kRnGh].ptr, has_z = a.t[kRnBz].ptr, gated = a.t[kRnBq].ptr;
+  const S *g = row.g + b.off, *x = row.x + b.off;
+  const I *gy = row.gy + b.off, *z = row.z + b.off;
+  A d[K][D], xv[K][D], zv[K][D], xy[K], pre[K];   // d starts as gy
+  A s[3] = {A(0), A(0), A(0)};                    // sums of x^2, of gy pre x, of z^2
 #pragma unroll
-      for (int m = 0; m < D; ++m) {
-        const A v = rn_get<A>(x + u * D + m);
-        sx += v * v;
-        xy += v * rn_get<A>(gy + u * D + m);
+  for (int k = 0; k < K; ++k) {
+    const int u = team.t + k * team.lanes;
+    xy[k] = pre[k] = A(0);
+#pragma unroll
+    for (int m = 0; m < D; ++m) d[k][m] = xv[k][m] = zv[k][m] = A(0);
+    if (u < b.mul) {
+      if (a.pre_norm) {
+        pre[k] = f.pre_at(b.coff + u);
+#pragma unroll
+        for (int m = 0; m < D; ++m) {
+          xv[k][m] = rn_get<A>(x + u * D + m);
+          d[k][m] = rn_get<A>(gy + u * D + m);
+          s[0] += xv[k][m] * xv[k][m];
+          xy[k] += xv[k][m] * d[k][m];
+        }
+        s[1] += pre[k] * xy[k];
       }
-      sxy += pre * xy;
+      if (has_z) {
+#pragma unroll
+        for (int m = 0; m < D; ++m) {
+          zv[k][m] = rn_get<A>(z + u * D + m);
+          s[2] += zv[k][m] * zv[k][m];
+        }
+      }
     }
-    p = rn_rsqrt(rn_team_sum(sx, a.team, scratch) * inv_n + eps);
-    k = p * p * p * inv_n * rn_team_sum(sxy, a.team, scratch);
   }
-  if (z && a.post_norm) {
-    A sz = A(0);
-    for (int u = t; u < b.mul; u += step)
+  A p = A(0), kx = A(0), r = A(1);
+  team.sum(s);
+  if (a.pre_norm) {
+    p = rn_rsqrt(s[0] * inv_n + eps);
+    kx = p * p * p * inv_n * s[1];
+  }
+  if (a.post_norm) r = rn_rsqrt(s[2] * inv_n + eps);
+  A along[1] = {A(0)}, w[K];   // sum over the block of w d z r
 #pragma unroll
-      for (int m = 0; m < D; ++m) {
-        const A v = rn_get<A>(z + u * D + m);
-        sz += v * v;
+  for (int k = 0; k < K; ++k) {
+    const int u = team.t + k * team.lanes, c = b.coff + u;
+    w[k] = A(0);
+    if (u < b.mul) {
+      const A gain = p * pre[k];
+      if (has_g) {
+#pragma unroll
+        for (int m = 0; m < D; ++m) d[k][m] = rn_get<A>(g + u * D + m) + (gain * d[k][m] - kx * xv[k][m]);
+      } else {
+#pragma unroll
+        for (int m = 0; m < D; ++m) d[k][m] = gain * d[k][m] - kx * xv[k][m];
       }
-    r = rn_rsqrt(rn_team_sum(sz, a.team, scratch) * inv_n + eps);
+      if (row.live && a.pre_norm) row.part[a.chan + c] += p * xy[k];
+      if (has_gh) {
+#pragma unroll
+        for (int m = 0; m < D; ++m) rn_put(row.gh + b.off + u * D + m, alpha * d[k][m]);
+      }
+      if (has_z) {
+        A P = A(0);
+#pragma unroll
+        for (int m = 0; m < D; ++m) P += d[k][m] * zv[k][m];
+        P *= r;
+        const A base = f.base_at(c);
+        A act = A(1), der = A(0);
+        if (gated) {
+          act = rn_gate<A>(a.act, rn_get<A>(row.q + c), &der);
+          rn_put(row.gq + c, base * der * P);
+        }
+        w[k] = base * act;
+        along[0] += w[k] * P;
+        if (row.live) row.part[c] += act * P;
+      }
+    }
   }
-  A along = A(0);   // sum over the block of w d z r
-  for (int u = t; u < b.mul; u += step) {
+  if (!has_z) return;
+  A kz = A(0);
+  if (a.post_norm) {
+    team.sum(along);
+    kz = r * r * inv_n * along[0];
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int u = team.t + k * team.lanes;
+    if (u < b.mul) {
+      const A wr = w[k] * r;
+#pragma unroll
+      for (int m = 0; m < D; ++m) rn_put(row.gz + b.off + u * D + m, wr * d[k][m] - kz * zv[k][m]);
+    }
+  }
+}
+
+template <int D, typename S, typename I, typename O, typename A, bool STAGED>
+__device__ __forceinline__ void rn_backward_block(const RnArgs& a, const RnBlock b,
+                                                  const RnBackwardRow<S, I, O, A>& row, const RnFactors<STAGED, A>& f,
+                                                  RnTeam<A>& team) {
+  const A inv_n = A(1) / static_cast<A>(b.mul * D), eps = static_cast<A>(a.eps), alpha = static_cast<A>(a.alpha);
+  const bool has_g = a.t[kRnGout].ptr, has_gh = a.t[kRnGh].ptr, has_z = a.t[kRnBz].ptr, gated = a.t[kRnBq].ptr;
+  const S *g = row.g + b.off, *x = row.x + b.off;
+  const I *gy = row.gy + b.off, *z = row.z + b.off, *q = row.q + b.coff;
+  S* gh = row.gh + b.off;
+  O *gz = row.gz + b.off, *gq = row.gq + b.coff;
+  A p = A(0), k = A(0), r = A(1);
+  if (a.pre_norm || (has_z && a.post_norm)) {
+    A s[3] = {A(0), A(0), A(0)};   // sums of x^2, of gy pre x, of z^2
+    for (int u = team.t; u < b.mul; u += team.lanes) {
+      if (a.pre_norm) {
+        A xy = A(0);
+#pragma unroll
+        for (int m = 0; m < D; ++m) {
+          const A v = rn_get<A>(x + u * D + m);
+          s[0] += v * v;
+          xy += v * rn_get<A>(gy + u * D + m);
+        }
+        s[1] += f.pre_at(b.coff + u) * xy;
+      }
+      if (has_z && a.post_norm)
+#pragma unroll
+        for (int m = 0; m < D; ++m) {
+          const A v = rn_get<A>(z + u * D + m);
+          s[2] += v * v;
+        }
+    }
+    team.sum(s);
+    if (a.pre_norm) {
+      p = rn_rsqrt(s[0] * inv_n + eps);
+      k = p * p * p * inv_n * s[1];
+    }
+    if (has_z && a.post_norm) r = rn_rsqrt(s[2] * inv_n + eps);
+  }
+  const bool again = has_z && a.post_norm;   // a third pass writes gh and gz
+  A along[1] = {A(0)};                       // sum over the block of w d z r
+  for (int u = team.t; u < b.mul; u += team.lanes) {
     const int c = b.coff + u;
-    const A pre = p * rn_param<A, A>(a.pre, c);
+    const A pre = a.pre_norm ? p * f.pre_at(c) : A(0);
     A P = A(0), xy = A(0), d[D];
 #pragma unroll
     for (int m = 0; m < D; ++m) {
-      A v = g ? rn_get<A>(g + u * D + m) : A(0);
-      if (gy) {
-        const A e = rn_get<A>(gy + u * D + m), f = rn_get<A>(x + u * D + m);
-        v += pre * e - k * f;
-        xy += e * f;
+      A v = has_g ? rn_get<A>(g + u * D + m) : A(0);
+      if (a.pre_norm) {
+        const A e = rn_get<A>(gy + u * D + m), o = rn_get<A>(x + u * D + m);
+        v += pre * e - k * o;
+        xy += e * o;
       }
       d[m] = v;
-      if (z) P += v * rn_get<A>(z + u * D + m);
+      if (has_z) P += v * rn_get<A>(z + u * D + m);
     }
-    if (live && gh)
-#pragma unroll
-      for (int m = 0; m < D; ++m) rn_put(gh + u * D + m, static_cast<A>(a.alpha) * d[m]);
-    if (live && gy) part[a.chan + c] += p * xy;
-    if (z) {
+    if (row.live && a.pre_norm) row.part[a.chan + c] += p * xy;
+    A w = A(0);
+    if (has_z) {
       P *= r;
-      const A base = rn_param<A, A>(a.post, c) * rn_param<A, A>(a.scale, c);
+      const A base = f.base_at(c);
       A act = A(1), der = A(0);
-      if (q) act = rn_gate<A>(a.act, rn_get<A>(q + u), &der);
-      along += base * act * P;
-      if (live) {
-        part[c] += act * P;
-        if (q) rn_put(gq + u, base * der * P);
-        if (!a.post_norm)
-#pragma unroll
-          for (int m = 0; m < D; ++m) rn_put(gz + u * D + m, base * act * d[m]);
-      }
+      if (gated) act = rn_gate<A>(a.act, rn_get<A>(q + u), &der);
+      w = base * act;
+      along[0] += w * P;
+      if (row.live) row.part[c] += act * P;
+      if (gated) rn_put(gq + u, base * der * P);
     }
+    if (!again)
+#pragma unroll
+      for (int m = 0; m < D; ++m) {
+        if (has_gh) rn_put(gh + u * D + m, alpha * d[m]);
+        if (has_z) rn_put(gz + u * D + m, w * d[m]);
+      }
   }
-  if (!z || !a.post_norm) return;
-  const A kz = r * r * inv_n * rn_team_sum(along, a.team, scratch);
-  if (!live) return;
-  for (int u = t; u < b.mul; u += step) {
+  if (!again) return;
+  team.sum(along);
+  const A kz = r * r * inv_n * along[0];
+  for (int u = team.t; u < b.mul; u += team.lanes) {
     const int c = b.coff + u;
-    const A pre = p * rn_param<A, A>(a.pre, c);
-    A w = r * rn_param<A, A>(a.post, c) * rn_param<A, A>(a.scale, c);
-    if (q) w *= rn_gate<A>(a.act, rn_get<A>(q + u), nullptr);
+    const A pre = a.pre_norm ? p * f.pre_at(c) : A(0);
+    A w = r * f.base_at(c);
+    if (gated) w *= rn_gate<A>(a.act, rn_get<A>(q + u), nullptr);
 #pragma unroll
     for (int m = 0; m < D; ++m) {
-      A v = g ? rn_get<A>(g + u * D + m) : A(0);
-      if (gy) v += pre * rn_get<A>(gy + u * D + m) - k * rn_get<A>(x + u * D + m);
-      rn_put(gz + u * D + m, w * v - kz * rn_get<A>(z + u * D + m));
+      A v = has_g ? rn_get<A>(g + u * D + m) : A(0);
+      if (a.pre_norm) v += pre * rn_get<A>(gy + u * D + m) - k * rn_get<A>(x + u * D + m);
+      const A e = w * v - kz * rn_get<A>(z + u * D + m);
+      if (has_gh) rn_put(gh + u * D + m, alpha * v);
+      rn_put(gz + u * D + m, e);
     }
   }
 }
 
-#define CGTP_RN_SWITCH(CALL)                                                                                      \
-  switch (b.D) {                                                                                                  \
-    case 1: CALL(1); break;                                                                                       \
-    case 3: CALL(3); break;                                                                                       \
-    case 5: CALL(5); break;                                                                                       \
-    case 7: CALL(7); break;                                                                                       \
-    case 9: CALL(9); break;                                                                                       \
-    case 11: CALL(11); break;                                                                                     \
-    case 13: CALL(13); break;                                                                                     \
-    default: CALL(15); break;                                                                                     \
+// A block by its number of components and the thread's share (rn_share).
+#define CGTP_RN_CASE(D, K) \
+  case D * 8 + K: HELD(D, K); break;
+#define CGTP_RN_HELD                                                                                          \
+  CGTP_RN_CASE(1, 1) CGTP_RN_CASE(1, 2) CGTP_RN_CASE(1, 4) CGTP_RN_CASE(3, 1) CGTP_RN_CASE(3, 2)             \
+  CGTP_RN_CASE(3, 4) CGTP_RN_CASE(5, 1) CGTP_RN_CASE(5, 2) CGTP_RN_CASE(7, 1) CGTP_RN_CASE(7, 2)             \
+  CGTP_RN_CASE(9, 1) CGTP_RN_CASE(11, 1) CGTP_RN_CASE(13, 1) CGTP_RN_CASE(15, 1)
+#define CGTP_RN_ANY                                                                                           \
+  switch (b.D) {                                                                                              \
+    case 1: ANY(1); break;                                                                                    \
+    case 3: ANY(3); break;                                                                                    \
+    case 5: ANY(5); break;                                                                                    \
+    case 7: ANY(7); break;                                                                                    \
+    case 9: ANY(9); break;                                                                                    \
+    case 11: ANY(11); break;                                                                                  \
+    case 13: ANY(13); break;                                                                                  \
+    default: ANY(15); break;                                                                                  \
   }
 
-template <typename S, typename I, typename O, typename A>
-__global__ void __launch_bounds__(kRnThreads) rn_forward_kernel(const RnArgs a) {
-  __shared__ A scratch[kRnThreads / 32];
-  const int teams = kRnThreads / a.team, t = threadIdx.x % a.team;
-  const int64_t all = (int64_t)gridDim.x * teams;
-  // every thread of a CTA runs the same number of rounds (the sums are collective)
-  for (int64_t n0 = (int64_t)blockIdx.x * teams; n0 < a.N; n0 += all) {
-    const int64_t mine = n0 + threadIdx.x / a.team;
-    const bool live = mine < a.N;
-    const int64_t n = live ? mine : a.N - 1;
-    for (int i = 0; i < a.n_blocks; ++i) {
-      const RnBlock b = a.blocks[i];
-#define CGTP_RN_CALL(D) rn_forward_block<S, I, O, A, D>(a, b, n, live, t, scratch)
-      CGTP_RN_SWITCH(CGTP_RN_CALL)
-#undef CGTP_RN_CALL
-    }
-  }
-}
-
-template <typename S, typename I, typename O, typename A>
-__global__ void __launch_bounds__(kRnThreads) rn_backward_kernel(const RnArgs a) {
-  __shared__ A scratch[kRnThreads / 32];
-  const int teams = kRnThreads / a.team, t = threadIdx.x % a.team;
-  const int64_t all = (int64_t)gridDim.x * teams;
-  const int64_t slot = (int64_t)blockIdx.x * teams + threadIdx.x / a.team;
-  A* part = static_cast<A*>(a.part) + slot * 2 * a.chan;
+template <bool STAGED, typename S, typename I, typename O, typename A>
+__device__ __forceinline__ void rn_row(const RnArgs& a, const RnBlock* blocks, const RnForwardRow<S, I, O>& row,
+                                       const RnFactors<STAGED, A>& f, RnTeam<A>& team) {
   for (int i = 0; i < a.n_blocks; ++i) {
-    const RnBlock b = a.blocks[i];
-    for (int u = t; u < b.mul; u += a.team) part[b.coff + u] = part[a.chan + b.coff + u] = A(0);
+    const RnBlock b = blocks[i];
+#define HELD(D, K) rn_forward_held<D, K>(a, b, row, f, team)
+#define ANY(D) rn_forward_block<D>(a, b, row, f, team)
+    if constexpr (STAGED) {
+      switch (b.D * 8 + rn_share(b.D, b.mul, team.lanes)) {
+        CGTP_RN_HELD
+        default: CGTP_RN_ANY
+      }
+    } else {
+      CGTP_RN_ANY
+    }
+#undef HELD
+#undef ANY
   }
-  for (int64_t n0 = (int64_t)blockIdx.x * teams; n0 < a.N; n0 += all) {
-    const int64_t mine = n0 + threadIdx.x / a.team;
-    const bool live = mine < a.N;
-    const int64_t n = live ? mine : a.N - 1;
-    for (int i = 0; i < a.n_blocks; ++i) {
-      const RnBlock b = a.blocks[i];
-#define CGTP_RN_CALL(D) rn_backward_block<S, I, O, A, D>(a, b, n, live, t, scratch, part)
-      CGTP_RN_SWITCH(CGTP_RN_CALL)
-#undef CGTP_RN_CALL
+}
+template <bool STAGED, typename S, typename I, typename O, typename A>
+__device__ __forceinline__ void rn_row(const RnArgs& a, const RnBlock* blocks, const RnBackwardRow<S, I, O, A>& row,
+                                       const RnFactors<STAGED, A>& f, RnTeam<A>& team) {
+  for (int i = 0; i < a.n_blocks; ++i) {
+    const RnBlock b = blocks[i];
+#define HELD(D, K) rn_backward_held<D, K>(a, b, row, f, team)
+#define ANY(D) rn_backward_block<D>(a, b, row, f, team)
+    if constexpr (STAGED) {
+      switch (b.D * 8 + rn_share(b.D, b.mul, team.lanes)) {
+        CGTP_RN_HELD
+        default: CGTP_RN_ANY
+      }
+    } else {
+      CGTP_RN_ANY
+    }
+#undef HELD
+#undef ANY
+  }
+}
+
+// row n of tensor i in memory
+template <typename T>
+__device__ __forceinline__ T* rn_at(const RnArgs& a, int i, int64_t n) {
+  return reinterpret_cast<T*>(a.t[i].ptr) + n * a.t[i].ld;
+}
+// row j of tensor i in a stage (the stage's first byte where the tensor has no region)
+template <typename T>
+__device__ __forceinline__ T* rn_in(const RnArgs& a, int i, char* stage, int j) {
+  return reinterpret_cast<T*>(stage + max(a.t[i].at, 0) + j * a.t[i].pitch);
+}
+
+// ---------------------------------------------------------------------------
+// Rows staged in shared memory
+// ---------------------------------------------------------------------------
+
+template <int V>
+__device__ __forceinline__ void rn_copy_in(char* dst, const char* src, int bytes, int t, int threads) {
+  const int whole = bytes / V;
+  for (int i = t; i < whole; i += threads) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst + i * V));
+    if constexpr (V == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src + i * V) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src + i * V), "n"(V) : "memory");
+  }
+  for (int i = whole * V + 2 * t; i < bytes; i += 2 * threads)
+    *reinterpret_cast<uint16_t*>(dst + i) = *reinterpret_cast<const uint16_t*>(src + i);
+}
+template <typename T>
+__device__ __forceinline__ void rn_copy_out(char* dst, const char* src, int bytes, int t, int threads) {
+  const int whole = bytes / static_cast<int>(sizeof(T));
+  for (int i = t; i < whole; i += threads) reinterpret_cast<T*>(dst)[i] = reinterpret_cast<const T*>(src)[i];
+  if constexpr (sizeof(T) > 2)
+    for (int i = whole * static_cast<int>(sizeof(T)) + 2 * t; i < bytes; i += 2 * threads)
+      *reinterpret_cast<uint16_t*>(dst + i) = *reinterpret_cast<const uint16_t*>(src + i);
+}
+
+// Rows [n0, n0 + count) of tensor r between memory and its region of the stage.
+template <bool IN>
+__device__ __forceinline__ void rn_move(const RnRows& r, char* stage, int64_t n0, int count, int t, int threads) {
+  char* mem = r.ptr + n0 * r.ld * r.es;
+  char* region = stage + r.at;
+  const int runs = r.linear ? 1 : count, bytes = r.width * r.es * (r.linear ? count : 1);
+  for (int j = 0; j < runs; ++j, mem += r.ld * r.es, region += r.pitch) {
+    if constexpr (IN) {
+      if (r.vec == 16) rn_copy_in<16>(region, mem, bytes, t, threads);
+      else if (r.vec == 8) rn_copy_in<8>(region, mem, bytes, t, threads);
+      else if (r.vec == 4) rn_copy_in<4>(region, mem, bytes, t, threads);
+      else for (int i = 2 * t; i < bytes; i += 2 * threads)
+        *reinterpret_cast<uint16_t*>(region + i) = *reinterpret_cast<const uint16_t*>(mem + i);
+    } else {
+      if (r.vec == 16) rn_copy_out<uint4>(mem, region, bytes, t, threads);
+      else if (r.vec == 8) rn_copy_out<uint2>(mem, region, bytes, t, threads);
+      else if (r.vec == 4) rn_copy_out<uint32_t>(mem, region, bytes, t, threads);
+      else rn_copy_out<uint16_t>(mem, region, bytes, t, threads);
     }
   }
 }
 
-// gpost = scale A, gscale = post A, gpre: the teams' partial sums added in team order.
-template <typename A>
-__global__ void rn_reduce_kernel(const RnArgs a, int slots) {
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= a.chan) return;
-  const A* part = static_cast<const A*>(a.part);
-  A s = A(0), g = A(0);
-  for (int i = 0; i < slots; ++i) {
-    s += part[(int64_t)i * 2 * a.chan + c];
-    g += part[(int64_t)i * 2 * a.chan + a.chan + c];
+template <bool BACKWARD, typename S, typename I, typename O, typename A>
+__global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __grid_constant__ RnArgs a) {
+  extern __shared__ __align__(16) char shared[];
+  __shared__ RnBlock few_blocks[16];
+  const int threads = a.warps * 32, g = threadIdx.x / threads, tg = threadIdx.x - g * threads;
+  const RnBlock* blocks = a.blocks;
+  if (a.n_blocks <= 16) {
+    for (int i = threadIdx.x; i < a.n_blocks; i += blockDim.x) few_blocks[i] = a.blocks[i];
+    blocks = few_blocks;
   }
-  if (a.gpost) static_cast<A*>(a.gpost)[c] = s * rn_param<A, A>(a.scale, c);
-  if (a.gscale) static_cast<A*>(a.gscale)[c] = s * rn_param<A, A>(a.post, c);
-  if (a.gpre) static_cast<A*>(a.gpre)[c] = g;
+  char* mine = shared + (size_t)g * a.group_bytes;
+  A* scratch = reinterpret_cast<A*>(mine + kRnStages * a.stage_bytes);
+  A* part = scratch + 8 * kRnWarps;                       // [rows at a time][2][C]
+  A* factors = reinterpret_cast<A*>(shared + (size_t)a.groups * a.group_bytes);   // post * scale [C], pre [C]
+  const RnFactors<false, A> read{static_cast<const A*>(a.post), static_cast<const A*>(a.scale), static_cast<const A*>(a.pre)};
+  for (int i = threadIdx.x; i < a.chan; i += blockDim.x) {
+    factors[i] = read.base_at(i);
+    factors[a.chan + i] = read.pre_at(i);
+  }
+  const RnFactors<true, A> f{factors, nullptr, factors + a.chan};
+  const int abreast = a.warps == 1 ? 32 / a.lanes : 1, sub = a.warps == 1 ? tg / a.lanes : 0;
+  RnTeam<A> team{tg - sub * a.lanes, a.lanes, a.warps, 1 + g, scratch, 0};
+  constexpr int first_out = kRnInputs[BACKWARD], last = BACKWARD ? kRnBackward : kRnForward;
+  if constexpr (BACKWARD)
+    for (int i = tg; i < abreast * 2 * a.chan; i += threads) part[i] = A(0);
+  __syncthreads();
+
+  const int64_t step = (int64_t)a.ctas * a.groups;
+  int64_t tile = (int64_t)g * a.ctas + blockIdx.x;
+  auto load = [&](int64_t k, char* stage) {
+    if (k < a.tiles) {
+      const int64_t n0 = k * a.rows;
+      const int count = static_cast<int>(min((int64_t)a.rows, a.N - n0));
+#pragma unroll
+      for (int i = 0; i < first_out; ++i)
+        if (a.t[i].ptr) rn_move<true>(a.t[i], stage, n0, count, tg, threads);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < kRnStages; ++s) load(tile + s * step, mine + s * a.stage_bytes);
+  for (int s = 0; tile < a.tiles; tile += step, s = s + 1 == kRnStages ? 0 : s + 1) {
+    char* stage = mine + s * a.stage_bytes;
+    const int64_t n0 = tile * a.rows;
+    const int count = static_cast<int>(min((int64_t)a.rows, a.N - n0));
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRnStages - 1) : "memory");
+    team.sync();
+    for (int j0 = 0; j0 < count; j0 += abreast) {
+      const int j = j0 + sub;
+      if constexpr (BACKWARD) {
+        const RnBackwardRow<S, I, O, A> row{
+            rn_in<S>(a, kRnGout, stage, j), rn_in<S>(a, kRnX, stage, j),  rn_in<I>(a, kRnGy, stage, j),
+            rn_in<I>(a, kRnBz, stage, j),   rn_in<I>(a, kRnBq, stage, j), rn_in<S>(a, kRnGh, stage, j),
+            rn_in<O>(a, kRnGz, stage, j),   rn_in<O>(a, kRnGq, stage, j), part + sub * 2 * a.chan, j < count};
+        rn_row(a, blocks, row, f, team);
+      } else {
+        const RnForwardRow<S, I, O> row{rn_in<S>(a, kRnH, stage, j), rn_in<I>(a, kRnZ, stage, j),
+                                        rn_in<I>(a, kRnQ, stage, j), rn_in<S>(a, kRnOut, stage, j),
+                                        rn_in<O>(a, kRnY, stage, j)};
+        rn_row(a, blocks, row, f, team);
+      }
+    }
+    team.sync();
+#pragma unroll
+    for (int i = first_out; i < last; ++i)
+      if (a.t[i].ptr) rn_move<false>(a.t[i], stage, n0, count, tg, threads);
+    team.sync();
+    load(tile + kRnStages * step, stage);
+  }
+  if constexpr (BACKWARD) {
+    // the CTA's sums: groups in order, and in a group the rows that ran side by side
+    __syncthreads();
+    A* to = static_cast<A*>(a.part) + (int64_t)blockIdx.x * 2 * a.chan;
+    for (int i = threadIdx.x; i < 2 * a.chan; i += blockDim.x) {
+      A v = A(0);
+      for (int k = 0; k < a.groups; ++k) {
+        const A* p = reinterpret_cast<const A*>(shared + (size_t)k * a.group_bytes + kRnStages * a.stage_bytes) + 8 * kRnWarps;
+        for (int j = 0; j < abreast; ++j) v += p[j * 2 * a.chan + i];
+      }
+      to[i] = v;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows that do not fit in shared memory: a CTA reads a row in place
+// ---------------------------------------------------------------------------
+
+template <bool BACKWARD, typename S, typename I, typename O, typename A>
+__global__ void __launch_bounds__(kRnDirectWarps * 32) rn_direct_kernel(const __grid_constant__ RnArgs a) {
+  __shared__ A scratch[8 * kRnWarps];
+  RnTeam<A> team{static_cast<int>(threadIdx.x), kRnDirectWarps * 32, kRnDirectWarps, 1, scratch, 0};
+  const RnFactors<false, A> f{static_cast<const A*>(a.post), static_cast<const A*>(a.scale), static_cast<const A*>(a.pre)};
+  A* part = static_cast<A*>(a.part) + (int64_t)blockIdx.x * 2 * a.chan;
+  if constexpr (BACKWARD) {
+    // a channel's sums are kept by the thread that owns the channel
+    for (int i = 0; i < a.n_blocks; ++i) {
+      const RnBlock b = a.blocks[i];
+      for (int u = team.t; u < b.mul; u += team.lanes) part[b.coff + u] = part[a.chan + b.coff + u] = A(0);
+    }
+  }
+  for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
+    if constexpr (BACKWARD) {
+      const RnBackwardRow<S, I, O, A> row{rn_at<S>(a, kRnGout, n), rn_at<S>(a, kRnX, n), rn_at<I>(a, kRnGy, n),
+                                          rn_at<I>(a, kRnBz, n),   rn_at<I>(a, kRnBq, n), rn_at<S>(a, kRnGh, n),
+                                          rn_at<O>(a, kRnGz, n),   rn_at<O>(a, kRnGq, n), part, true};
+      rn_row(a, a.blocks, row, f, team);
+    } else {
+      const RnForwardRow<S, I, O> row{rn_at<S>(a, kRnH, n), rn_at<I>(a, kRnZ, n), rn_at<I>(a, kRnQ, n),
+                                      rn_at<S>(a, kRnOut, n), rn_at<O>(a, kRnY, n)};
+      rn_row(a, a.blocks, row, f, team);
+    }
+  }
+}
+
+// gpost = scale A, gscale = post A, gpre from the CTAs' partial sums: 8 threads a column, then in order.
+template <typename A>
+__global__ void __launch_bounds__(256) rn_reduce_kernel(const void* part_, int ctas, int chan, const void* post, const void* scale,
+                                                        void* gpost, void* gscale, void* gpre) {
+  __shared__ A sums[8][33];
+  const A* part = static_cast<const A*>(part_);
+  const int lane = threadIdx.x & 31, seg = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
+  A v = A(0);
+  if (i < 2 * chan)
+    for (int k = seg; k < ctas; k += 8) v += part[(int64_t)k * 2 * chan + i];
+  sums[seg][lane] = v;
+  __syncthreads();
+  if (seg != 0 || i >= 2 * chan) return;
+  for (int k = 1; k < 8; ++k) v += sums[k][lane];
+  const int c = i < chan ? i : i - chan;
+  if (i < chan) {
+    if (gpost) static_cast<A*>(gpost)[c] = scale ? v * static_cast<const A*>(scale)[c] : v;
+    if (gscale) static_cast<A*>(gscale)[c] = post ? v * static_cast<const A*>(post)[c] : v;
+  } else if (gpre) {
+    static_cast<A*>(gpre)[c] = v;
+  }
+}
+
+template <bool BACKWARD, typename S, typename I, typename O, typename A>
+cudaError_t rn_launch_one(const RnArgs& a, cudaStream_t st) {
+  if (a.staged) {
+    if (smem_cap_cached(reinterpret_cast<const void*>(rn_staged_kernel<BACKWARD, S, I, O, A>)) < a.smem)
+      return cudaErrorInvalidConfiguration;
+    rn_staged_kernel<BACKWARD, S, I, O, A><<<a.ctas, a.groups * a.warps * 32, a.smem, st>>>(a);
+  } else {
+    rn_direct_kernel<BACKWARD, S, I, O, A><<<a.ctas, kRnDirectWarps * 32, 0, st>>>(a);
+  }
+  return cudaGetLastError();
 }
 
 template <typename S, typename I, typename O, typename A>
-cudaError_t rn_launch(const RnArgs& a, bool backward, int ctas, cudaStream_t st) {
-  if (!backward) {
-    rn_forward_kernel<S, I, O, A><<<ctas, kRnThreads, 0, st>>>(a);
-    return cudaGetLastError();
-  }
-  rn_backward_kernel<S, I, O, A><<<ctas, kRnThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+cudaError_t rn_launch(const RnArgs& a, bool backward, cudaStream_t st) {
+  if (!backward) return rn_launch_one<false, S, I, O, A>(a, st);
+  const cudaError_t e = rn_launch_one<true, S, I, O, A>(a, st);
   if (e != cudaSuccess || !(a.gpost || a.gscale || a.gpre)) return e;
-  rn_reduce_kernel<A><<<(a.chan + 127) / 128, 128, 0, st>>>(a, ctas * (kRnThreads / a.team));
+  rn_reduce_kernel<A><<<(2 * a.chan + 31) / 32, 256, 0, st>>>(a.part, a.ctas, a.chan, a.post, a.scale, a.gpost, a.gscale, a.gpre);
   return cudaGetLastError();
 }
 
