@@ -37,6 +37,7 @@ RnArgs base_args(const cgtp_resnorm_s* p, int64_t N) {
   a.N = N;
   a.blocks = p->blocks_dev;
   a.n_blocks = static_cast<int>(p->blocks.size());
+  std::copy(p->blocks.begin(), p->blocks.begin() + std::min<size_t>(p->blocks.size(), kRnInline), a.few);
   a.dim = static_cast<int>(p->dim);
   a.chan = static_cast<int>(p->chan);
   a.act = p->act;
@@ -44,6 +45,8 @@ RnArgs base_args(const cgtp_resnorm_s* p, int64_t N) {
   a.post_norm = p->flags & CGTP_RESNORM_POST;
   a.alpha = p->alpha;
   a.eps = p->eps;
+  a.alpha_f = static_cast<float>(p->alpha);
+  a.eps_f = static_cast<float>(p->eps);
   a.part = p->part;
   return a;
 }
@@ -51,6 +54,7 @@ RnArgs base_args(const cgtp_resnorm_s* p, int64_t N) {
 void set(RnRows* r, const void* ptr, int64_t ld, int64_t width, int es) {
   r->ptr = const_cast<char*>(static_cast<const char*>(ptr));
   r->ld = ld;
+  r->ld_bytes = ld * es;
   r->width = static_cast<int>(width);
   r->es = es;
 }
@@ -123,31 +127,35 @@ void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
     return true;
   };
   while (!aligned()) rows *= 2;
-  // The fewest warps a row that still fill the CTA: more warps a row need fewer tiles in
-  // shared memory, but exchange their sums through it.  Shares that stay in registers go first.
   const int factors = round16(2 * p->chan * ep);
+  const auto group_of = [&](int warps, int stages, int r) {
+    const int64_t kept = (warps > 1 ? 8 * kRnWarps : 0) + (backward ? int64_t(warps == 1 ? abreast : 1) * 2 * p->chan : 0);
+    return int64_t(stages) * lay_out(a, backward, r) + round16(kept * ep);
+  };
   int best = 0;
   for (int warps = 1; warps <= kRnWarps; warps *= 2) {
-    if (warps > 1 && (lanes < 32 || warps * 32 >= 2 * p->widest)) break;
+    if (warps > 1 && warps * 32 >= 2 * p->widest) break;
+    const int width = warps == 1 ? lanes : 32 * warps;
+    int held = p->blocks.size() <= kRnInline;
+    for (const RnBlock& b : p->blocks) held &= rn_share(b.D, b.mul, width) > 0;
+    if (warps == 1 && !held) continue;
     const int r = warps == 1 ? rows : std::max(1, rows / abreast);
-    const int stage = lay_out(a, backward, r);
-    const int64_t group = int64_t(kRnStages) * stage +
-                          round16(8 * kRnWarps * ep + (backward ? int64_t(warps == 1 ? abreast : 1) * 2 * p->chan * ep : 0));
-    const int groups = static_cast<int>(std::min<int64_t>((p->smem_cap - factors) / group, kRnWarps / warps));
-    int held = 1;
-    for (const RnBlock& b : p->blocks) held &= rn_share(b.D, b.mul, warps == 1 ? lanes : 32 * warps) > 0;
-    const int score = groups <= 0 ? 0 : held * 64 + groups * warps;
-    if (score > best) {
+    for (int stages = kRnMaxStages; stages >= 1; --stages) {
+      const int64_t group = group_of(warps, stages, r);
+      const int groups = static_cast<int>(std::min<int64_t>((p->smem_cap - factors) / group, kRnWarps / warps));
+      const int score = groups <= 0 ? 0 : held * 64 + groups * warps;
+      if (score <= best) continue;
       best = score;
-      a->staged = true;
+      a->kind = warps == 1 ? kRnOne : kRnMany;
+      a->stages = stages;
       a->warps = warps;
-      a->lanes = warps == 1 ? lanes : 32 * warps;
+      a->lanes = width;
       a->groups = groups;
       a->rows = r;
       a->group_bytes = static_cast<int>(group);
     }
   }
-  if (!a->staged) {
+  if (a->kind == kRnDirect) {
     a->ctas = static_cast<int>(std::min<int64_t>(a->N, int64_t(p->num_sms) * kRnCtasPerSm));
     return;
   }
@@ -155,6 +163,13 @@ void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
   a->smem = a->groups * a->group_bytes + factors;
   a->tiles = (a->N + a->rows - 1) / a->rows;
   a->ctas = static_cast<int>(std::min<int64_t>(a->tiles, p->num_sms));
+  for (size_t i = 0; i < std::min<size_t>(p->blocks.size(), kRnInline); ++i)
+    a->few[i].code = 8 * a->few[i].D + rn_share(a->few[i].D, a->few[i].mul, a->lanes);
+  if (a->kind == kRnOne && a->pre_norm && a->post_norm) {
+    bool full = true;
+    for (int i = 0; i < n_rows; ++i) full &= a->t[i].ptr != nullptr;
+    if (full) a->kind = kRnOneFull;
+  }
 }
 
 cgtp_status launch(const cgtp_resnorm_s* p, RnArgs& a, bool backward, cudaStream_t st) {
@@ -172,7 +187,9 @@ cgtp_status create(cgtp_resnorm_s* p, const char* irreps) {
   if (!parse_irreps(irreps, &ir, &err)) return fail(CGTP_EINVAL, err);
   for (const Irrep& i : ir) {
     if (i.mul < 1) return fail(CGTP_EINVAL, "irreps blocks of a norm must have a channel");
-    p->blocks.push_back({static_cast<int>(p->dim), static_cast<int>(p->chan), i.mul, 2 * i.l + 1});
+    const double inv_n = 1.0 / (double(i.mul) * (2 * i.l + 1));
+    p->blocks.push_back({static_cast<int>(p->dim), static_cast<int>(p->chan), i.mul, 2 * i.l + 1, 0,
+                         static_cast<float>(inv_n), inv_n});
     p->dim += int64_t(i.mul) * (2 * i.l + 1);
     p->chan += i.mul;
     p->widest = std::max(p->widest, i.mul);
@@ -267,6 +284,7 @@ cgtp_status cgtp_resnorm_forward(cgtp_resnorm p, int64_t N, const void* h, int64
   clear_error();
   if (!p) return fail(CGTP_EINVAL, "null plan");
   if (N < 0) return fail(CGTP_EINVAL, "N must be >= 0");
+  if (N >= (int64_t(1) << 30)) return fail(CGTP_EUNSUPPORTED, "N must be below 2^30");
   RnArgs a = base_args(p, N);
   if (N > 0) {
     if (!z && !h) return fail(CGTP_EINVAL, "null pointer: h and z");
@@ -301,6 +319,7 @@ cgtp_status cgtp_resnorm_backward(cgtp_resnorm p, int64_t N, const void* gout, i
   clear_error();
   if (!p) return fail(CGTP_EINVAL, "null plan");
   if (N < 0) return fail(CGTP_EINVAL, "N must be >= 0");
+  if (N >= (int64_t(1) << 30)) return fail(CGTP_EUNSUPPORTED, "N must be below 2^30");
   RnArgs a = base_args(p, N);
   const bool gated = z && p->act != CGTP_ACT_NONE;
   if (N > 0) {

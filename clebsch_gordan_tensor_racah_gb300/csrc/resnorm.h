@@ -11,12 +11,15 @@ namespace cgtp {
 // One irreps block of a row: channels [coff, coff + mul), elements [off, off + mul * D).
 struct RnBlock {
   int off, coff, mul, D;
+  int code;            // 8 D + channels of a thread (rn_share), set for a launch
+  float inv_n_f;       // 1 / (mul D)
+  double inv_n;
 };
 
 // A row tensor of a launch (distances in elements) and its place in a staged tile.
 struct RnRows {
   char* ptr = nullptr;
-  int64_t ld = 0;
+  int64_t ld = 0, ld_bytes = 0;
   int width = 0, es = 0;    // elements of a row, bytes of an element
   int at = -1, pitch = 0;   // first byte and row distance in bytes of its region of a stage; -1: no region
   int vec = 0;              // bytes of a copy between the region and memory
@@ -28,19 +31,27 @@ enum { kRnGout, kRnGy, kRnX, kRnBz, kRnBq, kRnGh, kRnGz, kRnGq, kRnBackward };  
 constexpr int kRnInputs[2] = {3, 5};
 constexpr int kRnMaxRows = kRnBackward;
 
+constexpr int kRnInline = 16;
+// kRnOneFull: a warp a row, every operand there.  kRnOne: a warp a row.  kRnMany: several warps a row, any
+// number and size of blocks.  kRnDirect: rows in place, a CTA a row.
+enum RnKind { kRnDirect, kRnMany, kRnOne, kRnOneFull };
+
 // Arguments of one launch.
 struct RnArgs {
   int64_t N = 0, tiles = 0;
   RnRows t[kRnMaxRows];
   const void *post = nullptr, *scale = nullptr, *pre = nullptr;
   void *gpost = nullptr, *gscale = nullptr, *gpre = nullptr;
-  const RnBlock* blocks = nullptr;
+  const RnBlock* blocks = nullptr;   // device table; the first kRnInline blocks also in `few`
+  RnBlock few[16];
   void* part = nullptr;       // [CTAs][2][C] partial sums: of a(q) P, of gpre
   int n_blocks = 0, dim = 0, chan = 0, act = 0;
   bool post_norm = false, pre_norm = false;
   double alpha = 1.0, eps = 0.0;
+  float alpha_f = 1.0f, eps_f = 0.0f;
   // how rows are dealt out
-  bool staged = false;
+  int kind = 0;               // RnKind
+  int stages = 1;             // tiles of a group in shared memory
   int lanes = 32;             // threads of a row: a power of two below a warp, or 32 * warps
   int warps = 1;              // warps of a group
   int groups = 1;             // groups of a CTA
@@ -76,12 +87,11 @@ cudaError_t rn_launch_bf16s(const RnArgs& a, bool backward, cudaStream_t st);
 __host__ __device__
 #endif
 inline int rn_share(int D, int mul, int lanes) {
-  const int k = (mul + lanes - 1) / lanes;
-  const int share = k <= 2 ? k : k <= 4 ? 4 : 0;
-  return D >= 9 ? (share == 1 ? 1 : 0) : D >= 5 ? (share <= 2 ? share : 0) : share;
+  const int share = mul <= lanes ? 1 : mul <= 2 * lanes ? 2 : mul <= 4 * lanes ? 4 : 0;
+  return share <= (D <= 5 ? 4 : D <= 7 ? 2 : 1) ? share : 0;
 }
 
-constexpr int kRnStages = 2;        // tiles of a group in shared memory
+constexpr int kRnMaxStages = 2;     // tiles of a group in shared memory
 constexpr int kRnWarps = 16;        // warps of a CTA at most
 constexpr int kRnDirectWarps = 8;   // warps of a row that is too long for shared memory
 constexpr int kRnCtasPerSm = 4;     // of the unstaged kernels

@@ -76,22 +76,24 @@ struct RnFactors {
   }
 };
 
-// The threads of a row.  Groups of several warps exchange sums through `scratch`
+// The threads of a row.  Groups of several warps (ONE = false) exchange sums through `scratch`
 // (two banks in turn, so that one barrier separates the uses of a bank).
-template <typename A>
+template <typename A, bool ONE>
 struct RnTeam {
   int t, lanes, warps, barrier;   // place in the row, threads of a row, warps of the group, its named barrier
   A* scratch;
   int bank;
 
   __device__ __forceinline__ void sync() const {
-    if (warps == 1) __syncwarp();
+    if constexpr (ONE) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(warps * 32) : "memory");
   }
+  // distance between a thread's channels; one warp: rows of fewer lanes have one channel a thread at most
+  __device__ __forceinline__ int stride() const { return ONE ? 32 : lanes; }
   // sums of K values over the row's threads; collective over the group
   template <int K>
   __device__ __forceinline__ void sum(A (&v)[K]) {
-    if (lanes >= 32) {
+    if (!ONE || lanes == 32) {
 #pragma unroll
       for (int o = 16; o; o >>= 1)
 #pragma unroll
@@ -101,7 +103,7 @@ struct RnTeam {
 #pragma unroll
         for (int i = 0; i < K; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     }
-    if (warps == 1) {
+    if constexpr (ONE) {
       __syncwarp();
       return;
     }
@@ -118,6 +120,22 @@ struct RnTeam {
     }
   }
 };
+
+template <typename A>
+__device__ __forceinline__ A rn_eps(const RnArgs& a) {
+  if constexpr (sizeof(A) == 8) return a.eps;
+  return a.eps_f;
+}
+template <typename A>
+__device__ __forceinline__ A rn_alpha(const RnArgs& a) {
+  if constexpr (sizeof(A) == 8) return a.alpha;
+  return a.alpha_f;
+}
+template <typename A>
+__device__ __forceinline__ A rn_inv_n(const RnBlock& b) {
+  if constexpr (sizeof(A) == 8) return b.inv_n;
+  return b.inv_n_f;
+}
 
 // Pointers to one row, in shared memory or in global memory.
 template <typename S, typename I, typename O>
@@ -142,11 +160,12 @@ struct RnBackwardRow {
 //
 // A block's values stay in registers where a thread's share, K channels of D components, is small
 // (every operand is then read once from shared memory); larger shares are read again for each pass.
-template <int D, int K, typename S, typename I, typename O, typename A, bool STAGED>
-__device__ __forceinline__ void rn_forward_held(const RnArgs& a, const RnBlock b, const RnForwardRow<S, I, O>& row,
-                                                const RnFactors<STAGED, A>& f, RnTeam<A>& team) {
-  const A inv_n = A(1) / static_cast<A>(b.mul * D), eps = static_cast<A>(a.eps);
-  const bool has_h = a.t[kRnH].ptr, has_z = a.t[kRnZ].ptr, gated = a.t[kRnQ].ptr;
+template <int D, int K, bool FULL, typename S, typename I, typename O, typename A, bool STAGED, bool ONE>
+__device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b, const RnForwardRow<S, I, O>& row,
+                                                const RnFactors<STAGED, A>& f, RnTeam<A, ONE>& team) {
+  const A inv_n = rn_inv_n<A>(b), eps = rn_eps<A>(a);
+  const bool has_h = FULL || a.t[kRnH].ptr, has_z = FULL || a.t[kRnZ].ptr, gated = FULL || a.t[kRnQ].ptr;
+  const bool pre_norm = FULL || a.pre_norm, post_norm = FULL || a.post_norm;
   A v[K][D], w[K];
   A s[1] = {A(0)};
   const I* z = row.z + b.off;
@@ -154,7 +173,7 @@ __device__ __forceinline__ void rn_forward_held(const RnArgs& a, const RnBlock b
   if (has_z) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int u = team.t + k * team.lanes;
+      const int u = team.t + k * team.stride();
       w[k] = A(0);
 #pragma unroll
       for (int m = 0; m < D; ++m) v[k][m] = A(0);
@@ -168,7 +187,7 @@ __device__ __forceinline__ void rn_forward_held(const RnArgs& a, const RnBlock b
         }
       }
     }
-    if (a.post_norm) {
+    if (post_norm) {
       team.sum(s);
       const A r = rn_rsqrt(s[0] * inv_n + eps);
 #pragma unroll
@@ -176,10 +195,10 @@ __device__ __forceinline__ void rn_forward_held(const RnArgs& a, const RnBlock b
     }
     s[0] = A(0);
     S* out = row.out + b.off;
-    const A alpha = static_cast<A>(a.alpha);
+    const A alpha = rn_alpha<A>(a);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int u = team.t + k * team.lanes;
+      const int u = team.t + k * team.stride();
       if (u < b.mul) {
         if (has_h) {
 #pragma unroll
@@ -198,7 +217,7 @@ __device__ __forceinline__ void rn_forward_held(const RnArgs& a, const RnBlock b
   } else {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int u = team.t + k * team.lanes;
+      const int u = team.t + k * team.stride();
 #pragma unroll
       for (int m = 0; m < D; ++m) v[k][m] = A(0);
       if (u < b.mul) {
@@ -210,13 +229,13 @@ __device__ __forceinline__ void rn_forward_held(const RnArgs& a, const RnBlock b
       }
     }
   }
-  if (!a.pre_norm) return;
+  if (!pre_norm) return;
   team.sum(s);
   const A p = rn_rsqrt(s[0] * inv_n + eps);
   O* y = row.y + b.off;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int u = team.t + k * team.lanes;
+    const int u = team.t + k * team.stride();
     if (u < b.mul) {
       const A g = p * f.pre_at(b.coff + u);
 #pragma unroll
@@ -225,10 +244,10 @@ __device__ __forceinline__ void rn_forward_held(const RnArgs& a, const RnBlock b
   }
 }
 
-template <int D, typename S, typename I, typename O, typename A, bool STAGED>
-__device__ __forceinline__ void rn_forward_block(const RnArgs& a, const RnBlock b, const RnForwardRow<S, I, O>& row,
-                                                 const RnFactors<STAGED, A>& f, RnTeam<A>& team) {
-  const A inv_n = A(1) / static_cast<A>(b.mul * D), eps = static_cast<A>(a.eps), alpha = static_cast<A>(a.alpha);
+template <int D, typename S, typename I, typename O, typename A, bool STAGED, bool ONE>
+__device__ __forceinline__ void rn_block_any(const RnArgs& a, const RnBlock b, const RnForwardRow<S, I, O>& row,
+                                                 const RnFactors<STAGED, A>& f, RnTeam<A, ONE>& team) {
+  const A inv_n = rn_inv_n<A>(b), eps = rn_eps<A>(a), alpha = rn_alpha<A>(a);
   const bool has_h = a.t[kRnH].ptr, has_z = a.t[kRnZ].ptr, gated = a.t[kRnQ].ptr;
   const S* h = row.h + b.off;
   const I *z = row.z + b.off, *q = row.q + b.coff;
@@ -278,24 +297,25 @@ __device__ __forceinline__ void rn_forward_block(const RnArgs& a, const RnBlock 
   }
 }
 
-template <int D, int K, typename S, typename I, typename O, typename A, bool STAGED>
-__device__ __forceinline__ void rn_backward_held(const RnArgs& a, const RnBlock b,
+template <int D, int K, bool FULL, typename S, typename I, typename O, typename A, bool STAGED, bool ONE>
+__device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b,
                                                  const RnBackwardRow<S, I, O, A>& row, const RnFactors<STAGED, A>& f,
-                                                 RnTeam<A>& team) {
-  const A inv_n = A(1) / static_cast<A>(b.mul * D), eps = static_cast<A>(a.eps), alpha = static_cast<A>(a.alpha);
-  const bool has_g = a.t[kRnGout].ptr, has_gh = a.t[kRnGh].ptr, has_z = a.t[kRnBz].ptr, gated = a.t[kRnBq].ptr;
+                                                 RnTeam<A, ONE>& team) {
+  const A inv_n = rn_inv_n<A>(b), eps = rn_eps<A>(a), alpha = rn_alpha<A>(a);
+  const bool has_g = FULL || a.t[kRnGout].ptr, has_gh = FULL || a.t[kRnGh].ptr, has_z = FULL || a.t[kRnBz].ptr,
+             gated = FULL || a.t[kRnBq].ptr, pre_norm = FULL || a.pre_norm, post_norm = FULL || a.post_norm;
   const S *g = row.g + b.off, *x = row.x + b.off;
   const I *gy = row.gy + b.off, *z = row.z + b.off;
   A d[K][D], xv[K][D], zv[K][D], xy[K], pre[K];   // d starts as gy
   A s[3] = {A(0), A(0), A(0)};                    // sums of x^2, of gy pre x, of z^2
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int u = team.t + k * team.lanes;
+    const int u = team.t + k * team.stride();
     xy[k] = pre[k] = A(0);
 #pragma unroll
     for (int m = 0; m < D; ++m) d[k][m] = xv[k][m] = zv[k][m] = A(0);
     if (u < b.mul) {
-      if (a.pre_norm) {
+      if (pre_norm) {
         pre[k] = f.pre_at(b.coff + u);
 #pragma unroll
         for (int m = 0; m < D; ++m) {
@@ -317,15 +337,15 @@ __device__ __forceinline__ void rn_backward_held(const RnArgs& a, const RnBlock 
   }
   A p = A(0), kx = A(0), r = A(1);
   team.sum(s);
-  if (a.pre_norm) {
+  if (pre_norm) {
     p = rn_rsqrt(s[0] * inv_n + eps);
     kx = p * p * p * inv_n * s[1];
   }
-  if (a.post_norm) r = rn_rsqrt(s[2] * inv_n + eps);
+  if (post_norm) r = rn_rsqrt(s[2] * inv_n + eps);
   A along[1] = {A(0)}, w[K];   // sum over the block of w d z r
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int u = team.t + k * team.lanes, c = b.coff + u;
+    const int u = team.t + k * team.stride(), c = b.coff + u;
     w[k] = A(0);
     if (u < b.mul) {
       const A gain = p * pre[k];
@@ -336,7 +356,7 @@ __device__ __forceinline__ void rn_backward_held(const RnArgs& a, const RnBlock 
 #pragma unroll
         for (int m = 0; m < D; ++m) d[k][m] = gain * d[k][m] - kx * xv[k][m];
       }
-      if (row.live && a.pre_norm) row.part[a.chan + c] += p * xy[k];
+      if (row.live && pre_norm) row.part[a.chan + c] += p * xy[k];
       if (has_gh) {
 #pragma unroll
         for (int m = 0; m < D; ++m) rn_put(row.gh + b.off + u * D + m, alpha * d[k][m]);
@@ -360,13 +380,13 @@ __device__ __forceinline__ void rn_backward_held(const RnArgs& a, const RnBlock 
   }
   if (!has_z) return;
   A kz = A(0);
-  if (a.post_norm) {
+  if (post_norm) {
     team.sum(along);
     kz = r * r * inv_n * along[0];
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int u = team.t + k * team.lanes;
+    const int u = team.t + k * team.stride();
     if (u < b.mul) {
       const A wr = w[k] * r;
 #pragma unroll
@@ -375,11 +395,11 @@ __device__ __forceinline__ void rn_backward_held(const RnArgs& a, const RnBlock 
   }
 }
 
-template <int D, typename S, typename I, typename O, typename A, bool STAGED>
-__device__ __forceinline__ void rn_backward_block(const RnArgs& a, const RnBlock b,
+template <int D, typename S, typename I, typename O, typename A, bool STAGED, bool ONE>
+__device__ __forceinline__ void rn_block_any(const RnArgs& a, const RnBlock b,
                                                   const RnBackwardRow<S, I, O, A>& row, const RnFactors<STAGED, A>& f,
-                                                  RnTeam<A>& team) {
-  const A inv_n = A(1) / static_cast<A>(b.mul * D), eps = static_cast<A>(a.eps), alpha = static_cast<A>(a.alpha);
+                                                  RnTeam<A, ONE>& team) {
+  const A inv_n = rn_inv_n<A>(b), eps = rn_eps<A>(a), alpha = rn_alpha<A>(a);
   const bool has_g = a.t[kRnGout].ptr, has_gh = a.t[kRnGh].ptr, has_z = a.t[kRnBz].ptr, gated = a.t[kRnBq].ptr;
   const S *g = row.g + b.off, *x = row.x + b.off;
   const I *gy = row.gy + b.off, *z = row.z + b.off, *q = row.q + b.coff;
@@ -473,8 +493,8 @@ __device__ __forceinline__ void rn_backward_block(const RnArgs& a, const RnBlock
   case D * 8 + K: HELD(D, K); break;
 #define CGTP_RN_HELD                                                                                          \
   CGTP_RN_CASE(1, 1) CGTP_RN_CASE(1, 2) CGTP_RN_CASE(1, 4) CGTP_RN_CASE(3, 1) CGTP_RN_CASE(3, 2)             \
-  CGTP_RN_CASE(3, 4) CGTP_RN_CASE(5, 1) CGTP_RN_CASE(5, 2) CGTP_RN_CASE(7, 1) CGTP_RN_CASE(7, 2)             \
-  CGTP_RN_CASE(9, 1) CGTP_RN_CASE(11, 1) CGTP_RN_CASE(13, 1) CGTP_RN_CASE(15, 1)
+  CGTP_RN_CASE(3, 4) CGTP_RN_CASE(5, 1) CGTP_RN_CASE(5, 2) CGTP_RN_CASE(5, 4) CGTP_RN_CASE(7, 1)             \
+  CGTP_RN_CASE(7, 2) CGTP_RN_CASE(9, 1) CGTP_RN_CASE(11, 1) CGTP_RN_CASE(13, 1) CGTP_RN_CASE(15, 1)
 #define CGTP_RN_ANY                                                                                           \
   switch (b.D) {                                                                                              \
     case 1: ANY(1); break;                                                                                    \
@@ -487,42 +507,31 @@ __device__ __forceinline__ void rn_backward_block(const RnArgs& a, const RnBlock
     default: ANY(15); break;                                                                                  \
   }
 
-template <bool STAGED, typename S, typename I, typename O, typename A>
-__device__ __forceinline__ void rn_row(const RnArgs& a, const RnBlock* blocks, const RnForwardRow<S, I, O>& row,
-                                       const RnFactors<STAGED, A>& f, RnTeam<A>& team) {
+template <int KIND, typename Row, typename A, bool STAGED, bool ONE>
+__device__ __forceinline__ void rn_row(const RnArgs& a, const Row& row, const RnFactors<STAGED, A>& f,
+                                       RnTeam<A, ONE>& team) {
   for (int i = 0; i < a.n_blocks; ++i) {
-    const RnBlock b = blocks[i];
-#define HELD(D, K) rn_forward_held<D, K>(a, b, row, f, team)
-#define ANY(D) rn_forward_block<D>(a, b, row, f, team)
-    if constexpr (STAGED) {
-      switch (b.D * 8 + rn_share(b.D, b.mul, team.lanes)) {
-        CGTP_RN_HELD
-        default: CGTP_RN_ANY
-      }
+    if constexpr (ONE) {
+      // at most kRnInline blocks, all held
+      const RnBlock& b = a.few[i];
+#define HELD(D, K) rn_block_held<D, K, KIND == kRnOneFull>(a, b, row, f, team)
+      switch (b.code) { CGTP_RN_HELD }
+#undef HELD
     } else {
-      CGTP_RN_ANY
-    }
+      const RnBlock b = i < kRnInline ? a.few[i] : a.blocks[i];
+#define HELD(D, K) rn_block_held<D, K, false>(a, b, row, f, team)
+#define ANY(D) rn_block_any<D>(a, b, row, f, team)
+      if constexpr (STAGED) {
+        switch (i < kRnInline ? b.code : 0) {
+          CGTP_RN_HELD
+          default: CGTP_RN_ANY
+        }
+      } else {
+        CGTP_RN_ANY
+      }
 #undef HELD
 #undef ANY
-  }
-}
-template <bool STAGED, typename S, typename I, typename O, typename A>
-__device__ __forceinline__ void rn_row(const RnArgs& a, const RnBlock* blocks, const RnBackwardRow<S, I, O, A>& row,
-                                       const RnFactors<STAGED, A>& f, RnTeam<A>& team) {
-  for (int i = 0; i < a.n_blocks; ++i) {
-    const RnBlock b = blocks[i];
-#define HELD(D, K) rn_backward_held<D, K>(a, b, row, f, team)
-#define ANY(D) rn_backward_block<D>(a, b, row, f, team)
-    if constexpr (STAGED) {
-      switch (b.D * 8 + rn_share(b.D, b.mul, team.lanes)) {
-        CGTP_RN_HELD
-        default: CGTP_RN_ANY
-      }
-    } else {
-      CGTP_RN_ANY
     }
-#undef HELD
-#undef ANY
   }
 }
 
@@ -541,33 +550,51 @@ __device__ __forceinline__ T* rn_in(const RnArgs& a, int i, char* stage, int j) 
 // Rows staged in shared memory
 // ---------------------------------------------------------------------------
 
+// `bytes` bytes from memory to shared memory in asynchronous copies of V bytes (the rest at once)
 template <int V>
 __device__ __forceinline__ void rn_copy_in(char* dst, const char* src, int bytes, int t, int threads) {
-  const int whole = bytes / V;
-  for (int i = t; i < whole; i += threads) {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst + i * V));
-    if constexpr (V == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src + i * V) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src + i * V), "n"(V) : "memory");
+  uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + t * V;
+  const char* s = src + t * V;
+  int left = bytes - t * V;
+  for (; left >= V; left -= 4 * threads * V, d += 4 * threads * V, s += 4 * threads * V) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (left - j * threads * V >= V) {
+        if constexpr (V == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + j * threads * V), "l"(s + j * threads * V) : "memory");
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d + j * threads * V), "l"(s + j * threads * V), "n"(V) : "memory");
+      }
   }
-  for (int i = whole * V + 2 * t; i < bytes; i += 2 * threads)
-    *reinterpret_cast<uint16_t*>(dst + i) = *reinterpret_cast<const uint16_t*>(src + i);
+  if (bytes % V)
+    for (int i = bytes / V * V + 2 * t; i < bytes; i += 2 * threads)
+      *reinterpret_cast<uint16_t*>(dst + i) = *reinterpret_cast<const uint16_t*>(src + i);
 }
 template <typename T>
 __device__ __forceinline__ void rn_copy_out(char* dst, const char* src, int bytes, int t, int threads) {
-  const int whole = bytes / static_cast<int>(sizeof(T));
-  for (int i = t; i < whole; i += threads) reinterpret_cast<T*>(dst)[i] = reinterpret_cast<const T*>(src)[i];
-  if constexpr (sizeof(T) > 2)
-    for (int i = whole * static_cast<int>(sizeof(T)) + 2 * t; i < bytes; i += 2 * threads)
+  constexpr int V = sizeof(T);
+  const char* s = src + t * V;
+  char* d = dst + t * V;
+  int left = bytes - t * V;
+  for (; left >= V; left -= 4 * threads * V, d += 4 * threads * V, s += 4 * threads * V) {
+    T v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (left - j * threads * V >= V) v[j] = *reinterpret_cast<const T*>(s + j * threads * V);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (left - j * threads * V >= V) *reinterpret_cast<T*>(d + j * threads * V) = v[j];
+  }
+  if (V > 2 && bytes % V)
+    for (int i = bytes / V * V + 2 * t; i < bytes; i += 2 * threads)
       *reinterpret_cast<uint16_t*>(dst + i) = *reinterpret_cast<const uint16_t*>(src + i);
 }
 
 // Rows [n0, n0 + count) of tensor r between memory and its region of the stage.
 template <bool IN>
-__device__ __forceinline__ void rn_move(const RnRows& r, char* stage, int64_t n0, int count, int t, int threads) {
-  char* mem = r.ptr + n0 * r.ld * r.es;
+__device__ __forceinline__ void rn_move(const RnRows& r, char* stage, int n0, int count, int t, int threads) {
+  char* mem = r.ptr + n0 * r.ld_bytes;
   char* region = stage + r.at;
   const int runs = r.linear ? 1 : count, bytes = r.width * r.es * (r.linear ? count : 1);
-  for (int j = 0; j < runs; ++j, mem += r.ld * r.es, region += r.pitch) {
+  for (int j = 0; j < runs; ++j, mem += r.ld_bytes, region += r.pitch) {
     if constexpr (IN) {
       if (r.vec == 16) rn_copy_in<16>(region, mem, bytes, t, threads);
       else if (r.vec == 8) rn_copy_in<8>(region, mem, bytes, t, threads);
@@ -583,52 +610,44 @@ __device__ __forceinline__ void rn_move(const RnRows& r, char* stage, int64_t n0
   }
 }
 
-template <bool BACKWARD, typename S, typename I, typename O, typename A>
+template <bool BACKWARD, int KIND, typename S, typename I, typename O, typename A>
 __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __grid_constant__ RnArgs a) {
   extern __shared__ __align__(16) char shared[];
-  __shared__ RnBlock few_blocks[16];
-  const int threads = a.warps * 32, g = threadIdx.x / threads, tg = threadIdx.x - g * threads;
-  const RnBlock* blocks = a.blocks;
-  if (a.n_blocks <= 16) {
-    for (int i = threadIdx.x; i < a.n_blocks; i += blockDim.x) few_blocks[i] = a.blocks[i];
-    blocks = few_blocks;
-  }
-  char* mine = shared + (size_t)g * a.group_bytes;
-  A* scratch = reinterpret_cast<A*>(mine + kRnStages * a.stage_bytes);
-  A* part = scratch + 8 * kRnWarps;                       // [rows at a time][2][C]
-  A* factors = reinterpret_cast<A*>(shared + (size_t)a.groups * a.group_bytes);   // post * scale [C], pre [C]
+  constexpr bool ONE = KIND != kRnMany;
+  const int warps = ONE ? 1 : a.warps, threads = warps * 32;
+  const int g = threadIdx.x / threads, tg = threadIdx.x - g * threads;
+  char* mine = shared + g * a.group_bytes;
+  A* scratch = reinterpret_cast<A*>(mine + a.stages * a.stage_bytes);
+  A* part = scratch + (ONE ? 0 : 8 * kRnWarps);           // [rows at a time][2][C]
+  A* factors = reinterpret_cast<A*>(shared + a.groups * a.group_bytes);   // post * scale [C], pre [C]
   const RnFactors<false, A> read{static_cast<const A*>(a.post), static_cast<const A*>(a.scale), static_cast<const A*>(a.pre)};
   for (int i = threadIdx.x; i < a.chan; i += blockDim.x) {
     factors[i] = read.base_at(i);
     factors[a.chan + i] = read.pre_at(i);
   }
   const RnFactors<true, A> f{factors, nullptr, factors + a.chan};
-  const int abreast = a.warps == 1 ? 32 / a.lanes : 1, sub = a.warps == 1 ? tg / a.lanes : 0;
-  RnTeam<A> team{tg - sub * a.lanes, a.lanes, a.warps, 1 + g, scratch, 0};
+  const int abreast = ONE ? 32 / a.lanes : 1, sub = ONE ? tg / a.lanes : 0;
+  RnTeam<A, ONE> team{tg - sub * a.lanes, a.lanes, warps, 1 + g, scratch, 0};
   constexpr int first_out = kRnInputs[BACKWARD], last = BACKWARD ? kRnBackward : kRnForward;
   if constexpr (BACKWARD)
     for (int i = tg; i < abreast * 2 * a.chan; i += threads) part[i] = A(0);
-  __syncthreads();
-
-  const int64_t step = (int64_t)a.ctas * a.groups;
-  int64_t tile = (int64_t)g * a.ctas + blockIdx.x;
-  auto load = [&](int64_t k, char* stage) {
-    if (k < a.tiles) {
-      const int64_t n0 = k * a.rows;
-      const int count = static_cast<int>(min((int64_t)a.rows, a.N - n0));
+  const int step = a.ctas * a.groups, N = static_cast<int>(a.N), tiles = static_cast<int>(a.tiles);
+  int tile = g * a.ctas + blockIdx.x;
+  const auto load = [&](int k, char* stage) {
+    if (k < tiles) {
+      const int n0 = k * a.rows, count = min(a.rows, N - n0);
 #pragma unroll
       for (int i = 0; i < first_out; ++i)
-        if (a.t[i].ptr) rn_move<true>(a.t[i], stage, n0, count, tg, threads);
+        if (KIND == kRnOneFull || a.t[i].ptr) rn_move<true>(a.t[i], stage, n0, count, tg, threads);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll
-  for (int s = 0; s < kRnStages; ++s) load(tile + s * step, mine + s * a.stage_bytes);
-  for (int s = 0; tile < a.tiles; tile += step, s = s + 1 == kRnStages ? 0 : s + 1) {
-    char* stage = mine + s * a.stage_bytes;
-    const int64_t n0 = tile * a.rows;
-    const int count = static_cast<int>(min((int64_t)a.rows, a.N - n0));
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRnStages - 1) : "memory");
+  for (int s = 0; s < a.stages; ++s) load(tile + s * step, mine + s * a.stage_bytes);
+  __syncthreads();
+  for (char* stage = mine; tile < tiles; tile += step) {
+    const int n0 = tile * a.rows, count = min(a.rows, N - n0);
+    if (a.stages == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else asm volatile("cp.async.wait_group 1;" ::: "memory");
     team.sync();
     for (int j0 = 0; j0 < count; j0 += abreast) {
       const int j = j0 + sub;
@@ -637,20 +656,21 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
             rn_in<S>(a, kRnGout, stage, j), rn_in<S>(a, kRnX, stage, j),  rn_in<I>(a, kRnGy, stage, j),
             rn_in<I>(a, kRnBz, stage, j),   rn_in<I>(a, kRnBq, stage, j), rn_in<S>(a, kRnGh, stage, j),
             rn_in<O>(a, kRnGz, stage, j),   rn_in<O>(a, kRnGq, stage, j), part + sub * 2 * a.chan, j < count};
-        rn_row(a, blocks, row, f, team);
+        rn_row<KIND>(a, row, f, team);
       } else {
         const RnForwardRow<S, I, O> row{rn_in<S>(a, kRnH, stage, j), rn_in<I>(a, kRnZ, stage, j),
                                         rn_in<I>(a, kRnQ, stage, j), rn_in<S>(a, kRnOut, stage, j),
                                         rn_in<O>(a, kRnY, stage, j)};
-        rn_row(a, blocks, row, f, team);
+        rn_row<KIND>(a, row, f, team);
       }
     }
     team.sync();
 #pragma unroll
     for (int i = first_out; i < last; ++i)
-      if (a.t[i].ptr) rn_move<false>(a.t[i], stage, n0, count, tg, threads);
+      if (KIND == kRnOneFull || a.t[i].ptr) rn_move<false>(a.t[i], stage, n0, count, tg, threads);
     team.sync();
-    load(tile + kRnStages * step, stage);
+    load(tile + a.stages * step, stage);
+    stage = a.stages == 1 || stage != mine ? mine : mine + a.stage_bytes;
   }
   if constexpr (BACKWARD) {
     // the CTA's sums: groups in order, and in a group the rows that ran side by side
@@ -659,7 +679,7 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
     for (int i = threadIdx.x; i < 2 * a.chan; i += blockDim.x) {
       A v = A(0);
       for (int k = 0; k < a.groups; ++k) {
-        const A* p = reinterpret_cast<const A*>(shared + (size_t)k * a.group_bytes + kRnStages * a.stage_bytes) + 8 * kRnWarps;
+        const A* p = part + (k - g) * (a.group_bytes / static_cast<int>(sizeof(A)));
         for (int j = 0; j < abreast; ++j) v += p[j * 2 * a.chan + i];
       }
       to[i] = v;
@@ -674,7 +694,7 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
 template <bool BACKWARD, typename S, typename I, typename O, typename A>
 __global__ void __launch_bounds__(kRnDirectWarps * 32) rn_direct_kernel(const __grid_constant__ RnArgs a) {
   __shared__ A scratch[8 * kRnWarps];
-  RnTeam<A> team{static_cast<int>(threadIdx.x), kRnDirectWarps * 32, kRnDirectWarps, 1, scratch, 0};
+  RnTeam<A, false> team{static_cast<int>(threadIdx.x), kRnDirectWarps * 32, kRnDirectWarps, 1, scratch, 0};
   const RnFactors<false, A> f{static_cast<const A*>(a.post), static_cast<const A*>(a.scale), static_cast<const A*>(a.pre)};
   A* part = static_cast<A*>(a.part) + (int64_t)blockIdx.x * 2 * a.chan;
   if constexpr (BACKWARD) {
@@ -689,11 +709,11 @@ __global__ void __launch_bounds__(kRnDirectWarps * 32) rn_direct_kernel(const __
       const RnBackwardRow<S, I, O, A> row{rn_at<S>(a, kRnGout, n), rn_at<S>(a, kRnX, n), rn_at<I>(a, kRnGy, n),
                                           rn_at<I>(a, kRnBz, n),   rn_at<I>(a, kRnBq, n), rn_at<S>(a, kRnGh, n),
                                           rn_at<O>(a, kRnGz, n),   rn_at<O>(a, kRnGq, n), part, true};
-      rn_row(a, a.blocks, row, f, team);
+      rn_row<kRnDirect>(a, row, f, team);
     } else {
       const RnForwardRow<S, I, O> row{rn_at<S>(a, kRnH, n), rn_at<I>(a, kRnZ, n), rn_at<I>(a, kRnQ, n),
                                       rn_at<S>(a, kRnOut, n), rn_at<O>(a, kRnY, n)};
-      rn_row(a, a.blocks, row, f, team);
+      rn_row<kRnDirect>(a, row, f, team);
     }
   }
 }
@@ -721,15 +741,22 @@ __global__ void __launch_bounds__(256) rn_reduce_kernel(const void* part_, int c
   }
 }
 
+template <bool BACKWARD, int KIND, typename S, typename I, typename O, typename A>
+cudaError_t rn_launch_staged(const RnArgs& a, cudaStream_t st) {
+  if (smem_cap_cached(reinterpret_cast<const void*>(rn_staged_kernel<BACKWARD, KIND, S, I, O, A>)) < a.smem)
+    return cudaErrorInvalidConfiguration;
+  rn_staged_kernel<BACKWARD, KIND, S, I, O, A><<<a.ctas, a.groups * a.warps * 32, a.smem, st>>>(a);
+  return cudaGetLastError();
+}
+
 template <bool BACKWARD, typename S, typename I, typename O, typename A>
 cudaError_t rn_launch_one(const RnArgs& a, cudaStream_t st) {
-  if (a.staged) {
-    if (smem_cap_cached(reinterpret_cast<const void*>(rn_staged_kernel<BACKWARD, S, I, O, A>)) < a.smem)
-      return cudaErrorInvalidConfiguration;
-    rn_staged_kernel<BACKWARD, S, I, O, A><<<a.ctas, a.groups * a.warps * 32, a.smem, st>>>(a);
-  } else {
-    rn_direct_kernel<BACKWARD, S, I, O, A><<<a.ctas, kRnDirectWarps * 32, 0, st>>>(a);
+  switch (a.kind) {
+    case kRnOneFull: return rn_launch_staged<BACKWARD, kRnOneFull, S, I, O, A>(a, st);
+    case kRnOne: return rn_launch_staged<BACKWARD, kRnOne, S, I, O, A>(a, st);
+    case kRnMany: return rn_launch_staged<BACKWARD, kRnMany, S, I, O, A>(a, st);
   }
+  rn_direct_kernel<BACKWARD, S, I, O, A><<<a.ctas, kRnDirectWarps * 32, 0, st>>>(a);
   return cudaGetLastError();
 }
 

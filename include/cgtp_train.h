@@ -65,7 +65,7 @@ cgtp_status cgtp_resnorm_device_bytes(cgtp_resnorm plan, int64_t* bytes);
  *  and scale are not read, and y is the norm of h); post, scale and pre may be
  *  NULL (factor 1).  q is read unless act is CGTP_ACT_NONE or z is NULL.  y must
  *  be NULL without CGTP_RESNORM_PRE, and given with it.
- *  Outputs may not overlap inputs.  N = 0 is allowed and launches nothing.
+ *  Outputs may not overlap inputs.  N = 0 is allowed and launches nothing; N < 2^30.
  */
 cgtp_status cgtp_resnorm_forward(cgtp_resnorm plan, int64_t N, const void* h, int64_t ld_h, const void* z,
                                  int64_t ld_z, const void* q, int64_t ld_q, const void* post, const void* scale,
