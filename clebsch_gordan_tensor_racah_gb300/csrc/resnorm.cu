@@ -167,7 +167,8 @@ void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
     a->few[i].code = 8 * a->few[i].D + rn_share(a->few[i].D, a->few[i].mul, a->lanes);
   if (a->kind == kRnOne && a->pre_norm && a->post_norm) {
     bool full = true;
-    for (int i = 0; i < n_rows; ++i) full &= a->t[i].ptr != nullptr;
+    for (int i = 0; i < n_rows; ++i) full &= a->t[i].ptr && a->t[i].vec == 16 && (a->t[i].linear || a->rows == 1);
+    for (const RnBlock& b : p->blocks) full &= b.mul == a->lanes * rn_share(b.D, b.mul, a->lanes);
     if (full) a->kind = kRnOneFull;
   }
 }

@@ -32,7 +32,8 @@ constexpr int kRnInputs[2] = {3, 5};
 constexpr int kRnMaxRows = kRnBackward;
 
 constexpr int kRnInline = 16;
-// kRnOneFull: a warp a row, every operand there.  kRnOne: a warp a row.  kRnMany: several warps a row, any
+// kRnOneFull: a warp a row, every operand there, tiles that are runs of 16-byte pieces, blocks that fill the
+// warp.  kRnOne: a warp a row.  kRnMany: several warps a row, any
 // number and size of blocks.  kRnDirect: rows in place, a CTA a row.
 enum RnKind { kRnDirect, kRnMany, kRnOne, kRnOneFull };
 

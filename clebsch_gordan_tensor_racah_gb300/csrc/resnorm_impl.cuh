@@ -177,7 +177,7 @@ __device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b, 
       w[k] = A(0);
 #pragma unroll
       for (int m = 0; m < D; ++m) v[k][m] = A(0);
-      if (u < b.mul) {
+      if (FULL || u < b.mul) {
         w[k] = f.base_at(b.coff + u);
         if (gated) w[k] *= rn_gate<A>(a.act, rn_get<A>(row.q + b.coff + u), nullptr);
 #pragma unroll
@@ -199,7 +199,7 @@ __device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b, 
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int u = team.t + k * team.stride();
-      if (u < b.mul) {
+      if (FULL || u < b.mul) {
         if (has_h) {
 #pragma unroll
           for (int m = 0; m < D; ++m) v[k][m] = w[k] * v[k][m] + alpha * rn_get<A>(h + u * D + m);
@@ -220,7 +220,7 @@ __device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b, 
       const int u = team.t + k * team.stride();
 #pragma unroll
       for (int m = 0; m < D; ++m) v[k][m] = A(0);
-      if (u < b.mul) {
+      if (FULL || u < b.mul) {
 #pragma unroll
         for (int m = 0; m < D; ++m) {
           v[k][m] = rn_get<A>(h + u * D + m);
@@ -236,7 +236,7 @@ __device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b, 
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int u = team.t + k * team.stride();
-    if (u < b.mul) {
+    if (FULL || u < b.mul) {
       const A g = p * f.pre_at(b.coff + u);
 #pragma unroll
       for (int m = 0; m < D; ++m) rn_put(y + u * D + m, g * v[k][m]);
@@ -314,7 +314,7 @@ __device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b,
     xy[k] = pre[k] = A(0);
 #pragma unroll
     for (int m = 0; m < D; ++m) d[k][m] = xv[k][m] = zv[k][m] = A(0);
-    if (u < b.mul) {
+    if (FULL || u < b.mul) {
       if (pre_norm) {
         pre[k] = f.pre_at(b.coff + u);
 #pragma unroll
@@ -347,7 +347,7 @@ __device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b,
   for (int k = 0; k < K; ++k) {
     const int u = team.t + k * team.stride(), c = b.coff + u;
     w[k] = A(0);
-    if (u < b.mul) {
+    if (FULL || u < b.mul) {
       const A gain = p * pre[k];
       if (has_g) {
 #pragma unroll
@@ -387,7 +387,7 @@ __device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b,
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int u = team.t + k * team.stride();
-    if (u < b.mul) {
+    if (FULL || u < b.mul) {
       const A wr = w[k] * r;
 #pragma unroll
       for (int m = 0; m < D; ++m) rn_put(row.gz + b.off + u * D + m, wr * d[k][m] - kz * zv[k][m]);
@@ -610,6 +610,62 @@ __device__ __forceinline__ void rn_move(const RnRows& r, char* stage, int n0, in
   }
 }
 
+// The same for NT tensors at once whose tiles are runs of `bytes` bytes, a multiple of 16 (a warp).
+template <int NT>
+__device__ __forceinline__ void rn_runs_in(const RnRows* const (&r)[NT], char* stage, int n0, int bytes, int lane) {
+  const char* src[NT];
+  uint32_t dst[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    src[i] = r[i]->ptr + n0 * r[i]->ld_bytes + lane * 16;
+    dst[i] = static_cast<uint32_t>(__cvta_generic_to_shared(stage)) + r[i]->at + lane * 16;
+  }
+  int left = bytes;
+  for (; left >= 4 * 512; left -= 4 * 512) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst[i] + j * 512), "l"(src[i] + j * 512) : "memory");
+#pragma unroll
+    for (int i = 0; i < NT; ++i) src[i] += 4 * 512, dst[i] += 4 * 512;
+  }
+  for (; left > lane * 16; left -= 512)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst[i]), "l"(src[i]) : "memory");
+      src[i] += 512, dst[i] += 512;
+    }
+}
+template <int NT>
+__device__ __forceinline__ void rn_runs_out(const RnRows* const (&r)[NT], const char* stage, int n0, int bytes, int lane) {
+  char* dst[NT];
+  const char* src[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    dst[i] = r[i]->ptr + n0 * r[i]->ld_bytes + lane * 16;
+    src[i] = stage + r[i]->at + lane * 16;
+  }
+  int left = bytes;
+  for (; left >= 4 * 512; left -= 4 * 512) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(src[i] + j * 512);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst[i] + j * 512) = v[j];
+      src[i] += 4 * 512, dst[i] += 4 * 512;
+    }
+  }
+  for (; left > lane * 16; left -= 512)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      *reinterpret_cast<uint4*>(dst[i]) = *reinterpret_cast<const uint4*>(src[i]);
+      src[i] += 512, dst[i] += 512;
+    }
+}
+
 template <bool BACKWARD, int KIND, typename S, typename I, typename O, typename A>
 __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __grid_constant__ RnArgs a) {
   extern __shared__ __align__(16) char shared[];
@@ -636,9 +692,22 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
   const auto load = [&](int k, char* stage) {
     if (k < tiles) {
       const int n0 = k * a.rows, count = min(a.rows, N - n0);
+      const int wide = count * a.dim * static_cast<int>(sizeof(S)), narrow = count * a.chan * static_cast<int>(sizeof(S));
+      if (KIND == kRnOneFull && ((wide | narrow) & 15) == 0) {
+        if constexpr (BACKWARD) {
+          const RnRows* const many[4] = {&a.t[kRnGout], &a.t[kRnGy], &a.t[kRnX], &a.t[kRnBz]};
+          rn_runs_in<4>(many, stage, n0, wide, tg);
+        } else {
+          const RnRows* const many[2] = {&a.t[kRnH], &a.t[kRnZ]};
+          rn_runs_in<2>(many, stage, n0, wide, tg);
+        }
+        const RnRows* const q[1] = {&a.t[BACKWARD ? kRnBq : kRnQ]};
+        rn_runs_in<1>(q, stage, n0, narrow, tg);
+      } else {
 #pragma unroll
-      for (int i = 0; i < first_out; ++i)
-        if (KIND == kRnOneFull || a.t[i].ptr) rn_move<true>(a.t[i], stage, n0, count, tg, threads);
+        for (int i = 0; i < first_out; ++i)
+          if (KIND == kRnOneFull || a.t[i].ptr) rn_move<true>(a.t[i], stage, n0, count, tg, threads);
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -665,9 +734,26 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
       }
     }
     team.sync();
+    const int wide = count * a.dim, narrow = count * a.chan;
+    if (KIND == kRnOneFull && ((wide | narrow) * static_cast<int>(sizeof(O)) & 15) == 0) {
+      const RnRows* const to[2] = {&a.t[first_out], &a.t[first_out + 1]};
+      if constexpr (sizeof(S) == sizeof(O)) {
+        rn_runs_out<2>(to, stage, n0, wide * static_cast<int>(sizeof(S)), tg);
+      } else {
+        const RnRows* const one[1] = {to[0]};
+        const RnRows* const two[1] = {to[1]};
+        rn_runs_out<1>(one, stage, n0, wide * static_cast<int>(sizeof(S)), tg);
+        rn_runs_out<1>(two, stage, n0, wide * static_cast<int>(sizeof(O)), tg);
+      }
+      if constexpr (BACKWARD) {
+        const RnRows* const gq[1] = {&a.t[kRnGq]};
+        rn_runs_out<1>(gq, stage, n0, narrow * static_cast<int>(sizeof(O)), tg);
+      }
+    } else {
 #pragma unroll
-    for (int i = first_out; i < last; ++i)
-      if (KIND == kRnOneFull || a.t[i].ptr) rn_move<false>(a.t[i], stage, n0, count, tg, threads);
+      for (int i = first_out; i < last; ++i)
+        if (KIND == kRnOneFull || a.t[i].ptr) rn_move<false>(a.t[i], stage, n0, count, tg, threads);
+    }
     team.sync();
     load(tile + a.stages * step, stage);
     stage = a.stages == 1 || stage != mine ? mine : mine + a.stage_bytes;
