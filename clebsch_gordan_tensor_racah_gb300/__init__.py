@@ -566,5 +566,14 @@ def cgtp_mixed_conv_double_backward(plan, graph, gout, x, Y, Wu, Ww, ggx, ggY, g
     return d_g, d_x, d_Y, d_Wu, d_Ww
 
 
-from .train import (AdamW, ResNormPlan, cgtp_adamw_state_values, cgtp_adamw_step, cgtp_grad_norm,  # noqa: E402
-                    cgtp_resnorm_backward, cgtp_resnorm_forward)
+_TRAIN = ("AdamW", "ResNormPlan", "cgtp_adamw_state_values", "cgtp_adamw_step", "cgtp_grad_norm",
+          "cgtp_resnorm_backward", "cgtp_resnorm_forward")
+
+
+def __getattr__(name):
+    """The operators of train.py, which needs torch as soon as it is imported."""
+    if name in _TRAIN:
+        from . import train
+        globals().update({k: getattr(train, k) for k in _TRAIN})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

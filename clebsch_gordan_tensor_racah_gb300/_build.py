@@ -23,7 +23,8 @@ CU_SOURCES = ["api.cu", "graph.cu", "uvu.cu", "uvu_f32.cu", "uvu_f32_l7.cu", "uv
               "uvu3_bf16_2.cu", "uvu3_bf16_8.cu", "uvu3_bf16_32.cu", "sh.cu",
               "uvu3_sh_f32_2.cu", "uvu3_sh_f32_8.cu", "uvu3_sh_f32_32.cu", "uvu3_sh_f64_2.cu",
               "uvu3_sh_f64_8.cu", "uvu3_sh_f64_32.cu", "uvwe.cu", "mixed.cu", "measure.cu",
-              "resnorm.cu", "resnorm_f32.cu", "resnorm_f64.cu", "resnorm_bf16.cu", "resnorm_bf16s.cu", "adamw.cu"]
+              "resnorm.cu", "resnorm_f32_fwd.cu", "resnorm_f32_bwd.cu", "resnorm_f64_fwd.cu", "resnorm_f64_bwd.cu",
+              "resnorm_bf16_fwd.cu", "resnorm_bf16_bwd.cu", "resnorm_bf16s_fwd.cu", "resnorm_bf16s_bwd.cu", "adamw.cu"]
 CPP_SOURCES = ["planner.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -109,7 +110,7 @@ def build(verbose=False, jobs=None):
     jobs = jobs or max(1, min(len(cmds), os.cpu_count() or 4))
     if cmds:
         # longest translation units first
-        cmds.sort(key=lambda c: ("_l7" not in c[-3] and "uvu3_" not in c[-3], c[-3]))
+        cmds.sort(key=lambda c: (not any(k in c[-3] for k in ("_l7", "uvu3_", "_bwd", "_fwd")), c[-3]))
         with cf.ThreadPoolExecutor(jobs) as ex:
             for out in ex.map(_run, cmds):
                 if verbose and out.strip():

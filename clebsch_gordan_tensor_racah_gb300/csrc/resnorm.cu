@@ -112,46 +112,51 @@ int lay_out(RnArgs* a, bool backward, int rows) {
   return at;
 }
 
-// How rows are dealt out (see resnorm_impl.cuh).
+// How rows are dealt out (see resnorm_impl.cuh): the cheapest of the launches that fit, by the
+// instructions that a row costs and the warps that hide their latency.
+//   instructions: an element of a thread's share, a channel, a step of the block sums and the fixed part of a
+//     block, fitted to counters of the kernels (a row of 64x0e+64x1o+64x2e: 1,330 backward, 875 forward);
+//   rate: grows with the warps of an SM as w / (w + 8).
 void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
   const int n_rows = backward ? kRnBackward : kRnForward, ep = es_param(p);
-  int lanes = 1;
-  while (lanes < 32 && lanes < p->widest) lanes *= 2;
-  const int abreast = 32 / lanes;
-  // Rows of a tile: as many as run side by side, and enough that a tile of every contiguous tensor
-  // starts at a multiple of 16 bytes.
-  int rows = abreast;
-  const auto aligned = [&] {
-    for (int i = 0; i < n_rows; ++i)
-      if (a->t[i].ptr && a->t[i].ld == a->t[i].width && (int64_t(rows) * a->t[i].width * a->t[i].es) % 16) return false;
-    return true;
-  };
-  while (!aligned()) rows *= 2;
   const int factors = round16(2 * p->chan * ep);
-  const auto group_of = [&](int warps, int stages, int r) {
-    const int64_t kept = (warps > 1 ? 8 * kRnWarps : 0) + (backward ? int64_t(warps == 1 ? abreast : 1) * 2 * p->chan : 0);
-    return int64_t(stages) * lay_out(a, backward, r) + round16(kept * ep);
-  };
-  int best = 0;
-  for (int warps = 1; warps <= kRnWarps; warps *= 2) {
-    if (warps > 1 && warps * 32 >= 2 * p->widest) break;
-    const int width = warps == 1 ? lanes : 32 * warps;
-    int held = p->blocks.size() <= kRnInline;
-    for (const RnBlock& b : p->blocks) held &= rn_share(b.D, b.mul, width) > 0;
-    if (warps == 1 && !held) continue;
-    const int r = warps == 1 ? rows : std::max(1, rows / abreast);
+  double best = 0.0;
+  for (int team = 1; team <= 32 * kRnWarps; team *= 2) {   // threads of a row
+    const int warps = std::max(1, team / 32), abreast = std::max(1, 32 / team);
+    if (team > 1 && team >= 2 * p->widest) break;
+    // Rows of a tile: as many as run side by side, and enough that a tile of every contiguous tensor
+    // starts at a multiple of 16 bytes.
+    int rows = abreast;
+    for (int i = 0; i < n_rows; ++i)
+      while (a->t[i].ptr && a->t[i].ld == a->t[i].width && (int64_t(rows) * a->t[i].width * a->t[i].es) % 16) rows *= 2;
+    bool held = p->blocks.size() <= kRnInline, fills = held;
+    double work = 0.0;
+    for (const RnBlock& b : p->blocks) {
+      const int share = rn_share(b.D, b.mul, team);
+      held &= share > 0;
+      fills &= b.mul == share * team;
+      work += share * ((backward ? 15 : 9) * b.D + (backward ? 40 : 25)) + (backward ? 8 : 4) * std::log2(std::min(team, 32)) +
+              (warps > 1 ? 120 : 0) + 40;
+    }
+    if (!held) continue;
+    const int stage = lay_out(a, backward, rows);
+    bool full = fills && a->pre_norm && a->post_norm && team >= 32;
+    for (int i = 0; i < n_rows; ++i) full &= a->t[i].ptr && a->t[i].vec == 16 && (a->t[i].linear || rows == 1);
+    const int64_t kept = (warps > 1 ? 8 * kRnWarps : 0) + (backward ? int64_t(abreast) * 2 * p->chan : 0);
     for (int stages = kRnMaxStages; stages >= 1; --stages) {
-      const int64_t group = group_of(warps, stages, r);
+      const int64_t group = int64_t(stages) * stage + round16(kept * ep);
       const int groups = static_cast<int>(std::min<int64_t>((p->smem_cap - factors) / group, kRnWarps / warps));
-      const int score = groups <= 0 ? 0 : held * 64 + groups * warps;
-      if (score <= best) continue;
-      best = score;
-      a->kind = warps == 1 ? kRnOne : kRnMany;
+      if (groups <= 0) continue;
+      const int busy = groups * warps;
+      const double rate = double(busy) / (busy + 8) / (work * warps / abreast * (full ? 1.0 : 1.5));
+      if (rate <= best) continue;
+      best = rate;
+      a->kind = warps == 1 ? (full ? kRnOneFull : kRnOne) : (full ? kRnManyFull : kRnMany);
       a->stages = stages;
       a->warps = warps;
-      a->lanes = width;
+      a->lanes = team;
       a->groups = groups;
-      a->rows = r;
+      a->rows = rows;
       a->group_bytes = static_cast<int>(group);
     }
   }
@@ -163,22 +168,17 @@ void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
   a->smem = a->groups * a->group_bytes + factors;
   a->tiles = (a->N + a->rows - 1) / a->rows;
   a->ctas = static_cast<int>(std::min<int64_t>(a->tiles, p->num_sms));
-  for (size_t i = 0; i < std::min<size_t>(p->blocks.size(), kRnInline); ++i)
-    a->few[i].code = 8 * a->few[i].D + rn_share(a->few[i].D, a->few[i].mul, a->lanes);
-  if (a->kind == kRnOne && a->pre_norm && a->post_norm) {
-    bool full = true;
-    for (int i = 0; i < n_rows; ++i) full &= a->t[i].ptr && a->t[i].vec == 16 && (a->t[i].linear || a->rows == 1);
-    for (const RnBlock& b : p->blocks) full &= b.mul == a->lanes * rn_share(b.D, b.mul, a->lanes);
-    if (full) a->kind = kRnOneFull;
-  }
+  for (size_t i = 0; i < p->blocks.size(); ++i)
+    a->few[i].code = rn_code(a->few[i].D, rn_share(a->few[i].D, a->few[i].mul, a->lanes));
 }
 
 cgtp_status launch(const cgtp_resnorm_s* p, RnArgs& a, bool backward, cudaStream_t st) {
   deal(p, &a, backward);
-  const cudaError_t e = p->dtype == CGTP_F64                ? rn_launch_f64(a, backward, st)
-                        : p->dtype == CGTP_F32              ? rn_launch_f32(a, backward, st)
-                        : (p->flags & CGTP_RESNORM_STORAGE) ? rn_launch_bf16s(a, backward, st)
-                                                            : rn_launch_bf16(a, backward, st);
+  const auto run = p->dtype == CGTP_F64                ? (backward ? rn_backward_f64 : rn_forward_f64)
+                   : p->dtype == CGTP_F32              ? (backward ? rn_backward_f32 : rn_forward_f32)
+                   : (p->flags & CGTP_RESNORM_STORAGE) ? (backward ? rn_backward_bf16s : rn_forward_bf16s)
+                                                       : (backward ? rn_backward_bf16 : rn_forward_bf16);
+  const cudaError_t e = run(a, st);
   return e == cudaSuccess ? CGTP_OK : fail(CGTP_ECUDA, std::string("resnorm: ") + cudaGetErrorString(e));
 }
 

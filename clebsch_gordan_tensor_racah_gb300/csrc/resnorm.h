@@ -11,7 +11,7 @@ namespace cgtp {
 // One irreps block of a row: channels [coff, coff + mul), elements [off, off + mul * D).
 struct RnBlock {
   int off, coff, mul, D;
-  int code;            // 8 D + channels of a thread (rn_share), set for a launch
+  int code;            // rn_code, set for a launch
   float inv_n_f;       // 1 / (mul D)
   double inv_n;
 };
@@ -31,11 +31,11 @@ enum { kRnGout, kRnGy, kRnX, kRnBz, kRnBq, kRnGh, kRnGz, kRnGq, kRnBackward };  
 constexpr int kRnInputs[2] = {3, 5};
 constexpr int kRnMaxRows = kRnBackward;
 
-constexpr int kRnInline = 16;
-// kRnOneFull: a warp a row, every operand there, tiles that are runs of 16-byte pieces, blocks that fill the
-// warp.  kRnOne: a warp a row.  kRnMany: several warps a row, any
-// number and size of blocks.  kRnDirect: rows in place, a CTA a row.
-enum RnKind { kRnDirect, kRnMany, kRnOne, kRnOneFull };
+constexpr int kRnInline = 64;
+// kRnOne: a warp a row, or several rows a warp.  kRnMany: several warps a row.  ..Full: every operand there, tiles that are runs of 16-byte pieces, blocks that fill the lanes (and a
+// warp a row).  kRnDirect: rows in place, a CTA a row,
+// any number and size of blocks.
+enum RnKind { kRnDirect, kRnMany, kRnManyFull, kRnOne, kRnOneFull };
 
 // Arguments of one launch.
 struct RnArgs {
@@ -43,8 +43,8 @@ struct RnArgs {
   RnRows t[kRnMaxRows];
   const void *post = nullptr, *scale = nullptr, *pre = nullptr;
   void *gpost = nullptr, *gscale = nullptr, *gpre = nullptr;
-  const RnBlock* blocks = nullptr;   // device table; the first kRnInline blocks also in `few`
-  RnBlock few[16];
+  const RnBlock* blocks = nullptr;   // device table, or `few` where they fit there
+  RnBlock few[kRnInline];
   void* part = nullptr;       // [CTAs][2][C] partial sums: of a(q) P, of gpre
   int n_blocks = 0, dim = 0, chan = 0, act = 0;
   bool post_norm = false, pre_norm = false;
@@ -76,20 +76,26 @@ struct cgtp_resnorm_s {
 
 namespace cgtp {
 
-// resnorm_*.cu: one translation unit per set of element types
-cudaError_t rn_launch_f32(const RnArgs& a, bool backward, cudaStream_t st);
-cudaError_t rn_launch_f64(const RnArgs& a, bool backward, cudaStream_t st);
-cudaError_t rn_launch_bf16(const RnArgs& a, bool backward, cudaStream_t st);
-cudaError_t rn_launch_bf16s(const RnArgs& a, bool backward, cudaStream_t st);
+// resnorm_*.cu: one translation unit per set of element types and direction
+#define CGTP_RN_DECLARE(name)                                   \
+  cudaError_t rn_forward_##name(const RnArgs& a, cudaStream_t st); \
+  cudaError_t rn_backward_##name(const RnArgs& a, cudaStream_t st);
+CGTP_RN_DECLARE(f32)
+CGTP_RN_DECLARE(f64)
+CGTP_RN_DECLARE(bf16)
+CGTP_RN_DECLARE(bf16s)
+#undef CGTP_RN_DECLARE
 
 // Channels of a block that a thread keeps in registers: mul / lanes rounded up to a share that the
-// kernels have code for, or 0.
-#ifdef __CUDACC__
-__host__ __device__
-#endif
+// kernels have code for (at most about 20 values), or 0.
 inline int rn_share(int D, int mul, int lanes) {
-  const int share = mul <= lanes ? 1 : mul <= 2 * lanes ? 2 : mul <= 4 * lanes ? 4 : 0;
-  return share <= (D <= 5 ? 4 : D <= 7 ? 2 : 1) ? share : 0;
+  const int share = mul <= lanes ? 1 : mul <= 2 * lanes ? 2 : mul <= 4 * lanes ? 4 : mul <= 8 * lanes ? 8 : 0;
+  return share <= (D == 1 ? 8 : D <= 5 ? 4 : D <= 9 ? 2 : 1) ? share : 0;
+}
+// Number of the code for blocks of D components and a share: CGTP_RN_HELD counts the same way.
+constexpr int rn_code(int D, int share) {
+  const int first[8] = {0, 4, 7, 10, 12, 14, 15, 16};
+  return first[D / 2] + (share >= 8 ? 3 : share >= 4 ? 2 : share - 1);
 }
 
 constexpr int kRnMaxStages = 2;     // tiles of a group in shared memory

@@ -77,20 +77,22 @@ struct RnFactors {
 };
 
 // The threads of a row.  Groups of several warps (ONE = false) exchange sums through `scratch`
-// (two banks in turn, so that one barrier separates the uses of a bank).
-template <typename A, bool ONE>
+// (two banks in turn, so that one barrier separates the uses of a bank).  WHOLE: one warp, 32 lanes a row.
+template <typename A, bool ONE, bool WHOLE>
 struct RnTeam {
   int t, lanes, warps, barrier;   // place in the row, threads of a row, warps of the group, its named barrier
   A* scratch;
   int bank;
 
+  // distance between a thread's channels
+  __device__ __forceinline__ int stride() const { return WHOLE ? 32 : lanes; }
   __device__ __forceinline__ void sync() const {
     if constexpr (ONE) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(warps * 32) : "memory");
   }
-  // distance between a thread's channels; one warp: rows of fewer lanes have one channel a thread at most
-  __device__ __forceinline__ int stride() const { return ONE ? 32 : lanes; }
-  // sums of K values over the row's threads; collective over the group
+  // Sums of K values over the row's threads; collective over the group.  The branch stays where every row has
+  // 32 lanes, too: without it the code around the sums was scheduled worse (200,000 x 576 rows: forward 315 us
+  // against 266 us, backward 510 us against 484 us).
   template <int K>
   __device__ __forceinline__ void sum(A (&v)[K]) {
     if (!ONE || lanes == 32) {
@@ -160,9 +162,9 @@ struct RnBackwardRow {
 //
 // A block's values stay in registers where a thread's share, K channels of D components, is small
 // (every operand is then read once from shared memory); larger shares are read again for each pass.
-template <int D, int K, bool FULL, typename S, typename I, typename O, typename A, bool STAGED, bool ONE>
+template <int D, int K, bool FULL, typename S, typename I, typename O, typename A, bool STAGED, bool ONE, bool WHOLE>
 __device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b, const RnForwardRow<S, I, O>& row,
-                                                const RnFactors<STAGED, A>& f, RnTeam<A, ONE>& team) {
+                                                const RnFactors<STAGED, A>& f, RnTeam<A, ONE, WHOLE>& team) {
   const A inv_n = rn_inv_n<A>(b), eps = rn_eps<A>(a);
   const bool has_h = FULL || a.t[kRnH].ptr, has_z = FULL || a.t[kRnZ].ptr, gated = FULL || a.t[kRnQ].ptr;
   const bool pre_norm = FULL || a.pre_norm, post_norm = FULL || a.post_norm;
@@ -244,9 +246,9 @@ __device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b, 
   }
 }
 
-template <int D, typename S, typename I, typename O, typename A, bool STAGED, bool ONE>
+template <int D, typename S, typename I, typename O, typename A, bool STAGED, bool ONE, bool WHOLE>
 __device__ __forceinline__ void rn_block_any(const RnArgs& a, const RnBlock b, const RnForwardRow<S, I, O>& row,
-                                                 const RnFactors<STAGED, A>& f, RnTeam<A, ONE>& team) {
+                                                 const RnFactors<STAGED, A>& f, RnTeam<A, ONE, WHOLE>& team) {
   const A inv_n = rn_inv_n<A>(b), eps = rn_eps<A>(a), alpha = rn_alpha<A>(a);
   const bool has_h = a.t[kRnH].ptr, has_z = a.t[kRnZ].ptr, gated = a.t[kRnQ].ptr;
   const S* h = row.h + b.off;
@@ -297,10 +299,10 @@ __device__ __forceinline__ void rn_block_any(const RnArgs& a, const RnBlock b, c
   }
 }
 
-template <int D, int K, bool FULL, typename S, typename I, typename O, typename A, bool STAGED, bool ONE>
+template <int D, int K, bool FULL, typename S, typename I, typename O, typename A, bool STAGED, bool ONE, bool WHOLE>
 __device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b,
                                                  const RnBackwardRow<S, I, O, A>& row, const RnFactors<STAGED, A>& f,
-                                                 RnTeam<A, ONE>& team) {
+                                                 RnTeam<A, ONE, WHOLE>& team) {
   const A inv_n = rn_inv_n<A>(b), eps = rn_eps<A>(a), alpha = rn_alpha<A>(a);
   const bool has_g = FULL || a.t[kRnGout].ptr, has_gh = FULL || a.t[kRnGh].ptr, has_z = FULL || a.t[kRnBz].ptr,
              gated = FULL || a.t[kRnBq].ptr, pre_norm = FULL || a.pre_norm, post_norm = FULL || a.post_norm;
@@ -395,10 +397,10 @@ __device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b,
   }
 }
 
-template <int D, typename S, typename I, typename O, typename A, bool STAGED, bool ONE>
+template <int D, typename S, typename I, typename O, typename A, bool STAGED, bool ONE, bool WHOLE>
 __device__ __forceinline__ void rn_block_any(const RnArgs& a, const RnBlock b,
                                                   const RnBackwardRow<S, I, O, A>& row, const RnFactors<STAGED, A>& f,
-                                                  RnTeam<A, ONE>& team) {
+                                                  RnTeam<A, ONE, WHOLE>& team) {
   const A inv_n = rn_inv_n<A>(b), eps = rn_eps<A>(a), alpha = rn_alpha<A>(a);
   const bool has_g = a.t[kRnGout].ptr, has_gh = a.t[kRnGh].ptr, has_z = a.t[kRnBz].ptr, gated = a.t[kRnBq].ptr;
   const S *g = row.g + b.off, *x = row.x + b.off;
@@ -489,12 +491,15 @@ __device__ __forceinline__ void rn_block_any(const RnArgs& a, const RnBlock b,
 }
 
 // A block by its number of components and the thread's share (rn_share).
+template <int D, int K>
+constexpr int kRnCode = rn_code(D, K);
 #define CGTP_RN_CASE(D, K) \
-  case D * 8 + K: HELD(D, K); break;
+  case kRnCode<D, K>: HELD(D, K); break;
 #define CGTP_RN_HELD                                                                                          \
-  CGTP_RN_CASE(1, 1) CGTP_RN_CASE(1, 2) CGTP_RN_CASE(1, 4) CGTP_RN_CASE(3, 1) CGTP_RN_CASE(3, 2)             \
-  CGTP_RN_CASE(3, 4) CGTP_RN_CASE(5, 1) CGTP_RN_CASE(5, 2) CGTP_RN_CASE(5, 4) CGTP_RN_CASE(7, 1)             \
-  CGTP_RN_CASE(7, 2) CGTP_RN_CASE(9, 1) CGTP_RN_CASE(11, 1) CGTP_RN_CASE(13, 1) CGTP_RN_CASE(15, 1)
+  CGTP_RN_CASE(1, 1) CGTP_RN_CASE(1, 2) CGTP_RN_CASE(1, 4) CGTP_RN_CASE(1, 8) CGTP_RN_CASE(3, 1)             \
+  CGTP_RN_CASE(3, 2) CGTP_RN_CASE(3, 4) CGTP_RN_CASE(5, 1) CGTP_RN_CASE(5, 2) CGTP_RN_CASE(5, 4)             \
+  CGTP_RN_CASE(7, 1) CGTP_RN_CASE(7, 2) CGTP_RN_CASE(9, 1) CGTP_RN_CASE(9, 2) CGTP_RN_CASE(11, 1)            \
+  CGTP_RN_CASE(13, 1) CGTP_RN_CASE(15, 1)
 #define CGTP_RN_ANY                                                                                           \
   switch (b.D) {                                                                                              \
     case 1: ANY(1); break;                                                                                    \
@@ -507,29 +512,19 @@ __device__ __forceinline__ void rn_block_any(const RnArgs& a, const RnBlock b,
     default: ANY(15); break;                                                                                  \
   }
 
-template <int KIND, typename Row, typename A, bool STAGED, bool ONE>
+template <int KIND, typename Row, typename A, bool STAGED, bool ONE, bool WHOLE>
 __device__ __forceinline__ void rn_row(const RnArgs& a, const Row& row, const RnFactors<STAGED, A>& f,
-                                       RnTeam<A, ONE>& team) {
+                                       RnTeam<A, ONE, WHOLE>& team) {
   for (int i = 0; i < a.n_blocks; ++i) {
-    if constexpr (ONE) {
-      // at most kRnInline blocks, all held
+    if constexpr (STAGED) {
       const RnBlock& b = a.few[i];
-#define HELD(D, K) rn_block_held<D, K, KIND == kRnOneFull>(a, b, row, f, team)
+#define HELD(D, K) rn_block_held<D, K, KIND == kRnOneFull || KIND == kRnManyFull>(a, b, row, f, team)
       switch (b.code) { CGTP_RN_HELD }
 #undef HELD
     } else {
-      const RnBlock b = i < kRnInline ? a.few[i] : a.blocks[i];
-#define HELD(D, K) rn_block_held<D, K, false>(a, b, row, f, team)
+      const RnBlock b = a.blocks[i];
 #define ANY(D) rn_block_any<D>(a, b, row, f, team)
-      if constexpr (STAGED) {
-        switch (i < kRnInline ? b.code : 0) {
-          CGTP_RN_HELD
-          default: CGTP_RN_ANY
-        }
-      } else {
-        CGTP_RN_ANY
-      }
-#undef HELD
+      CGTP_RN_ANY
 #undef ANY
     }
   }
@@ -610,66 +605,69 @@ __device__ __forceinline__ void rn_move(const RnRows& r, char* stage, int n0, in
   }
 }
 
-// The same for NT tensors at once whose tiles are runs of `bytes` bytes, a multiple of 16 (a warp).
+// The same for NT tensors at once whose tiles are runs of `bytes` bytes, a multiple of 16.
 template <int NT>
-__device__ __forceinline__ void rn_runs_in(const RnRows* const (&r)[NT], char* stage, int n0, int bytes, int lane) {
+__device__ __forceinline__ void rn_runs_in(const RnRows* const (&r)[NT], char* stage, int n0, int bytes, int t, int threads) {
   const char* src[NT];
   uint32_t dst[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    src[i] = r[i]->ptr + n0 * r[i]->ld_bytes + lane * 16;
-    dst[i] = static_cast<uint32_t>(__cvta_generic_to_shared(stage)) + r[i]->at + lane * 16;
+    src[i] = r[i]->ptr + n0 * r[i]->ld_bytes + t * 16;
+    dst[i] = static_cast<uint32_t>(__cvta_generic_to_shared(stage)) + r[i]->at + t * 16;
   }
+  const int run = threads * 16;
   int left = bytes;
-  for (; left >= 4 * 512; left -= 4 * 512) {
+  for (; left >= 4 * run; left -= 4 * run) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < NT; ++i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst[i] + j * 512), "l"(src[i] + j * 512) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst[i] + j * run), "l"(src[i] + j * run) : "memory");
 #pragma unroll
-    for (int i = 0; i < NT; ++i) src[i] += 4 * 512, dst[i] += 4 * 512;
+    for (int i = 0; i < NT; ++i) src[i] += 4 * run, dst[i] += 4 * run;
   }
-  for (; left > lane * 16; left -= 512)
+  for (; left > t * 16; left -= run)
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst[i]), "l"(src[i]) : "memory");
-      src[i] += 512, dst[i] += 512;
+      src[i] += run, dst[i] += run;
     }
 }
 template <int NT>
-__device__ __forceinline__ void rn_runs_out(const RnRows* const (&r)[NT], const char* stage, int n0, int bytes, int lane) {
+__device__ __forceinline__ void rn_runs_out(const RnRows* const (&r)[NT], const char* stage, int n0, int bytes, int t, int threads) {
   char* dst[NT];
   const char* src[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    dst[i] = r[i]->ptr + n0 * r[i]->ld_bytes + lane * 16;
-    src[i] = stage + r[i]->at + lane * 16;
+    dst[i] = r[i]->ptr + n0 * r[i]->ld_bytes + t * 16;
+    src[i] = stage + r[i]->at + t * 16;
   }
+  const int run = threads * 16;
   int left = bytes;
-  for (; left >= 4 * 512; left -= 4 * 512) {
+  for (; left >= 4 * run; left -= 4 * run) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       uint4 v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(src[i] + j * 512);
+      for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(src[i] + j * run);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst[i] + j * 512) = v[j];
-      src[i] += 4 * 512, dst[i] += 4 * 512;
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst[i] + j * run) = v[j];
+      src[i] += 4 * run, dst[i] += 4 * run;
     }
   }
-  for (; left > lane * 16; left -= 512)
+  for (; left > t * 16; left -= run)
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       *reinterpret_cast<uint4*>(dst[i]) = *reinterpret_cast<const uint4*>(src[i]);
-      src[i] += 512, dst[i] += 512;
+      src[i] += run, dst[i] += run;
     }
 }
 
 template <bool BACKWARD, int KIND, typename S, typename I, typename O, typename A>
 __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __grid_constant__ RnArgs a) {
   extern __shared__ __align__(16) char shared[];
-  constexpr bool ONE = KIND != kRnMany;
+  constexpr bool ONE = KIND == kRnOne || KIND == kRnOneFull, FULL = KIND == kRnOneFull || KIND == kRnManyFull;
+  constexpr bool WHOLE = KIND == kRnOneFull;
   const int warps = ONE ? 1 : a.warps, threads = warps * 32;
   const int g = threadIdx.x / threads, tg = threadIdx.x - g * threads;
   char* mine = shared + g * a.group_bytes;
@@ -683,7 +681,7 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
   }
   const RnFactors<true, A> f{factors, nullptr, factors + a.chan};
   const int abreast = ONE ? 32 / a.lanes : 1, sub = ONE ? tg / a.lanes : 0;
-  RnTeam<A, ONE> team{tg - sub * a.lanes, a.lanes, warps, 1 + g, scratch, 0};
+  RnTeam<A, ONE, WHOLE> team{tg - sub * a.lanes, a.lanes, warps, 1 + g, scratch, 0};
   constexpr int first_out = kRnInputs[BACKWARD], last = BACKWARD ? kRnBackward : kRnForward;
   if constexpr (BACKWARD)
     for (int i = tg; i < abreast * 2 * a.chan; i += threads) part[i] = A(0);
@@ -693,20 +691,20 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
     if (k < tiles) {
       const int n0 = k * a.rows, count = min(a.rows, N - n0);
       const int wide = count * a.dim * static_cast<int>(sizeof(S)), narrow = count * a.chan * static_cast<int>(sizeof(S));
-      if (KIND == kRnOneFull && ((wide | narrow) & 15) == 0) {
+      if (FULL && ((wide | narrow) & 15) == 0) {
         if constexpr (BACKWARD) {
           const RnRows* const many[4] = {&a.t[kRnGout], &a.t[kRnGy], &a.t[kRnX], &a.t[kRnBz]};
-          rn_runs_in<4>(many, stage, n0, wide, tg);
+          rn_runs_in<4>(many, stage, n0, wide, tg, threads);
         } else {
           const RnRows* const many[2] = {&a.t[kRnH], &a.t[kRnZ]};
-          rn_runs_in<2>(many, stage, n0, wide, tg);
+          rn_runs_in<2>(many, stage, n0, wide, tg, threads);
         }
         const RnRows* const q[1] = {&a.t[BACKWARD ? kRnBq : kRnQ]};
-        rn_runs_in<1>(q, stage, n0, narrow, tg);
+        rn_runs_in<1>(q, stage, n0, narrow, tg, threads);
       } else {
 #pragma unroll
         for (int i = 0; i < first_out; ++i)
-          if (KIND == kRnOneFull || a.t[i].ptr) rn_move<true>(a.t[i], stage, n0, count, tg, threads);
+          if (FULL || a.t[i].ptr) rn_move<true>(a.t[i], stage, n0, count, tg, threads);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -735,24 +733,24 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
     }
     team.sync();
     const int wide = count * a.dim, narrow = count * a.chan;
-    if (KIND == kRnOneFull && ((wide | narrow) * static_cast<int>(sizeof(O)) & 15) == 0) {
+    if (FULL && ((wide | narrow) * static_cast<int>(sizeof(O)) & 15) == 0) {
       const RnRows* const to[2] = {&a.t[first_out], &a.t[first_out + 1]};
       if constexpr (sizeof(S) == sizeof(O)) {
-        rn_runs_out<2>(to, stage, n0, wide * static_cast<int>(sizeof(S)), tg);
+        rn_runs_out<2>(to, stage, n0, wide * static_cast<int>(sizeof(S)), tg, threads);
       } else {
         const RnRows* const one[1] = {to[0]};
         const RnRows* const two[1] = {to[1]};
-        rn_runs_out<1>(one, stage, n0, wide * static_cast<int>(sizeof(S)), tg);
-        rn_runs_out<1>(two, stage, n0, wide * static_cast<int>(sizeof(O)), tg);
+        rn_runs_out<1>(one, stage, n0, wide * static_cast<int>(sizeof(S)), tg, threads);
+        rn_runs_out<1>(two, stage, n0, wide * static_cast<int>(sizeof(O)), tg, threads);
       }
       if constexpr (BACKWARD) {
         const RnRows* const gq[1] = {&a.t[kRnGq]};
-        rn_runs_out<1>(gq, stage, n0, narrow * static_cast<int>(sizeof(O)), tg);
+        rn_runs_out<1>(gq, stage, n0, narrow * static_cast<int>(sizeof(O)), tg, threads);
       }
     } else {
 #pragma unroll
       for (int i = first_out; i < last; ++i)
-        if (KIND == kRnOneFull || a.t[i].ptr) rn_move<false>(a.t[i], stage, n0, count, tg, threads);
+        if (FULL || a.t[i].ptr) rn_move<false>(a.t[i], stage, n0, count, tg, threads);
     }
     team.sync();
     load(tile + a.stages * step, stage);
@@ -780,7 +778,7 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
 template <bool BACKWARD, typename S, typename I, typename O, typename A>
 __global__ void __launch_bounds__(kRnDirectWarps * 32) rn_direct_kernel(const __grid_constant__ RnArgs a) {
   __shared__ A scratch[8 * kRnWarps];
-  RnTeam<A, false> team{static_cast<int>(threadIdx.x), kRnDirectWarps * 32, kRnDirectWarps, 1, scratch, 0};
+  RnTeam<A, false, false> team{static_cast<int>(threadIdx.x), kRnDirectWarps * 32, kRnDirectWarps, 1, scratch, 0};
   const RnFactors<false, A> f{static_cast<const A*>(a.post), static_cast<const A*>(a.scale), static_cast<const A*>(a.pre)};
   A* part = static_cast<A*>(a.part) + (int64_t)blockIdx.x * 2 * a.chan;
   if constexpr (BACKWARD) {
@@ -835,22 +833,21 @@ cudaError_t rn_launch_staged(const RnArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// FP64 has no kernels of its own for full rows: its tiles are twice as long, its shares spill
 template <bool BACKWARD, typename S, typename I, typename O, typename A>
-cudaError_t rn_launch_one(const RnArgs& a, cudaStream_t st) {
+cudaError_t rn_launch(const RnArgs& a, cudaStream_t st) {
+  constexpr bool wide = sizeof(A) == 8;
+  cudaError_t e;
   switch (a.kind) {
-    case kRnOneFull: return rn_launch_staged<BACKWARD, kRnOneFull, S, I, O, A>(a, st);
-    case kRnOne: return rn_launch_staged<BACKWARD, kRnOne, S, I, O, A>(a, st);
-    case kRnMany: return rn_launch_staged<BACKWARD, kRnMany, S, I, O, A>(a, st);
+    case kRnOneFull: e = rn_launch_staged<BACKWARD, wide ? kRnOne : kRnOneFull, S, I, O, A>(a, st); break;
+    case kRnOne: e = rn_launch_staged<BACKWARD, kRnOne, S, I, O, A>(a, st); break;
+    case kRnManyFull: e = rn_launch_staged<BACKWARD, wide ? kRnMany : kRnManyFull, S, I, O, A>(a, st); break;
+    case kRnMany: e = rn_launch_staged<BACKWARD, kRnMany, S, I, O, A>(a, st); break;
+    default:
+      rn_direct_kernel<BACKWARD, S, I, O, A><<<a.ctas, kRnDirectWarps * 32, 0, st>>>(a);
+      e = cudaGetLastError();
   }
-  rn_direct_kernel<BACKWARD, S, I, O, A><<<a.ctas, kRnDirectWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
-}
-
-template <typename S, typename I, typename O, typename A>
-cudaError_t rn_launch(const RnArgs& a, bool backward, cudaStream_t st) {
-  if (!backward) return rn_launch_one<false, S, I, O, A>(a, st);
-  const cudaError_t e = rn_launch_one<true, S, I, O, A>(a, st);
-  if (e != cudaSuccess || !(a.gpost || a.gscale || a.gpre)) return e;
+  if (!BACKWARD || e != cudaSuccess || !(a.gpost || a.gscale || a.gpre)) return e;
   rn_reduce_kernel<A><<<(2 * a.chan + 31) / 32, 256, 0, st>>>(a.part, a.ctas, a.chan, a.post, a.scale, a.gpost, a.gscale, a.gpre);
   return cudaGetLastError();
 }
