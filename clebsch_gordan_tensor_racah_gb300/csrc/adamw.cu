@@ -1,8 +1,10 @@
 // adamw.cu -- AdamW over many tensors, with states in the parameters' type or in 8 bits, and
 // the global gradient norm (declared in include/cgtp_train.h).
 //
-// Work is cut into blocks of 128 elements, numbered over all tensors; a warp takes a block, a
-// lane 4 elements of it.  The tensors' pointers travel in the kernel's parameters.
+// Work is cut into units of up to eight blocks of 128 elements of one tensor (a table made with
+// the optimizer: no search in the kernels); a warp takes a unit, a lane 4 elements of a block.  The
+// tensors' pointers and decays travel in the kernel's parameters, so that the loads of a unit wait for
+// one table entry only, which is read a unit ahead.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -18,10 +20,11 @@
 struct cgtp_adamw_s {
   int param_dtype = 0, grad_dtype = 0, state = 0, num_sms = 0;
   std::vector<int64_t> numel, begin;   // begin[i]: first block of tensor i
-  int64_t* begin_dev = nullptr;
-  int64_t* numel_dev = nullptr;
-  float* decay_dev = nullptr;
+  std::vector<float> decay;
+  void* units_dev = nullptr;
+  std::vector<int64_t> unit_begin;     // first unit of every kMostTensors-th tensor, and their number
   double* part = nullptr;              // one partial sum of squares per CTA
+  unsigned* ticket = nullptr;          // CTAs of the norm that are done
   void* base = nullptr;
   size_t device_bytes = 0;
 };
@@ -36,33 +39,29 @@ constexpr int kENan = 255;         // block exponent of a block of NaNs
 constexpr int kStepThreads = 256;
 constexpr int kWarpsPerCta = kStepThreads / 32;
 
-struct Table {
-  const int64_t *begin, *numel;
-  const float* decay;
+constexpr int kUnit = 8;           // blocks of a unit at most
+constexpr int kMostTensors = 1024, kFewTensors = 64;   // of a launch
+
+struct __align__(16) Unit {
+  int tensor;       // within its launch
+  unsigned block;   // first block within the tensor
+  unsigned state;   // first block within the states
+  int elements;     // up to kUnit * kBlock
 };
 
-// pointers of tensors [t0, t0 + n)
+// pointers and decay factors of a launch's tensors
 template <int K>
-struct Pointers {
+struct Tensors {
   void* p[K];
   const void* g[K];
   void* c[K];
+  float decay[K];
 };
 
 struct Scalars {
   double lr_decay, b1, one_b1, b2, one_b2, rate, root, eps;
   uint32_t key0, key1;
 };
-
-// index of the tensor that holds block k: the last one that begins at or before it
-__device__ __forceinline__ int tensor_of(const int64_t* begin, int lo, int hi, int64_t k) {
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(begin + mid) <= k) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
 
 // 32 pseudo-random bits of element i: a Weyl step and two multiply-xorshift rounds
 __device__ __forceinline__ uint32_t noise_of(uint64_t i, uint32_t key0, uint32_t key1) {
@@ -73,24 +72,41 @@ __device__ __forceinline__ uint32_t noise_of(uint64_t i, uint32_t key0, uint32_t
 }
 
 // A code of a block with exponent E and largest exponent field TOP stands for
-//   field f > 0:  2^(E - TOP + f - 127) (1 + mantissa / 8),   field 0:  mantissa 2^(E - TOP + 1 - 130).
+//   field f > 0:  2^(E - TOP + f - 127) (1 + mantissa / 8),   field 0:  mantissa 2^(E - TOP + 1 - 130),
+// which is 2^(E - TOP) times the float whose bits are the code << 20 (a denormal for field 0).  The
+// power goes in as two factors, since it may pass the largest float; both products are exact.
+struct Power {
+  float first, second;
+};
 template <int TOP>
-__device__ __forceinline__ float code_value(uint32_t code, int E) {
-  const int base = max(E, kEMin) - TOP;
-  const float low = static_cast<float>(code) * __uint_as_float(static_cast<uint32_t>(base - 2) << 23);
-  const float v = code >= 8 ? __uint_as_float((static_cast<uint32_t>(base) << 23) + (code << 20)) : low;
-  return E == kENan ? __uint_as_float(0x7FC00000u) : v;
+__device__ __forceinline__ Power code_power(int E) {
+  const int base = max(E, kEMin) - TOP, half = base >> 1;
+  return {E == kENan ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(half + 127) << 23),
+          __uint_as_float(static_cast<uint32_t>(base - half + 127) << 23)};
+}
+// bits of the float of byte j of a word of four codes: m (sign and 7 bits) and v (8 bits)
+__device__ __forceinline__ float m_bits(uint32_t word, int j) {
+  const uint32_t at = j == 3 ? word >> 4 : word << (20 - 8 * j);
+  return __uint_as_float((at & 0x07F00000u) | (word << (24 - 8 * j) & 0x80000000u));
+}
+__device__ __forceinline__ float v_bits(uint32_t word, int j) {
+  return __uint_as_float((j == 3 ? word >> 4 : word << (20 - 8 * j)) & 0x0FF00000u);
 }
 
-// The code of x >= 0, rounded up with probability = its distance above the code below it; r: 20 random bits.
-// E leaves room for the largest value of the block to be rounded up.
+// The code of x >= 0 (its bits), rounded up with probability = its distance above the code below it; r: 20
+// random bits.  E leaves room for the largest value of the block to be rounded up.
 template <int TOP>
-__device__ __forceinline__ uint32_t code_of(float x, int E, uint32_t r) {
+__device__ __forceinline__ uint32_t code_of(uint32_t bits, int E, uint32_t r) {
+  return (bits + r - (static_cast<uint32_t>(E - TOP) << 23)) >> 20;
+}
+// The same where x may be below the smallest exponent of the codes.
+template <int TOP>
+__device__ __forceinline__ uint32_t code_of_any(uint32_t bits, int E, uint32_t r) {
   const int base = E - TOP;
-  const uint32_t bits = __float_as_uint(x);
-  const float fine = x * __uint_as_float(static_cast<uint32_t>(256 - base) << 23);
-  const uint32_t low = static_cast<uint32_t>(floorf(__fadd_rn(fine, static_cast<float>(r) * 9.5367431640625e-7f)));
-  return bits >= (static_cast<uint32_t>(base + 1) << 23) ? ((bits + r) >> 20) - (static_cast<uint32_t>(base) << 3) : low;
+  const float fine = __fmul_rn(__uint_as_float(bits), __uint_as_float(static_cast<uint32_t>(256 - base) << 23));
+  const float noise = __fadd_rn(__uint_as_float(0x3F800000u | r << 3), -1.0f);   // r 2^-20
+  const uint32_t low = __float_as_uint(__fadd_rd(__fadd_rn(fine, noise), 8388608.0f)) & 15u;
+  return bits >= (static_cast<uint32_t>(base + 1) << 23) ? code_of<TOP>(bits, E, r) : low;
 }
 
 __device__ __forceinline__ int block_exponent(uint32_t max_bits) {
@@ -154,107 +170,391 @@ __device__ __forceinline__ bool wide_ok(const G* p) {
 }
 
 // m and v without contraction: every product and sum is rounded as written, so that the codes of
-// the 8-bit states do not depend on how the compiler pairs them.
-__device__ __forceinline__ float mul_rn(float a, float b) { return __fmul_rn(a, b); }
-__device__ __forceinline__ double mul_rn(double a, double b) { return __dmul_rn(a, b); }
-__device__ __forceinline__ float add_rn(float a, float b) { return __fadd_rn(a, b); }
-__device__ __forceinline__ double add_rn(double a, double b) { return __dadd_rn(a, b); }
+// the 8-bit states do not depend on how the compiler pairs them.  FP32 products in pairs (one instruction for two).
+template <typename A>
+struct Pair {
+  A x, y;
+};
+__device__ __forceinline__ uint64_t bits_of(Pair<float> v) {
+  return static_cast<uint64_t>(__float_as_uint(v.y)) << 32 | __float_as_uint(v.x);
+}
+__device__ __forceinline__ Pair<float> pair_of(uint64_t b) {
+  return {__uint_as_float(static_cast<uint32_t>(b)), __uint_as_float(static_cast<uint32_t>(b >> 32))};
+}
+__device__ __forceinline__ Pair<float> mul_rn(Pair<float> a, Pair<float> b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits_of(a)), "l"(bits_of(b)));
+  return pair_of(r);
+}
+// Sums one by one: a paired sum after a paired product came out contracted to one rounding.
+__device__ __forceinline__ Pair<float> add_rn(Pair<float> a, Pair<float> b) { return {__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)}; }
+__device__ __forceinline__ Pair<double> mul_rn(Pair<double> a, Pair<double> b) { return {__dmul_rn(a.x, b.x), __dmul_rn(a.y, b.y)}; }
+__device__ __forceinline__ Pair<double> add_rn(Pair<double> a, Pair<double> b) { return {__dadd_rn(a.x, b.x), __dadd_rn(a.y, b.y)}; }
+template <typename A>
+__device__ __forceinline__ Pair<A> mul_rn(Pair<A> a, A b) {
+  return mul_rn(a, Pair<A>{b, b});
+}
 
-template <typename A, typename G, bool EIGHT, int K>
-__global__ void __launch_bounds__(kStepThreads) adamw_kernel(const __grid_constant__ Pointers<K> ptrs, const Table tab, int t0,
-                                                         int n, int64_t k0, int64_t k1, void* m_, void* v_, uint8_t* m_exp,
-                                                         uint8_t* v_exp, const Scalars s, const A* clip) {
-  const int lane = threadIdx.x & 31;
-  const int64_t k = k0 + (int64_t)blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
-  if (k >= k1) return;
-  const A coef = clip ? __ldg(clip + 1) : A(1);
-  if (!isfinite(coef)) return;
-  const int t = tensor_of(tab.begin, t0, t0 + n, k);
-  const int64_t at = (k - __ldg(tab.begin + t)) * kBlock + lane * 4;
-  const int64_t left = __ldg(tab.numel + t) - at;
-  const G* g = static_cast<const G*>(ptrs.g[t - t0]);
-  if (!g) return;
-  A* p = static_cast<A*>(ptrs.p[t - t0]) + at;
-  g += at;
-  const int64_t place = k * kBlock + lane * 4;
-  A pv[4], gv[4], mv[4], vv[4];
-  load4<A, A>(p, left, wide_ok(p), pv);
-  load4<G, A>(g, left, wide_ok(g), gv);
-  if constexpr (EIGHT) {
-    const uint32_t mc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(m_) + place);
-    const uint32_t vc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(v_) + place);
-    const int me = m_exp[k], ve = v_exp[k];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = code_value<kMTop>(mc >> (8 * i) & 127u, me);
-      mv[i] = mc >> (8 * i) & 128u ? -a : a;
-      vv[i] = code_value<kVTop>(vc >> (8 * i) & 255u, ve);
-    }
-  } else {
-    load4<A, A>(static_cast<const A*>(m_) + place, 4, true, mv);
-    load4<A, A>(static_cast<const A*>(v_) + place, 4, true, vv);
+// rate m / (sqrt(v) root + eps).  FP32: the move's relative error of a few units matters less than p's own
+// rounding.  FAST: eps is large enough that a v below the smallest normal float counts as zero.
+template <bool FAST>
+__device__ __forceinline__ float move_of(float m, float v, float rate, float root, float eps) {
+  float s, r;
+  if constexpr (FAST) {
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(v));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s * root + eps));
+    return rate * m * r;
   }
-  const A keep = A(1) - static_cast<A>(s.lr_decay) * static_cast<A>(__ldg(tab.decay + t));
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(s) : "f"(v));
+  return __fdividef(rate * m, s * root + eps);
+}
+template <bool FAST>
+__device__ __forceinline__ double move_of(double m, double v, double rate, double root, double eps) {
+  return rate * m / (sqrt(v) * root + eps);
+}
+
+template <typename A>
+struct StepScalars {
+  A coef, keep, b1, one_b1, b2, one_b2, rate, root, eps;
+  uint32_t key0, key1;
+};
+
+// One block: p, g, m and v of a lane are there; m is m_scale times mv (a power of two or 1) before b1, and so is v.
+template <typename A>
+__device__ __forceinline__ void step_values(A (&p)[4], const A (&g)[4], A (&m)[4], A (&v)[4], const StepScalars<A>& s,
+                                            A m_scale, A v_scale) {
+  const A b1 = s.b1 * m_scale, b2 = s.b2 * v_scale;   // exact
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const Pair<A> gi = mul_rn(Pair<A>{g[i], g[i + 1]}, s.coef);
+    const Pair<A> mn = add_rn(mul_rn(Pair<A>{m[i], m[i + 1]}, b1), mul_rn(gi, s.one_b1));
+    const Pair<A> vn = add_rn(mul_rn(Pair<A>{v[i], v[i + 1]}, b2), mul_rn(mul_rn(gi, gi), s.one_b2));
+    m[i] = mn.x, m[i + 1] = mn.y, v[i] = vn.x, v[i + 1] = vn.y;
+  }
+  // eps + sqrt(v) for v < 2^-126: 1.1e-19 of 1e-12 is below FP32's rounding
+  if (s.eps >= A(1e-12)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = p[i] * s.keep - move_of<true>(m[i], v[i], s.rate, s.root, s.eps);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = p[i] * s.keep - move_of<false>(m[i], v[i], s.rate, s.root, s.eps);
+  }
+}
+
+// Rounds a block's m and v to codes: words of four codes a lane, and the block's exponents.
+__device__ __forceinline__ void encode_block(const float (&m)[4], const float (&v)[4], int64_t place, const StepScalars<float>& s,
+                                             uint32_t* m_word, uint32_t* v_word, uint32_t* m_exp, uint32_t* v_exp) {
+  uint32_t a[4], b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = __float_as_uint(m[i]) & 0x7FFFFFFFu, b[i] = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+  const uint32_t mb = max(max(a[0], a[1]), max(a[2], a[3])), vb = max(max(b[0], b[1]), max(b[2], b[3]));
+  const int me = block_exponent(__reduce_max_sync(0xffffffffu, mb)), ve = block_exponent(__reduce_max_sync(0xffffffffu, vb));
+  const uint32_t key = static_cast<uint32_t>(place >> 32) * 0x85A308D3u + s.key0;
+  const uint32_t m_low = static_cast<uint32_t>(me - kMTop + 1) << 23, v_low = static_cast<uint32_t>(ve - kVTop + 1) << 23;
+  uint32_t mc = 0, vc = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const A gi = mul_rn(gv[i], coef);
-    mv[i] = add_rn(mul_rn(mv[i], static_cast<A>(s.b1)), mul_rn(gi, static_cast<A>(s.one_b1)));
-    vv[i] = add_rn(mul_rn(vv[i], static_cast<A>(s.b2)), mul_rn(mul_rn(gi, gi), static_cast<A>(s.one_b2)));
-    pv[i] = pv[i] * keep - static_cast<A>(s.rate) * mv[i] / (sqrt(vv[i]) * static_cast<A>(s.root) + static_cast<A>(s.eps));
+    const uint32_t r = noise_of(static_cast<uint32_t>(place) + i, key, s.key1);
+    const uint32_t rm = r >> 12 & 0xFFFF0u, rv = r << 4 & 0xFFFF0u;
+    // a warp looks for values below the smallest exponent: m has some in every third vote where gradients are
+    // heavy-tailed, v hardly any but zeros
+    uint32_t cm, cv;
+    if (__any_sync(0xffffffffu, a[i] < m_low)) cm = code_of_any<kMTop>(a[i], me, rm);
+    else cm = code_of<kMTop>(a[i], me, rm);
+    if (__any_sync(0xffffffffu, b[i] < v_low)) {
+      cv = code_of_any<kVTop>(b[i], ve, rv);
+      cv = b[i] ? max(cv, 1u) : cv;
+    } else {
+      cv = code_of<kVTop>(b[i], ve, rv);
+    }
+    mc |= (cm | (__float_as_uint(m[i]) >> 24 & 128u)) << (8 * i);
+    vc |= cv << (8 * i);
   }
-  store4<A, A>(p, left, wide_ok(p), pv);
-  if constexpr (sizeof(A) == 4) {
-    if (ptrs.c[t - t0]) {
-      __nv_bfloat16* c = static_cast<__nv_bfloat16*>(ptrs.c[t - t0]) + at;
-      store4<__nv_bfloat16, A>(c, left, wide_ok(c), pv);
-    }
+  *m_word = me >= kENan ? 0 : mc;
+  *v_word = ve >= kENan ? 0 : vc;
+  *m_exp = static_cast<uint32_t>(min(me, kENan));
+  *v_exp = static_cast<uint32_t>(min(ve, kENan));
+}
+
+template <typename A>
+__device__ __forceinline__ StepScalars<A> scalars_of(const Scalars& host, A coef) {
+  StepScalars<A> s;
+  s.coef = coef;
+  s.b1 = static_cast<A>(host.b1), s.one_b1 = static_cast<A>(host.one_b1);
+  s.b2 = static_cast<A>(host.b2), s.one_b2 = static_cast<A>(host.one_b2);
+  s.rate = static_cast<A>(host.rate), s.root = static_cast<A>(host.root), s.eps = static_cast<A>(host.eps);
+  s.key0 = host.key0, s.key1 = host.key1;
+  return s;
+}
+
+// ---------------------------------------------------------------------------
+// States in the parameters' type: a lane holds its elements of NB blocks, and the loads of the next NB are
+// in flight while these are computed.
+// ---------------------------------------------------------------------------
+
+template <typename A, int NB>
+struct Held {
+  A p[NB][4], g[NB][4], m[NB][4], v[NB][4];
+};
+
+// k: the first block's place in the states; p, g, c point at the lane's elements of it, of which `left` are
+// in the tensor.  WHOLE: every element is there and every address allows 16-byte (bfloat16: 8-byte) accesses.
+template <typename A, typename G, bool WHOLE, int NB>
+__device__ __forceinline__ void get_blocks(Held<A, NB>& h, unsigned k, int left, const A* p, const G* g, const A* m, const A* v) {
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int64_t place = (int64_t)(k + b) * kBlock + (threadIdx.x & 31) * 4;
+    load4<A, A>(p + b * kBlock, WHOLE ? 4 : left - b * kBlock, WHOLE || wide_ok(p), h.p[b]);
+    load4<G, A>(g + b * kBlock, WHOLE ? 4 : left - b * kBlock, WHOLE || wide_ok(g), h.g[b]);
+    load4<A, A>(m + place, 4, true, h.m[b]);
+    load4<A, A>(v + place, 4, true, h.v[b]);
   }
-  if constexpr (EIGHT) {
-    uint32_t mb = 0, vb = 0;
+}
+template <typename A, bool WHOLE, int NB>
+__device__ __forceinline__ void put_blocks(Held<A, NB>& h, unsigned k, int left, A* p, __nv_bfloat16* c, A* m, A* v,
+                                           const StepScalars<A>& s) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i >= left) mv[i] = vv[i] = 0.0f;   // the place behind the tensor's end
-      mb = max(mb, __float_as_uint(mv[i]) & 0x7FFFFFFFu);
-      vb = max(vb, __float_as_uint(vv[i]) & 0x7FFFFFFFu);
+  for (int b = 0; b < NB; ++b) {
+    const int64_t place = (int64_t)(k + b) * kBlock + (threadIdx.x & 31) * 4;
+    const int rest = WHOLE ? 4 : left - b * kBlock;
+    step_values<A>(h.p[b], h.g[b], h.m[b], h.v[b], s, A(1), A(1));
+    store4<A, A>(p + b * kBlock, rest, WHOLE || wide_ok(p), h.p[b]);
+    if constexpr (sizeof(A) == 4)
+      if (c) store4<__nv_bfloat16, A>(c + b * kBlock, rest, WHOLE || wide_ok(c), h.p[b]);
+    store4<A, A>(m + place, 4, true, h.m[b]);
+    store4<A, A>(v + place, 4, true, h.v[b]);
+  }
+}
+
+template <typename A, typename G, int K>
+__global__ void __launch_bounds__(kStepThreads) adamw_kernel(const __grid_constant__ Tensors<K> ts, const Unit* units,
+                                                             unsigned n_units, A* m, A* v, const Scalars host, const A* clip) {
+  constexpr int NB = sizeof(A) == 8 ? 1 : 2;
+  const int lane = threadIdx.x & 31;
+  const unsigned stride = gridDim.x * kWarpsPerCta;
+  unsigned u = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
+  if (u >= n_units) return;
+  Unit next = units[u];
+  const A coef = clip ? __ldg(clip + 1) : A(1);
+  if (!isfinite(coef)) return;
+  StepScalars<A> s = scalars_of<A>(host, coef);
+  const A lr_decay = static_cast<A>(host.lr_decay);
+  for (;;) {
+    const Unit unit = next;
+    u += stride;
+    if (u < n_units) next = units[u];
+    const G* g = static_cast<const G*>(ts.g[unit.tensor]);
+    if (g) {
+      s.keep = A(1) - lr_decay * static_cast<A>(ts.decay[unit.tensor]);
+      const int64_t at = (int64_t)unit.block * kBlock + lane * 4;
+      A* p = static_cast<A*>(ts.p[unit.tensor]) + at;
+      __nv_bfloat16* c = ts.c[unit.tensor] ? static_cast<__nv_bfloat16*>(ts.c[unit.tensor]) + at : nullptr;
+      g += at;
+      if (unit.elements == kUnit * kBlock && wide_ok(p) && wide_ok(g) && (!c || wide_ok(c))) {
+        Held<A, NB> h, ahead;
+        get_blocks<A, G, true, NB>(h, unit.state, 4, p, g, m, v);
+#pragma unroll 1
+        for (int b = 0; b < kUnit; b += NB) {
+          if (b + NB < kUnit) get_blocks<A, G, true, NB>(ahead, unit.state + b + NB, 4, p + (b + NB) * kBlock, g + (b + NB) * kBlock, m, v);
+          put_blocks<A, true, NB>(h, unit.state + b, 4, p + b * kBlock, c ? c + b * kBlock : nullptr, m, v, s);
+          h = ahead;
+        }
+      } else {
+#pragma unroll 1
+        for (int b = 0; b * kBlock < unit.elements; ++b) {
+          Held<A, 1> h;
+          const int left = unit.elements - b * kBlock - lane * 4;
+          get_blocks<A, G, false, 1>(h, unit.state + b, left, p + b * kBlock, g + b * kBlock, m, v);
+          put_blocks<A, false, 1>(h, unit.state + b, left, p + b * kBlock, c ? c + b * kBlock : nullptr, m, v, s);
+        }
+      }
     }
-    const int me = block_exponent(__reduce_max_sync(0xffffffffu, mb));
-    const int ve = block_exponent(__reduce_max_sync(0xffffffffu, vb));
-    uint32_t mc = 0, vc = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t r = noise_of(static_cast<uint64_t>(place + i), s.key0, s.key1);
-      const uint32_t a = code_of<kMTop>(fabsf(mv[i]), me, (r >> 16) << 4) | (mv[i] < 0.0f ? 128u : 0u);
-      uint32_t b = code_of<kVTop>(vv[i], ve, (r & 0xFFFFu) << 4);
-      b = vv[i] > 0.0f ? max(b, 1u) : b;
-      mc |= a << (8 * i);
-      vc |= b << (8 * i);
+    if (u >= n_units) return;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit states.  Decoding and rounding take about 300 instructions a block, so a warp that waits for
+// its loads costs issue slots: operands come through a ring of asynchronous copies in shared memory, two blocks
+// a stage, that runs ahead over the warp's units.
+// ---------------------------------------------------------------------------
+
+constexpr int kRing = 3, kStageBlocks = 2;
+
+template <typename G>
+struct __align__(16) Stage {
+  float p[kStageBlocks * kBlock];
+  G g[kStageBlocks * kBlock];
+  uint8_t m[kStageBlocks * kBlock], v[kStageBlocks * kBlock];
+  float* to;            // the first block's parameters, and their copy
+  __nv_bfloat16* copy;
+  unsigned state;       // the first block's place in the states
+  int elements;         // from there to the end of the unit
+  float keep;
+  int wide;             // whole blocks at aligned addresses
+};
+
+__device__ __forceinline__ void copy_async16(void* shared, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(shared))), "l"(global) : "memory");
+}
+__device__ __forceinline__ void copy_async8(void* shared, const void* global) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(shared))), "l"(global) : "memory");
+}
+
+// The warp's units in order, a stage's blocks at a time.
+template <typename G, int K>
+struct Feed {
+  const Tensors<K>& ts;
+  const Unit* units;
+  unsigned n_units, stride, next_index;
+  Unit unit, next;
+  int block;            // next block of the unit
+  const uint8_t *m, *v;
+  float lr_decay;
+
+  __device__ __forceinline__ void advance() {
+    unit = next;
+    block = 0;
+    next_index += stride;
+    next.elements = 0;
+    if (next_index < n_units) next = units[next_index];
+  }
+  // fills a stage; false behind the last unit
+  __device__ __forceinline__ bool fill(Stage<G>& st) {
+    const int lane = threadIdx.x & 31;
+    while (block * kBlock >= unit.elements || !ts.g[unit.tensor]) {
+      if (next.elements == 0) return false;
+      advance();
     }
-    if (me >= kENan) mc = 0;
-    if (ve >= kENan) vc = 0;
-    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(m_) + place) = mc;
-    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(v_) + place) = vc;
+    const int elements = unit.elements - block * kBlock;
+    const int64_t at = (int64_t)(unit.block + block) * kBlock;
+    float* p = static_cast<float*>(ts.p[unit.tensor]) + at;
+    const G* g = static_cast<const G*>(ts.g[unit.tensor]) + at;
+    __nv_bfloat16* c = ts.c[unit.tensor] ? static_cast<__nv_bfloat16*>(ts.c[unit.tensor]) + at : nullptr;
+    const unsigned state = unit.state + block;
+    const bool wide = elements >= kStageBlocks * kBlock && wide_ok(p) && wide_ok(g) && (!c || wide_ok(c));
     if (lane == 0) {
-      m_exp[k] = static_cast<uint8_t>(min(me, kENan));
-      v_exp[k] = static_cast<uint8_t>(min(ve, kENan));
+      st.to = p, st.copy = c;
+      st.state = state, st.elements = elements;
+      st.keep = 1.0f - lr_decay * ts.decay[unit.tensor];
+      st.wide = wide;
     }
-  } else {
-    store4<A, A>(static_cast<A*>(m_) + place, left, true, mv);
-    store4<A, A>(static_cast<A*>(v_) + place, left, true, vv);
+    if (wide) {
+#pragma unroll
+      for (int b = 0; b < kStageBlocks; ++b) {
+        copy_async16(st.p + b * kBlock + lane * 4, p + b * kBlock + lane * 4);
+        if constexpr (sizeof(G) == 4) copy_async16(st.g + b * kBlock + lane * 4, g + b * kBlock + lane * 4);
+        else copy_async8(st.g + b * kBlock + lane * 4, g + b * kBlock + lane * 4);
+      }
+      // 16 lanes the codes of m, 16 those of v
+      const uint8_t* codes = (lane < 16 ? m : v) + (int64_t)state * kBlock + (lane & 15) * 16;
+      copy_async16((lane < 16 ? st.m : st.v) + (lane & 15) * 16, codes);
+    } else {
+      for (int i = lane; i < min(elements, kStageBlocks * kBlock); i += 32) st.p[i] = p[i], st.g[i] = g[i];
+      const int words = min(kStageBlocks, (elements + kBlock - 1) / kBlock) * (kBlock / 4);
+      for (int i = lane; i < words; i += 32) {
+        reinterpret_cast<uint32_t*>(st.m)[i] = reinterpret_cast<const uint32_t*>(m + (int64_t)state * kBlock)[i];
+        reinterpret_cast<uint32_t*>(st.v)[i] = reinterpret_cast<const uint32_t*>(v + (int64_t)state * kBlock)[i];
+      }
+    }
+    block += kStageBlocks;
+    return true;
+  }
+};
+
+template <typename G, int K>
+__global__ void __launch_bounds__(kStepThreads, 3) adamw8_kernel(const __grid_constant__ Tensors<K> ts, const Unit* units,
+                                                                 unsigned n_units, uint8_t* m_, uint8_t* v_, uint8_t* m_exp,
+                                                                 uint8_t* v_exp, const Scalars host, const float* clip) {
+  extern __shared__ __align__(16) unsigned char shared[];
+  const int lane = threadIdx.x & 31;
+  Stage<G>* ring = reinterpret_cast<Stage<G>*>(shared) + (threadIdx.x >> 5) * kRing;
+  const unsigned first = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
+  if (first >= n_units) return;
+  const float coef = clip ? __ldg(clip + 1) : 1.0f;
+  if (!isfinite(coef)) return;
+  StepScalars<float> s = scalars_of<float>(host, coef);
+  Feed<G, K> feed{ts, units, n_units, gridDim.x * kWarpsPerCta, first, {}, units[first], 0, m_, v_, static_cast<float>(host.lr_decay)};
+  feed.advance();
+  int filled = 0, done = 0;
+  bool more = true;
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) {
+    more = more && feed.fill(ring[i]);
+    filled += more;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __syncwarp();
+  // exponents of a stage's blocks: lanes 0 and 1 those of m, 2 and 3 those of v, a stage ahead
+  static_assert(kStageBlocks == 2, "lanes 0 to 3 hold the exponents of a stage");
+  const auto exponent_at = [&](const Stage<G>& st) { return (lane < 2 ? m_exp : v_exp) + st.state + (lane & 1); };
+  const auto exponents = [&](const Stage<G>& st) -> uint32_t {
+    return lane < 4 && (lane & 1) * kBlock < st.elements ? *exponent_at(st) : 0u;
+  };
+  uint32_t e = done < filled ? exponents(ring[0]) : 0u;
+  for (int at = 0; done < filled; ++done, at = at + 1 == kRing ? 0 : at + 1) {
+    const int free = at == 0 ? kRing - 1 : at - 1;   // the stage of the last turn
+    more = more && feed.fill(ring[free]);
+    filled += more;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    __syncwarp();
+    const Stage<G>& st = ring[at];
+    const uint32_t e_now = e;
+    if (done + 1 < filled) e = exponents(ring[at + 1 == kRing ? 0 : at + 1]);
+    s.keep = st.keep;
+    uint32_t e_new = 0;
+#pragma unroll
+    for (int b = 0; b < kStageBlocks; ++b) {
+      if (b * kBlock < st.elements) {
+        const int64_t place = (int64_t)(st.state + b) * kBlock + lane * 4;
+        const int left = st.elements - b * kBlock - lane * 4;
+        float p[4], g[4], m[4], v[4];
+        load4<float, float>(st.p + b * kBlock + lane * 4, 4, true, p);
+        load4<G, float>(st.g + b * kBlock + lane * 4, 4, true, g);
+        const uint32_t mw = reinterpret_cast<const uint32_t*>(st.m + b * kBlock)[lane], vw = reinterpret_cast<const uint32_t*>(st.v + b * kBlock)[lane];
+        const Power mp = code_power<kMTop>(__shfl_sync(0xffffffffu, e_now, b)), vp = code_power<kVTop>(__shfl_sync(0xffffffffu, e_now, 2 + b));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          m[i] = m_bits(mw, i) * mp.first;
+          v[i] = v_bits(vw, i) * vp.first;
+        }
+        step_values<float>(p, g, m, v, s, mp.second, vp.second);
+        float* to = st.to + b * kBlock + lane * 4;
+        __nv_bfloat16* copy = st.copy ? st.copy + b * kBlock + lane * 4 : nullptr;
+        if (st.wide) {
+          store4<float, float>(to, 4, true, p);
+          if (copy) store4<__nv_bfloat16, float>(copy, 4, true, p);
+        } else {
+          store4<float, float>(to, left, wide_ok(to), p);
+          if (copy) store4<__nv_bfloat16, float>(copy, left, wide_ok(copy), p);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i >= left) m[i] = v[i] = 0.0f;   // the place behind the tensor's end
+        }
+        uint32_t m_word, v_word, me, ve;
+        encode_block(m, v, place, s, &m_word, &v_word, &me, &ve);
+        *reinterpret_cast<uint32_t*>(m_ + place) = m_word;
+        *reinterpret_cast<uint32_t*>(v_ + place) = v_word;
+        e_new = lane == b ? me : lane == 2 + b ? ve : e_new;
+      }
+    }
+    if (lane < 4 && (lane & 1) * kBlock < st.elements) *exponent_at(st) = static_cast<uint8_t>(e_new);
+    __syncwarp();
   }
 }
 
 __global__ void __launch_bounds__(kStepThreads) state_values_kernel(const uint8_t* m, const uint8_t* v, const uint8_t* m_exp,
-                                                                const uint8_t* v_exp, float* m_out, float* v_out, int64_t n4) {
+                                                                    const uint8_t* v_exp, float* m_out, float* v_out, int64_t n4) {
   const int64_t i = (int64_t)blockIdx.x * kStepThreads + threadIdx.x;
   if (i >= n4) return;
   const uint32_t mc = reinterpret_cast<const uint32_t*>(m)[i], vc = reinterpret_cast<const uint32_t*>(v)[i];
-  const int me = m_exp[i >> 5], ve = v_exp[i >> 5];
+  const Power mp = code_power<kMTop>(m_exp[i >> 5]), vp = code_power<kVTop>(v_exp[i >> 5]);
   float a[4], b[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float t = code_value<kMTop>(mc >> (8 * j) & 127u, me);
-    a[j] = mc >> (8 * j) & 128u ? -t : t;
-    b[j] = code_value<kVTop>(vc >> (8 * j) & 255u, ve);
+    a[j] = __fmul_rn(__fmul_rn(m_bits(mc, j), mp.first), mp.second);
+    b[j] = __fmul_rn(__fmul_rn(v_bits(vc, j), vp.first), vp.second);
   }
   reinterpret_cast<float4*>(m_out)[i] = make_float4(a[0], a[1], a[2], a[3]);
   reinterpret_cast<float4*>(v_out)[i] = make_float4(b[0], b[1], b[2], b[3]);
@@ -263,6 +563,7 @@ __global__ void __launch_bounds__(kStepThreads) state_values_kernel(const uint8_
 __device__ __forceinline__ double cta_sum(double v) {
   __shared__ double warp_sum[kWarpsPerCta];
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
   if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = v;
   __syncthreads();
   double t = 0.0;
@@ -270,53 +571,67 @@ __device__ __forceinline__ double cta_sum(double v) {
   return t;
 }
 
-// sum of squares of the CTA's blocks: a thread's own in A, the rest in FP64
+// Sum of squares of the CTA's units: a thread's own in A, the rest in FP64.  The last CTA of the last launch
+// (a counter; the order of the sums does not depend on it) adds the CTAs' sums and leaves the counter at zero.
 template <typename A, typename G, int K>
-__global__ void __launch_bounds__(kStepThreads) square_sum_kernel(const __grid_constant__ Pointers<K> ptrs, const Table tab, int t0,
-                                                              int n, int64_t k0, int64_t k1, double* part) {
+__global__ void __launch_bounds__(kStepThreads) norm_kernel(const __grid_constant__ Tensors<K> ts, const Unit* units,
+                                                            unsigned n_units, double* part, int before, bool last,
+                                                            unsigned* ticket, double max_norm, A* out) {
   const int lane = threadIdx.x & 31;
-  A sum = A(0);
-  for (int64_t k = k0 + (int64_t)blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5); k < k1; k += (int64_t)gridDim.x * kWarpsPerCta) {
-    const int t = tensor_of(tab.begin, t0, t0 + n, k);
-    const G* g = static_cast<const G*>(ptrs.g[t - t0]);
+  A sum[4] = {A(0), A(0), A(0), A(0)};
+  for (unsigned u = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5); u < n_units; u += gridDim.x * kWarpsPerCta) {
+    const Unit unit = units[u];
+    const G* g = static_cast<const G*>(ts.g[unit.tensor]);
     if (!g) continue;
-    const int64_t at = (k - __ldg(tab.begin + t)) * kBlock + lane * 4;
-    A v[4];
-    load4<G, A>(g + at, __ldg(tab.numel + t) - at, wide_ok(g + at), v);
+    g += (int64_t)unit.block * kBlock + lane * 4;
+    A v[kUnit][4];
+    if (unit.elements == kUnit * kBlock && wide_ok(g)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum += v[i] * v[i];
+      for (int b = 0; b < kUnit; ++b) load4<G, A>(g + b * kBlock, 4, true, v[b]);
+    } else {
+#pragma unroll
+      for (int b = 0; b < kUnit; ++b) load4<G, A>(g + b * kBlock, unit.elements - b * kBlock - lane * 4, wide_ok(g), v[b]);
+    }
+#pragma unroll
+    for (int b = 0; b < kUnit; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] += v[b][i] * v[b][i];
   }
-  const double total = cta_sum(static_cast<double>(sum));
-  if (threadIdx.x == 0) part[blockIdx.x] = total;
-}
-
-template <typename A>
-__global__ void __launch_bounds__(kStepThreads) norm_kernel(const double* part, int count, double max_norm, A* out) {
+  const double mine = cta_sum(static_cast<double>((sum[0] + sum[1]) + (sum[2] + sum[3])));
+  __shared__ bool finish;
+  if (threadIdx.x == 0) {
+    part[before + blockIdx.x] = mine;
+    __threadfence();
+    finish = last && atomicAdd(ticket, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!finish) return;
+  __threadfence();
+  const int count = before + static_cast<int>(gridDim.x);
   double v = 0.0;
-  for (int i = threadIdx.x; i < count; i += kStepThreads) v += part[i];
+  for (int i = threadIdx.x; i < count; i += kStepThreads) v += __ldcg(part + i);
   v = cta_sum(v);
   if (threadIdx.x != 0) return;
+  *ticket = 0;
   const double norm = sqrt(v);
   out[0] = static_cast<A>(norm);
   out[1] = isfinite(norm) ? static_cast<A>(norm > max_norm ? max_norm / norm : 1.0) : static_cast<A>(nan(""));
 }
 
-constexpr int kMostTensors = 1024, kFewTensors = 64;
-constexpr int kNormCtasPerSm = 8;
+constexpr int kNormCtasPerSm = 8, kStepCtasPerSm = 8;
 
 cgtp_status launched(const char* what) {
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? CGTP_OK : fail(CGTP_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
-Table table(const cgtp_adamw_s* o) { return {o->begin_dev, o->numel_dev, o->decay_dev}; }
-
 template <int K>
-void fill(Pointers<K>* a, int t0, int n, void* const* params, const void* const* grads, void* const* copies) {
+void fill(Tensors<K>* a, const cgtp_adamw_s* o, int t0, int n, void* const* params, const void* const* grads, void* const* copies) {
   for (int i = 0; i < n; ++i) {
     a->p[i] = params ? params[t0 + i] : nullptr;
     a->g[i] = grads[t0 + i];
     a->c[i] = copies ? copies[t0 + i] : nullptr;
+    a->decay[i] = o->decay[t0 + i];
   }
 }
 
@@ -327,16 +642,29 @@ struct StepArgs {
   const void* clip;
 };
 
+int ctas_for(const cgtp_adamw_s* o, int64_t units, int per_sm) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((units + kWarpsPerCta - 1) / kWarpsPerCta, int64_t(o->num_sms) * per_sm)));
+}
+
 template <typename A, typename G, bool EIGHT, int K>
 cgtp_status step_launch(const cgtp_adamw_s* o, int t0, int n, void* const* params, const void* const* grads,
                         void* const* copies, const StepArgs& a, cudaStream_t st) {
-  Pointers<K> ptrs;
-  fill(&ptrs, t0, n, params, grads, copies);
-  const int64_t k0 = o->begin[t0], k1 = o->begin[t0 + n];
-  if (k1 == k0) return CGTP_OK;
-  const int64_t ctas = (k1 - k0 + kWarpsPerCta - 1) / kWarpsPerCta;
-  adamw_kernel<A, G, EIGHT, K><<<static_cast<unsigned>(ctas), kStepThreads, 0, st>>>(
-      ptrs, table(o), t0, n, k0, k1, a.m, a.v, a.m_exp, a.v_exp, a.s, static_cast<const A*>(a.clip));
+  Tensors<K> ts;
+  fill(&ts, o, t0, n, params, grads, copies);
+  const int64_t u0 = o->unit_begin[t0 / kMostTensors], u1 = o->unit_begin[t0 / kMostTensors + 1];
+  if (u1 == u0) return CGTP_OK;
+  const Unit* units = static_cast<const Unit*>(o->units_dev) + u0;
+  const unsigned n_units = static_cast<unsigned>(u1 - u0);
+  if constexpr (EIGHT) {
+    constexpr int bytes = kWarpsPerCta * kRing * sizeof(Stage<G>);
+    if (smem_cap_cached(reinterpret_cast<const void*>(adamw8_kernel<G, K>)) < bytes) return fail(CGTP_ECUDA, "adamw step: shared memory");
+    adamw8_kernel<G, K><<<ctas_for(o, n_units, 3), kStepThreads, bytes, st>>>(
+        ts, units, n_units, static_cast<uint8_t*>(a.m), static_cast<uint8_t*>(a.v), a.m_exp, a.v_exp, a.s,
+        static_cast<const float*>(a.clip));
+  } else {
+    adamw_kernel<A, G, K><<<ctas_for(o, n_units, kStepCtasPerSm), kStepThreads, 0, st>>>(
+        ts, units, n_units, static_cast<A*>(a.m), static_cast<A*>(a.v), a.s, static_cast<const A*>(a.clip));
+  }
   return launched("adamw step");
 }
 
@@ -353,31 +681,28 @@ cgtp_status step_all(const cgtp_adamw_s* o, void* const* params, const void* con
   return CGTP_OK;
 }
 
-template <typename A, typename G, int K>
-cgtp_status norm_launch(const cgtp_adamw_s* o, int t0, int n, const void* const* grads, int ctas, double* part,
-                        cudaStream_t st) {
-  Pointers<K> ptrs;
-  fill(&ptrs, t0, n, nullptr, grads, nullptr);
-  square_sum_kernel<A, G, K><<<ctas, kStepThreads, 0, st>>>(ptrs, table(o), t0, n, o->begin[t0], o->begin[t0 + n], part);
-  return launched("gradient norm");
-}
-
 template <typename A, typename G>
 cgtp_status norm_all(const cgtp_adamw_s* o, const void* const* grads, double max_norm, void* out, cudaStream_t st) {
   const int all = static_cast<int>(o->numel.size());
-  int count = 0;
+  int before = 0;
   for (int t0 = 0; t0 < all; t0 += kMostTensors) {
     const int n = std::min(kMostTensors, all - t0);
-    const int64_t blocks = o->begin[t0 + n] - o->begin[t0];
-    const int ctas = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>((blocks + kWarpsPerCta - 1) / kWarpsPerCta, o->num_sms * kNormCtasPerSm)));
-    const cgtp_status s = n <= kFewTensors ? norm_launch<A, G, kFewTensors>(o, t0, n, grads, ctas, o->part + count, st)
-                                           : norm_launch<A, G, kMostTensors>(o, t0, n, grads, ctas, o->part + count, st);
+    const int64_t u0 = o->unit_begin[t0 / kMostTensors], u1 = o->unit_begin[t0 / kMostTensors + 1];
+    const int ctas = ctas_for(o, u1 - u0, kNormCtasPerSm);
+    const bool last = t0 + n == all;
+    const auto run = [&](auto few, auto kernel) {
+      decltype(few) ts;
+      fill(&ts, o, t0, n, nullptr, grads, nullptr);
+      kernel<<<ctas, kStepThreads, 0, st>>>(ts, static_cast<const Unit*>(o->units_dev) + u0, static_cast<unsigned>(u1 - u0),
+                                            o->part, before, last, o->ticket, max_norm, static_cast<A*>(out));
+    };
+    if (n <= kFewTensors) run(Tensors<kFewTensors>{}, norm_kernel<A, G, kFewTensors>);
+    else run(Tensors<kMostTensors>{}, norm_kernel<A, G, kMostTensors>);
+    const cgtp_status s = launched("gradient norm");
     if (s != CGTP_OK) return s;
-    count += ctas;
+    before += ctas;
   }
-  norm_kernel<A><<<1, kStepThreads, 0, st>>>(o->part, count, max_norm, static_cast<A*>(out));
-  return launched("gradient norm");
+  return CGTP_OK;
 }
 
 int es_of(int dtype) { return dtype == CGTP_F64 ? 8 : dtype == CGTP_BF16 ? 2 : 4; }
@@ -418,23 +743,30 @@ cgtp_status create(cgtp_adamw_s* o, int n, const int64_t* numel, const float* de
     cudaGetLastError();
     return fail(CGTP_ECUDA, "no CUDA device");
   }
-  const std::vector<float> decay = decay_scale ? std::vector<float>(decay_scale, decay_scale + n) : std::vector<float>(n, 1.0f);
-  const size_t parts = size_t(o->num_sms) * kNormCtasPerSm * ((n + kMostTensors - 1) / kMostTensors);
-  const size_t b_begin = (n + 1) * sizeof(int64_t), b_numel = n * sizeof(int64_t), b_part = parts * sizeof(double);
-  const size_t bytes = b_begin + b_numel + b_part + n * sizeof(float);
+  o->decay.assign(n, 1.0f);
+  if (decay_scale) o->decay.assign(decay_scale, decay_scale + n);
+  std::vector<Unit> units;
+  for (int i = 0; i < n; ++i) {
+    if (i % kMostTensors == 0) o->unit_begin.push_back(static_cast<int64_t>(units.size()));
+    for (int64_t b = 0; b < o->begin[i + 1] - o->begin[i]; b += kUnit)
+      units.push_back({i % kMostTensors, static_cast<unsigned>(b), static_cast<unsigned>(o->begin[i] + b),
+                       static_cast<int>(std::min<int64_t>(kUnit * kBlock, numel[i] - b * kBlock))});
+  }
+  o->unit_begin.push_back(static_cast<int64_t>(units.size()));
+  const size_t parts = size_t(o->num_sms) * kNormCtasPerSm * (o->unit_begin.size() - 1);
+  const size_t b_units = units.size() * sizeof(Unit), b_part = parts * sizeof(double);
+  const size_t bytes = b_units + b_part + sizeof(unsigned);
   if (cudaMalloc(&o->base, bytes) != cudaSuccess) {
     cudaGetLastError();
     return fail(CGTP_ENOMEM, "optimizer table allocation failed");
   }
   o->device_bytes = bytes;
   unsigned char* at = static_cast<unsigned char*>(o->base);
-  o->begin_dev = reinterpret_cast<int64_t*>(at);
-  o->numel_dev = reinterpret_cast<int64_t*>(at + b_begin);
-  o->part = reinterpret_cast<double*>(at + b_begin + b_numel);
-  o->decay_dev = reinterpret_cast<float*>(at + b_begin + b_numel + b_part);
-  if (cudaMemcpy(o->begin_dev, o->begin.data(), b_begin, cudaMemcpyHostToDevice) != cudaSuccess ||
-      cudaMemcpy(o->numel_dev, o->numel.data(), b_numel, cudaMemcpyHostToDevice) != cudaSuccess ||
-      cudaMemcpy(o->decay_dev, decay.data(), n * sizeof(float), cudaMemcpyHostToDevice) != cudaSuccess) {
+  o->units_dev = at;
+  o->part = reinterpret_cast<double*>(at + b_units);
+  o->ticket = reinterpret_cast<unsigned*>(at + b_units + b_part);
+  if ((b_units && cudaMemcpy(o->units_dev, units.data(), b_units, cudaMemcpyHostToDevice) != cudaSuccess) ||
+      cudaMemset(o->ticket, 0, sizeof(unsigned)) != cudaSuccess) {
     cudaGetLastError();
     return fail(CGTP_ECUDA, "optimizer table upload failed");
   }
