@@ -250,26 +250,29 @@ __device__ __forceinline__ void encode_block(const float (&m)[4], const float (&
   const uint32_t mb = max(max(a[0], a[1]), max(a[2], a[3])), vb = max(max(b[0], b[1]), max(b[2], b[3]));
   const int me = block_exponent(__reduce_max_sync(0xffffffffu, mb)), ve = block_exponent(__reduce_max_sync(0xffffffffu, vb));
   const uint32_t key = static_cast<uint32_t>(place >> 32) * 0x85A308D3u + s.key0;
-  const uint32_t m_low = static_cast<uint32_t>(me - kMTop + 1) << 23, v_low = static_cast<uint32_t>(ve - kVTop + 1) << 23;
-  uint32_t mc = 0, vc = 0;
+  // m has values below its smallest exponent in most blocks where gradients are heavy-tailed; v hardly any but
+  // zeros, which the warp looks for once
+  const bool v_low = __any_sync(0xffffffffu, min(min(b[0], b[1]), min(b[2], b[3])) < static_cast<uint32_t>(ve - kVTop + 1) << 23);
+  uint32_t r[4], cm[4], cv[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t r = noise_of(static_cast<uint32_t>(place) + i, key, s.key1);
-    const uint32_t rm = r >> 12 & 0xFFFF0u, rv = r << 4 & 0xFFFF0u;
-    // a warp looks for values below the smallest exponent: m has some in every third vote where gradients are
-    // heavy-tailed, v hardly any but zeros
-    uint32_t cm, cv;
-    if (__any_sync(0xffffffffu, a[i] < m_low)) cm = code_of_any<kMTop>(a[i], me, rm);
-    else cm = code_of<kMTop>(a[i], me, rm);
-    if (__any_sync(0xffffffffu, b[i] < v_low)) {
-      cv = code_of_any<kVTop>(b[i], ve, rv);
-      cv = b[i] ? max(cv, 1u) : cv;
-    } else {
-      cv = code_of<kVTop>(b[i], ve, rv);
-    }
-    mc |= (cm | (__float_as_uint(m[i]) >> 24 & 128u)) << (8 * i);
-    vc |= cv << (8 * i);
+    r[i] = noise_of(static_cast<uint32_t>(place) + i, key, s.key1);
+    cm[i] = code_of_any<kMTop>(a[i], me, r[i] >> 12 & 0xFFFF0u);
   }
+  if (v_low) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      cv[i] = code_of_any<kVTop>(b[i], ve, r[i] << 4 & 0xFFFF0u);
+      cv[i] = b[i] ? max(cv[i], 1u) : cv[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cv[i] = code_of<kVTop>(b[i], ve, r[i] << 4 & 0xFFFF0u);
+  }
+  const uint32_t signs = __byte_perm(__byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0073),
+                                     __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0073), 0x5410);
+  const uint32_t mc = __byte_perm(__byte_perm(cm[0], cm[1], 0x0040), __byte_perm(cm[2], cm[3], 0x0040), 0x5410) | (signs & 0x80808080u);
+  const uint32_t vc = __byte_perm(__byte_perm(cv[0], cv[1], 0x0040), __byte_perm(cv[2], cv[3], 0x0040), 0x5410);
   *m_word = me >= kENan ? 0 : mc;
   *v_word = ve >= kENan ? 0 : vc;
   *m_exp = static_cast<uint32_t>(min(me, kENan));
