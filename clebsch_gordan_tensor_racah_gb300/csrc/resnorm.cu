@@ -174,6 +174,10 @@ void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
 
 cgtp_status launch(const cgtp_resnorm_s* p, RnArgs& a, bool backward, cudaStream_t st) {
   deal(p, &a, backward);
+  const int sums_smem = 33 * a.groups * a.warps * es_param(p);   // of the last CTA
+  if (backward && a.kind != kRnDirect && (a.gpost || a.gscale || a.gpre) && int64_t(a.ctas) * 2 * a.chan <= kRnTailSums &&
+      sums_smem <= a.smem)
+    a.ticket = p->ticket;
   const auto run = p->dtype == CGTP_F64                ? (backward ? rn_backward_f64 : rn_forward_f64)
                    : p->dtype == CGTP_F32              ? (backward ? rn_backward_f32 : rn_forward_f32)
                    : (p->flags & CGTP_RESNORM_STORAGE) ? (backward ? rn_backward_bf16s : rn_forward_bf16s)
@@ -205,13 +209,15 @@ cgtp_status create(cgtp_resnorm_s* p, const char* irreps) {
   }
   p->smem_cap -= 512;   // the kernels' static shared memory
   const size_t tab = p->blocks.size() * sizeof(RnBlock);
-  const size_t part = size_t(p->num_sms) * kRnCtasPerSm * 2 * p->chan * es_param(p);
+  const size_t part = size_t(p->num_sms) * kRnCtasPerSm * 2 * p->chan * es_param(p) + sizeof(unsigned);
   if (cudaMalloc(reinterpret_cast<void**>(&p->blocks_dev), tab) != cudaSuccess || cudaMalloc(&p->part, part) != cudaSuccess) {
     cudaGetLastError();
     return fail(CGTP_ENOMEM, "norm table allocation failed");
   }
   p->device_bytes = tab + part;
-  if (cudaMemcpy(p->blocks_dev, p->blocks.data(), tab, cudaMemcpyHostToDevice) != cudaSuccess) {
+  p->ticket = reinterpret_cast<unsigned*>(static_cast<char*>(p->part) + part - sizeof(unsigned));
+  if (cudaMemcpy(p->blocks_dev, p->blocks.data(), tab, cudaMemcpyHostToDevice) != cudaSuccess ||
+      cudaMemset(p->ticket, 0, sizeof(unsigned)) != cudaSuccess) {
     cudaGetLastError();
     return fail(CGTP_ECUDA, "norm table upload failed");
   }

@@ -46,6 +46,7 @@ struct RnArgs {
   const RnBlock* blocks = nullptr;   // device table, or `few` where they fit there
   RnBlock few[kRnInline];
   void* part = nullptr;       // [CTAs][2][C] partial sums: of a(q) P, of gpre
+  unsigned* ticket = nullptr; // CTAs that are done, where the last one adds the partial sums (null: another launch does)
   int n_blocks = 0, dim = 0, chan = 0, act = 0;
   bool post_norm = false, pre_norm = false;
   double alpha = 1.0, eps = 0.0;
@@ -70,6 +71,7 @@ struct cgtp_resnorm_s {
   std::vector<cgtp::RnBlock> blocks;
   cgtp::RnBlock* blocks_dev = nullptr;
   void* part = nullptr;
+  unsigned* ticket = nullptr;
   int num_sms = 0, smem_cap = 0;
   size_t device_bytes = 0;
 };
@@ -98,6 +100,9 @@ constexpr int rn_code(int D, int share) {
   return first[D / 2] + (share >= 8 ? 3 : share >= 4 ? 2 : share - 1);
 }
 
+// Partial sums (CTAs x 2 C) that the last CTA of a backward adds itself: below, its 16 loads a thread are
+// shorter than another launch (64 rows of 8x0e+8x1o: 42 us a call with the launch, 35 us without).
+constexpr int kRnTailSums = 8192;
 constexpr int kRnMaxStages = 2;     // tiles of a group in shared memory
 constexpr int kRnWarps = 16;        // warps of a CTA at most
 constexpr int kRnDirectWarps = 8;   // warps of a row that is too long for shared memory

@@ -545,6 +545,38 @@ __device__ __forceinline__ T* rn_in(const RnArgs& a, int i, char* stage, int j) 
 // Rows staged in shared memory
 // ---------------------------------------------------------------------------
 
+// Column i of the partial sums, added in CTA order within each of `segments` threads and then in their order:
+// gpost = scale A, gscale = post A, gpre.
+template <typename A>
+__device__ __forceinline__ void rn_columns(const A* part, int ctas, int chan, const void* post, const void* scale, void* gpost,
+                                           void* gscale, void* gpre, A (*sums)[33], int i, int seg, int segments) {
+  A v = A(0);
+  if (i < 2 * chan)
+    for (int k = seg; k < ctas; k += segments) v += __ldcg(part + (int64_t)k * 2 * chan + i);
+  const int lane = threadIdx.x & 31;
+  sums[seg][lane] = v;
+  __syncthreads();
+  if (seg == 0 && i < 2 * chan) {
+    for (int k = 1; k < segments; ++k) v += sums[k][lane];
+    const int c = i < chan ? i : i - chan;
+    if (i < chan) {
+      if (gpost) static_cast<A*>(gpost)[c] = scale ? v * static_cast<const A*>(scale)[c] : v;
+      if (gscale) static_cast<A*>(gscale)[c] = post ? v * static_cast<const A*>(post)[c] : v;
+    } else if (gpre) {
+      static_cast<A*>(gpre)[c] = v;
+    }
+  }
+  __syncthreads();
+}
+
+template <typename A>
+__global__ void __launch_bounds__(256) rn_reduce_kernel(const void* part, int ctas, int chan, const void* post, const void* scale,
+                                                        void* gpost, void* gscale, void* gpre) {
+  __shared__ A sums[8][33];
+  rn_columns<A>(static_cast<const A*>(part), ctas, chan, post, scale, gpost, gscale, gpre, sums,
+                blockIdx.x * 32 + (threadIdx.x & 31), threadIdx.x >> 5, 8);
+}
+
 // `bytes` bytes from memory to shared memory in asynchronous copies of V bytes (the rest at once)
 template <int V>
 __device__ __forceinline__ void rn_copy_in(char* dst, const char* src, int bytes, int t, int threads) {
@@ -768,6 +800,21 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
       }
       to[i] = v;
     }
+    if (a.ticket) {
+      __shared__ bool last;
+      __threadfence();
+      __syncthreads();   // the groups' sums have been read, too
+      if (threadIdx.x == 0) last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+      __syncthreads();
+      if (!last) return;
+      __threadfence();
+      A(*sums)[33] = reinterpret_cast<A(*)[33]>(shared);
+      const int segments = blockDim.x >> 5;
+      for (int i = threadIdx.x & 31; i < (2 * a.chan + 31) / 32 * 32; i += 32)
+        rn_columns<A>(static_cast<const A*>(a.part), a.ctas, a.chan, a.post, a.scale, a.gpost, a.gscale, a.gpre, sums, i,
+                      threadIdx.x >> 5, segments);
+      if (threadIdx.x == 0) *a.ticket = 0;
+    }
   }
 }
 
@@ -802,29 +849,6 @@ __global__ void __launch_bounds__(kRnDirectWarps * 32) rn_direct_kernel(const __
   }
 }
 
-// gpost = scale A, gscale = post A, gpre from the CTAs' partial sums: 8 threads a column, then in order.
-template <typename A>
-__global__ void __launch_bounds__(256) rn_reduce_kernel(const void* part_, int ctas, int chan, const void* post, const void* scale,
-                                                        void* gpost, void* gscale, void* gpre) {
-  __shared__ A sums[8][33];
-  const A* part = static_cast<const A*>(part_);
-  const int lane = threadIdx.x & 31, seg = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
-  A v = A(0);
-  if (i < 2 * chan)
-    for (int k = seg; k < ctas; k += 8) v += part[(int64_t)k * 2 * chan + i];
-  sums[seg][lane] = v;
-  __syncthreads();
-  if (seg != 0 || i >= 2 * chan) return;
-  for (int k = 1; k < 8; ++k) v += sums[k][lane];
-  const int c = i < chan ? i : i - chan;
-  if (i < chan) {
-    if (gpost) static_cast<A*>(gpost)[c] = scale ? v * static_cast<const A*>(scale)[c] : v;
-    if (gscale) static_cast<A*>(gscale)[c] = post ? v * static_cast<const A*>(post)[c] : v;
-  } else if (gpre) {
-    static_cast<A*>(gpre)[c] = v;
-  }
-}
-
 template <bool BACKWARD, int KIND, typename S, typename I, typename O, typename A>
 cudaError_t rn_launch_staged(const RnArgs& a, cudaStream_t st) {
   if (smem_cap_cached(reinterpret_cast<const void*>(rn_staged_kernel<BACKWARD, KIND, S, I, O, A>)) < a.smem)
@@ -847,7 +871,7 @@ cudaError_t rn_launch(const RnArgs& a, cudaStream_t st) {
       rn_direct_kernel<BACKWARD, S, I, O, A><<<a.ctas, kRnDirectWarps * 32, 0, st>>>(a);
       e = cudaGetLastError();
   }
-  if (!BACKWARD || e != cudaSuccess || !(a.gpost || a.gscale || a.gpre)) return e;
+  if (!BACKWARD || e != cudaSuccess || a.ticket || !(a.gpost || a.gscale || a.gpre)) return e;
   rn_reduce_kernel<A><<<(2 * a.chan + 31) / 32, 256, 0, st>>>(a.part, a.ctas, a.chan, a.post, a.scale, a.gpost, a.gscale, a.gpre);
   return cudaGetLastError();
 }

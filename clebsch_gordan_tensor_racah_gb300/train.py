@@ -161,10 +161,10 @@ def cgtp_resnorm_backward(plan, gout, gy, x, z=None, q=None, post=None, scale=No
         gh = empty((n, dim), dtype=st, device=device) if need_gh else None
         gz = empty((n, dim), dtype=ot, device=device) if z is not None else None
         gq = empty((n, chan), dtype=ot, device=device) if z is not None and plan.act != "none" else None
-        three = empty((3, chan), dtype=pt, device=device)      # one allocation for the sums
-        at, step = three.data_ptr(), chan * three.element_size()
-        gpost, gscale, gpre = (None if p is None else g for p, g in zip((post, scale, pre), three))
-        sums = [None if p is None else at + i * step for i, p in enumerate((post, scale, pre))]
+        gpost = None if post is None else empty(chan, dtype=pt, device=device)
+        gscale = None if scale is None else empty(chan, dtype=pt, device=device)
+        gpre = None if pre is None else empty(chan, dtype=pt, device=device)
+        sums = [None if g is None else g.data_ptr() for g in (gpost, gscale, gpre)]
     status = lib().cgtp_resnorm_backward(
         plan.handle, n, *gp, *yp, *xp, *zp, *qp, _vector(post, "post", pt, chan), _vector(scale, "scale", pt, chan),
         _vector(pre, "pre", pt, chan), *_rows(gh, "gh", st, n, dim), *_rows(gz, "gz", ot, n, dim),
@@ -233,7 +233,7 @@ class AdamW:
             # whole lists at C speed: a step has hundreds of small tensors
             fits = (len(tensors) == len(self.numel) and list(map(_numel, given)) == sizes
                     and all(map(_is_contiguous, given)) and all(map(_is_cuda, given))
-                    and all(d is dtype for d in map(_dtype_of, given)))
+                    and (not given or set(map(_dtype_of, given)) == {dtype}))
             if fits:
                 if len(given) == len(tensors):
                     return self._list(*map(_data_ptr, given))
