@@ -116,14 +116,24 @@ int lay_out(RnArgs* a, bool backward, int rows) {
 // instructions that a row costs and the warps that hide their latency.
 //   instructions: an element of a thread's share, a channel, a step of the block sums and the fixed part of a
 //     block, fitted to counters of the kernels (a row of 64x0e+64x1o+64x2e: 1,330 backward, 875 forward);
+//     half as many again where operands are missing, blocks do not fill the lanes or copies are ragged.
 //   rate: grows with the warps of an SM as w / (w + 8).
+// Measured on both sides (GB300, share of the copy bandwidth):
+//   threads a row: 32x0e+32x1o+32x2e+32x3o, 200,000 rows: 32 threads 96% / 90% (forward / backward), 16 threads
+//     90% / 81%; 8x0e+8x1o, 2,000,000 rows: 8 threads 44% / 46%, 4 threads 57% / 49%, 2 threads 35% / 28% (16
+//     rows a warp start in the same bank: 4 threads are the fewest); 33x0e+17x1o+5x2e forward: 32 threads 21%, 16
+//     threads 28%, 8 threads 46%; 128x0e+128x1o+128x2e backward, 60,000 rows: 32 threads 90%, 64 threads 74%.
+//   stages: two where that leaves as many warps, else one: 64x0e+64x1o+64x2e forward, 200,000 rows: two 100%, one 83%;
+//     128x0e+128x1o+128x2e backward: two (4 warps) 62%, one (9 warps) 90%.
 void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
   const int n_rows = backward ? kRnBackward : kRnForward, ep = es_param(p);
   const int factors = round16(2 * p->chan * ep);
   double best = 0.0;
-  for (int team = 1; team <= 32 * kRnWarps; team *= 2) {   // threads of a row
+  int fewest = 1;
+  while (fewest < 4 && fewest < p->widest) fewest *= 2;
+  for (int team = fewest; team <= 32 * kRnWarps; team *= 2) {   // threads of a row
     const int warps = std::max(1, team / 32), abreast = std::max(1, 32 / team);
-    if (team > 1 && team >= 2 * p->widest) break;
+    if (team > fewest && team >= 2 * p->widest) break;
     // Rows of a tile: as many as run side by side, and enough that a tile of every contiguous tensor
     // starts at a multiple of 16 bytes.
     int rows = abreast;
@@ -140,7 +150,7 @@ void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
     }
     if (!held) continue;
     const int stage = lay_out(a, backward, rows);
-    bool full = fills && a->pre_norm && a->post_norm && team >= 32;
+    bool full = fills && a->pre_norm && a->post_norm;
     for (int i = 0; i < n_rows; ++i) full &= a->t[i].ptr && a->t[i].vec == 16 && (a->t[i].linear || rows == 1);
     const int64_t kept = (warps > 1 ? 8 * kRnWarps : 0) + (backward ? int64_t(abreast) * 2 * p->chan : 0);
     for (int stages = kRnMaxStages; stages >= 1; --stages) {
@@ -148,10 +158,10 @@ void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
       const int groups = static_cast<int>(std::min<int64_t>((p->smem_cap - factors) / group, kRnWarps / warps));
       if (groups <= 0) continue;
       const int busy = groups * warps;
-      const double rate = double(busy) / (busy + 8) / (work * warps / abreast * (full ? 1.0 : 1.5));
+      const double rate = double(busy) / (busy + 8) / (work * warps / abreast * (!full ? 1.5 : team < 32 ? 1.35 : 1.0));
       if (rate <= best) continue;
       best = rate;
-      a->kind = warps == 1 ? (full ? kRnOneFull : kRnOne) : (full ? kRnManyFull : kRnMany);
+      a->kind = warps > 1 ? (full ? kRnManyFull : kRnMany) : !full ? kRnOne : team == 32 ? kRnOneFull : kRnFewFull;
       a->stages = stages;
       a->warps = warps;
       a->lanes = team;

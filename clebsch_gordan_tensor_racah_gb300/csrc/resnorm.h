@@ -33,9 +33,9 @@ constexpr int kRnMaxRows = kRnBackward;
 
 constexpr int kRnInline = 64;
 // kRnOne: a warp a row, or several rows a warp.  kRnMany: several warps a row.  ..Full: every operand there, tiles that are runs of 16-byte pieces, blocks that fill the lanes (and a
-// warp a row).  kRnDirect: rows in place, a CTA a row,
+// warp a row; kRnFewFull: several rows a warp).  kRnDirect: rows in place, a CTA a row,
 // any number and size of blocks.
-enum RnKind { kRnDirect, kRnMany, kRnManyFull, kRnOne, kRnOneFull };
+enum RnKind { kRnDirect, kRnMany, kRnManyFull, kRnOne, kRnFewFull, kRnOneFull };
 
 // Arguments of one launch.
 struct RnArgs {

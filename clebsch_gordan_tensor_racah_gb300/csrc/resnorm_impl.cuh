@@ -518,7 +518,7 @@ __device__ __forceinline__ void rn_row(const RnArgs& a, const Row& row, const Rn
   for (int i = 0; i < a.n_blocks; ++i) {
     if constexpr (STAGED) {
       const RnBlock& b = a.few[i];
-#define HELD(D, K) rn_block_held<D, K, KIND == kRnOneFull || KIND == kRnManyFull>(a, b, row, f, team)
+#define HELD(D, K) rn_block_held<D, K, KIND != kRnOne && KIND != kRnMany>(a, b, row, f, team)
       switch (b.code) { CGTP_RN_HELD }
 #undef HELD
     } else {
@@ -698,7 +698,7 @@ __device__ __forceinline__ void rn_runs_out(const RnRows* const (&r)[NT], const 
 template <bool BACKWARD, int KIND, typename S, typename I, typename O, typename A>
 __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __grid_constant__ RnArgs a) {
   extern __shared__ __align__(16) char shared[];
-  constexpr bool ONE = KIND == kRnOne || KIND == kRnOneFull, FULL = KIND == kRnOneFull || KIND == kRnManyFull;
+  constexpr bool ONE = KIND >= kRnOne, FULL = KIND != kRnOne && KIND != kRnMany;
   constexpr bool WHOLE = KIND == kRnOneFull;
   const int warps = ONE ? 1 : a.warps, threads = warps * 32;
   const int g = threadIdx.x / threads, tg = threadIdx.x - g * threads;
@@ -864,6 +864,7 @@ cudaError_t rn_launch(const RnArgs& a, cudaStream_t st) {
   cudaError_t e;
   switch (a.kind) {
     case kRnOneFull: e = rn_launch_staged<BACKWARD, wide ? kRnOne : kRnOneFull, S, I, O, A>(a, st); break;
+    case kRnFewFull: e = rn_launch_staged<BACKWARD, wide ? kRnOne : kRnFewFull, S, I, O, A>(a, st); break;
     case kRnOne: e = rn_launch_staged<BACKWARD, kRnOne, S, I, O, A>(a, st); break;
     case kRnManyFull: e = rn_launch_staged<BACKWARD, wide ? kRnMany : kRnManyFull, S, I, O, A>(a, st); break;
     case kRnMany: e = rn_launch_staged<BACKWARD, kRnMany, S, I, O, A>(a, st); break;

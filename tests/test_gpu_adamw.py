@@ -151,6 +151,57 @@ def test_eight_bit_states(offset, grad):
         assert np.all(m1[sure] * m[sure] > 0)
 
 
+def _encode(x, top, noise, sign):
+    """Codes and block exponents of FP32 values x >= 0, rounded up where 20 random bits reach the next code."""
+    bits = x.view(np.uint32).astype(np.int64).reshape(-1, 128)
+    exp = np.maximum((bits.max(axis=1, keepdims=True) + 0xFFFFF) >> 23, otr.E_MIN)
+    base, noise = exp - top, noise.reshape(-1, 128)
+    normal = ((bits + noise) >> 20) - (base << 3)
+    fine = x.reshape(-1, 128) * ((256 - base) << 23).astype(np.uint32).view(np.float32)
+    low = np.floor(fine + noise.astype(np.float32) * np.float32(2.0 ** -20)).astype(np.int64)
+    code = np.where(bits >= (base + 1) << 23, normal, low)
+    if top == 31:
+        code = np.where(bits > 0, np.maximum(code, 1), code)
+    return (code.reshape(-1) | sign.astype(np.int64) << 7).astype(np.uint8), exp.reshape(-1).astype(np.uint8)
+
+
+def _noise(total, seed, step):
+    mask, low = (1 << 64) - 1, 0xFFFFFFFF
+    z = (seed + step * 0x9E3779B97F4A7C15) & mask
+    z = ((z ^ (z >> 29)) * 0xBB67AE8584CAA73B) & mask
+    z = ((z ^ (z >> 32)) * 0x9E3779B97F4A7C15) & mask
+    z ^= z >> 29
+    x = (np.arange(total, dtype=np.uint64) * np.uint64(0x9E3779B1) + np.uint64(z & low)) & np.uint64(low)
+    x = ((x ^ (x >> np.uint64(15))) * np.uint64(0xBB67AE85)) & np.uint64(low)
+    x = ((x ^ (x >> np.uint64(13))) * np.uint64(0x3C6EF373) + np.uint64(z >> 32)) & np.uint64(low)
+    return (x ^ (x >> np.uint64(16))).astype(np.int64)
+
+
+@pytest.mark.parametrize("offset,grad", [(0, "float32"), (1, "float32"), (0, "bfloat16")])
+def test_eight_bit_codes_are_a_function_of_the_fp32_arithmetic(offset, grad):
+    # every product and sum of m and v is rounded once, so the codes can be had from FP32 arithmetic on the CPU, bit for bit
+    rng = np.random.default_rng(20)
+    shapes = SHAPES + [(300, 1024)]
+    numel = [int(np.prod(s)) for s in shapes]
+    p, g = _sets(rng, torch.float32, getattr(torch, grad), offset, shapes)
+    starts, f = _starts(numel), np.float32
+    flat = np.zeros(starts[-1], dtype=f)
+    for i, k in enumerate(numel):
+        flat[starts[i]:starts[i] + k] = g[i].float().cpu().numpy().reshape(-1)
+    opt = cg().AdamW(numel, grad_dtype=getattr(torch, grad), state="8bit")
+    state = opt.new_state()
+    for step in (1, 2, 3):
+        m, v = (t.cpu().numpy() for t in cg().cgtp_adamw_state_values(opt, state))
+        cg().cgtp_adamw_step(opt, p, g, state, lr=1e-2, step=step, seed=77)
+        m = m * f(0.9) + flat * f(1 - 0.9)
+        v = v * f(0.999) + (flat * flat) * f(1 - 0.999)
+        r = _noise(starts[-1], 77, step)
+        got = {k: t.cpu().numpy() for k, t in state.items()}
+        for name, x, top, noise, sign in (("m", np.abs(m), 15, (r >> 16) << 4, np.signbit(m)), ("v", v, 31, (r & 0xFFFF) << 4, np.zeros(m.shape, bool))):
+            code, exp = _encode(x, top, noise, sign)
+            assert np.array_equal(got[name], code) and np.array_equal(got[name + "_exp"], exp), (name, step)
+
+
 def test_eight_bit_rounding_is_unbiased_and_a_function_of_seed_and_step():
     # v = 1 with beta2 = 0.999 and a zero gradient: 0.1% a step, far below the grid's 12.5%
     k = 1 << 16

@@ -18,7 +18,7 @@ pytestmark = pytest.mark.gpu
 
 K = 64
 MANY = "+".join(["4x0e", "3x1o", "2x2e"] * 14)
-IRREPS = ["8x0e+8x1o", "1x0e", "1x3o", "33x0e+17x1o+5x2e", "32x0e+32x1o+32x2e+32x3o", "3x7o+2x4e+1x0e+5x6e+2x5o",
+IRREPS = ["128x0e+128x1o+128x2e", "64x0e+64x1o+64x2e", "128x0e+128x3o", "8x0e+8x1o", "1x0e", "1x3o", "33x0e+17x1o+5x2e", "32x0e+32x1o+32x2e+32x3o", "3x7o+2x4e+1x0e+5x6e+2x5o",
           "300x0e", "16x0e+16x1o+16x2e+16x3o+16x4e+16x5o+16x6e+16x7o"]
 KINDS = ["f32", "f64", "bf16", "bf16s"]
 
@@ -88,7 +88,7 @@ def _rowmax(a):
 
 
 def check(irreps, kind, n, layout="plain", act="sigmoid", pre_norm=True, post_norm=True, has_h=True, has_z=True,
-          factors=True, alpha=1.0, eps=1e-5, seed=0, stream=None):
+          factors=True, alpha=1.0, eps=1e-5, seed=0, row_units=K):
     rng = np.random.default_rng(seed + n)
     opt = dict(act=act, pre_norm=pre_norm, post_norm=post_norm, alpha=alpha, eps=eps)
     plan = _plan(irreps, kind, **opt)
@@ -137,6 +137,7 @@ def check(irreps, kind, n, layout="plain", act="sigmoid", pre_norm=True, post_no
         return
     amax = d * (zr * _rowmax(a) if has_z else 0)
     terms = 15 * amax.sum()            # at most 15 components a channel
+    u = row_units * _unit(kind)
     for i, (name, other) in enumerate((("gpost", o["scale"]), ("gscale", o["post"]))):
         if has_z:
             _close(grads[3 + i], want[3 + i], u * terms * np.abs(other).max(), None, name)
@@ -181,6 +182,16 @@ def test_parts(act, has_h, has_z, pre_norm, post_norm):
               alpha=0.6, eps=1e-3)
         check("12x0e+7x1o+9x2e", kind, 21, act=act, has_h=has_h, has_z=has_z, pre_norm=pre_norm, post_norm=post_norm,
               factors=False)
+
+
+@pytest.mark.parametrize("irreps,n", [
+    ("64x0e+64x1o+64x2e", 5001), ("128x0e+128x1o+128x2e", 3001), ("128x0e+128x3o", 3003), ("16x0e+16x1o+16x7o", 5003),
+    ("8x0e+8x1o", 40001), ("33x0e+17x1o+5x2e", 20001), ("1024x0e", 1001), ("3x1o", 30001)])
+@pytest.mark.parametrize("kind,layout", [("f32", "plain"), ("bf16", "range"), ("bf16s", "plain"), ("f32", "odd")])
+def test_more_rows_than_one_turn_of_the_grid(irreps, n, kind, layout):
+    # every group takes several tiles, with a last one that is not full.  Sums over rows have up to 250
+    # additions in a row (a group's rows, 128 rows side by side or groups of a CTA, CTAs): 256 u of the terms.
+    check(irreps, kind, n, layout=layout, act="silu", seed=11, row_units=256)
 
 
 def test_many_rows_sum_in_a_fixed_order():
