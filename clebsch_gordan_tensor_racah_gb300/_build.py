@@ -16,6 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INC = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libcgtp.so")
+BINDING = os.path.join(PKG, "_binding.so")      # native part of train.py's binding
+BINDING_STAMP = os.path.join(BUILD, "binding.torch")   # version of torch that it was built for
 
 CU_SOURCES = ["api.cu", "graph.cu", "uvu.cu", "uvu_f32.cu", "uvu_f32_l7.cu", "uvu_f64.cu",
               "uvu_f64_l7.cu", "uvu2.cu", "uvu3.cu", "uvu3_f32_2.cu", "uvu3_f32_8.cu", "uvu3_f32_32.cu",
@@ -88,8 +90,23 @@ def _bake():
     return os.path.getmtime(out)
 
 
+def _binding_command():
+    """g++ command that builds _binding.so against this machine's torch, or None where it is up to date."""
+    import sysconfig
+    import torch
+    src = os.path.join(CSRC, "binding.cpp")
+    if not _stale(src, BINDING) and os.path.exists(BINDING_STAMP) and open(BINDING_STAMP).read() == torch.__version__:
+        return None
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], INC]
+    lib = os.path.join(root, "lib")
+    return ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f"-I{p}" for p in inc], src, "-o", BINDING, f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def build(verbose=False, jobs=None):
-    """Compile (incrementally) and link libcgtp.so; returns its path."""
+    """Compile (incrementally) and link libcgtp.so and _binding.so; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     _bake()
@@ -107,15 +124,23 @@ def build(verbose=False, jobs=None):
         if _stale(src, obj):
             cmds.append(["g++", "-std=c++17", "-O2", "-fPIC", "-ffp-contract=off", "-I", INC,
                          "-c", src, "-o", obj])
+    binding = _binding_command()
+    native = bool(cmds)
+    if binding:
+        cmds.append(binding)
     jobs = jobs or max(1, min(len(cmds), os.cpu_count() or 4))
     if cmds:
         # longest translation units first
-        cmds.sort(key=lambda c: (not any(k in c[-3] for k in ("_l7", "uvu3_", "_bwd", "_fwd")), c[-3]))
+        cmds.sort(key=lambda c: (not any(k in c[-3] for k in ("_l7", "uvu3_", "_bwd", "_fwd", "torch")), c[-3]))
         with cf.ThreadPoolExecutor(jobs) as ex:
             for out in ex.map(_run, cmds):
                 if verbose and out.strip():
                     print(out)
-    if cmds or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
+    if binding:
+        import torch
+        with open(BINDING_STAMP, "w") as f:
+            f.write(torch.__version__)
+    if native or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         tmp = LIB + ".tmp"
         _run([nvcc, "-shared", *ARCH, "-o", tmp, *objs, "-cudart=static"])
         os.replace(tmp, LIB)

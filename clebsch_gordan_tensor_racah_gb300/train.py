@@ -1,19 +1,20 @@
 """Binding of include/cgtp_train.h: the gated residual norm of a block and the AdamW step.
 
 Argument marshalling only, like the rest of the package: the computation runs in the CUDA
-kernels of ``libcgtp.so``.
+kernels of ``libcgtp.so``.  The calls of a training step go through ``_binding`` (csrc/binding.cpp),
+which checks its arguments in native code; an argument that does not fit comes back to the
+checks here, which say what is wrong.
 """
 
 import ctypes
-import operator
 
 import torch
 
+from . import _binding
 from . import CGTP_BF16, CGTP_F32, CGTP_F64, _check, _ptr, lib
 
-_Tensor = torch.Tensor
-_numel, _data_ptr, _is_contiguous = _Tensor.numel, _Tensor.data_ptr, _Tensor.is_contiguous
-_dtype_of, _is_cuda = operator.attrgetter("dtype"), operator.attrgetter("is_cuda")
+_binding.connect(*(ctypes.cast(getattr(lib(), f), ctypes.c_void_p).value for f in (
+    "cgtp_resnorm_forward", "cgtp_resnorm_backward", "cgtp_adamw_step", "cgtp_grad_norm", "cgtp_adamw_state_values")))
 
 ACTS = {"none": 0, "identity": 1, "sigmoid": 2, "silu": 3}
 RESNORM_POST, RESNORM_PRE, RESNORM_STORAGE = 1, 2, 4
@@ -28,47 +29,57 @@ def _dtype(dtype, name, allowed):
     return code
 
 
-def _rows(t, name, dtype, n, width):
-    """Device pointer and row distance of a row tensor [n, width] (a column range of wider rows is fine)."""
+def _explain_rows(name, t, dtype, n, width):
+    """Raises where a row tensor (or None) does not fit."""
     if t is None:
-        return None, 0
-    try:
-        (rows, cols), (ld, inner) = t.shape, t.stride()
-    except (AttributeError, TypeError, ValueError):
-        raise _misfit(t, name, dtype, n, width) from None
-    if t.dtype is dtype and t.is_cuda and rows == n and cols == width and (inner == 1 or width == 1 or n == 0):
-        if n <= 1:
-            return t.data_ptr(), 0
-        if ld >= width:
-            return t.data_ptr(), ld
-    raise _misfit(t, name, dtype, n, width)
-
-
-def _misfit(t, name, dtype, n, width):
-    """What is wrong with a row tensor that _rows refused."""
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        return TypeError(f"{name} must be a CUDA tensor")
+        raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
-        return TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != (n, width):
-        return ValueError(f"{name} must have shape ({n}, {width}), got {tuple(t.shape)}")
-    return ValueError(f"{name}: elements of a row must be contiguous and rows must not overlap")
+        raise ValueError(f"{name} must have shape ({n}, {width}), got {tuple(t.shape)}")
+    if (t.stride(1) != 1 and width > 1 and n > 0) or (n > 1 and t.stride(0) < width):
+        raise ValueError(f"{name}: elements of a row must be contiguous and rows must not overlap")
 
 
-def _vector(t, name, dtype, width):
-    """Device pointer of a contiguous tensor [width] or None."""
+def _explain_vector(name, t, dtype, width):
+    """Raises where a contiguous tensor [width] (or None) does not fit."""
     if t is None:
-        return None
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == (width,) and t.is_contiguous():
-        return t.data_ptr()
-    if isinstance(t, torch.Tensor) and t.shape != (width,):
+        return
+    _ptr(t, name, dtype)
+    if t.shape != (width,):
         raise ValueError(f"{name} must have shape ({width},), got {tuple(t.shape)}")
-    return _ptr(t, name, dtype)
 
 
-def _current(stream, device):
-    """cudaStream_t of `stream`, or of the device's current stream."""
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+def _explain_list(name, tensors, numel, dtype):
+    """Raises where a list of tensors (or None) does not fit the optimizer's."""
+    if len(tensors) != len(numel):
+        raise ValueError(f"{name}: {len(numel)} tensors expected, got {len(tensors)}")
+    for t, k in zip(tensors, numel):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
+            raise TypeError(f"{name} must be {dtype} CUDA tensors")
+        if t.numel() != k or not t.is_contiguous():
+            raise ValueError(f"{name}: a contiguous tensor of {k} elements expected, got {tuple(t.shape)}")
+
+
+def _result(r, explain):
+    """A native call's results, or its refusal as an exception."""
+    if r is NotImplemented:
+        explain()
+        raise TypeError("arguments of unexpected types")
+    if type(r) is int:
+        _check(r)
+    return r
+
+
+def _current(stream, t):
+    """cudaStream_t of `stream`, or of the current stream of a tensor's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.device.index) if getattr(t, "is_cuda", False) else 0
 
 
 class ResNormPlan:
@@ -97,6 +108,9 @@ class ResNormPlan:
         self.out_dtype = dtype
         self.stream_dtype = self.in_dtype = torch.float32 if half and not storage else dtype
         self.param_dtype = torch.float32 if half else dtype
+        types = [_dtype(t, "dtype", (CGTP_F32, CGTP_F64, CGTP_BF16))
+                 for t in (self.stream_dtype, self.in_dtype, self.out_dtype, self.param_dtype)]
+        self._native = (h.value, *types, self.dim, self.channels, int(self.pre_norm), int(act != "none"))
 
     @property
     def handle(self):
@@ -124,20 +138,17 @@ def cgtp_resnorm_forward(plan, h, z=None, q=None, post=None, scale=None, pre=Non
     ref = h if h is not None else z
     if ref is None:
         raise ValueError("h or z must be given")
-    n, dim, chan, device = ref.shape[0], plan.dim, plan.channels, ref.device
-    st, it, ot, pt, empty = plan.stream_dtype, plan.in_dtype, plan.out_dtype, plan.param_dtype, torch.empty
-    # operands are checked before results are allocated
-    hp, zp, qp = _rows(h, "h", st, n, dim), _rows(z, "z", it, n, dim), _rows(q, "q", it, n, chan)
-    if z is not None and out is None:
-        out = empty((n, dim), dtype=st, device=device)
-    if plan.pre_norm and y is None:
-        y = empty((n, dim), dtype=ot, device=device)
-    status = lib().cgtp_resnorm_forward(
-        plan.handle, n, *hp, *zp, *qp, _vector(post, "post", pt, chan), _vector(scale, "scale", pt, chan),
-        _vector(pre, "pre", pt, chan), *_rows(out, "out", st, n, dim), *_rows(y, "y", ot, n, dim), _current(stream, device))
-    if status:
-        _check(status)
-    return (out if z is not None else h), y
+
+    def explain():
+        n, dim, chan = ref.shape[0], plan.dim, plan.channels
+        for name, t, dtype, width in (("h", h, plan.stream_dtype, dim), ("z", z, plan.in_dtype, dim), ("q", q, plan.in_dtype, chan),
+                                      ("out", out, plan.stream_dtype, dim), ("y", y, plan.out_dtype, dim)):
+            _explain_rows(name, t, dtype, n, width)
+        for name, t in (("post", post), ("scale", scale), ("pre", pre)):
+            _explain_vector(name, t, plan.param_dtype, chan)
+
+    r = _binding.resnorm_forward(plan._native, h, z, q, post, scale, pre, out, y, _current(stream, ref))
+    return r if type(r) is tuple else _result(r, explain)
 
 
 def cgtp_resnorm_backward(plan, gout, gy, x, z=None, q=None, post=None, scale=None, pre=None, need_gh=True,
@@ -150,28 +161,20 @@ def cgtp_resnorm_backward(plan, gout, gy, x, z=None, q=None, post=None, scale=No
     ref = gout if gout is not None else gy
     if ref is None:
         raise ValueError("gout or gy must be given")
-    n, dim, chan, device = ref.shape[0], plan.dim, plan.channels, ref.device
-    st, it, ot, pt, empty = plan.stream_dtype, plan.in_dtype, plan.out_dtype, plan.param_dtype, torch.empty
-    gp, yp, xp = _rows(gout, "gout", st, n, dim), _rows(gy, "gy", it, n, dim), _rows(x, "x", st, n, dim)
-    zp, qp = _rows(z, "z", it, n, dim), _rows(q, "q", it, n, chan)
-    if outs is not None:
-        gh, gz, gq, gpost, gscale, gpre = outs
-        sums = _vector(gpost, "gpost", pt, chan), _vector(gscale, "gscale", pt, chan), _vector(gpre, "gpre", pt, chan)
-    else:
-        gh = empty((n, dim), dtype=st, device=device) if need_gh else None
-        gz = empty((n, dim), dtype=ot, device=device) if z is not None else None
-        gq = empty((n, chan), dtype=ot, device=device) if z is not None and plan.act != "none" else None
-        gpost = None if post is None else empty(chan, dtype=pt, device=device)
-        gscale = None if scale is None else empty(chan, dtype=pt, device=device)
-        gpre = None if pre is None else empty(chan, dtype=pt, device=device)
-        sums = [None if g is None else g.data_ptr() for g in (gpost, gscale, gpre)]
-    status = lib().cgtp_resnorm_backward(
-        plan.handle, n, *gp, *yp, *xp, *zp, *qp, _vector(post, "post", pt, chan), _vector(scale, "scale", pt, chan),
-        _vector(pre, "pre", pt, chan), *_rows(gh, "gh", st, n, dim), *_rows(gz, "gz", ot, n, dim),
-        *_rows(gq, "gq", ot, n, chan), *sums, _current(stream, device))
-    if status:
-        _check(status)
-    return gh, gz, gq, gpost, gscale, gpre
+    outs = None if outs is None else tuple(outs)
+
+    def explain():
+        n, dim, chan = ref.shape[0], plan.dim, plan.channels
+        gh, gz, gq, *sums = outs or (None,) * 6
+        for name, t, dtype, width in (("gout", gout, plan.stream_dtype, dim), ("gy", gy, plan.in_dtype, dim),
+                                      ("x", x, plan.stream_dtype, dim), ("z", z, plan.in_dtype, dim), ("q", q, plan.in_dtype, chan),
+                                      ("gh", gh, plan.stream_dtype, dim), ("gz", gz, plan.out_dtype, dim), ("gq", gq, plan.out_dtype, chan)):
+            _explain_rows(name, t, dtype, n, width)
+        for name, t in zip(("post", "scale", "pre", "gpost", "gscale", "gpre"), (post, scale, pre, *sums)):
+            _explain_vector(name, t, plan.param_dtype, chan)
+
+    r = _binding.resnorm_backward(plan._native, gout, gy, x, z, q, post, scale, pre, need_gh, outs, _current(stream, ref))
+    return r if type(r) is tuple else _result(r, explain)
 
 
 class AdamW:
@@ -202,7 +205,10 @@ class AdamW:
         total = ctypes.c_int64()
         _check(lib().cgtp_adamw_info(h, ctypes.byref(total)))
         self.state_numel = total.value
-        self._list = ctypes.c_void_p * max(n, 1)
+        self._sizes = sizes                     # read by the native calls
+        self._native = (h.value, _dtype(self.param_dtype, "param_dtype", (CGTP_F32, CGTP_F64)),
+                        _dtype(self.grad_dtype, "grad_dtype", (CGTP_F32, CGTP_F64, CGTP_BF16)), STATES[state],
+                        self.state_numel, n, ctypes.addressof(sizes))
 
     @property
     def handle(self):
@@ -223,48 +229,19 @@ class AdamW:
         _check(lib().cgtp_adamw_device_bytes(self._h, ctypes.byref(nb)))
         return nb.value
 
-    def pointers(self, tensors, name, dtype):
-        """HOST array of the tensors' device pointers; their number and sizes are the optimizer's."""
-        given = [t for t in tensors if t is not None]
-        sizes = self.numel
-        if len(given) != len(tensors):
-            sizes = [k for k, t in zip(sizes, tensors) if t is not None]
-        try:
-            # whole lists at C speed: a step has hundreds of small tensors
-            fits = (len(tensors) == len(self.numel) and list(map(_numel, given)) == sizes
-                    and all(map(_is_contiguous, given)) and all(map(_is_cuda, given))
-                    and (not given or set(map(_dtype_of, given)) == {dtype}))
-            if fits:
-                if len(given) == len(tensors):
-                    return self._list(*map(_data_ptr, given))
-                return self._list(*[None if t is None else t.data_ptr() for t in tensors])
-        except TypeError:
-            pass
-        raise self._misfit(tensors, name, dtype)
-
-    def _misfit(self, tensors, name, dtype):
-        """What is wrong with a list of tensors that `pointers` refused."""
-        if len(tensors) != len(self.numel):
-            return ValueError(f"{name}: {len(self.numel)} tensors expected, got {len(tensors)}")
-        for t, k in zip(tensors, self.numel):
-            if t is None:
-                continue
-            if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
-                return TypeError(f"{name} must be {dtype} CUDA tensors")
-            if t.numel() != k or not t.is_contiguous():
-                return ValueError(f"{name}: a contiguous tensor of {k} elements expected, got {tuple(t.shape)}")
-        return TypeError(f"{name} must be {dtype} CUDA tensors")
-
-    def states(self, state):
-        """Device pointers of m, v, m_exp, v_exp after checks of type and size."""
-        n, eight = self.state_numel, self.state == "8bit"
-        dt = torch.uint8 if eight else self.param_dtype
-        if eight and (state["m_exp"] is None or state["v_exp"] is None):
-            raise ValueError("8-bit states need m_exp and v_exp")
-        blocks = n // STATE_BLOCK
-        return (_vector(state["m"], "state m", dt, n), _vector(state["v"], "state v", dt, n),
-                _vector(state["m_exp"], "state m_exp", dt, blocks) if eight else None,
-                _vector(state["v_exp"], "state v_exp", dt, blocks) if eight else None)
+    def explain(self, lists, state=None, clip=None):
+        """Raises what is wrong with the arguments of a step."""
+        for name, tensors, dtype in lists:
+            if tensors is not None:
+                _explain_list(name, tensors, self.numel, dtype)
+        if state is not None:
+            n, eight = self.state_numel, self.state == "8bit"
+            for name in ("m", "v") + (("m_exp", "v_exp") if eight else ()):
+                if state[name] is None:
+                    raise ValueError(f"state {name} is missing")
+                _explain_vector("state " + name, state[name], torch.uint8 if eight else self.param_dtype,
+                                n // STATE_BLOCK if name.endswith("exp") else n)
+        _explain_vector("norm and coefficient", clip, self.param_dtype, 2)
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -275,32 +252,27 @@ class AdamW:
 
 def cgtp_grad_norm(opt, grads, max_norm=float("inf"), out=None, stream=None):
     """Tensor [norm of all gradients, min(1, max_norm / norm)]; None gradients count as zero."""
-    found = opt.pointers(grads, "grads", opt.grad_dtype)
-    if out is None:
-        given = next((t for t in grads if t is not None), None)
-        out = torch.empty(2, dtype=opt.param_dtype, device="cuda" if given is None else given.device)
-    _check(lib().cgtp_grad_norm(opt.handle, found, float(max_norm), _vector(out, "out", opt.param_dtype, 2),
-                                _current(stream, out.device)))
-    return out
+    ref = out if out is not None else next((g for g in grads if g is not None), None)
+    if ref is None:
+        out = ref = torch.empty(2, dtype=opt.param_dtype, device="cuda")
+    r = _binding.grad_norm(opt._native, grads, max_norm, out, _current(stream, ref))
+    return r if type(r) is torch.Tensor else _result(r, lambda: opt.explain([("grads", grads, opt.grad_dtype)], clip=out))
 
 
 def cgtp_adamw_step(opt, params, grads, state, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, step=1,
                     copies=None, clip=None, seed=0, stream=None):
     """One AdamW step in place.  A None gradient skips its tensor.  copies: bfloat16 tensors (or None)
     that receive the new parameters.  clip: result of cgtp_grad_norm.  seed: rounding of 8-bit states."""
-    _check(lib().cgtp_adamw_step(
-        opt.handle, opt.pointers(params, "params", opt.param_dtype), opt.pointers(grads, "grads", opt.grad_dtype),
-        None if copies is None else opt.pointers(copies, "copies", torch.bfloat16), *opt.states(state), float(lr),
-        float(betas[0]), float(betas[1]), float(eps), float(weight_decay), int(step), int(seed) & 0xFFFFFFFFFFFFFFFF,
-        _vector(clip, "clip", opt.param_dtype, 2), _current(stream, state["m"].device)))
+    r = _binding.adamw_step(opt._native, params, grads, copies, state["m"], state["v"], state["m_exp"], state["v_exp"], lr, betas[0],
+                            betas[1], eps, weight_decay, step, seed, clip, _current(stream, state["m"]))
+    if r is not None:
+        _result(r, lambda: opt.explain([("params", params, opt.param_dtype), ("grads", grads, opt.grad_dtype),
+                                        ("copies", copies, torch.bfloat16)], state, clip))
 
 
 def cgtp_adamw_state_values(opt, state, stream=None):
     """(m, v) as the FP32 values the 8-bit states stand for (the states themselves otherwise)."""
     if opt.state != "8bit":
         return state["m"], state["v"]
-    m, v = (torch.empty(opt.state_numel, dtype=torch.float32, device=state[k].device) for k in ("m", "v"))
-    p = opt.states(state)
-    _check(lib().cgtp_adamw_state_values(opt.handle, p[0], p[1], p[2], p[3], m.data_ptr(), v.data_ptr(),
-                                         _current(stream, m.device)))
-    return m, v
+    r = _binding.state_values(opt._native, state["m"], state["v"], state["m_exp"], state["v_exp"], _current(stream, state["m"]))
+    return r if type(r) is tuple else _result(r, lambda: opt.explain([], state))
