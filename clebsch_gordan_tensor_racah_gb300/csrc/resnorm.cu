@@ -100,7 +100,10 @@ int lay_out(RnArgs* a, bool backward, int rows) {
       if (t[kRnGy].ptr && t[kRnGz].es == t[kRnGy].es) over(&t[kRnGz], t[kRnGy]);
       else own(&t[kRnGz]);
     }
-    if (t[kRnGq].ptr) own(&t[kRnGq]);
+    if (t[kRnGq].ptr) {
+      if (t[kRnGq].es == t[kRnBq].es) over(&t[kRnGq], t[kRnBq]);
+      else own(&t[kRnGq]);
+    }
   }
   for (int i = 0; i < (backward ? kRnBackward : kRnForward); ++i) {
     RnRows& r = t[i];
@@ -175,9 +178,15 @@ void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
     return;
   }
   a->stage_bytes = lay_out(a, backward, a->rows);
+  // as many turns of the grid as the tiles need, with no more groups than those turns keep busy
+  const int64_t tiles = (a->N + a->rows - 1) / a->rows;
+  const int64_t turns = (tiles + int64_t(p->num_sms) * a->groups - 1) / (int64_t(p->num_sms) * a->groups);
+  // (a backward of so few rows runs in one CTA, whose sums are the sums over all rows)
+  const bool one = backward && tiles <= a->groups;
+  a->groups = static_cast<int>(one ? tiles : (tiles + p->num_sms * turns - 1) / (p->num_sms * turns));
   a->smem = a->groups * a->group_bytes + factors;
-  a->tiles = (a->N + a->rows - 1) / a->rows;
-  a->ctas = static_cast<int>(std::min<int64_t>(a->tiles, p->num_sms));
+  a->tiles = tiles;
+  a->ctas = one ? 1 : static_cast<int>(std::min<int64_t>(a->tiles, p->num_sms));
   for (size_t i = 0; i < p->blocks.size(); ++i)
     a->few[i].code = rn_code(a->few[i].D, rn_share(a->few[i].D, a->few[i].mul, a->lanes));
 }
@@ -185,7 +194,8 @@ void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
 cgtp_status launch(const cgtp_resnorm_s* p, RnArgs& a, bool backward, cudaStream_t st) {
   deal(p, &a, backward);
   const int sums_smem = 33 * a.groups * a.warps * es_param(p);   // of the last CTA
-  if (backward && a.kind != kRnDirect && (a.gpost || a.gscale || a.gpre) && int64_t(a.ctas) * 2 * a.chan <= kRnTailSums &&
+  if (backward && a.kind != kRnDirect && (a.gpost || a.gscale || a.gpre) && a.ctas > 1 &&
+      int64_t(a.ctas) * 2 * a.chan <= kRnTailSums &&
       sums_smem <= a.smem)
     a.ticket = p->ticket;
   const auto run = p->dtype == CGTP_F64                ? (backward ? rn_backward_f64 : rn_forward_f64)

@@ -100,8 +100,8 @@ constexpr int rn_code(int D, int share) {
   return first[D / 2] + (share >= 8 ? 3 : share >= 4 ? 2 : share - 1);
 }
 
-// Partial sums (CTAs x 2 C) that the last CTA of a backward adds itself: below, its 16 loads a thread are
-// shorter than another launch (64 rows of 8x0e+8x1o: 42 us a call with the launch, 35 us without).
+// Partial sums (CTAs x 2 C) that the last CTA of a backward adds itself: up to 16 loads a thread, which is
+// less than another launch (2,000 rows of 8x0e+8x1o).  Above, the launch takes 6 us and one CTA would take longer.
 constexpr int kRnTailSums = 8192;
 constexpr int kRnMaxStages = 2;     // tiles of a group in shared memory
 constexpr int kRnWarps = 16;        // warps of a CTA at most

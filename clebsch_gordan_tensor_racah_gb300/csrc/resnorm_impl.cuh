@@ -545,8 +545,19 @@ __device__ __forceinline__ T* rn_in(const RnArgs& a, int i, char* stage, int j) 
 // Rows staged in shared memory
 // ---------------------------------------------------------------------------
 
-// Column i of the partial sums, added in CTA order within each of `segments` threads and then in their order:
-// gpost = scale A, gscale = post A, gpre.
+// Column i of the sums over rows: gpost = scale A, gscale = post A, gpre.
+template <typename A>
+__device__ __forceinline__ void rn_put_sums(A v, int i, int chan, const void* post, const void* scale, void* gpost, void* gscale,
+                                            void* gpre) {
+  if (i < chan) {
+    if (gpost) static_cast<A*>(gpost)[i] = scale ? v * static_cast<const A*>(scale)[i] : v;
+    if (gscale) static_cast<A*>(gscale)[i] = post ? v * static_cast<const A*>(post)[i] : v;
+  } else if (gpre) {
+    static_cast<A*>(gpre)[i - chan] = v;
+  }
+}
+
+// Column i of the partial sums, added in CTA order within each of `segments` threads and then in their order.
 template <typename A>
 __device__ __forceinline__ void rn_columns(const A* part, int ctas, int chan, const void* post, const void* scale, void* gpost,
                                            void* gscale, void* gpre, A (*sums)[33], int i, int seg, int segments) {
@@ -558,13 +569,7 @@ __device__ __forceinline__ void rn_columns(const A* part, int ctas, int chan, co
   __syncthreads();
   if (seg == 0 && i < 2 * chan) {
     for (int k = 1; k < segments; ++k) v += sums[k][lane];
-    const int c = i < chan ? i : i - chan;
-    if (i < chan) {
-      if (gpost) static_cast<A*>(gpost)[c] = scale ? v * static_cast<const A*>(scale)[c] : v;
-      if (gscale) static_cast<A*>(gscale)[c] = post ? v * static_cast<const A*>(post)[c] : v;
-    } else if (gpre) {
-      static_cast<A*>(gpre)[c] = v;
-    }
+    rn_put_sums<A>(v, i, chan, post, scale, gpost, gscale, gpre);
   }
   __syncthreads();
 }
@@ -798,7 +803,8 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
         const A* p = part + (k - g) * (a.group_bytes / static_cast<int>(sizeof(A)));
         for (int j = 0; j < abreast; ++j) v += p[j * 2 * a.chan + i];
       }
-      to[i] = v;
+      if (a.ctas == 1) rn_put_sums<A>(v, i, a.chan, a.post, a.scale, a.gpost, a.gscale, a.gpre);
+      else to[i] = v;
     }
     if (a.ticket) {
       __shared__ bool last;
@@ -872,7 +878,7 @@ cudaError_t rn_launch(const RnArgs& a, cudaStream_t st) {
       rn_direct_kernel<BACKWARD, S, I, O, A><<<a.ctas, kRnDirectWarps * 32, 0, st>>>(a);
       e = cudaGetLastError();
   }
-  if (!BACKWARD || e != cudaSuccess || a.ticket || !(a.gpost || a.gscale || a.gpre)) return e;
+  if (!BACKWARD || e != cudaSuccess || a.ticket || (a.kind != kRnDirect && a.ctas == 1) || !(a.gpost || a.gscale || a.gpre)) return e;
   rn_reduce_kernel<A><<<(2 * a.chan + 31) / 32, 256, 0, st>>>(a.part, a.ctas, a.chan, a.post, a.scale, a.gpost, a.gscale, a.gpre);
   return cudaGetLastError();
 }
