@@ -63,13 +63,16 @@ struct Scalars {
   uint32_t key0, key1;
 };
 
-// 32 pseudo-random bits of element i: a Weyl step and two multiply-xorshift rounds
-__device__ __forceinline__ uint32_t noise_of(uint64_t i, uint32_t key0, uint32_t key1) {
-  uint32_t x = static_cast<uint32_t>(i) * 0x9E3779B1u + static_cast<uint32_t>(i >> 32) * 0x85A308D3u + key0;
+// Pseudo-random bits of element i (its low 32 bits; key0 holds the high ones too): a Weyl step and two
+// multiply-xorshift rounds, of which the last xorshift is left to the two halves below.
+__device__ __forceinline__ uint32_t noise_of(uint32_t i, uint32_t key0, uint32_t key1) {
+  uint32_t x = i * 0x9E3779B1u + key0;
   x = (x ^ (x >> 15)) * 0xBB67AE85u;
-  x = (x ^ (x >> 13)) * 0x3C6EF373u + key1;
-  return x ^ (x >> 16);
+  return (x ^ (x >> 13)) * 0x3C6EF373u + key1;
 }
+// the upper and the lower 16 bits of x ^ x >> 16, as the upper 16 of 20 bits
+__device__ __forceinline__ uint32_t m_noise(uint32_t x) { return x >> 12 & 0xFFFF0u; }
+__device__ __forceinline__ uint32_t v_noise(uint32_t x) { return (x << 4 ^ x >> 12) & 0xFFFF0u; }
 
 // A code of a block with exponent E and largest exponent field TOP stands for
 //   field f > 0:  2^(E - TOP + f - 127) (1 + mantissa / 8),   field 0:  mantissa 2^(E - TOP + 1 - 130),
@@ -78,16 +81,14 @@ __device__ __forceinline__ uint32_t noise_of(uint64_t i, uint32_t key0, uint32_t
 struct Power {
   float first, second;
 };
-template <int TOP>
-__device__ __forceinline__ Power code_power(int E) {
-  const int base = max(E, kEMin) - TOP, half = base >> 1;
+__device__ __forceinline__ Power code_power(int E, int top) {
+  const int base = max(E, kEMin) - top, half = base >> 1;
   return {E == kENan ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(half + 127) << 23),
           __uint_as_float(static_cast<uint32_t>(base - half + 127) << 23)};
 }
 // bits of the float of byte j of a word of four codes: m (sign and 7 bits) and v (8 bits)
 __device__ __forceinline__ float m_bits(uint32_t word, int j) {
-  const uint32_t at = j == 3 ? word >> 4 : word << (20 - 8 * j);
-  return __uint_as_float((at & 0x07F00000u) | (word << (24 - 8 * j) & 0x80000000u));
+  return __uint_as_float(static_cast<uint32_t>(static_cast<int32_t>(word << (24 - 8 * j)) >> 4) & 0x87F00000u);
 }
 __device__ __forceinline__ float v_bits(uint32_t word, int j) {
   return __uint_as_float((j == 3 ? word >> 4 : word << (20 - 8 * j)) & 0x0FF00000u);
@@ -99,13 +100,13 @@ template <int TOP>
 __device__ __forceinline__ uint32_t code_of(uint32_t bits, int E, uint32_t r) {
   return (bits + r - (static_cast<uint32_t>(E - TOP) << 23)) >> 20;
 }
-// The same where x may be below the smallest exponent of the codes.
+// The same where x may be below the smallest exponent of the codes; the code is the lowest byte.
 template <int TOP>
 __device__ __forceinline__ uint32_t code_of_any(uint32_t bits, int E, uint32_t r) {
   const int base = E - TOP;
   const float fine = __fmul_rn(__uint_as_float(bits), __uint_as_float(static_cast<uint32_t>(256 - base) << 23));
   const float noise = __fadd_rn(__uint_as_float(0x3F800000u | r << 3), -1.0f);   // r 2^-20
-  const uint32_t low = __float_as_uint(__fadd_rd(__fadd_rn(fine, noise), 8388608.0f)) & 15u;
+  const uint32_t low = __float_as_uint(__fadd_rd(__fadd_rn(fine, noise), 8388608.0f));   // 2^23 + the floor
   return bits >= (static_cast<uint32_t>(base + 1) << 23) ? code_of<TOP>(bits, E, r) : low;
 }
 
@@ -246,7 +247,7 @@ __device__ __forceinline__ void encode_block(const float (&m)[4], const float (&
                                              uint32_t* m_word, uint32_t* v_word, uint32_t* m_exp, uint32_t* v_exp) {
   uint32_t a[4], b[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] = __float_as_uint(m[i]) & 0x7FFFFFFFu, b[i] = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+  for (int i = 0; i < 4; ++i) a[i] = __float_as_uint(m[i]) & 0x7FFFFFFFu, b[i] = __float_as_uint(v[i]);   // v >= 0, or a NaN
   const uint32_t mb = max(max(a[0], a[1]), max(a[2], a[3])), vb = max(max(b[0], b[1]), max(b[2], b[3]));
   const int me = block_exponent(__reduce_max_sync(0xffffffffu, mb)), ve = block_exponent(__reduce_max_sync(0xffffffffu, vb));
   const uint32_t key = static_cast<uint32_t>(place >> 32) * 0x85A308D3u + s.key0;
@@ -257,17 +258,17 @@ __device__ __forceinline__ void encode_block(const float (&m)[4], const float (&
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     r[i] = noise_of(static_cast<uint32_t>(place) + i, key, s.key1);
-    cm[i] = code_of_any<kMTop>(a[i], me, r[i] >> 12 & 0xFFFF0u);
+    cm[i] = code_of_any<kMTop>(a[i], me, m_noise(r[i]));
   }
   if (v_low) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      cv[i] = code_of_any<kVTop>(b[i], ve, r[i] << 4 & 0xFFFF0u);
+      cv[i] = code_of_any<kVTop>(b[i], ve, v_noise(r[i])) & 255u;
       cv[i] = b[i] ? max(cv[i], 1u) : cv[i];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) cv[i] = code_of<kVTop>(b[i], ve, r[i] << 4 & 0xFFFF0u);
+    for (int i = 0; i < 4; ++i) cv[i] = code_of<kVTop>(b[i], ve, v_noise(r[i]));
   }
   const uint32_t signs = __byte_perm(__byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0073),
                                      __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0073), 0x5410);
@@ -507,25 +508,32 @@ __global__ void __launch_bounds__(kStepThreads, 3) adamw8_kernel(const __grid_co
     if (done + 1 < filled) e = exponents(ring[at + 1 == kRing ? 0 : at + 1]);
     s.keep = st.keep;
     uint32_t e_new = 0;
+    const Power power = code_power(static_cast<int>(e_now), lane < 2 ? kMTop : kVTop);   // of lanes 0 to 3
+    const int64_t first_place = (int64_t)st.state * kBlock + lane * 4;
+    uint32_t *m_words = reinterpret_cast<uint32_t*>(m_ + first_place), *v_words = reinterpret_cast<uint32_t*>(v_ + first_place);
+    const int elements = st.elements;
+    float* const first_to = st.to + lane * 4;
+    __nv_bfloat16* const first_copy = st.copy ? st.copy + lane * 4 : nullptr;
+    const bool wide = st.wide;
 #pragma unroll
     for (int b = 0; b < kStageBlocks; ++b) {
-      if (b * kBlock < st.elements) {
-        const int64_t place = (int64_t)(st.state + b) * kBlock + lane * 4;
-        const int left = st.elements - b * kBlock - lane * 4;
+      if (b * kBlock < elements) {
+        const int left = elements - b * kBlock - lane * 4;
         float p[4], g[4], m[4], v[4];
         load4<float, float>(st.p + b * kBlock + lane * 4, 4, true, p);
         load4<G, float>(st.g + b * kBlock + lane * 4, 4, true, g);
         const uint32_t mw = reinterpret_cast<const uint32_t*>(st.m + b * kBlock)[lane], vw = reinterpret_cast<const uint32_t*>(st.v + b * kBlock)[lane];
-        const Power mp = code_power<kMTop>(__shfl_sync(0xffffffffu, e_now, b)), vp = code_power<kVTop>(__shfl_sync(0xffffffffu, e_now, 2 + b));
+        const Power mp{__shfl_sync(0xffffffffu, power.first, b), __shfl_sync(0xffffffffu, power.second, b)};
+        const Power vp{__shfl_sync(0xffffffffu, power.first, 2 + b), __shfl_sync(0xffffffffu, power.second, 2 + b)};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           m[i] = m_bits(mw, i) * mp.first;
           v[i] = v_bits(vw, i) * vp.first;
         }
         step_values<float>(p, g, m, v, s, mp.second, vp.second);
-        float* to = st.to + b * kBlock + lane * 4;
-        __nv_bfloat16* copy = st.copy ? st.copy + b * kBlock + lane * 4 : nullptr;
-        if (st.wide) {
+        float* to = first_to + b * kBlock;
+        __nv_bfloat16* copy = first_copy ? first_copy + b * kBlock : nullptr;
+        if (wide) {
           store4<float, float>(to, 4, true, p);
           if (copy) store4<__nv_bfloat16, float>(copy, 4, true, p);
         } else {
@@ -536,13 +544,13 @@ __global__ void __launch_bounds__(kStepThreads, 3) adamw8_kernel(const __grid_co
             if (i >= left) m[i] = v[i] = 0.0f;   // the place behind the tensor's end
         }
         uint32_t m_word, v_word, me, ve;
-        encode_block(m, v, place, s, &m_word, &v_word, &me, &ve);
-        *reinterpret_cast<uint32_t*>(m_ + place) = m_word;
-        *reinterpret_cast<uint32_t*>(v_ + place) = v_word;
+        encode_block(m, v, first_place + b * kBlock, s, &m_word, &v_word, &me, &ve);
+        m_words[b * (kBlock / 4)] = m_word;
+        v_words[b * (kBlock / 4)] = v_word;
         e_new = lane == b ? me : lane == 2 + b ? ve : e_new;
       }
     }
-    if (lane < 4 && (lane & 1) * kBlock < st.elements) *exponent_at(st) = static_cast<uint8_t>(e_new);
+    if (lane < 4 && (lane & 1) * kBlock < elements) *exponent_at(st) = static_cast<uint8_t>(e_new);
     __syncwarp();
   }
 }
@@ -552,7 +560,7 @@ __global__ void __launch_bounds__(kStepThreads) state_values_kernel(const uint8_
   const int64_t i = (int64_t)blockIdx.x * kStepThreads + threadIdx.x;
   if (i >= n4) return;
   const uint32_t mc = reinterpret_cast<const uint32_t*>(m)[i], vc = reinterpret_cast<const uint32_t*>(v)[i];
-  const Power mp = code_power<kMTop>(m_exp[i >> 5]), vp = code_power<kVTop>(v_exp[i >> 5]);
+  const Power mp = code_power(m_exp[i >> 5], kMTop), vp = code_power(v_exp[i >> 5], kVTop);
   float a[4], b[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
