@@ -756,28 +756,26 @@ cgtp_status create(cgtp_adamw_s* o, int n, const int64_t* numel, const float* de
   }
   o->decay.assign(n, 1.0f);
   if (decay_scale) o->decay.assign(decay_scale, decay_scale + n);
-  std::vector<Unit> units;
+  // one allocation: the ticket (in the place of a unit), the units, the partial sums
+  std::vector<Unit> units(1, Unit{});
   for (int i = 0; i < n; ++i) {
-    if (i % kMostTensors == 0) o->unit_begin.push_back(static_cast<int64_t>(units.size()));
+    if (i % kMostTensors == 0) o->unit_begin.push_back(static_cast<int64_t>(units.size()) - 1);
     for (int64_t b = 0; b < o->begin[i + 1] - o->begin[i]; b += kUnit)
       units.push_back({i % kMostTensors, static_cast<unsigned>(b), static_cast<unsigned>(o->begin[i] + b),
                        static_cast<int>(std::min<int64_t>(kUnit * kBlock, numel[i] - b * kBlock))});
   }
-  o->unit_begin.push_back(static_cast<int64_t>(units.size()));
+  o->unit_begin.push_back(static_cast<int64_t>(units.size()) - 1);
   const size_t parts = size_t(o->num_sms) * kNormCtasPerSm * (o->unit_begin.size() - 1);
-  const size_t b_units = units.size() * sizeof(Unit), b_part = parts * sizeof(double);
-  const size_t bytes = b_units + b_part + sizeof(unsigned);
+  const size_t b_units = units.size() * sizeof(Unit), bytes = b_units + parts * sizeof(double);
   if (cudaMalloc(&o->base, bytes) != cudaSuccess) {
     cudaGetLastError();
     return fail(CGTP_ENOMEM, "optimizer table allocation failed");
   }
   o->device_bytes = bytes;
-  unsigned char* at = static_cast<unsigned char*>(o->base);
-  o->units_dev = at;
-  o->part = reinterpret_cast<double*>(at + b_units);
-  o->ticket = reinterpret_cast<unsigned*>(at + b_units + b_part);
-  if ((b_units && cudaMemcpy(o->units_dev, units.data(), b_units, cudaMemcpyHostToDevice) != cudaSuccess) ||
-      cudaMemset(o->ticket, 0, sizeof(unsigned)) != cudaSuccess) {
+  o->ticket = static_cast<unsigned*>(o->base);
+  o->units_dev = static_cast<Unit*>(o->base) + 1;
+  o->part = reinterpret_cast<double*>(static_cast<unsigned char*>(o->base) + b_units);
+  if (cudaMemcpy(o->base, units.data(), b_units, cudaMemcpyHostToDevice) != cudaSuccess) {
     cudaGetLastError();
     return fail(CGTP_ECUDA, "optimizer table upload failed");
   }

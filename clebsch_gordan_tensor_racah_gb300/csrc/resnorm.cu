@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 #include <new>
 #include <string>
 
@@ -228,16 +229,20 @@ cgtp_status create(cgtp_resnorm_s* p, const char* irreps) {
     return fail(CGTP_ECUDA, "no CUDA device");
   }
   p->smem_cap -= 512;   // the kernels' static shared memory
-  const size_t tab = p->blocks.size() * sizeof(RnBlock);
-  const size_t part = size_t(p->num_sms) * kRnCtasPerSm * 2 * p->chan * es_param(p) + sizeof(unsigned);
-  if (cudaMalloc(reinterpret_cast<void**>(&p->blocks_dev), tab) != cudaSuccess || cudaMalloc(&p->part, part) != cudaSuccess) {
+  // one allocation: the ticket, the block table, the partial sums
+  const size_t tab = p->blocks.size() * sizeof(RnBlock), head = (16 + tab + 255) / 256 * 256;
+  const size_t part = size_t(p->num_sms) * kRnCtasPerSm * 2 * p->chan * es_param(p);
+  std::vector<char> table(16 + tab, 0);
+  std::memcpy(table.data() + 16, p->blocks.data(), tab);
+  if (cudaMalloc(&p->base, head + part) != cudaSuccess) {
     cudaGetLastError();
     return fail(CGTP_ENOMEM, "norm table allocation failed");
   }
-  p->device_bytes = tab + part;
-  p->ticket = reinterpret_cast<unsigned*>(static_cast<char*>(p->part) + part - sizeof(unsigned));
-  if (cudaMemcpy(p->blocks_dev, p->blocks.data(), tab, cudaMemcpyHostToDevice) != cudaSuccess ||
-      cudaMemset(p->ticket, 0, sizeof(unsigned)) != cudaSuccess) {
+  p->device_bytes = head + part;
+  p->ticket = static_cast<unsigned*>(p->base);
+  p->blocks_dev = reinterpret_cast<RnBlock*>(static_cast<char*>(p->base) + 16);
+  p->part = static_cast<char*>(p->base) + head;
+  if (cudaMemcpy(p->base, table.data(), table.size(), cudaMemcpyHostToDevice) != cudaSuccess) {
     cudaGetLastError();
     return fail(CGTP_ECUDA, "norm table upload failed");
   }
@@ -284,8 +289,7 @@ cgtp_status cgtp_resnorm_create(cgtp_resnorm* out, const char* irreps, int dtype
 
 void cgtp_resnorm_destroy(cgtp_resnorm p) {
   if (!p) return;
-  if (p->blocks_dev) cudaFree(p->blocks_dev);
-  if (p->part) cudaFree(p->part);
+  if (p->base) cudaFree(p->base);
   delete p;
 }
 

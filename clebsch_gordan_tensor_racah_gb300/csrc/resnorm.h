@@ -69,6 +69,7 @@ struct cgtp_resnorm_s {
   int64_t dim = 0, chan = 0;
   int widest = 1;             // channels of the widest block
   std::vector<cgtp::RnBlock> blocks;
+  void* base = nullptr;       // the device allocation that holds the next three
   cgtp::RnBlock* blocks_dev = nullptr;
   void* part = nullptr;
   unsigned* ticket = nullptr;

@@ -124,7 +124,7 @@ class ResNormPlan:
 
     def __del__(self):
         h = getattr(self, "_h", None)
-        if h is not None and h.value:
+        if h is not None and h.value and lib is not None:
             lib().cgtp_resnorm_destroy(h)
             self._h = None
 
@@ -245,7 +245,7 @@ class AdamW:
 
     def __del__(self):
         h = getattr(self, "_h", None)
-        if h is not None and h.value:
+        if h is not None and h.value and lib is not None:
             lib().cgtp_adamw_destroy(h)
             self._h = None
 

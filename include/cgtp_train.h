@@ -40,7 +40,8 @@ typedef enum { CGTP_ACT_NONE = 0, CGTP_ACT_IDENTITY = 1, CGTP_ACT_SIGMOID = 2, C
  *      CGTP_RESNORM_STORAGE every row tensor in bfloat16.  Parameters (post,
  *      scale, pre) and their gradients are FP32 (FP64 for CGTP_F64), arithmetic
  *      and sums too.
- *  alpha : factor of the residual.  eps >= 0.
+ *  alpha : factor of the residual.  eps >= 0; with eps = 0 a block of zeros has no norm
+ *      (NaN).  Squares are summed in FP32 (FP64): elements above 1.8e19 overflow them.
  * The plan owns its tables and the partial sums of the parameter gradients.
  */
 #define CGTP_RESNORM_POST 1
