@@ -75,10 +75,14 @@ def _result(r, explain):
     return r
 
 
-def _current(stream, t):
-    """cudaStream_t of `stream`, or of the current stream of a tensor's device."""
-    if stream is not None:
-        return stream.cuda_stream
+def _on(stream, call, *args, **kwargs):
+    """`call` with `stream` as the current one, so that its results belong to that stream."""
+    with torch.cuda.stream(stream):
+        return call(*args, **kwargs)
+
+
+def _current(t):
+    """cudaStream_t of the current stream of a tensor's device."""
     return torch._C._cuda_getCurrentRawStream(t.device.index) if getattr(t, "is_cuda", False) else 0
 
 
@@ -135,6 +139,8 @@ def cgtp_resnorm_forward(plan, h, z=None, q=None, post=None, scale=None, pre=Non
     z = None: y is the norm of h and the first result is h itself.  h = None: no residual.  y is
     None for plans with pre_norm = False.  Row tensors [N, dim] (q: [N, channels]) may be column
     ranges of wider ones."""
+    if stream is not None:
+        return _on(stream, cgtp_resnorm_forward, plan, h, z, q, post, scale, pre, out, y)
     ref = h if h is not None else z
     if ref is None:
         raise ValueError("h or z must be given")
@@ -147,7 +153,7 @@ def cgtp_resnorm_forward(plan, h, z=None, q=None, post=None, scale=None, pre=Non
         for name, t in (("post", post), ("scale", scale), ("pre", pre)):
             _explain_vector(name, t, plan.param_dtype, chan)
 
-    r = _binding.resnorm_forward(plan._native, h, z, q, post, scale, pre, out, y, _current(stream, ref))
+    r = _binding.resnorm_forward(plan._native, h, z, q, post, scale, pre, out, y, _current(ref))
     return r if type(r) is tuple else _result(r, explain)
 
 
@@ -158,6 +164,8 @@ def cgtp_resnorm_backward(plan, gout, gy, x, z=None, q=None, post=None, scale=No
     x is what the forward returned first.  gz and gq are None without z or a gate; gpost, gscale
     and gpre are None where that factor is.  outs: optional preallocated results in that order
     (column ranges of wider rows are fine for gh, gz and gq)."""
+    if stream is not None:
+        return _on(stream, cgtp_resnorm_backward, plan, gout, gy, x, z, q, post, scale, pre, need_gh, outs)
     ref = gout if gout is not None else gy
     if ref is None:
         raise ValueError("gout or gy must be given")
@@ -173,7 +181,7 @@ def cgtp_resnorm_backward(plan, gout, gy, x, z=None, q=None, post=None, scale=No
         for name, t in zip(("post", "scale", "pre", "gpost", "gscale", "gpre"), (post, scale, pre, *sums)):
             _explain_vector(name, t, plan.param_dtype, chan)
 
-    r = _binding.resnorm_backward(plan._native, gout, gy, x, z, q, post, scale, pre, need_gh, outs, _current(stream, ref))
+    r = _binding.resnorm_backward(plan._native, gout, gy, x, z, q, post, scale, pre, need_gh, outs, _current(ref))
     return r if type(r) is tuple else _result(r, explain)
 
 
@@ -252,10 +260,12 @@ class AdamW:
 
 def cgtp_grad_norm(opt, grads, max_norm=float("inf"), out=None, stream=None):
     """Tensor [norm of all gradients, min(1, max_norm / norm)]; None gradients count as zero."""
+    if stream is not None:
+        return _on(stream, cgtp_grad_norm, opt, grads, max_norm, out)
     ref = out if out is not None else next((g for g in grads if g is not None), None)
     if ref is None:
         out = ref = torch.empty(2, dtype=opt.param_dtype, device="cuda")
-    r = _binding.grad_norm(opt._native, grads, max_norm, out, _current(stream, ref))
+    r = _binding.grad_norm(opt._native, grads, max_norm, out, _current(ref))
     return r if type(r) is torch.Tensor else _result(r, lambda: opt.explain([("grads", grads, opt.grad_dtype)], clip=out))
 
 
@@ -263,8 +273,10 @@ def cgtp_adamw_step(opt, params, grads, state, lr, betas=(0.9, 0.999), eps=1e-8,
                     copies=None, clip=None, seed=0, stream=None):
     """One AdamW step in place.  A None gradient skips its tensor.  copies: bfloat16 tensors (or None)
     that receive the new parameters.  clip: result of cgtp_grad_norm.  seed: rounding of 8-bit states."""
+    if stream is not None:
+        return _on(stream, cgtp_adamw_step, opt, params, grads, state, lr, betas, eps, weight_decay, step, copies, clip, seed)
     r = _binding.adamw_step(opt._native, params, grads, copies, state["m"], state["v"], state["m_exp"], state["v_exp"], lr, betas[0],
-                            betas[1], eps, weight_decay, step, seed, clip, _current(stream, state["m"]))
+                            betas[1], eps, weight_decay, step, seed, clip, _current(state["m"]))
     if r is not None:
         _result(r, lambda: opt.explain([("params", params, opt.param_dtype), ("grads", grads, opt.grad_dtype),
                                         ("copies", copies, torch.bfloat16)], state, clip))
@@ -274,5 +286,7 @@ def cgtp_adamw_state_values(opt, state, stream=None):
     """(m, v) as the FP32 values the 8-bit states stand for (the states themselves otherwise)."""
     if opt.state != "8bit":
         return state["m"], state["v"]
-    r = _binding.state_values(opt._native, state["m"], state["v"], state["m_exp"], state["v_exp"], _current(stream, state["m"]))
+    if stream is not None:
+        return _on(stream, cgtp_adamw_state_values, opt, state)
+    r = _binding.state_values(opt._native, state["m"], state["v"], state["m_exp"], state["v_exp"], _current(state["m"]))
     return r if type(r) is tuple else _result(r, lambda: opt.explain([], state))

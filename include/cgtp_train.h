@@ -42,7 +42,8 @@ typedef enum { CGTP_ACT_NONE = 0, CGTP_ACT_IDENTITY = 1, CGTP_ACT_SIGMOID = 2, C
  *      and sums too.
  *  alpha : factor of the residual.  eps >= 0; with eps = 0 a block of zeros has no norm
  *      (NaN).  Squares are summed in FP32 (FP64): elements above 1.8e19 overflow them.
- * The plan owns its tables and the partial sums of the parameter gradients.
+ * The plan owns its tables and the partial sums of the parameter gradients: backwards
+ * of the same plan must not overlap on the GPU.
  */
 #define CGTP_RESNORM_POST 1
 #define CGTP_RESNORM_PRE 2
@@ -117,6 +118,8 @@ typedef enum { CGTP_STATE_FULL = 0, CGTP_STATE_8BIT = 1 } cgtp_state;
 /*
  *  numel [n_tensors] : HOST array, elements of each tensor (0 is allowed).
  *  decay_scale [n_tensors] : HOST array or NULL (1 for every tensor).
+ *  The optimizer owns its tables and the gradient norm's partial sums: norms of
+ *  the same optimizer must not overlap on the GPU.
  *  param_dtype : CGTP_F32 or CGTP_F64.  grad_dtype : that type, or CGTP_BF16 with
  *      CGTP_F32 parameters.
  */

@@ -291,6 +291,37 @@ def test_states_of_extreme_size():
     assert bool((v[2::4] > 0).all())
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-15, 1e-12, 1e-8])
+@pytest.mark.parametrize("state_kind", ["f32", "8bit"])
+def test_small_eps_and_small_gradients(eps, state_kind):
+    # from zero states the step is lr |g| / (|g| + eps).  FP32 keeps (1 - beta2) g^2 of g = 1e-18 as 1e-39, a
+    # denormal with 19 bits: 2^-19 of v, plus the bounds above; 1e-19: 13 bits
+    for size, bits in ((1.0, 20), (1e-6, 20), (1e-18, 18), (1e-19, 12)):
+        g = [torch.full((200,), size, device="cuda")]
+        p = [torch.zeros(200, device="cuda")]
+        opt = cg().AdamW([200], state=state_kind)
+        cg().cgtp_adamw_step(opt, p, g, opt.new_state(), lr=1e-2, eps=eps, step=1)
+        want = 1e-2 * size / (size + eps)
+        assert float((p[0] + want).abs().max()) <= 2.0 ** -bits * want, (size, float(p[0][0]), want)
+
+
+def test_other_streams():
+    g, p = [torch.randn(5000, device="cuda")], [torch.randn(5000, device="cuda")]
+    opt = cg().AdamW([5000], state="8bit")
+    runs = []
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, s):
+        q, state = [p[0].clone()], opt.new_state()
+        torch.cuda.synchronize()
+        clip = cg().cgtp_grad_norm(opt, g, 1.0, stream=stream)
+        cg().cgtp_adamw_step(opt, q, g, state, lr=1e-2, clip=clip, stream=stream)
+        m, v = cg().cgtp_adamw_state_values(opt, state, stream=stream)
+        torch.cuda.synchronize()
+        runs.append((clip, q[0], m, v))
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
 def test_more_tensors_than_one_launch_holds():
     for count in (64, 65, 1024, 1025, 2100):
         rng = np.random.default_rng(count)

@@ -295,6 +295,15 @@ def test_another_stream():
         got = cg().cgtp_resnorm_forward(plan, t["h"], z, post=t["post"], scale=t["scale"], pre=t["pre"])
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+    # a stream given by name, while another is current
+    with torch.cuda.stream(s):
+        z = t["z"] * 1.0
+    got = cg().cgtp_resnorm_forward(plan, t["h"], z, post=t["post"], scale=t["scale"], pre=t["pre"], stream=s)
+    grads = cg().cgtp_resnorm_backward(plan, t["gout"], t["gy"], got[0], z, post=t["post"], scale=t["scale"], pre=t["pre"], stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    ref = cg().cgtp_resnorm_backward(plan, t["gout"], t["gy"], want[0], t["z"], post=t["post"], scale=t["scale"], pre=t["pre"])
+    assert all(a is None or torch.equal(a, b) for a, b in zip(grads, ref))
 
 
 def test_nothing_outside_the_rows_is_written():
