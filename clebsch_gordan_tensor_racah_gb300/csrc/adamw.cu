@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "cgtp_train.h"
+#include "chain.cuh"
 #include "internal.h"
 
 struct cgtp_adamw_s {
@@ -334,6 +335,7 @@ template <typename A, typename G, int K>
 __global__ void __launch_bounds__(kStepThreads) adamw_kernel(const __grid_constant__ Tensors<K> ts, const Unit* units,
                                                              unsigned n_units, A* m, A* v, const Scalars host, const A* clip) {
   constexpr int NB = sizeof(A) == 8 ? 1 : 2;
+  chain_enter();
   const int lane = threadIdx.x & 31;
   const unsigned stride = gridDim.x * kWarpsPerCta;
   unsigned u = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
@@ -471,6 +473,7 @@ __global__ void __launch_bounds__(kStepThreads, 3) adamw8_kernel(const __grid_co
                                                                  unsigned n_units, uint8_t* m_, uint8_t* v_, uint8_t* m_exp,
                                                                  uint8_t* v_exp, const Scalars host, const float* clip) {
   extern __shared__ __align__(16) unsigned char shared[];
+  chain_enter();
   const int lane = threadIdx.x & 31;
   Stage<G>* ring = reinterpret_cast<Stage<G>*>(shared) + (threadIdx.x >> 5) * kRing;
   const unsigned first = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
@@ -557,6 +560,7 @@ __global__ void __launch_bounds__(kStepThreads, 3) adamw8_kernel(const __grid_co
 
 __global__ void __launch_bounds__(kStepThreads) state_values_kernel(const uint8_t* m, const uint8_t* v, const uint8_t* m_exp,
                                                                     const uint8_t* v_exp, float* m_out, float* v_out, int64_t n4) {
+  chain_enter();
   const int64_t i = (int64_t)blockIdx.x * kStepThreads + threadIdx.x;
   if (i >= n4) return;
   const uint32_t mc = reinterpret_cast<const uint32_t*>(m)[i], vc = reinterpret_cast<const uint32_t*>(v)[i];
@@ -588,6 +592,7 @@ template <typename A, typename G, int K>
 __global__ void __launch_bounds__(kStepThreads) norm_kernel(const __grid_constant__ Tensors<K> ts, const Unit* units,
                                                             unsigned n_units, double* part, int before, bool last,
                                                             unsigned* ticket, double max_norm, A* out) {
+  chain_enter();
   const int lane = threadIdx.x & 31;
   A sum[4] = {A(0), A(0), A(0), A(0)};
   for (unsigned u = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5); u < n_units; u += gridDim.x * kWarpsPerCta) {
@@ -631,8 +636,7 @@ __global__ void __launch_bounds__(kStepThreads) norm_kernel(const __grid_constan
 
 constexpr int kNormCtasPerSm = 8, kStepCtasPerSm = 8;
 
-cgtp_status launched(const char* what) {
-  const cudaError_t e = cudaGetLastError();
+cgtp_status launched(cudaError_t e, const char* what) {
   return e == cudaSuccess ? CGTP_OK : fail(CGTP_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
@@ -669,14 +673,14 @@ cgtp_status step_launch(const cgtp_adamw_s* o, int t0, int n, void* const* param
   if constexpr (EIGHT) {
     constexpr int bytes = kWarpsPerCta * kRing * sizeof(Stage<G>);
     if (smem_cap_cached(reinterpret_cast<const void*>(adamw8_kernel<G, K>)) < bytes) return fail(CGTP_ECUDA, "adamw step: shared memory");
-    adamw8_kernel<G, K><<<ctas_for(o, n_units, 3), kStepThreads, bytes, st>>>(
-        ts, units, n_units, static_cast<uint8_t*>(a.m), static_cast<uint8_t*>(a.v), a.m_exp, a.v_exp, a.s,
-        static_cast<const float*>(a.clip));
+    return launched(chain_launch(adamw8_kernel<G, K>, ctas_for(o, n_units, 3), kStepThreads, bytes, st, ts, units, n_units, a.m, a.v,
+                                 a.m_exp, a.v_exp, a.s, a.clip),
+                    "adamw step");
   } else {
-    adamw_kernel<A, G, K><<<ctas_for(o, n_units, kStepCtasPerSm), kStepThreads, 0, st>>>(
-        ts, units, n_units, static_cast<A*>(a.m), static_cast<A*>(a.v), a.s, static_cast<const A*>(a.clip));
+    return launched(chain_launch(adamw_kernel<A, G, K>, ctas_for(o, n_units, kStepCtasPerSm), kStepThreads, 0, st, ts, units, n_units,
+                                 a.m, a.v, a.s, a.clip),
+                    "adamw step");
   }
-  return launched("adamw step");
 }
 
 template <typename A, typename G, bool EIGHT>
@@ -701,15 +705,16 @@ cgtp_status norm_all(const cgtp_adamw_s* o, const void* const* grads, double max
     const int64_t u0 = o->unit_begin[t0 / kMostTensors], u1 = o->unit_begin[t0 / kMostTensors + 1];
     const int ctas = ctas_for(o, u1 - u0, kNormCtasPerSm);
     const bool last = t0 + n == all;
+    cudaError_t e = cudaSuccess;
     const auto run = [&](auto few, auto kernel) {
       decltype(few) ts;
       fill(&ts, o, t0, n, nullptr, grads, nullptr);
-      kernel<<<ctas, kStepThreads, 0, st>>>(ts, static_cast<const Unit*>(o->units_dev) + u0, static_cast<unsigned>(u1 - u0),
-                                            o->part, before, last, o->ticket, max_norm, static_cast<A*>(out));
+      e = chain_launch(kernel, ctas, kStepThreads, 0, st, ts, static_cast<const Unit*>(o->units_dev) + u0, u1 - u0, o->part, before, last,
+                       o->ticket, max_norm, out);
     };
     if (n <= kFewTensors) run(Tensors<kFewTensors>{}, norm_kernel<A, G, kFewTensors>);
     else run(Tensors<kMostTensors>{}, norm_kernel<A, G, kMostTensors>);
-    const cgtp_status s = launched("gradient norm");
+    const cgtp_status s = launched(e, "gradient norm");
     if (s != CGTP_OK) return s;
     before += ctas;
   }
@@ -906,10 +911,9 @@ cgtp_status cgtp_adamw_state_values(cgtp_adamw o, const void* m, const void* v, 
   if ((s = buffer(m, "m")) || (s = buffer(v, "v")) || (s = buffer(m_out, "m_out")) || (s = buffer(v_out, "v_out"))) return s;
   if (!m_exp || !v_exp) return fail(CGTP_EINVAL, "null pointer: m_exp or v_exp");
   const unsigned ctas = static_cast<unsigned>((n4 + kStepThreads - 1) / kStepThreads);
-  state_values_kernel<<<ctas, kStepThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-      static_cast<const uint8_t*>(m), static_cast<const uint8_t*>(v), static_cast<const uint8_t*>(m_exp),
-      static_cast<const uint8_t*>(v_exp), m_out, v_out, n4);
-  return launched("optimizer state values");
+  return launched(chain_launch(state_values_kernel, ctas, kStepThreads, 0, static_cast<cudaStream_t>(stream), m, v, m_exp, v_exp, m_out,
+                               v_out, n4),
+                  "optimizer state values");
 }
 
 }  // extern "C"

@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "chain.cuh"
 #include "resnorm.h"
 
 namespace cgtp {
@@ -578,6 +579,7 @@ template <typename A>
 __global__ void __launch_bounds__(256) rn_reduce_kernel(const void* part, int ctas, int chan, const void* post, const void* scale,
                                                         void* gpost, void* gscale, void* gpre) {
   __shared__ A sums[8][33];
+  chain_enter();
   rn_columns<A>(static_cast<const A*>(part), ctas, chan, post, scale, gpost, gscale, gpre, sums,
                 blockIdx.x * 32 + (threadIdx.x & 31), threadIdx.x >> 5, 8);
 }
@@ -703,6 +705,7 @@ __device__ __forceinline__ void rn_runs_out(const RnRows* const (&r)[NT], const 
 template <bool BACKWARD, int KIND, typename S, typename I, typename O, typename A>
 __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __grid_constant__ RnArgs a) {
   extern __shared__ __align__(16) char shared[];
+  chain_enter();
   constexpr bool ONE = KIND >= kRnOne, FULL = KIND != kRnOne && KIND != kRnMany;
   constexpr bool WHOLE = KIND == kRnOneFull;
   const int warps = ONE ? 1 : a.warps, threads = warps * 32;
@@ -831,6 +834,7 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
 template <bool BACKWARD, typename S, typename I, typename O, typename A>
 __global__ void __launch_bounds__(kRnDirectWarps * 32) rn_direct_kernel(const __grid_constant__ RnArgs a) {
   __shared__ A scratch[8 * kRnWarps];
+  chain_enter();
   RnTeam<A, false, false> team{static_cast<int>(threadIdx.x), kRnDirectWarps * 32, kRnDirectWarps, 1, scratch, 0};
   const RnFactors<false, A> f{static_cast<const A*>(a.post), static_cast<const A*>(a.scale), static_cast<const A*>(a.pre)};
   A* part = static_cast<A*>(a.part) + (int64_t)blockIdx.x * 2 * a.chan;
@@ -859,8 +863,7 @@ template <bool BACKWARD, int KIND, typename S, typename I, typename O, typename 
 cudaError_t rn_launch_staged(const RnArgs& a, cudaStream_t st) {
   if (smem_cap_cached(reinterpret_cast<const void*>(rn_staged_kernel<BACKWARD, KIND, S, I, O, A>)) < a.smem)
     return cudaErrorInvalidConfiguration;
-  rn_staged_kernel<BACKWARD, KIND, S, I, O, A><<<a.ctas, a.groups * a.warps * 32, a.smem, st>>>(a);
-  return cudaGetLastError();
+  return chain_launch(rn_staged_kernel<BACKWARD, KIND, S, I, O, A>, a.ctas, a.groups * a.warps * 32, a.smem, st, a);
 }
 
 // FP64 has no kernels of its own for full rows: its tiles are twice as long, its shares spill
@@ -875,12 +878,11 @@ cudaError_t rn_launch(const RnArgs& a, cudaStream_t st) {
     case kRnManyFull: e = rn_launch_staged<BACKWARD, wide ? kRnMany : kRnManyFull, S, I, O, A>(a, st); break;
     case kRnMany: e = rn_launch_staged<BACKWARD, kRnMany, S, I, O, A>(a, st); break;
     default:
-      rn_direct_kernel<BACKWARD, S, I, O, A><<<a.ctas, kRnDirectWarps * 32, 0, st>>>(a);
-      e = cudaGetLastError();
+      e = chain_launch(rn_direct_kernel<BACKWARD, S, I, O, A>, a.ctas, kRnDirectWarps * 32, 0, st, a);
   }
   if (!BACKWARD || e != cudaSuccess || a.ticket || (a.kind != kRnDirect && a.ctas == 1) || !(a.gpost || a.gscale || a.gpre)) return e;
-  rn_reduce_kernel<A><<<(2 * a.chan + 31) / 32, 256, 0, st>>>(a.part, a.ctas, a.chan, a.post, a.scale, a.gpost, a.gscale, a.gpre);
-  return cudaGetLastError();
+  return chain_launch(rn_reduce_kernel<A>, (2 * a.chan + 31) / 32, 256, 0, st, a.part, a.ctas, a.chan, a.post, a.scale, a.gpost,
+                      a.gscale, a.gpre);
 }
 
 }  // namespace
