@@ -58,3 +58,38 @@ def test_training_lowers_the_loss(state):
     assert np.all(np.isfinite(losses))
     # the teacher has the same form: most of the variance is learned in 60 steps of 5e-3
     assert np.mean(losses[-5:]) < 0.5 * losses[0]
+
+
+def test_a_step_in_a_cuda_graph():
+    # the operators only enqueue kernels, so a training step can be captured and replayed
+    import clebsch_gordan_tensor_racah_gb300 as cg
+    torch.manual_seed(5)
+    plan = cg.ResNormPlan("64x0e+64x1o", act="silu")
+    n, dim, chan = 3000, plan.dim, plan.channels
+    h, z, gout, gy = (torch.randn(n, dim, device="cuda") for _ in range(4))
+    q, gains = torch.randn(n, chan, device="cuda"), [1 + 0.1 * torch.randn(chan, device="cuda") for _ in range(3)]
+    opt = cg.AdamW([chan] * 3, state="8bit")
+
+    def step(params, state):
+        out, y = cg.cgtp_resnorm_forward(plan, h, z, q, post=params[0], scale=params[1], pre=params[2])
+        grads = cg.cgtp_resnorm_backward(plan, gout, gy, out, z, q, post=params[0], scale=params[1], pre=params[2])
+        clip = cg.cgtp_grad_norm(opt, list(grads[3:]), 1.0)
+        cg.cgtp_adamw_step(opt, params, list(grads[3:]), state, lr=1e-2, clip=clip, seed=1)
+        return out, y, grads[0], grads[1], grads[2]
+
+    eager, captured = [g.clone() for g in gains], [g.clone() for g in gains]
+    s_eager, s_captured = opt.new_state(), opt.new_state()
+    for _ in range(3):
+        want = step(eager, s_eager)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        got = step(captured, s_captured)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert all(torch.equal(a, b) for a, b in zip(eager, captured))
+    assert all(torch.equal(s_eager[k], s_captured[k]) for k in s_eager)
