@@ -131,7 +131,8 @@ int lay_out(RnArgs* a, bool backward, int rows) {
 //     128x0e+128x1o+128x2e backward: two (4 warps) 62%, one (9 warps) 90%.
 void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
   const int n_rows = backward ? kRnBackward : kRnForward, ep = es_param(p);
-  const int factors = round16(2 * p->chan * ep);
+  const bool listed = p->blocks.size() <= kRnInline;
+  const int factors = round16(2 * p->chan * ep) + (listed ? 0 : round16(p->blocks.size() * sizeof(RnBlock)));
   double best = 0.0;
   int fewest = 1;
   while (fewest < 4 && fewest < p->widest) fewest *= 2;
@@ -143,7 +144,7 @@ void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
     int rows = abreast;
     for (int i = 0; i < n_rows; ++i)
       while (a->t[i].ptr && a->t[i].ld == a->t[i].width && (int64_t(rows) * a->t[i].width * a->t[i].es) % 16) rows *= 2;
-    bool held = p->blocks.size() <= kRnInline, fills = held;
+    bool held = true, fills = listed;
     double work = 0.0;
     for (const RnBlock& b : p->blocks) {
       const int share = rn_share(b.D, b.mul, team);
@@ -185,10 +186,11 @@ void deal(const cgtp_resnorm_s* p, RnArgs* a, bool backward) {
   // (a backward of so few rows runs in one CTA, whose sums are the sums over all rows)
   const bool one = backward && tiles <= a->groups;
   a->groups = static_cast<int>(one ? tiles : (tiles + p->num_sms * turns - 1) / (p->num_sms * turns));
+  a->table_at = a->groups * a->group_bytes + round16(2 * p->chan * ep);
   a->smem = a->groups * a->group_bytes + factors;
   a->tiles = tiles;
   a->ctas = one ? 1 : static_cast<int>(std::min<int64_t>(a->tiles, p->num_sms));
-  for (size_t i = 0; i < p->blocks.size(); ++i)
+  for (size_t i = 0; listed && i < p->blocks.size(); ++i)
     a->few[i].code = rn_code(a->few[i].D, rn_share(a->few[i].D, a->few[i].mul, a->lanes));
 }
 

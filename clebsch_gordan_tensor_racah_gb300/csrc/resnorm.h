@@ -43,7 +43,7 @@ struct RnArgs {
   RnRows t[kRnMaxRows];
   const void *post = nullptr, *scale = nullptr, *pre = nullptr;
   void *gpost = nullptr, *gscale = nullptr, *gpre = nullptr;
-  const RnBlock* blocks = nullptr;   // device table, or `few` where they fit there
+  const RnBlock* blocks = nullptr;   // device table; also in `few` where they fit there
   RnBlock few[kRnInline];
   void* part = nullptr;       // [CTAs][2][C] partial sums: of a(q) P, of gpre
   unsigned* ticket = nullptr; // CTAs that are done, where the last one adds the partial sums (null: another launch does)
@@ -58,7 +58,7 @@ struct RnArgs {
   int warps = 1;              // warps of a group
   int groups = 1;             // groups of a CTA
   int rows = 1;               // rows of a tile
-  int stage_bytes = 0, group_bytes = 0, smem = 0, ctas = 1;
+  int stage_bytes = 0, group_bytes = 0, table_at = 0, smem = 0, ctas = 1;
 };
 
 }  // namespace cgtp
@@ -89,16 +89,22 @@ CGTP_RN_DECLARE(bf16)
 CGTP_RN_DECLARE(bf16s)
 #undef CGTP_RN_DECLARE
 
+#ifdef __CUDACC__
+#define CGTP_HOST_DEVICE __host__ __device__
+#else
+#define CGTP_HOST_DEVICE
+#endif
+
 // Channels of a block that a thread keeps in registers: mul / lanes rounded up to a share that the
 // kernels have code for (at most about 20 values), or 0.
-inline int rn_share(int D, int mul, int lanes) {
+CGTP_HOST_DEVICE inline int rn_share(int D, int mul, int lanes) {
   const int share = mul <= lanes ? 1 : mul <= 2 * lanes ? 2 : mul <= 4 * lanes ? 4 : mul <= 8 * lanes ? 8 : 0;
   return share <= (D == 1 ? 8 : D <= 5 ? 4 : D <= 9 ? 2 : 1) ? share : 0;
 }
 // Number of the code for blocks of D components and a share: CGTP_RN_HELD counts the same way.
-constexpr int rn_code(int D, int share) {
-  const int first[8] = {0, 4, 7, 10, 12, 14, 15, 16};
-  return first[D / 2] + (share >= 8 ? 3 : share >= 4 ? 2 : share - 1);
+CGTP_HOST_DEVICE constexpr int rn_code(int D, int share) {
+  return (D <= 3 ? (D == 1 ? 0 : 4) : D <= 7 ? (D == 5 ? 7 : 10) : D == 9 ? 12 : 14 + (D - 11) / 2) +
+         (share >= 8 ? 3 : share >= 4 ? 2 : share - 1);
 }
 
 // Partial sums (CTAs x 2 C) that the last CTA of a backward adds itself: up to 16 loads a thread, which is

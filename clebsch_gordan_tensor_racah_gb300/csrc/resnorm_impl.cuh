@@ -492,10 +492,8 @@ __device__ __forceinline__ void rn_block_any(const RnArgs& a, const RnBlock b,
 }
 
 // A block by its number of components and the thread's share (rn_share).
-template <int D, int K>
-constexpr int kRnCode = rn_code(D, K);
 #define CGTP_RN_CASE(D, K) \
-  case kRnCode<D, K>: HELD(D, K); break;
+  case rn_code(D, K): HELD(D, K); break;
 #define CGTP_RN_HELD                                                                                          \
   CGTP_RN_CASE(1, 1) CGTP_RN_CASE(1, 2) CGTP_RN_CASE(1, 4) CGTP_RN_CASE(1, 8) CGTP_RN_CASE(3, 1)             \
   CGTP_RN_CASE(3, 2) CGTP_RN_CASE(3, 4) CGTP_RN_CASE(5, 1) CGTP_RN_CASE(5, 2) CGTP_RN_CASE(5, 4)             \
@@ -514,16 +512,22 @@ constexpr int kRnCode = rn_code(D, K);
   }
 
 template <int KIND, typename Row, typename A, bool STAGED, bool ONE, bool WHOLE>
-__device__ __forceinline__ void rn_row(const RnArgs& a, const Row& row, const RnFactors<STAGED, A>& f,
+__device__ __forceinline__ void rn_row(const RnArgs& a, const RnBlock* table, const Row& row, const RnFactors<STAGED, A>& f,
                                        RnTeam<A, ONE, WHOLE>& team) {
   for (int i = 0; i < a.n_blocks; ++i) {
-    if constexpr (STAGED) {
-      const RnBlock& b = a.few[i];
 #define HELD(D, K) rn_block_held<D, K, KIND != kRnOne && KIND != kRnMany>(a, b, row, f, team)
+    if constexpr (KIND == kRnOne || KIND == kRnMany) {
+      // many blocks come from the table in shared memory, others from the kernel's parameters
+      RnBlock b;
+      if (table) b = table[i];
+      else b = a.few[i];
+      switch (b.code) { CGTP_RN_HELD }
+    } else if constexpr (STAGED) {
+      const RnBlock& b = a.few[i];
       switch (b.code) { CGTP_RN_HELD }
 #undef HELD
     } else {
-      const RnBlock b = a.blocks[i];
+      const RnBlock b = table[i];
 #define ANY(D) rn_block_any<D>(a, b, row, f, team)
       CGTP_RN_ANY
 #undef ANY
@@ -720,6 +724,14 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
     factors[a.chan + i] = read.pre_at(i);
   }
   const RnFactors<true, A> f{factors, nullptr, factors + a.chan};
+  RnBlock* table = nullptr;
+  if (!FULL && a.n_blocks > kRnInline) {
+    table = reinterpret_cast<RnBlock*>(shared + a.table_at);
+    for (int i = threadIdx.x; i < a.n_blocks; i += blockDim.x) {
+      table[i] = a.blocks[i];
+      table[i].code = rn_code(table[i].D, rn_share(table[i].D, table[i].mul, a.lanes));
+    }
+  }
   const int abreast = ONE ? 32 / a.lanes : 1, sub = ONE ? tg / a.lanes : 0;
   RnTeam<A, ONE, WHOLE> team{tg - sub * a.lanes, a.lanes, warps, 1 + g, scratch, 0};
   constexpr int first_out = kRnInputs[BACKWARD], last = BACKWARD ? kRnBackward : kRnForward;
@@ -763,12 +775,12 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
             rn_in<S>(a, kRnGout, stage, j), rn_in<S>(a, kRnX, stage, j),  rn_in<I>(a, kRnGy, stage, j),
             rn_in<I>(a, kRnBz, stage, j),   rn_in<I>(a, kRnBq, stage, j), rn_in<S>(a, kRnGh, stage, j),
             rn_in<O>(a, kRnGz, stage, j),   rn_in<O>(a, kRnGq, stage, j), part + sub * 2 * a.chan, j < count};
-        rn_row<KIND>(a, row, f, team);
+        rn_row<KIND>(a, table, row, f, team);
       } else {
         const RnForwardRow<S, I, O> row{rn_in<S>(a, kRnH, stage, j), rn_in<I>(a, kRnZ, stage, j),
                                         rn_in<I>(a, kRnQ, stage, j), rn_in<S>(a, kRnOut, stage, j),
                                         rn_in<O>(a, kRnY, stage, j)};
-        rn_row<KIND>(a, row, f, team);
+        rn_row<KIND>(a, table, row, f, team);
       }
     }
     team.sync();
@@ -850,11 +862,11 @@ __global__ void __launch_bounds__(kRnDirectWarps * 32) rn_direct_kernel(const __
       const RnBackwardRow<S, I, O, A> row{rn_at<S>(a, kRnGout, n), rn_at<S>(a, kRnX, n), rn_at<I>(a, kRnGy, n),
                                           rn_at<I>(a, kRnBz, n),   rn_at<I>(a, kRnBq, n), rn_at<S>(a, kRnGh, n),
                                           rn_at<O>(a, kRnGz, n),   rn_at<O>(a, kRnGq, n), part, true};
-      rn_row<kRnDirect>(a, row, f, team);
+      rn_row<kRnDirect>(a, a.blocks, row, f, team);
     } else {
       const RnForwardRow<S, I, O> row{rn_at<S>(a, kRnH, n), rn_at<I>(a, kRnZ, n), rn_at<I>(a, kRnQ, n),
                                       rn_at<S>(a, kRnOut, n), rn_at<O>(a, kRnY, n)};
-      rn_row<kRnDirect>(a, row, f, team);
+      rn_row<kRnDirect>(a, a.blocks, row, f, team);
     }
   }
 }

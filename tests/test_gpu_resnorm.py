@@ -18,6 +18,7 @@ pytestmark = pytest.mark.gpu
 
 K = 64
 MANY = "+".join(["4x0e", "3x1o", "2x2e"] * 14)
+MORE = "+".join(["4x0e", "3x1o", "2x2e", "40x0e", "33x1o", "1x7o"] * 13)
 IRREPS = ["128x0e+128x1o+128x2e", "64x0e+64x1o+64x2e", "128x0e+128x3o", "8x0e+8x1o", "1x0e", "1x3o", "33x0e+17x1o+5x2e", "32x0e+32x1o+32x2e+32x3o", "3x7o+2x4e+1x0e+5x6e+2x5o",
           "300x0e", "16x0e+16x1o+16x2e+16x3o+16x4e+16x5o+16x6e+16x7o"]
 KINDS = ["f32", "f64", "bf16", "bf16s"]
@@ -157,7 +158,7 @@ def test_matches_oracle(irreps, kind):
         check(irreps, kind, n)
 
 
-@pytest.mark.parametrize("irreps", ["700x0e+700x1o+701x2e", "5000x0e", MANY, "64x0e+64x1o+64x2e+64x3o+64x4e+64x5o+64x6e+64x7o"])
+@pytest.mark.parametrize("irreps", ["700x0e+700x1o+701x2e", "5000x0e", MANY, MORE, "64x0e+64x1o+64x2e+64x3o+64x4e+64x5o+64x6e+64x7o"])
 def test_wide_rows_and_many_blocks(irreps):
     check(irreps, "f32", 9)
     check(irreps, "bf16", 9, layout="range")
@@ -186,7 +187,7 @@ def test_parts(act, has_h, has_z, pre_norm, post_norm):
 
 @pytest.mark.parametrize("irreps,n", [
     ("64x0e+64x1o+64x2e", 5001), ("128x0e+128x1o+128x2e", 3001), ("128x0e+128x3o", 3003), ("16x0e+16x1o+16x7o", 5003),
-    ("8x0e+8x1o", 40001), ("33x0e+17x1o+5x2e", 20001), ("1024x0e", 1001), ("3x1o", 30001)])
+    ("8x0e+8x1o", 40001), ("33x0e+17x1o+5x2e", 20001), ("1024x0e", 1001), ("3x1o", 30001), (MORE, 301), (MANY, 5001)])
 @pytest.mark.parametrize("kind,layout", [("f32", "plain"), ("bf16", "range"), ("bf16s", "plain"), ("f32", "odd")])
 def test_more_rows_than_one_turn_of_the_grid(irreps, n, kind, layout):
     # every group takes several tiles, with a last one that is not full.  Sums over rows have up to 250
