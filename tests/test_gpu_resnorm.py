@@ -187,7 +187,7 @@ def test_parts(act, has_h, has_z, pre_norm, post_norm):
 
 @pytest.mark.parametrize("irreps,n", [
     ("64x0e+64x1o+64x2e", 5001), ("128x0e+128x1o+128x2e", 3001), ("128x0e+128x3o", 3003), ("16x0e+16x1o+16x7o", 5003),
-    ("8x0e+8x1o", 40001), ("33x0e+17x1o+5x2e", 20001), ("1024x0e", 1001), ("3x1o", 30001), (MORE, 301), (MANY, 5001)])
+    ("8x0e+8x1o", 40001), ("33x0e+17x1o+5x2e", 20001), ("1024x0e", 1001), ("3x1o", 30001), ("4x0e", 1003), ("2x0e+2x1o", 777), (MORE, 301), (MANY, 5001)])
 @pytest.mark.parametrize("kind,layout", [("f32", "plain"), ("bf16", "range"), ("bf16s", "plain"), ("f32", "odd")])
 def test_more_rows_than_one_turn_of_the_grid(irreps, n, kind, layout):
     # every group takes several tiles, with a last one that is not full.  Sums over rows have up to 250
