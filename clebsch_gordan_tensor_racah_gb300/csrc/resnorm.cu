@@ -381,6 +381,7 @@ cgtp_status cgtp_resnorm_backward(cgtp_resnorm p, int64_t N, const void* gout, i
       }
     return CGTP_OK;
   }
+  if (!z) a.alpha = 1.0, a.alpha_f = 1.0f;   // the stream is h itself
   set(&a.t[kRnGout], gout, ld_gout, p->dim, es);
   set(&a.t[kRnGy], gy, ld_gy, p->dim, es);
   set(&a.t[kRnX], a.pre_norm ? x : nullptr, ld_x, p->dim, es);

@@ -161,7 +161,7 @@ def cgtp_resnorm_backward(plan, gout, gy, x, z=None, q=None, post=None, scale=No
                           outs=None, stream=None):
     """(gh, gz, gq, gpost, gscale, gpre) for the gradients gout (or None) and gy of the results.
 
-    x is what the forward returned first.  gz and gq are None without z or a gate; gpost, gscale
+    Without z the stream is h itself and alpha does not enter gh.  x is what the forward returned first.  gz and gq are None without z or a gate; gpost, gscale
     and gpre are None where that factor is.  outs: optional preallocated results in that order
     (column ranges of wider rows are fine for gh, gz and gq)."""
     if stream is not None:

@@ -64,9 +64,10 @@ cgtp_status cgtp_resnorm_device_bytes(cgtp_resnorm plan, int64_t* bytes);
  *      tensors need the alignment of their element only; 16-byte aligned rows
  *      are faster.
  *  h may be NULL (no residual); z may be NULL (then out must be NULL, q, post
- *  and scale are not read, and y is the norm of h); post, scale and pre may be
- *  NULL (factor 1).  q is read unless act is CGTP_ACT_NONE or z is NULL.  y must
- *  be NULL without CGTP_RESNORM_PRE, and given with it.
+ *  and scale are not read, the stream is h itself, without alpha, and y is its
+ *  norm); post, scale and pre may be NULL (factor 1).  q is read unless act is
+ *  CGTP_ACT_NONE or z is NULL.  y must be NULL without CGTP_RESNORM_PRE, and given
+ *  with it.
  *  Outputs may not overlap inputs.  N = 0 is allowed and launches nothing; N < 2^30.
  */
 cgtp_status cgtp_resnorm_forward(cgtp_resnorm plan, int64_t N, const void* h, int64_t ld_h, const void* z,
@@ -77,8 +78,8 @@ cgtp_status cgtp_resnorm_forward(cgtp_resnorm plan, int64_t N, const void* h, in
  * cgtp_resnorm_backward -- adjoint for gout [N,dim] (NULL: zero) and gy [N,dim]
  *  (given exactly with CGTP_RESNORM_PRE).  x is the forward's `out`, or h when z is NULL;
  *  it is read for the norm of y only and may be NULL without CGTP_RESNORM_PRE.
- *  gh [N,dim] (NULL: not wanted), gz [N,dim] and gq [N,C] (given exactly when z is,
- *  and q is read); gpost, gscale, gpre [C] (NULL: not wanted; a sum over the N
+ *  gh [N,dim] (NULL: not wanted; alpha enters it only where z is given), gz [N,dim]
+ *  and gq [N,C] (given exactly when z is, and q is read); gpost, gscale, gpre [C] (NULL: not wanted; a sum over the N
  *  rows in a fixed order, zero for N = 0).  A NULL factor's gradient may be asked for.
  */
 cgtp_status cgtp_resnorm_backward(cgtp_resnorm plan, int64_t N, const void* gout, int64_t ld_gout, const void* gy,

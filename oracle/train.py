@@ -86,7 +86,7 @@ def resnorm_backward(irreps, gout, gy, x, z=None, q=None, post=None, scale=None,
             w = k * pre[c][:, None]
             g = g + p * w - p ** 3 * b * (w * b).mean(axis=(1, 2), keepdims=True)
             gpre[c] = (p * b * k).sum(axis=(0, 2))
-        gh[:, e] = alpha * g.reshape(n, mul * d)
+        gh[:, e] = (1.0 if z is None else alpha) * g.reshape(n, mul * d)     # without z the stream is h itself
         if z is None:
             continue
         b = z[:, e].reshape(n, mul, d)
