@@ -9,6 +9,9 @@
 //   gq_c = scale post a'(q) P_c,   A_c = sum_n a(q) P_c,   gpost = scale A,   gscale = post A,
 //   gpre_c = sum_n p sum_m gy out.
 //
+// Powers of p and r are never formed alone: d = gout + p (pre gy - out (p (p S / n_b))), so that a block of zeros
+// under a small eps, or a block of tiny elements, gives gradients as large as they are and no inf * 0.
+//
 // A thread owns whole channels of a row (u, u + lanes, ... of every block), so the sums over m
 // (gates, parameter gradients) stay inside a thread and the only exchange is the block sum of an
 // rms.  A channel's 2l+1 components lie side by side, so reading channel by channel would
@@ -342,7 +345,7 @@ __device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b,
   team.sum(s);
   if (pre_norm) {
     p = rn_rsqrt(s[0] * inv_n + eps);
-    kx = p * p * p * inv_n * s[1];
+    kx = p * (p * (s[1] * inv_n));   // times p below
   }
   if (post_norm) r = rn_rsqrt(s[2] * inv_n + eps);
   A along[1] = {A(0)}, w[K];   // sum over the block of w d z r
@@ -351,13 +354,12 @@ __device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b,
     const int u = team.t + k * team.stride(), c = b.coff + u;
     w[k] = A(0);
     if (FULL || u < b.mul) {
-      const A gain = p * pre[k];
       if (has_g) {
 #pragma unroll
-        for (int m = 0; m < D; ++m) d[k][m] = rn_get<A>(g + u * D + m) + (gain * d[k][m] - kx * xv[k][m]);
+        for (int m = 0; m < D; ++m) d[k][m] = rn_get<A>(g + u * D + m) + p * (pre[k] * d[k][m] - kx * xv[k][m]);
       } else {
 #pragma unroll
-        for (int m = 0; m < D; ++m) d[k][m] = gain * d[k][m] - kx * xv[k][m];
+        for (int m = 0; m < D; ++m) d[k][m] = p * (pre[k] * d[k][m] - kx * xv[k][m]);
       }
       if (row.live && pre_norm) row.part[a.chan + c] += p * xy[k];
       if (has_gh) {
@@ -385,7 +387,7 @@ __device__ __forceinline__ void rn_block_held(const RnArgs& a, const RnBlock b,
   A kz = A(0);
   if (post_norm) {
     team.sum(along);
-    kz = r * r * inv_n * along[0];
+    kz = r * (r * (along[0] * inv_n));
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -432,7 +434,7 @@ __device__ __forceinline__ void rn_block_any(const RnArgs& a, const RnBlock b,
     team.sum(s);
     if (a.pre_norm) {
       p = rn_rsqrt(s[0] * inv_n + eps);
-      k = p * p * p * inv_n * s[1];
+      k = p * (p * (s[1] * inv_n));   // times p below
     }
     if (has_z && a.post_norm) r = rn_rsqrt(s[2] * inv_n + eps);
   }
@@ -440,14 +442,14 @@ __device__ __forceinline__ void rn_block_any(const RnArgs& a, const RnBlock b,
   A along[1] = {A(0)};                       // sum over the block of w d z r
   for (int u = team.t; u < b.mul; u += team.lanes) {
     const int c = b.coff + u;
-    const A pre = a.pre_norm ? p * f.pre_at(c) : A(0);
+    const A pre = a.pre_norm ? f.pre_at(c) : A(0);
     A P = A(0), xy = A(0), d[D];
 #pragma unroll
     for (int m = 0; m < D; ++m) {
       A v = has_g ? rn_get<A>(g + u * D + m) : A(0);
       if (a.pre_norm) {
         const A e = rn_get<A>(gy + u * D + m), o = rn_get<A>(x + u * D + m);
-        v += pre * e - k * o;
+        v += p * (pre * e - k * o);
         xy += e * o;
       }
       d[m] = v;
@@ -474,16 +476,16 @@ __device__ __forceinline__ void rn_block_any(const RnArgs& a, const RnBlock b,
   }
   if (!again) return;
   team.sum(along);
-  const A kz = r * r * inv_n * along[0];
+  const A kz = r * (r * (along[0] * inv_n));
   for (int u = team.t; u < b.mul; u += team.lanes) {
     const int c = b.coff + u;
-    const A pre = a.pre_norm ? p * f.pre_at(c) : A(0);
+    const A pre = a.pre_norm ? f.pre_at(c) : A(0);
     A w = r * f.base_at(c);
     if (gated) w *= rn_gate<A>(a.act, rn_get<A>(q + u), nullptr);
 #pragma unroll
     for (int m = 0; m < D; ++m) {
       A v = has_g ? rn_get<A>(g + u * D + m) : A(0);
-      if (a.pre_norm) v += pre * rn_get<A>(gy + u * D + m) - k * rn_get<A>(x + u * D + m);
+      if (a.pre_norm) v += p * (pre * rn_get<A>(gy + u * D + m) - k * rn_get<A>(x + u * D + m));
       const A e = w * v - kz * rn_get<A>(z + u * D + m);
       if (has_gh) rn_put(gh + u * D + m, alpha * v);
       rn_put(gz + u * D + m, e);

@@ -65,3 +65,56 @@ def test_gradients_without_z_against_differences_of_the_kernel(irreps):
             at.append(loss(moved))
         # the loss is a sum of up to 13,500 terms of size 1: 1e-13 of it over 2e-5, and the third derivative x 1e-10
         assert abs((at[0] - at[1]) / 2e-5 - float(gh[i])) < 1e-6, i
+
+
+@pytest.mark.parametrize("irreps", ["8x0e+4x1o", "64x0e+64x1o", "128x0e+128x1o+128x2e", "5000x0e"])
+@pytest.mark.parametrize("eps,size", [(1e-26, 0.0), (1e-30, 0.0), (1e-37, 0.0), (0.0, 1e-13), (0.0, 1e-15), (1e-30, 1e-14)])
+@pytest.mark.parametrize("has_z", [False, True])
+def test_tiny_blocks_and_small_eps(irreps, eps, size, has_z):
+    # The inverse rms p is up to 3e18 here, and every gradient is a number that FP32 holds: where z is given, z is of
+    # size 1 and alpha = 0, so that x = out = w z stays normal or, with w = size, as small as without z.
+    # 64 u of the largest term of a row of d (the terms of d are of size |gout| + 2 p |pre gy|): see the derivation
+    # with the other norm tests.
+    rng = np.random.default_rng(3)
+    plan = _plan(irreps, "f32", alpha=0.0, eps=eps, post_norm=has_z)
+    dim, chan = plan.dim, plan.channels
+    dev = lambda a: torch.from_numpy(a.astype(np.float32)).cuda()  # noqa: E731
+    f = rng.standard_normal
+    x, gout, gy, pre = dev(f((5, dim)) * size), dev(f((5, dim))), dev(f((5, dim))), dev(1 + 0.3 * f(chan))
+    z = dev(f((5, dim))) if has_z else None
+    scale = dev(np.full(chan, size)) if has_z else None
+    if has_z:
+        x = cg().cgtp_resnorm_forward(plan, None, z, scale=scale, pre=pre)[0]
+    got = cg().cgtp_resnorm_backward(plan, gout, gy, x, z, scale=scale, pre=pre, need_gh=True)
+    o = [_num(t) for t in (gout, gy, x)]
+    want = otr.resnorm_backward(irreps, *o, z=None if z is None else _num(z), scale=None if z is None else _num(scale), pre=_num(pre),
+                                alpha=0.0, eps=eps, post_norm=has_z)
+    u = 64 * 2.0 ** -24
+    at = 0
+    for mul, d in otr.parse(irreps):
+        cut = slice(at, at + mul * d)
+        at += mul * d
+        rms = np.sqrt((o[2][:, cut] ** 2).mean(axis=1, keepdims=True) + eps)
+        bound = _rowmax(o[0][:, cut]) + 2 * np.abs(_num(pre)).max() * _rowmax(o[1][:, cut]) / rms * np.maximum(1, _rowmax(o[2][:, cut]) / rms)
+        if not has_z:
+            assert np.all(np.abs(_num(got[0])[:, cut] - want[0][:, cut]) <= u * bound)
+        else:
+            zb = _num(z)[:, cut]
+            r = 1 / np.sqrt((zb ** 2).mean(axis=1, keepdims=True) + eps)
+            assert np.all(np.abs(_num(got[1])[:, cut] - want[1][:, cut]) <= u * 2 * r * size * bound * np.maximum(1, (r * _rowmax(zb)) ** 2) + 1e-37)
+    assert all(g is None or bool(torch.isfinite(g).all()) for g in got)
+
+
+@pytest.mark.parametrize("irreps", ["8x0e+4x1o", "128x0e+128x1o+128x2e", "5000x0e"])
+def test_zero_z_and_small_eps(irreps):
+    # a block of zeros under the rms of z: out = alpha h, gz = r w d with r = 3e19, d = gout: finite
+    plan = _plan(irreps, "f32", pre_norm=False, eps=1e-39)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    h, gout = (torch.randn(4, plan.dim, device="cuda", generator=gen) for _ in range(2))
+    z = torch.zeros_like(h)
+    out, _ = cg().cgtp_resnorm_forward(plan, h, z)
+    assert torch.equal(out, h)
+    gh, gz, _, _, _, _ = cg().cgtp_resnorm_backward(plan, gout, None, out, z)
+    assert torch.equal(gh, gout)
+    want = _num(gout) / np.sqrt(float(np.float32(1e-39)))
+    assert np.all(np.abs(_num(gz) - want) <= 8 * 2.0 ** -24 * np.abs(want))
