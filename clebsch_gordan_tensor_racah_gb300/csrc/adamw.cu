@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kStepThreads) adamw_kernel(const __grid_consta
   unsigned u = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
   if (u >= n_units) return;
   Unit next = units[u];
-  const A coef = clip ? __ldg(clip + 1) : A(1);
+  const A coef = clip ? clip[1] : A(1);
   if (!isfinite(coef)) return;
   StepScalars<A> s = scalars_of<A>(host, coef);
   const A lr_decay = static_cast<A>(host.lr_decay);
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kStepThreads, 3) adamw8_kernel(const __grid_co
   Stage<G>* ring = reinterpret_cast<Stage<G>*>(shared) + (threadIdx.x >> 5) * kRing;
   const unsigned first = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
   if (first >= n_units) return;
-  const float coef = clip ? __ldg(clip + 1) : 1.0f;
+  const float coef = clip ? clip[1] : 1.0f;
   if (!isfinite(coef)) return;
   StepScalars<float> s = scalars_of<float>(host, coef);
   Feed<G, K> feed{ts, units, n_units, gridDim.x * kWarpsPerCta, first, {}, units[first], 0, m_, v_, static_cast<float>(host.lr_decay)};

@@ -1,5 +1,9 @@
 // chain.cuh -- launches that overlap their start with the end of the kernel before them on the stream
 // (programmatic dependent launch), for operators whose small calls are short beside a launch.
+//
+// Such a kernel is resident while the one before it still writes, so nothing that a kernel writes is constant for
+// as long as it runs: gains, coefficients and rows are read by ordinary loads behind the wait, never through
+// the read-only path, whose contract is that the memory does not change during the grid's whole life.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -72,11 +72,11 @@ struct RnFactors {
   const A *post, *scale, *pre;   // STAGED: post holds the product, and no pointer is null
   __device__ __forceinline__ A base_at(int c) const {
     if constexpr (STAGED) return post[c];
-    return (post ? __ldg(post + c) : A(1)) * (scale ? __ldg(scale + c) : A(1));
+    return (post ? post[c] : A(1)) * (scale ? scale[c] : A(1));
   }
   __device__ __forceinline__ A pre_at(int c) const {
     if constexpr (STAGED) return pre[c];
-    return pre ? __ldg(pre + c) : A(1);
+    return pre ? pre[c] : A(1);
   }
 };
 

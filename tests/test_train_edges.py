@@ -1,7 +1,11 @@
 """Operators of a training step at the ends of their ranges, as far as that needs no GPU."""
 
+import os
+import re
+
 import numpy as np
 
+import clebsch_gordan_tensor_racah_gb300 as cg
 from oracle import train as otr
 
 
@@ -24,3 +28,24 @@ def test_oracle_gradient_of_a_norm_without_z_matches_differences():
         num[i] = (loss(h + d) - loss(h - d)) / 2e-6
     # truncation 1e-12 x third derivative, rounding 1e-16 / 1e-6
     assert np.abs(num - gh).max() < 1e-7 * max(1.0, np.abs(gh).max())
+
+
+def _with_headers(path, seen):
+    """Names of a source and of the quoted headers beside it, transitively."""
+    if path in seen or not os.path.exists(path):
+        return seen
+    seen.add(path)
+    for name in re.findall(r'^\s*#\s*include\s+"([^"]+)"', open(path).read(), re.M):
+        _with_headers(os.path.join(os.path.dirname(path), name), seen)
+    return seen
+
+
+def test_kernels_that_start_early_read_nothing_through_the_read_only_path():
+    # a kernel that chain.cuh launches is resident while the one before it writes: its operands change during its life
+    csrc = os.path.join(os.path.dirname(cg.__file__), "csrc")
+    early = [s for s in map(lambda f: os.path.join(csrc, f), sorted(os.listdir(csrc)))
+             if s.endswith(".cu") and "chain_enter()" in "".join(open(p).read() for p in _with_headers(s, set()) if not p.endswith("chain.cuh"))]
+    assert any(s.endswith("adamw.cu") for s in early) and any(s.endswith("resnorm_f32_bwd.cu") for s in early)
+    for path in set().union(*(_with_headers(s, set()) for s in early)):
+        code = re.sub(r"//[^\n]*|/\*.*?\*/", "", open(path).read(), flags=re.S)
+        assert not re.search(r"__ldg\s*\(|ld\.global(\.\w+)*\.nc|__restrict__", code), path
