@@ -784,7 +784,7 @@ cgtp_status create(cgtp_adamw_s* o, int n, const int64_t* numel, const float* de
   o->ticket = static_cast<unsigned*>(o->base);
   o->units_dev = static_cast<Unit*>(o->base) + 1;
   o->part = reinterpret_cast<double*>(static_cast<unsigned char*>(o->base) + b_units);
-  if (cudaMemcpy(o->base, units.data(), b_units, cudaMemcpyHostToDevice) != cudaSuccess) {
+  if (!upload(o->base, units.data(), b_units)) {
     cudaGetLastError();
     return fail(CGTP_ECUDA, "optimizer table upload failed");
   }

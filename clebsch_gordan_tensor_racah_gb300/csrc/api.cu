@@ -53,6 +53,10 @@ int smem_cap_cached(const void* kernel) {
   return cap;
 }
 
+bool upload(void* device, const void* host, size_t bytes) {
+  return cudaMemcpy(device, host, bytes, cudaMemcpyHostToDevice) == cudaSuccess && cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess;
+}
+
 int raise_smem_limit(const void* kernel) {
   int dev = 0, optin = 0;
   cudaFuncAttributes fa{};

@@ -183,6 +183,11 @@ int raise_smem_limit(const void* kernel);
 // The same, done once per (kernel, device) and remembered (thread-safe).
 int smem_cap_cached(const void* kernel);
 
+// Copies a table from pageable host memory and waits until it has arrived: cudaMemcpy alone may return once the
+// bytes are staged, with the transfer ordered on the default stream only, and a first call on a stream
+// that does not wait for that one would read what was there before.  False: a CUDA call failed.
+bool upload(void* device, const void* host, size_t bytes);
+
 bool parse_irreps(const char* s, std::vector<Irrep>* out, std::string* err);
 double cg_complex(int j1, int m1, int j2, int m2, int J, int M);
 std::vector<double> real_cg_block(int l1, int l2, int l3);

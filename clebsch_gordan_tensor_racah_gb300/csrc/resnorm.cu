@@ -244,7 +244,7 @@ cgtp_status create(cgtp_resnorm_s* p, const char* irreps) {
   p->ticket = static_cast<unsigned*>(p->base);
   p->blocks_dev = reinterpret_cast<RnBlock*>(static_cast<char*>(p->base) + 16);
   p->part = static_cast<char*>(p->base) + head;
-  if (cudaMemcpy(p->base, table.data(), table.size(), cudaMemcpyHostToDevice) != cudaSuccess) {
+  if (!upload(p->base, table.data(), table.size())) {
     cudaGetLastError();
     return fail(CGTP_ECUDA, "norm table upload failed");
   }

@@ -118,3 +118,25 @@ def test_zero_z_and_small_eps(irreps):
     assert torch.equal(gh, gout)
     want = _num(gout) / np.sqrt(float(np.float32(1e-39)))
     assert np.all(np.abs(_num(gz) - want) <= 8 * 2.0 ** -24 * np.abs(want))
+
+
+def test_first_calls_on_another_stream():
+    # a plan's and an optimizer's tables are there when they are made, whatever stream the first call is on
+    side = torch.cuda.Stream()
+    rng = np.random.default_rng(2)
+    irreps = "+".join(["4x0e", "3x1o", "2x2e"] * 40)       # more blocks than travel in the kernel's parameters
+    numel = [int(v) for v in rng.integers(1, 40000, size=1500)]
+    g = [torch.from_numpy(rng.standard_normal(k)).float().cuda() for k in numel]
+    h, pre = torch.randn(500, otr.sizes(irreps)[0], device="cuda"), torch.ones(otr.sizes(irreps)[1], device="cuda")
+    torch.cuda.synchronize()
+    runs = []
+    for stream in (None, side, side, side):
+        plan = _plan(irreps, "f32")
+        opt = cg().AdamW(numel)
+        clip = cg().cgtp_grad_norm(opt, g, 1.0, stream=stream)
+        y = cg().cgtp_resnorm_forward(plan, h, stream=stream)[1]
+        gpre = cg().cgtp_resnorm_backward(plan, h, h, h, pre=pre, stream=stream)[5]
+        torch.cuda.synchronize()
+        runs.append((clip, y, gpre))
+    for got in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got, runs[0]))
