@@ -115,7 +115,7 @@ cgtp_status upload_layout(const cgtp_plan_s* plan, const LayoutHost& h, LayoutDe
   if (cudaMalloc(&base, std::max<size_t>(buf.size(), 16)) != cudaSuccess)
     return fail(CGTP_ENOMEM, "plan table allocation failed");
   const_cast<cgtp_plan_s*>(plan)->device_bytes += std::max<size_t>(buf.size(), 16);
-  if (cudaMemcpy(base, buf.data(), buf.size(), cudaMemcpyHostToDevice) != cudaSuccess) {
+  if (!upload(base, buf.data(), buf.size())) {
     cudaFree(base);
     return fail(CGTP_ECUDA, "plan table upload failed");
   }

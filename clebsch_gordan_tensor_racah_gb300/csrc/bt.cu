@@ -665,7 +665,7 @@ cgtp_status bt_create(cgtp_plan_s* plan) {
     delete st;
     return fail(CGTP_ENOMEM, "batched-product table allocation failed");
   }
-  if (cudaMemcpy(st->tables, buf.data(), buf.size(), cudaMemcpyHostToDevice) != cudaSuccess) {
+  if (!upload(st->tables, buf.data(), buf.size())) {
     cudaFree(st->tables);
     delete st;
     return fail(CGTP_ECUDA, "batched-product table upload failed");

@@ -251,7 +251,7 @@ cgtp_status cgtp_mixed_plan_create(cgtp_mixed_plan* out, const char* irreps_in1,
     cgtp_mixed_plan_destroy(p);
     return fail(CGTP_ENOMEM, "mixed plan: table allocation failed");
   }
-  if (cudaMemcpy(p->tables, tab.data(), tab.size() * sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) {
+  if (!upload(p->tables, tab.data(), tab.size() * sizeof(int))) {
     cgtp_mixed_plan_destroy(p);
     return fail(CGTP_ECUDA, "mixed plan: table upload failed");
   }

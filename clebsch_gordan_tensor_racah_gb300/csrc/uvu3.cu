@@ -120,7 +120,7 @@ cgtp_status build_v3(cgtp_plan_s* plan) {
   void* base = nullptr;
   if (cudaMalloc(&base, buf.size()) != cudaSuccess) return fail(CGTP_ENOMEM, "plan table allocation failed");
   plan->device_bytes += buf.size();
-  if (cudaMemcpy(base, buf.data(), buf.size(), cudaMemcpyHostToDevice) != cudaSuccess) {
+  if (!upload(base, buf.data(), buf.size())) {
     cudaFree(base);
     return fail(CGTP_ECUDA, "plan table upload failed");
   }

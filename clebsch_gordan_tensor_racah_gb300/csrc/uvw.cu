@@ -1118,7 +1118,7 @@ cgtp_status uvw_create(cgtp_plan_s* plan) {
   const size_t o_f3 = put(f3.data(), f3.size() * sizeof(Item));
   if (cudaMalloc(&st->tables, buf.size()) != cudaSuccess) return fail(CGTP_ENOMEM, "uvw tables");
   plan->device_bytes += buf.size();
-  cudaMemcpy(st->tables, buf.data(), buf.size(), cudaMemcpyHostToDevice);
+  if (!upload(st->tables, buf.data(), buf.size())) return fail(CGTP_ECUDA, "uvw table upload failed");
   auto at = [&](size_t o) { return static_cast<unsigned char*>(st->tables) + o; };
   st->paths = reinterpret_cast<UvwPath*>(at(o_paths));
   st->fwd_probs = reinterpret_cast<GemmProb*>(at(o_fp)); st->fwd_np = int(fp.size());
@@ -1147,8 +1147,8 @@ cgtp_status uvw_create(cgtp_plan_s* plan) {
     return fail(CGTP_ENOMEM, "uvw error flag allocation failed");
   plan->device_bytes += st->scratch_elems * sizeof(float) + sizeof(float) * kGmSplits * st->K * plan->w_numel +
                         sizeof(int);
-  cudaMemset(st->err_dev, 0, sizeof(int));
   *st->err_host = 0;
+  if (!upload(st->err_dev, st->err_host, sizeof(int))) return fail(CGTP_ECUDA, "uvw error flag upload failed");
   const int np_max = std::max(std::max(st->fwd_np, st->pre_np), std::max(st->gx_np, st->gm_np));
   if (gemm_smem(np_max) > 113 * 1024)  // two CTAs per SM
     return fail(CGTP_EUNSUPPORTED, "uvw plan has too many GEMM problems for the tile table");

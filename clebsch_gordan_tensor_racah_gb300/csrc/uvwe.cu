@@ -561,7 +561,7 @@ cgtp_status uvwe_create(cgtp_plan_s* plan) {
     delete st;
     return fail(CGTP_ENOMEM, "per-edge uvw table allocation failed");
   }
-  if (cudaMemcpy(st->tables, buf.data(), buf.size(), cudaMemcpyHostToDevice) != cudaSuccess) {
+  if (!upload(st->tables, buf.data(), buf.size())) {
     cudaFree(st->tables);
     delete st;
     return fail(CGTP_ECUDA, "per-edge uvw table upload failed");

@@ -49,3 +49,12 @@ def test_kernels_that_start_early_read_nothing_through_the_read_only_path():
     for path in set().union(*(_with_headers(s, set()) for s in early)):
         code = re.sub(r"//[^\n]*|/\*.*?\*/", "", open(path).read(), flags=re.S)
         assert not re.search(r"__ldg\s*\(|ld\.global(\.\w+)*\.nc|__restrict__", code), path
+
+
+def test_tables_are_complete_when_a_plan_is_returned():
+    # a synchronous copy from pageable memory may return before it has arrived, and orders only the default stream behind it:
+    # every table goes through upload(), which waits
+    csrc = os.path.join(os.path.dirname(cg.__file__), "csrc")
+    calls = [(f, m) for f in sorted(os.listdir(csrc)) if f.endswith((".cu", ".cuh", ".h"))
+             for m in re.findall(r"[^\n]*\b(?:cudaMemcpy|cudaMemset)\s*\([^\n]*", re.sub(r"//[^\n]*", "", open(os.path.join(csrc, f)).read()))]
+    assert [f for f, _ in calls] == ["api.cu"] and "cudaStreamSynchronize(cudaStreamLegacy)" in calls[0][1]
