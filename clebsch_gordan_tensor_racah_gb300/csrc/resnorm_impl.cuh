@@ -49,8 +49,13 @@ __device__ __forceinline__ float rn_put(__nv_bfloat16* p, float v) {
 
 __device__ __forceinline__ float rn_rsqrt(float v) { return rsqrtf(v); }
 __device__ __forceinline__ double rn_rsqrt(double v) { return rsqrt(v); }
-// 1 / (1 + e^-q): exponential and quotient to a few units in the last place, 0 and 1 far out
-__device__ __forceinline__ float rn_sigmoid(float q) { return __fdividef(1.0f, 1.0f + __expf(-q)); }
+// 1 / (1 + e^-q): exponential and reciprocal to a unit in the last place each for every q (the fast exponential's
+// error grows with |q|: 37 units at q = -30); 0 below -87.3, where the value is no normal number
+__device__ __forceinline__ float rn_sigmoid(float q) {
+  float s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + expf(-q)));
+  return s;
+}
 __device__ __forceinline__ double rn_sigmoid(double q) { return 1.0 / (1.0 + exp(-q)); }
 
 // a(q) and, when asked for, a'(q)

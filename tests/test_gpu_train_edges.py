@@ -140,3 +140,22 @@ def test_first_calls_on_another_stream():
         runs.append((clip, y, gpre))
     for got in runs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got, runs[0]))
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_far_gates_keep_their_relative_accuracy(act):
+    # An exponential and a reciprocal (a unit in the last place, 2 u, each), a sum and two products (u each): 8 u; the gradient
+    # s (1 - s) or s (1 + q (1 - s)) has another four roundings.  Both without cancellation for q <= -2 (silu: 1 + q (1 - s)
+    # is below -0.76 there, and the error of q (1 - s) at most 4 times its size).
+    q = torch.linspace(-86.0, 40.0, 4096, device="cuda")[None, :].contiguous()
+    plan = cg().ResNormPlan("4096x0e", act=act, pre_norm=False, post_norm=False)
+    one = torch.ones_like(q)
+    out, _ = cg().cgtp_resnorm_forward(plan, None, one, q)
+    u, x = 2.0 ** -24, _num(q)
+    s = 1 / (1 + np.exp(-x))
+    want = s if act == "sigmoid" else x * s
+    assert (np.abs(_num(out) - want) / np.abs(want)).max() <= 8 * u
+    gq = _num(cg().cgtp_resnorm_backward(plan, one, None, None, one, q, need_gh=False)[2])
+    want = s * (1 - s) if act == "sigmoid" else s * (1 + x * (1 - s))
+    low = x <= -2
+    assert (np.abs(gq - want)[low] / np.abs(want[low])).max() <= (8 + 4 * (1 if act == "sigmoid" else 4)) * u
