@@ -62,7 +62,12 @@ struct Tensors {
 struct Scalars {
   double lr_decay, b1, one_b1, b2, one_b2, rate, root, eps;
   uint32_t key0, key1;
+  int flush;   // move_of<true>
 };
+
+// A v below the smallest normal float adds at most sqrt(2^-126) root = 1.1e-19 root to eps: less than 2^-25 of it, half
+// the rounding of the sum, where eps is at least 4e-12 root (root: 31.6 in the first step of beta2 = 0.999).
+constexpr double kFlushEps = 4e-12;
 
 // Pseudo-random bits of element i (its low 32 bits; key0 holds the high ones too): a Weyl step and two
 // multiply-xorshift rounds, of which the last xorshift is left to the two halves below.
@@ -197,8 +202,9 @@ __device__ __forceinline__ Pair<A> mul_rn(Pair<A> a, A b) {
   return mul_rn(a, Pair<A>{b, b});
 }
 
-// rate m / (sqrt(v) root + eps).  FP32: the move's relative error of a few units matters less than p's own
-// rounding.  FAST: eps is large enough that a v below the smallest normal float counts as zero.
+// rate m / (sqrt(v) root + eps).  FP32: root and reciprocal to a unit in the last place each, the move to a few;
+// p's own rounding is larger unless the move is as large as p.  FAST: a v below the smallest normal float counts as
+// zero (kFlushEps).
 template <bool FAST>
 __device__ __forceinline__ float move_of(float m, float v, float rate, float root, float eps) {
   float s, r;
@@ -219,6 +225,7 @@ template <typename A>
 struct StepScalars {
   A coef, keep, b1, one_b1, b2, one_b2, rate, root, eps;
   uint32_t key0, key1;
+  bool flush;
 };
 
 // One block: p, g, m and v of a lane are there; m is m_scale times mv (a power of two or 1) before b1, and so is v.
@@ -233,8 +240,7 @@ __device__ __forceinline__ void step_values(A (&p)[4], const A (&g)[4], A (&m)[4
     const Pair<A> vn = add_rn(mul_rn(Pair<A>{v[i], v[i + 1]}, b2), mul_rn(mul_rn(gi, gi), s.one_b2));
     m[i] = mn.x, m[i + 1] = mn.y, v[i] = vn.x, v[i + 1] = vn.y;
   }
-  // eps + sqrt(v) for v < 2^-126: 1.1e-19 of 1e-12 is below FP32's rounding
-  if (s.eps >= A(1e-12)) {
+  if (s.flush) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = p[i] * s.keep - move_of<true>(m[i], v[i], s.rate, s.root, s.eps);
   } else {
@@ -289,6 +295,7 @@ __device__ __forceinline__ StepScalars<A> scalars_of(const Scalars& host, A coef
   s.b2 = static_cast<A>(host.b2), s.one_b2 = static_cast<A>(host.one_b2);
   s.rate = static_cast<A>(host.rate), s.root = static_cast<A>(host.root), s.eps = static_cast<A>(host.eps);
   s.key0 = host.key0, s.key1 = host.key1;
+  s.flush = host.flush;
   return s;
 }
 
@@ -875,10 +882,10 @@ cgtp_status cgtp_adamw_step(cgtp_adamw o, void* const* params, const void* const
   if (eight && (!m_exp || !v_exp)) return fail(CGTP_EINVAL, "8-bit states need m_exp and v_exp");
   const uint64_t key = step_key(seed, step);
   const double t = static_cast<double>(step);
+  const double root = 1.0 / std::sqrt(1.0 - std::pow(beta2, t));
   StepArgs a{m, v, static_cast<uint8_t*>(m_exp), static_cast<uint8_t*>(v_exp),
-             Scalars{lr * weight_decay, beta1, 1.0 - beta1, beta2, 1.0 - beta2, lr / (1.0 - std::pow(beta1, t)),
-                     1.0 / std::sqrt(1.0 - std::pow(beta2, t)), eps, static_cast<uint32_t>(key),
-                     static_cast<uint32_t>(key >> 32)},
+             Scalars{lr * weight_decay, beta1, 1.0 - beta1, beta2, 1.0 - beta2, lr / (1.0 - std::pow(beta1, t)), root, eps,
+                     static_cast<uint32_t>(key), static_cast<uint32_t>(key >> 32), eps >= kFlushEps * root},
              clip};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (o->param_dtype == CGTP_F64) return step_all<double, double, false>(o, params, grads, copies, a, st);

@@ -159,3 +159,18 @@ def test_far_gates_keep_their_relative_accuracy(act):
     want = s * (1 - s) if act == "sigmoid" else s * (1 + x * (1 - s))
     low = x <= -2
     assert (np.abs(gq - want)[low] / np.abs(want[low])).max() <= (8 + 4 * (1 if act == "sigmoid" else 4)) * u
+
+
+@pytest.mark.parametrize("state_kind", ["f32", "8bit"])
+@pytest.mark.parametrize("beta2", [0.999, 0.99999])
+def test_small_averages_under_a_small_eps(state_kind, beta2):
+    # From zero states the step is lr |g| / (|g| + eps).  v = (1 - beta2) g^2 just below the smallest normal float keeps
+    # 22 bits, of which the root halves the error; 16 u for the step's other roundings: 2^-20 in all.
+    size = (0.9 * 2.0 ** -126 / (1 - beta2)) ** 0.5
+    for eps in (1e-12, 1e-11, 1e-10, 1e-9):
+        g, p = [torch.full((200,), size, device="cuda")], [torch.zeros(200, device="cuda")]
+        opt = cg().AdamW([200], state=state_kind)
+        cg().cgtp_adamw_step(opt, p, g, opt.new_state(), lr=1e-2, betas=(0.9, beta2), eps=eps, step=1)
+        g64 = float(g[0][0])
+        want = 1e-2 * g64 / (g64 + eps)
+        assert float((p[0].double() + want).abs().max()) <= 2.0 ** -20 * want, (eps, float(p[0][0]), want)
