@@ -221,9 +221,17 @@ __device__ __forceinline__ double move_of(double m, double v, double rate, doubl
   return rate * m / (sqrt(v) * root + eps);
 }
 
+// p (1 - decay) - move.  Decay and move are added before anything is rounded to p's size: 1 - decay alone would lose a
+// decay below 2^-25, and be off by a tenth at 3e-7.  An infinite p stays (decay p is infinite or 0 * inf).
+template <typename A>
+__device__ __forceinline__ A moved(A p, A decay, A move) {
+  const A t = decay * p + move;
+  return fabs(p) < A(INFINITY) ? p - t : p;
+}
+
 template <typename A>
 struct StepScalars {
-  A coef, keep, b1, one_b1, b2, one_b2, rate, root, eps;
+  A coef, decay, b1, one_b1, b2, one_b2, rate, root, eps;
   uint32_t key0, key1;
   bool flush;
 };
@@ -242,10 +250,10 @@ __device__ __forceinline__ void step_values(A (&p)[4], const A (&g)[4], A (&m)[4
   }
   if (s.flush) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = p[i] * s.keep - move_of<true>(m[i], v[i], s.rate, s.root, s.eps);
+    for (int i = 0; i < 4; ++i) p[i] = moved(p[i], s.decay, move_of<true>(m[i], v[i], s.rate, s.root, s.eps));
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = p[i] * s.keep - move_of<false>(m[i], v[i], s.rate, s.root, s.eps);
+    for (int i = 0; i < 4; ++i) p[i] = moved(p[i], s.decay, move_of<false>(m[i], v[i], s.rate, s.root, s.eps));
   }
 }
 
@@ -359,7 +367,7 @@ __global__ void __launch_bounds__(kStepThreads) adamw_kernel(const __grid_consta
     if (u < n_units) next = units[u];
     const G* g = static_cast<const G*>(ts.g[unit.tensor]);
     if (g) {
-      s.keep = A(1) - lr_decay * static_cast<A>(ts.decay[unit.tensor]);
+      s.decay = lr_decay * static_cast<A>(ts.decay[unit.tensor]);
       const int64_t at = (int64_t)unit.block * kBlock + lane * 4;
       A* p = static_cast<A*>(ts.p[unit.tensor]) + at;
       __nv_bfloat16* c = ts.c[unit.tensor] ? static_cast<__nv_bfloat16*>(ts.c[unit.tensor]) + at : nullptr;
@@ -405,7 +413,7 @@ struct __align__(16) Stage {
   __nv_bfloat16* copy;
   unsigned state;       // the first block's place in the states
   int elements;         // from there to the end of the unit
-  float keep;
+  float decay;
   int wide;             // whole blocks at aligned addresses
 };
 
@@ -451,7 +459,7 @@ struct Feed {
     if (lane == 0) {
       st.to = p, st.copy = c;
       st.state = state, st.elements = elements;
-      st.keep = 1.0f - lr_decay * ts.decay[unit.tensor];
+      st.decay = lr_decay * ts.decay[unit.tensor];
       st.wide = wide;
     }
     if (wide) {
@@ -518,7 +526,7 @@ __global__ void __launch_bounds__(kStepThreads, 3) adamw8_kernel(const __grid_co
     const Stage<G>& st = ring[at];
     const uint32_t e_now = e;
     if (done + 1 < filled) e = exponents(ring[at + 1 == kRing ? 0 : at + 1]);
-    s.keep = st.keep;
+    s.decay = st.decay;
     uint32_t e_new = 0;
     const Power power = code_power(static_cast<int>(e_now), lane < 2 ? kMTop : kVTop);   // of lanes 0 to 3
     const int64_t first_place = (int64_t)st.state * kBlock + lane * 4;

@@ -174,3 +174,42 @@ def test_small_averages_under_a_small_eps(state_kind, beta2):
         g64 = float(g[0][0])
         want = 1e-2 * g64 / (g64 + eps)
         assert float((p[0].double() + want).abs().max()) <= 2.0 ** -20 * want, (eps, float(p[0][0]), want)
+
+
+@pytest.mark.parametrize("state_kind,dtype", [("f32", "float32"), ("f32", "float64"), ("8bit", "float32")])
+@pytest.mark.parametrize("lr,wd", [(1e-3, 1e-4), (1e-4, 1e-4), (1e-5, 1e-2), (1e-3, 1e-2)])
+def test_small_decays_act_in_the_mean(state_kind, dtype, lr, wd):
+    # lr wd down to 1e-8, far below the rounding of 1 - lr wd.  The parameters lie in [1, 2) and a moving step of random
+    # size makes the rounding of each new value independent: its standard deviation is 2^-23 / sqrt(12), and the mean over 2^20
+    # elements stays within 5 x 2^-23 / sqrt(12) / 2^10 = 1.7e-10.  The step itself has errors of at most 16 u of its size
+    # that are odd in m: 16 u lr / 2^10 in the mean.
+    k = 1 << 20
+    dtype = getattr(torch, dtype)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    p = [1 + torch.rand(k, device="cuda", generator=gen, dtype=dtype)]
+    opt = cg().AdamW([k], param_dtype=dtype, state=state_kind)
+    state = opt.new_state()
+    if state_kind == "8bit":
+        state["m"].copy_(torch.randint(0, 256, (k,), device="cuda", generator=gen))
+        state["m_exp"].fill_(126)
+        state["v"].fill_(8 * 31)
+        state["v_exp"].fill_(127)
+    else:
+        state["m"].copy_(2 * torch.rand(k, device="cuda", generator=gen, dtype=dtype) - 1)
+        state["v"].fill_(1.0)
+    g = 2 * torch.rand(k, device="cuda", generator=gen, dtype=dtype) - 1
+    m, v = cg().cgtp_adamw_state_values(opt, state)
+    want, _, _ = otr.adamw(_num(p[0]), _num(g), _num(m), _num(v), lr, (0.9, 0.999), 1e-8, wd, 1000000)
+    cg().cgtp_adamw_step(opt, p, [g], state, lr=lr, eps=1e-8, weight_decay=wd, step=1000000)
+    assert abs((_num(p[0]) - want).mean()) <= 1.7e-10 + 16 * 2.0 ** -24 * lr / 2 ** 10
+
+
+def test_infinite_parameters_stay():
+    inf = float("inf")
+    for state_kind in ("f32", "8bit"):
+        for wd in (0.0, 0.1):
+            p = [torch.tensor([inf, -inf, 1.0, float("nan")] * 40, device="cuda")]
+            opt = cg().AdamW([160], state=state_kind)
+            cg().cgtp_adamw_step(opt, p, [torch.ones(160, device="cuda")], opt.new_state(), lr=1e-2, weight_decay=wd, step=1)
+            q = p[0].view(-1, 4)
+            assert bool((q[:, 0] == inf).all()) and bool((q[:, 1] == -inf).all()) and bool(torch.isfinite(q[:, 2]).all()) and bool(torch.isnan(q[:, 3]).all())
