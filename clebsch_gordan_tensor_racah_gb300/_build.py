@@ -91,9 +91,13 @@ def _bake():
 
 
 def _binding_command():
-    """g++ command that builds _binding.so against this machine's torch, or None where it is up to date."""
+    """g++ command that builds _binding.so (under a temporary name) against this machine's torch, or None where it is up
+    to date or there is no torch: the library alone needs none."""
     import sysconfig
-    import torch
+    try:
+        import torch
+    except ImportError:
+        return None
     src = os.path.join(CSRC, "binding.cpp")
     if not _stale(src, BINDING) and os.path.exists(BINDING_STAMP) and open(BINDING_STAMP).read() == torch.__version__:
         return None
@@ -102,11 +106,11 @@ def _binding_command():
            sysconfig.get_paths()["include"], INC]
     lib = os.path.join(root, "lib")
     return ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-            *[f"-I{p}" for p in inc], src, "-o", BINDING, f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+            *[f"-I{p}" for p in inc], src, "-o", BINDING + ".tmp", f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def build(verbose=False, jobs=None):
-    """Compile (incrementally) and link libcgtp.so and _binding.so; returns the library's path."""
+    """Compile (incrementally) and link libcgtp.so and, where torch is there, _binding.so; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     _bake()
@@ -138,6 +142,7 @@ def build(verbose=False, jobs=None):
                     print(out)
     if binding:
         import torch
+        os.replace(BINDING + ".tmp", BINDING)
         with open(BINDING_STAMP, "w") as f:
             f.write(torch.__version__)
     if native or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):

@@ -2,10 +2,14 @@
 
 import os
 import re
+import subprocess
+import sys
 
 import numpy as np
+import pytest
 
 import clebsch_gordan_tensor_racah_gb300 as cg
+from clebsch_gordan_tensor_racah_gb300 import _build
 from oracle import train as otr
 
 
@@ -58,3 +62,33 @@ def test_tables_are_complete_when_a_plan_is_returned():
     calls = [(f, m) for f in sorted(os.listdir(csrc)) if f.endswith((".cu", ".cuh", ".h"))
              for m in re.findall(r"[^\n]*\b(?:cudaMemcpy|cudaMemset)\s*\([^\n]*", re.sub(r"//[^\n]*", "", open(os.path.join(csrc, f)).read()))]
     assert [f for f, _ in calls] == ["api.cu"] and "cudaStreamSynchronize(cudaStreamLegacy)" in calls[0][1]
+
+
+def test_the_library_builds_and_loads_without_torch():
+    # None in sys.modules: importing torch raises ImportError, as on a machine that has none
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "from clebsch_gordan_tensor_racah_gb300 import _build\n"
+            "assert _build.build() == _build.LIB\n"
+            "import clebsch_gordan_tensor_racah_gb300 as cg\n"
+            "assert cg.cgtp_real_cg_block(1, 1, 1) is not None\n")
+    root = os.path.dirname(os.path.dirname(cg.__file__))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_an_interrupted_link_of_the_binding_is_not_up_to_date(tmp_path, monkeypatch):
+    torch = pytest.importorskip("torch")
+    _build.build()
+    monkeypatch.setattr(_build, "BINDING", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(_build, "BINDING_STAMP", str(tmp_path / "stamp"))
+    (tmp_path / "stamp").write_text(torch.__version__)      # of an earlier build with the same torch
+
+    def interrupted(cmd):
+        with open(cmd[cmd.index("-o") + 1], "wb") as f:
+            f.write(b"half")
+        raise RuntimeError("interrupted")
+
+    monkeypatch.setattr(_build, "_run", interrupted)
+    with pytest.raises(RuntimeError, match="interrupted"):
+        _build.build()
+    assert _build._binding_command() is not None
