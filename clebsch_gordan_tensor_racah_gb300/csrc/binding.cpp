@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -53,10 +54,19 @@ double real(PyObject* o) {
 }
 void* address(PyObject* o) { return reinterpret_cast<void*>(static_cast<uintptr_t>(number(o))); }
 
-const at::Tensor& tensor(PyObject* o, at::ScalarType type) {
+// The device of a plan or optimizer.  Its tables are there, and the library launches on the current device: a call
+// needs both to be the same, and every tensor there.
+struct Device {
+  int64_t index;
+  explicit Device(PyObject* o) : index(number(o)) {
+    if (c10::impl::VirtualGuardImpl(c10::DeviceType::CUDA).getDevice().index() != index) throw Misfit();
+  }
+};
+
+const at::Tensor& tensor(PyObject* o, at::ScalarType type, const Device& device) {
   if (!THPVariable_Check(o)) throw Misfit();
   const at::Tensor& t = THPVariable_Unpack(o);
-  if (!t.is_cuda() || t.scalar_type() != type || t.layout() != at::kStrided) throw Misfit();
+  if (!t.is_cuda() || t.get_device() != device.index || t.scalar_type() != type || t.layout() != at::kStrided) throw Misfit();
   return t;
 }
 
@@ -65,17 +75,17 @@ struct Rows {
   void* p = nullptr;
   int64_t ld = 0;
 };
-Rows rows(PyObject* o, at::ScalarType type, int64_t n, int64_t width) {
+Rows rows(PyObject* o, at::ScalarType type, const Device& device, int64_t n, int64_t width) {
   if (o == Py_None) return {};
-  const at::Tensor& t = tensor(o, type);
+  const at::Tensor& t = tensor(o, type, device);
   if (t.dim() != 2 || t.size(0) != n || t.size(1) != width || (t.stride(1) != 1 && width > 1 && n > 0)) throw Misfit();
   if (n <= 1) return {t.data_ptr(), 0};
   if (t.stride(0) < width) throw Misfit();
   return {t.data_ptr(), t.stride(0)};
 }
-void* vector(PyObject* o, at::ScalarType type, int64_t width) {
+void* vector(PyObject* o, at::ScalarType type, const Device& device, int64_t width) {
   if (o == Py_None) return nullptr;
-  const at::Tensor& t = tensor(o, type);
+  const at::Tensor& t = tensor(o, type, device);
   if (t.dim() != 1 || t.size(0) != width || !t.is_contiguous()) throw Misfit();
   return t.data_ptr();
 }
@@ -118,14 +128,20 @@ struct Held {
   }
 };
 
+// field i of a tuple of `size`
+PyObject* field(PyObject* t, Py_ssize_t size, Py_ssize_t i) {
+  if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != size) throw Misfit();
+  return PyTuple_GET_ITEM(t, i);
+}
+
 // ResNormPlan._native
 struct NormPlan {
   cgtp_resnorm handle;
   at::ScalarType stream, in, out, param;
   int64_t dim, chan;
   bool pre_norm, gated;
-  explicit NormPlan(PyObject* t) {
-    if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 9) throw Misfit();
+  Device device;
+  explicit NormPlan(PyObject* t) : device(field(t, 10, 9)) {
     const auto at_ = [&](int i) { return PyTuple_GET_ITEM(t, i); };
     handle = static_cast<cgtp_resnorm>(address(at_(0)));
     stream = type_of(number(at_(1))), in = type_of(number(at_(2))), out = type_of(number(at_(3))), param = type_of(number(at_(4)));
@@ -151,12 +167,12 @@ PyObject* resnorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if (n_args != 10) throw Misfit();
     const NormPlan p(a[0]);
     PyObject* ref = a[1] != Py_None ? a[1] : a[2];
-    const at::Tensor& like = tensor(ref, a[1] != Py_None ? p.stream : p.in);
+    const at::Tensor& like = tensor(ref, a[1] != Py_None ? p.stream : p.in, p.device);
     if (like.dim() != 2) throw Misfit();
     const int64_t n = like.size(0);
-    const Rows h = rows(a[1], p.stream, n, p.dim), z = rows(a[2], p.in, n, p.dim), q = rows(a[3], p.in, n, p.chan);
-    const void *post = vector(a[4], p.param, p.chan), *scale = vector(a[5], p.param, p.chan), *pre = vector(a[6], p.param, p.chan);
-    Rows out = rows(a[7], p.stream, n, p.dim), y = rows(a[8], p.out, n, p.dim);
+    const Rows h = rows(a[1], p.stream, p.device, n, p.dim), z = rows(a[2], p.in, p.device, n, p.dim), q = rows(a[3], p.in, p.device, n, p.chan);
+    const void *post = vector(a[4], p.param, p.device, p.chan), *scale = vector(a[5], p.param, p.device, p.chan), *pre = vector(a[6], p.param, p.device, p.chan);
+    Rows out = rows(a[7], p.stream, p.device, n, p.dim), y = rows(a[8], p.out, p.device, n, p.dim);
     Held held;
     if (a[2] == Py_None) {
       held.same(a[1]);
@@ -184,13 +200,13 @@ PyObject* resnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
     if (n_args != 12) throw Misfit();
     const NormPlan p(a[0]);
-    const at::Tensor& like = tensor(a[1] != Py_None ? a[1] : a[2], a[1] != Py_None ? p.stream : p.in);
+    const at::Tensor& like = tensor(a[1] != Py_None ? a[1] : a[2], a[1] != Py_None ? p.stream : p.in, p.device);
     if (like.dim() != 2) throw Misfit();
     const int64_t n = like.size(0);
-    const Rows gout = rows(a[1], p.stream, n, p.dim), gy = rows(a[2], p.in, n, p.dim), x = rows(a[3], p.stream, n, p.dim),
-               z = rows(a[4], p.in, n, p.dim), q = rows(a[5], p.in, n, p.chan);
+    const Rows gout = rows(a[1], p.stream, p.device, n, p.dim), gy = rows(a[2], p.in, p.device, n, p.dim), x = rows(a[3], p.stream, p.device, n, p.dim),
+               z = rows(a[4], p.in, p.device, n, p.dim), q = rows(a[5], p.in, p.device, n, p.chan);
     const void* factors[3];
-    for (int i = 0; i < 3; ++i) factors[i] = vector(a[6 + i], p.param, p.chan);
+    for (int i = 0; i < 3; ++i) factors[i] = vector(a[6 + i], p.param, p.device, p.chan);
     Held held;
     Rows g[3];      // gh, gz, gq
     void* sums[3];  // gpost, gscale, gpre
@@ -198,8 +214,8 @@ PyObject* resnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int64_t widths[3] = {p.dim, p.dim, p.chan};
     if (a[10] != Py_None) {
       if (!PyTuple_Check(a[10]) || PyTuple_GET_SIZE(a[10]) != 6) throw Misfit();
-      for (int i = 0; i < 3; ++i) g[i] = rows(held.same(PyTuple_GET_ITEM(a[10], i)), types[i], n, widths[i]);
-      for (int i = 0; i < 3; ++i) sums[i] = vector(held.same(PyTuple_GET_ITEM(a[10], 3 + i)), p.param, p.chan);
+      for (int i = 0; i < 3; ++i) g[i] = rows(held.same(PyTuple_GET_ITEM(a[10], i)), types[i], p.device, n, widths[i]);
+      for (int i = 0; i < 3; ++i) sums[i] = vector(held.same(PyTuple_GET_ITEM(a[10], 3 + i)), p.param, p.device, p.chan);
     } else {
       const bool wanted[3] = {PyObject_IsTrue(a[9]) == 1, a[4] != Py_None, a[4] != Py_None && p.gated};
       for (int i = 0; i < 3; ++i) {
@@ -236,8 +252,8 @@ struct Optimizer {
   int64_t state_numel, count;
   const int64_t* numel;
   bool eight;
-  explicit Optimizer(PyObject* t) {
-    if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 7) throw Misfit();
+  Device device;
+  explicit Optimizer(PyObject* t) : device(field(t, 8, 7)) {
     const auto at_ = [&](int i) { return PyTuple_GET_ITEM(t, i); };
     handle = static_cast<cgtp_adamw>(address(at_(0)));
     param = type_of(number(at_(1))), grad = type_of(number(at_(2)));
@@ -258,7 +274,7 @@ void gather(PyObject* list, const Optimizer& o, at::ScalarType type, std::vector
     PyObject* item = is_list ? PyList_GET_ITEM(list, i) : PyTuple_GET_ITEM(list, i);
     (*out)[i] = nullptr;
     if (item == Py_None) continue;
-    const at::Tensor& t = tensor(item, type);
+    const at::Tensor& t = tensor(item, type, o.device);
     if (t.numel() != o.numel[i] || !t.is_contiguous()) throw Misfit();
     (*out)[i] = t.data_ptr();
     if (first && !*first) *first = &t;
@@ -269,9 +285,9 @@ struct StatePointers {
   void *m, *v, *m_exp, *v_exp;
   StatePointers(const Optimizer& o, PyObject* const* a) {
     if (a[0] == Py_None || a[1] == Py_None || (o.eight && (a[2] == Py_None || a[3] == Py_None))) throw Misfit();
-    m = vector(a[0], o.state, o.state_numel), v = vector(a[1], o.state, o.state_numel);
-    m_exp = o.eight ? vector(a[2], at::kByte, o.state_numel / 128) : nullptr;
-    v_exp = o.eight ? vector(a[3], at::kByte, o.state_numel / 128) : nullptr;
+    m = vector(a[0], o.state, o.device, o.state_numel), v = vector(a[1], o.state, o.device, o.state_numel);
+    m_exp = o.eight ? vector(a[2], at::kByte, o.device, o.state_numel / 128) : nullptr;
+    v_exp = o.eight ? vector(a[3], at::kByte, o.device, o.state_numel / 128) : nullptr;
   }
 };
 
@@ -292,7 +308,7 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     }
     const cgtp_status r = lib_step(o.handle, p.data(), const_cast<const void* const*>(g.data()), a[3] == Py_None ? nullptr : c.data(), s.m,
                                    s.v, s.m_exp, s.v_exp, real(a[8]), real(a[9]), real(a[10]), real(a[11]), real(a[12]), number(a[13]),
-                                   seed, vector(a[15], o.param, 2), address(a[16]));
+                                   seed, vector(a[15], o.param, o.device, 2), address(a[16]));
     if (r != CGTP_OK) return PyLong_FromLong(r);
     Py_RETURN_NONE;
   });
@@ -315,7 +331,7 @@ PyObject* grad_norm(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
       result = held.keep(r.object);
       out = r.p;
     } else {
-      out = vector(a[3], o.param, 2);
+      out = vector(a[3], o.param, o.device, 2);
       result = held.same(a[3]);
     }
     const cgtp_status r = lib_norm(o.handle, const_cast<const void* const*>(g.data()), real(a[2]), out, address(a[4]));

@@ -29,12 +29,25 @@ def _dtype(dtype, name, allowed):
     return code
 
 
-def _explain_rows(name, t, dtype, n, width):
+def _here():
+    """The current device: the one that a plan or optimizer is made on."""
+    return torch.device("cuda", torch.cuda.current_device())
+
+
+def _explain_device(device):
+    """Raises where calls of a plan or optimizer of `device` would be launched on another one."""
+    if _here() != device:
+        raise ValueError(f"the plan or optimizer is on {device}, the current device is {_here()}")
+
+
+def _explain_rows(name, t, dtype, n, width, device):
     """Raises where a row tensor (or None) does not fit."""
     if t is None:
         return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != (n, width):
@@ -43,16 +56,18 @@ def _explain_rows(name, t, dtype, n, width):
         raise ValueError(f"{name}: elements of a row must be contiguous and rows must not overlap")
 
 
-def _explain_vector(name, t, dtype, width):
+def _explain_vector(name, t, dtype, width, device):
     """Raises where a contiguous tensor [width] (or None) does not fit."""
     if t is None:
         return
     _ptr(t, name, dtype)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.shape != (width,):
         raise ValueError(f"{name} must have shape ({width},), got {tuple(t.shape)}")
 
 
-def _explain_list(name, tensors, numel, dtype):
+def _explain_list(name, tensors, numel, dtype, device):
     """Raises where a list of tensors (or None) does not fit the optimizer's."""
     if len(tensors) != len(numel):
         raise ValueError(f"{name}: {len(numel)} tensors expected, got {len(tensors)}")
@@ -61,6 +76,8 @@ def _explain_list(name, tensors, numel, dtype):
             continue
         if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
             raise TypeError(f"{name} must be {dtype} CUDA tensors")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
         if t.numel() != k or not t.is_contiguous():
             raise ValueError(f"{name}: a contiguous tensor of {k} elements expected, got {tuple(t.shape)}")
 
@@ -104,6 +121,7 @@ class ResNormPlan:
         h = ctypes.c_void_p()
         _check(lib().cgtp_resnorm_create(ctypes.byref(h), irreps.encode(), code, flags, ACTS[act], float(alpha), float(eps)))
         self._h = h
+        self.device = _here()
         dim, channels, blocks = ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int()
         _check(lib().cgtp_resnorm_info(h, ctypes.byref(dim), ctypes.byref(channels), ctypes.byref(blocks)))
         self.dim, self.channels, self.n_blocks = dim.value, channels.value, blocks.value
@@ -114,7 +132,7 @@ class ResNormPlan:
         self.param_dtype = torch.float32 if half else dtype
         types = [_dtype(t, "dtype", (CGTP_F32, CGTP_F64, CGTP_BF16))
                  for t in (self.stream_dtype, self.in_dtype, self.out_dtype, self.param_dtype)]
-        self._native = (h.value, *types, self.dim, self.channels, int(self.pre_norm), int(act != "none"))
+        self._native = (h.value, *types, self.dim, self.channels, int(self.pre_norm), int(act != "none"), self.device.index)
 
     @property
     def handle(self):
@@ -146,12 +164,13 @@ def cgtp_resnorm_forward(plan, h, z=None, q=None, post=None, scale=None, pre=Non
         raise ValueError("h or z must be given")
 
     def explain():
+        _explain_device(plan.device)
         n, dim, chan = ref.shape[0], plan.dim, plan.channels
         for name, t, dtype, width in (("h", h, plan.stream_dtype, dim), ("z", z, plan.in_dtype, dim), ("q", q, plan.in_dtype, chan),
                                       ("out", out, plan.stream_dtype, dim), ("y", y, plan.out_dtype, dim)):
-            _explain_rows(name, t, dtype, n, width)
+            _explain_rows(name, t, dtype, n, width, plan.device)
         for name, t in (("post", post), ("scale", scale), ("pre", pre)):
-            _explain_vector(name, t, plan.param_dtype, chan)
+            _explain_vector(name, t, plan.param_dtype, chan, plan.device)
 
     r = _binding.resnorm_forward(plan._native, h, z, q, post, scale, pre, out, y, _current(ref))
     return r if type(r) is tuple else _result(r, explain)
@@ -172,14 +191,15 @@ def cgtp_resnorm_backward(plan, gout, gy, x, z=None, q=None, post=None, scale=No
     outs = None if outs is None else tuple(outs)
 
     def explain():
+        _explain_device(plan.device)
         n, dim, chan = ref.shape[0], plan.dim, plan.channels
         gh, gz, gq, *sums = outs or (None,) * 6
         for name, t, dtype, width in (("gout", gout, plan.stream_dtype, dim), ("gy", gy, plan.in_dtype, dim),
                                       ("x", x, plan.stream_dtype, dim), ("z", z, plan.in_dtype, dim), ("q", q, plan.in_dtype, chan),
                                       ("gh", gh, plan.stream_dtype, dim), ("gz", gz, plan.out_dtype, dim), ("gq", gq, plan.out_dtype, chan)):
-            _explain_rows(name, t, dtype, n, width)
+            _explain_rows(name, t, dtype, n, width, plan.device)
         for name, t in zip(("post", "scale", "pre", "gpost", "gscale", "gpre"), (post, scale, pre, *sums)):
-            _explain_vector(name, t, plan.param_dtype, chan)
+            _explain_vector(name, t, plan.param_dtype, chan, plan.device)
 
     r = _binding.resnorm_backward(plan._native, gout, gy, x, z, q, post, scale, pre, need_gh, outs, _current(ref))
     return r if type(r) is tuple else _result(r, explain)
@@ -210,13 +230,14 @@ class AdamW:
                                        _dtype(self.grad_dtype, "grad_dtype", (CGTP_F32, CGTP_F64, CGTP_BF16)),
                                        STATES[state]))
         self._h = h
+        self.device = _here()
         total = ctypes.c_int64()
         _check(lib().cgtp_adamw_info(h, ctypes.byref(total)))
         self.state_numel = total.value
         self._sizes = sizes                     # read by the native calls
         self._native = (h.value, _dtype(self.param_dtype, "param_dtype", (CGTP_F32, CGTP_F64)),
                         _dtype(self.grad_dtype, "grad_dtype", (CGTP_F32, CGTP_F64, CGTP_BF16)), STATES[state],
-                        self.state_numel, n, ctypes.addressof(sizes))
+                        self.state_numel, n, ctypes.addressof(sizes), self.device.index)
 
     @property
     def handle(self):
@@ -239,17 +260,18 @@ class AdamW:
 
     def explain(self, lists, state=None, clip=None):
         """Raises what is wrong with the arguments of a step."""
+        _explain_device(self.device)
         for name, tensors, dtype in lists:
             if tensors is not None:
-                _explain_list(name, tensors, self.numel, dtype)
+                _explain_list(name, tensors, self.numel, dtype, self.device)
         if state is not None:
             n, eight = self.state_numel, self.state == "8bit"
             for name in ("m", "v") + (("m_exp", "v_exp") if eight else ()):
                 if state[name] is None:
                     raise ValueError(f"state {name} is missing")
                 _explain_vector("state " + name, state[name], torch.uint8 if eight else self.param_dtype,
-                                n // STATE_BLOCK if name.endswith("exp") else n)
-        _explain_vector("norm and coefficient", clip, self.param_dtype, 2)
+                                n // STATE_BLOCK if name.endswith("exp") else n, self.device)
+        _explain_vector("norm and coefficient", clip, self.param_dtype, 2, self.device)
 
     def __del__(self):
         h = getattr(self, "_h", None)

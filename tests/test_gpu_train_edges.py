@@ -213,3 +213,23 @@ def test_infinite_parameters_stay():
             cg().cgtp_adamw_step(opt, p, [torch.ones(160, device="cuda")], opt.new_state(), lr=1e-2, weight_decay=wd, step=1)
             q = p[0].view(-1, 4)
             assert bool((q[:, 0] == inf).all()) and bool((q[:, 1] == -inf).all()) and bool(torch.isfinite(q[:, 2]).all()) and bool(torch.isnan(q[:, 3]).all())
+
+
+def test_calls_on_another_device_than_the_plans_are_refused():
+    # a plan that says that it lives on a second device: its tables would not be where the current device launches
+    def moved(o):
+        o.device, o._native = torch.device("cuda", 1), o._native[:-1] + (1,)
+        return o
+
+    m = cg()
+    plan, opt, full = m.ResNormPlan("4x0e+4x1o"), m.AdamW([7], state="8bit"), m.AdamW([7])
+    h, g, state = torch.ones(5, 16, device="cuda"), [torch.ones(7, device="cuda")], opt.new_state()
+    assert plan.device == opt.device == h.device
+    m.cgtp_resnorm_forward(plan, h)
+    plan, opt, full = moved(plan), moved(opt), moved(full)
+    for call in (lambda: m.cgtp_resnorm_forward(plan, h), lambda: m.cgtp_resnorm_backward(plan, h, h, h),
+                 lambda: m.cgtp_grad_norm(opt, g, 1.0), lambda: m.cgtp_adamw_step(opt, g, g, state, lr=1.0),
+                 lambda: m.cgtp_adamw_step(full, g, g, full.new_state(), lr=1.0), lambda: m.cgtp_adamw_state_values(opt, state)):
+        with pytest.raises(ValueError, match="cuda:1.*cuda:0"):
+            call()
+    assert bool((g[0] == 1).all()) and not state["m"].any()
