@@ -13,6 +13,7 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/core/impl/VirtualGuardImpl.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -155,8 +156,8 @@ PyObject* guarded(F&& f) {
     return f();
   } catch (const Misfit&) {
     Py_RETURN_NOTIMPLEMENTED;
-  } catch (const std::exception& e) {   // torch's allocator
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {   // torch's allocator: torch.OutOfMemoryError and what else its own calls raise
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }

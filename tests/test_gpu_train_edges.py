@@ -233,3 +233,18 @@ def test_calls_on_another_device_than_the_plans_are_refused():
         with pytest.raises(ValueError, match="cuda:1.*cuda:0"):
             call()
     assert bool((g[0] == 1).all()) and not state["m"].any()
+
+
+def test_out_of_memory_is_torchs_own_error():
+    # an allocation that the caching allocator refuses under a limit on this process: nothing is asked of the device
+    plan = cg().ResNormPlan("64x0e+64x1o")
+    h = torch.zeros(100000, plan.dim, device="cuda")
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 20)) / total)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            cg().cgtp_resnorm_forward(plan, h)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert bool((cg().cgtp_resnorm_forward(plan, h)[1] == 0).all())
