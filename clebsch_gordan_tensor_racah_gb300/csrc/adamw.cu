@@ -100,8 +100,9 @@ __device__ __forceinline__ float v_bits(uint32_t word, int j) {
   return __uint_as_float((j == 3 ? word >> 4 : word << (20 - 8 * j)) & 0x0FF00000u);
 }
 
-// The code of x >= 0 (its bits), rounded up with probability = its distance above the code below it; r: 20
-// random bits.  E leaves room for the largest value of the block to be rounded up.
+// The code of x >= 0 (its bits), rounded up with probability = its distance above the code below it; r: 16 random
+// bits, then four zeros, so that the distance counts in whole 2^-16 of a code step, rounded down (2^-17 in the
+// mean).  E leaves room for the largest value of the block to be rounded up.
 template <int TOP>
 __device__ __forceinline__ uint32_t code_of(uint32_t bits, int E, uint32_t r) {
   return (bits + r - (static_cast<uint32_t>(E - TOP) << 23)) >> 20;

@@ -109,6 +109,9 @@ class ResNormPlan:
     ``stream_dtype`` is the type of h, out, gout, gh; ``in_dtype`` of z, q, gy (what comes from a
     product); ``out_dtype`` of y, gz, gq (what goes to one); ``param_dtype`` of post, scale, pre and
     their gradients.  ``storage`` (bfloat16 only) keeps every row tensor in bfloat16.
+
+    The plan owns the partial sums of the parameter gradients: its backwards must not overlap on the GPU.  Give
+    each stream that runs them at the same time a plan of its own.
     """
 
     def __init__(self, irreps, dtype=None, storage=False, act="none", pre_norm=True, post_norm=True, alpha=1.0,
@@ -209,7 +212,9 @@ class AdamW:
     """cgtp_adamw_create: AdamW over tensors of ``numel`` elements each.
 
     state "f32" (or "full": the parameters' type) or "8bit".  decay_scale: factor of the weight
-    decay for each tensor (0: not decayed)."""
+    decay for each tensor (0: not decayed).
+
+    The optimizer owns the partial sums of the gradient norm: its norms must not overlap on the GPU."""
 
     def __init__(self, numel, param_dtype=None, grad_dtype=None, state="f32", decay_scale=None):
         self.param_dtype = param_dtype or torch.float32
@@ -294,7 +299,10 @@ def cgtp_grad_norm(opt, grads, max_norm=float("inf"), out=None, stream=None):
 def cgtp_adamw_step(opt, params, grads, state, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, step=1,
                     copies=None, clip=None, seed=0, stream=None):
     """One AdamW step in place.  A None gradient skips its tensor.  copies: bfloat16 tensors (or None)
-    that receive the new parameters.  clip: result of cgtp_grad_norm.  seed: rounding of 8-bit states."""
+    that receive the new parameters.  clip: result of cgtp_grad_norm.  seed: rounding of 8-bit states.
+
+    lr, step and seed are taken at the call: a captured graph repeats the captured step's bias correction and rounding
+    bits, so a training loop calls the step outside its graphs."""
     if stream is not None:
         return _on(stream, cgtp_adamw_step, opt, params, grads, state, lr, betas, eps, weight_decay, step, copies, clip, seed)
     r = _binding.adamw_step(opt._native, params, grads, copies, state["m"], state["v"], state["m_exp"], state["v_exp"], lr, betas[0],

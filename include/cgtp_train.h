@@ -40,8 +40,9 @@ typedef enum { CGTP_ACT_NONE = 0, CGTP_ACT_IDENTITY = 1, CGTP_ACT_SIGMOID = 2, C
  *      CGTP_RESNORM_STORAGE every row tensor in bfloat16.  Parameters (post,
  *      scale, pre) and their gradients are FP32 (FP64 for CGTP_F64), arithmetic
  *      and sums too.
- *  alpha : factor of the residual.  eps >= 0; with eps = 0 a block of zeros has no norm
- *      (NaN).  Squares are summed in FP32 (FP64): elements above 1.8e19 overflow them.
+ *  alpha : factor of the residual.  eps >= 0, rounded to the type of the arithmetic;
+ *      with eps = 0 a block of zeros has no norm (NaN).  Squares are summed in FP32 (FP64):
+ *      elements above 1.8e19 overflow them, elements below 1e-19 lose digits in them.
  * The plan owns its tables and the partial sums of the parameter gradients: backwards
  * of the same plan must not overlap on the GPU.
  */
@@ -108,10 +109,12 @@ cgtp_status cgtp_resnorm_backward(cgtp_resnorm plan, int64_t N, const void* gout
  *      from step to step.  m: sign, 4-bit exponent, 3-bit mantissa; v: 5-bit
  *      exponent, 3-bit mantissa; below the smallest exponent the codes are
  *      linear to zero.  The update uses the unrounded m and v; what is stored is
- *      rounded stochastically (unbiased: changes far below one code step, such
- *      as 0.1% of v, still move it on average), with bits that depend on seed, t
- *      and the element's place alone.  A positive v is never stored as zero.
- *      A block that holds an infinity or a NaN is stored as NaNs.
+ *      rounded stochastically (changes far below one code step, such as 0.1% of
+ *      v, still move it on average), with 16 bits that depend on seed, t and the
+ *      element's place alone.  The mean of what is stored lies up to 2^-17 of a
+ *      code step nearer to zero: v settles up to 0.1% low for beta2 = 0.999, 10%
+ *      for 0.99999.  A positive v is never stored as zero.  A block that holds an
+ *      infinity, a NaN or a number above 3.19e38 is stored as NaNs.
  */
 typedef struct cgtp_adamw_s* cgtp_adamw;
 typedef enum { CGTP_STATE_FULL = 0, CGTP_STATE_8BIT = 1 } cgtp_state;
@@ -143,6 +146,11 @@ cgtp_status cgtp_adamw_device_bytes(cgtp_adamw opt, int64_t* bytes);
  *      CGTP_STATE_FULL).
  *  clip : NULL, or what cgtp_grad_norm wrote.  Where its coefficient is not a
  *      finite number the step changes nothing.
+ *  lr, step, seed and the other numbers are host values, taken at the call.  In a
+ *      captured graph they are those of the capture: every replay repeats that
+ *      step's bias correction and rounding bits (an 8-bit v that is always rounded
+ *      with the same bits may stop moving).  A training loop captures its passes
+ *      and calls the step outside the graph, or captures the step anew.
  */
 cgtp_status cgtp_adamw_step(cgtp_adamw opt, void* const* params, const void* const* grads, void* const* copies,
                             void* m, void* v, void* m_exp, void* v_exp, double lr, double beta1, double beta2,

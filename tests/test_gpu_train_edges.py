@@ -248,3 +248,67 @@ def test_out_of_memory_is_torchs_own_error():
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert bool((cg().cgtp_resnorm_forward(plan, h)[1] == 0).all())
+
+
+def test_gradients_of_extreme_size():
+    # 3e38 squared is infinite: v of its block is stored as NaNs, as a block that holds an infinity is.  Its own step is zero
+    # (a finite m over an infinite root); the others of the block move by lr |g| / (|g| + eps) with their unrounded v.
+    list_ = [3e38, 1e-38, 1e-45, 0.0, -3e38, 1e19, 1e-20, -0.0]
+    g = torch.tensor(list_ * 16, device="cuda")
+    for state_kind in ("8bit", "f32"):
+        opt = cg().AdamW([128], state=state_kind)
+        state, p = opt.new_state(), [torch.zeros(128, device="cuda")]
+        cg().cgtp_adamw_step(opt, p, [g], state, lr=1e-3, step=1)
+        q = p[0].view(16, 8)
+        assert bool(torch.isfinite(q).all()) and not q[:, [0, 3, 4, 7]].any()
+        assert float((q[:, 5] + 1e-3).abs().max()) <= 16 * 2.0 ** -24 * 1e-3
+        m, v = cg().cgtp_adamw_state_values(opt, state)
+        assert bool(torch.isfinite(m).all())
+        assert bool(torch.isnan(v).all()) if state_kind == "8bit" else bool(torch.isinf(v.view(16, 8)[:, [0, 4]]).all())
+        if state_kind == "8bit":      # codes of 8 steps a binade: next to 0.1 g
+            assert float((m.view(16, 8)[:, 0] / 3e37 - 1).abs().max()) <= 0.125
+    # large numbers whose squares are finite
+    g = torch.tensor([1e19, -1e19, 1e18, 3e17] * 32, device="cuda")
+    opt = cg().AdamW([128], state="8bit")
+    state, p = opt.new_state(), [torch.zeros(128, device="cuda")]
+    cg().cgtp_adamw_step(opt, p, [g], state, lr=1e-3, step=1)
+    m, v = cg().cgtp_adamw_state_values(opt, state)
+    assert float((p[0] + 1e-3 * torch.sign(g)).abs().max()) <= 16 * 2.0 ** -24 * 1e-3
+    assert float((m / (0.1 * g) - 1).abs().max()) <= 0.125 and float((v / (1e-3 * g * g) - 1).abs().max()) <= 0.125
+
+
+@pytest.mark.parametrize("state_kind", ["f32", "8bit"])
+def test_passes_in_a_cuda_graph_with_the_step_outside(state_kind):
+    # step count, rate and seed are values of the call: a loop that captures its passes and calls the step outside the
+    # graph is the eager loop, bit for bit
+    torch.manual_seed(6)
+    plan = cg().ResNormPlan("64x0e+64x1o", act="silu")
+    n, dim, chan = 1000, plan.dim, plan.channels
+    h, z, gout, gy = (torch.randn(n, dim, device="cuda") for _ in range(4))
+    q, gains = torch.randn(n, chan, device="cuda"), [1 + 0.1 * torch.randn(chan, device="cuda") for _ in range(3)]
+    opt = cg().AdamW([chan] * 3, state=state_kind)
+
+    def passes(p):
+        out, _ = cg().cgtp_resnorm_forward(plan, h, z, q, post=p[0], scale=p[1], pre=p[2])
+        grads = list(cg().cgtp_resnorm_backward(plan, gout, gy, out, z, q, post=p[0], scale=p[1], pre=p[2])[3:])
+        return grads, cg().cgtp_grad_norm(opt, grads, 1.0)
+
+    def step(p, state, grads, clip, t):
+        cg().cgtp_adamw_step(opt, p, grads, state, lr=1e-2 / t, weight_decay=0.1, step=t, clip=clip, seed=t)
+
+    eager, captured = [g.clone() for g in gains], [g.clone() for g in gains]
+    s_eager, s_captured = opt.new_state(), opt.new_state()
+    passes(eager)                      # before the capture: the first launch of a kernel sets its attributes
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        grads, clip = passes(captured)
+    for t in range(1, 5):
+        step(eager, s_eager, *passes(eager), t)
+        graph.replay()
+        step(captured, s_captured, grads, clip, t)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(eager, captured))
+    assert all(a is None or torch.equal(a, s_captured[k]) for k, a in s_eager.items())
