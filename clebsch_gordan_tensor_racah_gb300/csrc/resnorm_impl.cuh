@@ -49,11 +49,18 @@ __device__ __forceinline__ float rn_put(__nv_bfloat16* p, float v) {
 
 __device__ __forceinline__ float rn_rsqrt(float v) { return rsqrtf(v); }
 __device__ __forceinline__ double rn_rsqrt(double v) { return rsqrt(v); }
-// 1 / (1 + e^-q): exponential and reciprocal to a unit in the last place each for every q (the fast exponential's
-// error grows with |q|: 37 units at q = -30); 0 below -87.3, where the value is no normal number
+// 1 / (1 + e^-q) to a few units in the last place for every q; 0 below -87.3, where the value is no normal number.
+// e^-q = 2^(hi + lo) with hi the rounded product -q log2(e) and lo what its rounding and the constant's left out (the
+// fast exponential leaves lo out, which costs 37 units at q = -30), 2^lo = 1 + lo ln 2.  For a q without such a
+// split (infinite, or so far out that 2^hi is 0 or infinite) the correction only has to be positive.  expf in its
+// place: 5,000 x 128x0e+128x1o+128x2e backward 46.1 us against 44.7 us, 200,000 x 32x0e+32x1o+32x2e+32x3o 458 against 442.
 __device__ __forceinline__ float rn_sigmoid(float q) {
-  float s;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + expf(-q)));
+  const float hi = -1.44269502f * q;
+  const float lo = fmaf(-1.92596303e-8f, q, fmaf(-1.44269502f, q, -hi));
+  const float c = fminf(fabsf(fmaf(lo, 0.693147182f, 1.0f)), 2.0f);
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(hi));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(fmaf(e, c, 1.0f)));
   return s;
 }
 __device__ __forceinline__ double rn_sigmoid(double q) { return 1.0 / (1.0 + exp(-q)); }

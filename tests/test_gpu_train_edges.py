@@ -312,3 +312,26 @@ def test_passes_in_a_cuda_graph_with_the_step_outside(state_kind):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(eager, captured))
     assert all(a is None or torch.equal(a, s_captured[k]) for k, a in s_eager.items())
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16s"])
+def test_gates_at_the_ends_of_the_type(kind):
+    inf, nan = float("inf"), float("nan")
+    dtype = torch.bfloat16 if kind == "bf16s" else torch.float32
+    top = float(torch.finfo(dtype).max)
+    far = [-(2.0 ** k) * f for k in range(7, 128, 3) for f in (1.0, 1.2578125, 1.734375)]    # exact in both types
+    q = torch.tensor([[-inf, inf, nan, -top, top, 0.0, -0.0] + far + [-v for v in far]], device="cuda").to(dtype)
+    width = q.shape[1]
+    one = torch.ones_like(q)
+    n = len(far)
+    for act in ("sigmoid", "silu"):
+        plan = _plan("%dx0e" % width, kind, act=act, pre_norm=False, post_norm=False)
+        out = cg().cgtp_resnorm_forward(plan, None, one, q)[0][0]
+        gq = cg().cgtp_resnorm_backward(plan, one, None, None, one, q, need_gh=False)[2][0]
+        up = torch.ones(n, device="cuda", dtype=dtype) if act == "sigmoid" else q[0, 7 + n:]
+        assert torch.equal(out[7:7 + n], torch.zeros_like(up)) and torch.equal(out[7 + n:], up)
+        assert not gq[7:7 + n].any() and torch.equal(gq[7 + n:], torch.full_like(up, 0.0 if act == "sigmoid" else 1.0))
+        first = out[:7].tolist()
+        assert first[3:] == ([0.0, 1.0, 0.5, 0.5] if act == "sigmoid" else [0.0, top, 0.0, 0.0]) and first[2] != first[2]
+        assert first[1] == (1.0 if act == "sigmoid" else inf) and (first[0] == 0.0 if act == "sigmoid" else first[0] != first[0])
+        assert gq[3:5].tolist() == [0.0, 0.0 if act == "sigmoid" else 1.0] and bool(torch.isnan(gq[2]))
