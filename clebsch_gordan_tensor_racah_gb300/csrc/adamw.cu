@@ -311,7 +311,7 @@ __device__ __forceinline__ StepScalars<A> scalars_of(const Scalars& host, A coef
 // ---------------------------------------------------------------------------
 // States in the parameters' type: a lane holds its elements of NB blocks, and the loads of the next NB are
 // in flight while these are computed.  Bound by HBM: 100.7 M FP32 parameters with bfloat16 gradients and copies,
-// 28 bytes an element, 426 us (6.6 TB/s; a copy reaches 6.7); without loads ahead 445 us, a block a warp 495 us.
+// 28 bytes an element, 425 us (6.6 TB/s; a copy reaches 6.7); without loads ahead 445 us, a block a warp 495 us.
 // ---------------------------------------------------------------------------
 
 template <typename A, int NB>
@@ -399,8 +399,8 @@ __global__ void __launch_bounds__(kStepThreads) adamw_kernel(const __grid_consta
 // ---------------------------------------------------------------------------
 // 8-bit states.  Decoding and rounding take about 300 instructions a block, so a warp that waits for
 // its loads costs issue slots: operands come through a ring of asynchronous copies in shared memory, two blocks
-// a stage, that runs ahead over the warp's units.  100.7 M parameters, 16 bytes an element: 355 us (4.5 TB/s) at 348
-// warp instructions a block and 2.7 a cycle; loads into registers instead of the ring 470 us at best.
+// a stage, that runs ahead over the warp's units.  100.7 M parameters, 16 bytes an element: 364 to 371 us (4.4 TB/s) at 365
+// warp instructions a block and 2.8 a cycle; loads into registers instead of the ring 470 us at best.
 // ---------------------------------------------------------------------------
 
 constexpr int kRing = 3, kStageBlocks = 2;
@@ -605,7 +605,7 @@ __device__ __forceinline__ double cta_sum(double v) {
   return t;
 }
 
-// Bound by HBM reads: 100.7 M FP32 gradients 66 us (6.1 TB/s).
+// Bound by HBM reads: 100.7 M FP32 gradients 67 us (6.0 TB/s).
 // Sum of squares of the CTA's units: a thread's own in A, the rest in FP64.  The last CTA of the last launch
 // (a counter; the order of the sums does not depend on it) adds the CTAs' sums and leaves the counter at zero.
 template <typename A, typename G, int K>

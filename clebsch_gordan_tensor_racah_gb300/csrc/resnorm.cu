@@ -119,7 +119,7 @@ int lay_out(RnArgs* a, bool backward, int rows) {
 // How rows are dealt out (see resnorm_impl.cuh): the cheapest of the launches that fit, by the
 // instructions that a row costs and the warps that hide their latency.
 //   instructions: an element of a thread's share, a channel, a step of the block sums and the fixed part of a
-//     block, fitted to counters of the kernels (a row of 64x0e+64x1o+64x2e: 1,330 backward, 875 forward);
+//     block, fitted to counters of the kernels (a row of 64x0e+64x1o+64x2e: 1,328 backward, 885 forward);
 //     half as many again where operands are missing, blocks do not fill the lanes or copies are ragged.
 //   rate: grows with the warps of an SM as w / (w + 8).
 // Measured on both sides (GB300, share of the copy bandwidth):

@@ -721,10 +721,10 @@ __device__ __forceinline__ void rn_runs_out(const RnRows* const (&r)[NT], const 
     }
 }
 
-// Bound by HBM where blocks fill the warp: 200,000 rows of 64x0e+64x1o+64x2e forward with bfloat16 y 260 us (6.8 TB/s;
-// a copy reaches 6.7), backward 482 to 500 us (6.1 to 6.4 TB/s); 60,000 x 128x0e+128x1o+128x2e backward 310 to
-// 335 us (5.5 to 5.9 TB/s, nine warps fit).  Elsewhere by instructions: 400,000 x 33x0e+17x1o+5x2e 120 us (2.9 TB/s);
-// and by bank conflicts of rows side by side: 2,000,000 x 8x0e+8x1o 302 us (3.8 TB/s).  One CTA an SM, 128 registers a thread:
+// Bound by HBM where blocks fill the warp: 200,000 rows of 64x0e+64x1o+64x2e forward with bfloat16 y 259 us (6.8 TB/s;
+// a copy reaches 6.7), backward 482 to 506 us (6.1 to 6.4 TB/s; the cards differ); 60,000 x 128x0e+128x1o+128x2e backward 310 to
+// 335 us (5.5 to 5.9 TB/s, nine warps fit).  Elsewhere by instructions: 400,000 x 33x0e+17x1o+5x2e 119 us (2.9 TB/s);
+// and by bank conflicts of rows side by side: 2,000,000 x 8x0e+8x1o 300 us (3.8 TB/s).  One CTA an SM, 128 registers a thread:
 // what a warp holds of a block is worth more than a second CTA.
 template <bool BACKWARD, int KIND, typename S, typename I, typename O, typename A>
 __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __grid_constant__ RnArgs a) {
@@ -861,7 +861,7 @@ __global__ void __launch_bounds__(kRnWarps * 32, 1) rn_staged_kernel(const __gri
 
 // ---------------------------------------------------------------------------
 // Rows that do not fit in shared memory, or whose blocks a thread cannot hold: a CTA reads a row in place, and
-// again for each pass (from L1 or L2).  20,000 rows of 8192x0e: forward 1.73 ms (1.9 TB/s), backward 4.4 ms (1.2 TB/s).
+// again for each pass (from L1 or L2).  20,000 rows of 8192x0e: forward 1.75 ms (1.9 TB/s), backward 4.1 ms (1.3 TB/s).
 // ---------------------------------------------------------------------------
 
 template <bool BACKWARD, typename S, typename I, typename O, typename A>
