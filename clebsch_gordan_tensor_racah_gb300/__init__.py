@@ -6,20 +6,24 @@ for device memory and streams.  There is no CPU fallback: if the library is
 missing or no GPU is present the calls raise.
 
 Names follow the C ABI in ``include/cgtp.h`` (``include/cgtp_train.h`` for the operators of a
-training step, which ``train.py`` binds, and ``include/cgtp_measure.h`` for the measurement
+training step, which ``train.py`` binds, ``include/cgtp_attn.h`` for attention, which ``attn.py`` binds, and ``include/cgtp_measure.h`` for the measurement
 kernels ``measure_fma`` / ``measure_read``):
 
 * ``Plan(irreps_in1, irreps_in2, irreps_out, mode, dtype, radial_k)`` --
   ``cgtp_plan_create``; ``plan.d1, d2, d_out, w_numel, n_paths``;
   ``plan.path(p)`` -> (ints, CG block).
 * ``cgtp_forward(plan, x1, x2, W)`` / ``cgtp_backward(plan, gout, x1, x2, W)``.
-* ``Graph(rowptr, col, N)`` -- ``cgtp_graph_create``; ``graph.transpose()``.
+* ``Graph(rowptr, col, N)`` -- ``cgtp_graph_create``; ``graph.transpose()``; ``Graph(rowptr, col, N, n_src=M)`` --
+  ``cgtp_graph_create_cross``.
 * ``cgtp_conv_forward(plan, graph, x, Y, W_or_R, M=None)`` and
   ``cgtp_conv_backward(plan, graph, gout, x, Y, W_or_R, M=None)``.
 * ``cgtp_real_cg_block(l1, l2, l3)`` -- host-only query of the planner's block.
 * ``ResNormPlan(irreps, ...)`` with ``cgtp_resnorm_forward`` / ``cgtp_resnorm_backward`` -- the
   norms, gate and residual around a block.
 * ``AdamW(numel, ...)`` with ``cgtp_grad_norm``, ``cgtp_adamw_step``, ``cgtp_adamw_state_values``.
+* ``AttentionPlan(irreps_qk, irreps_v, heads, ...)`` with ``cgtp_attn_forward`` / ``cgtp_attn_backward`` and
+  ``cgtp_attn_edges_forward`` / ``cgtp_attn_edges_backward`` -- attention along a graph's edges, of the sources' values
+  and of a convolution's per-edge weights; ``attention_borders``, ``attention_rows``.
 """
 
 import ctypes
@@ -50,7 +54,10 @@ EXPORTS = ["cgtp_plan_create", "cgtp_plan_destroy", "cgtp_plan_info", "cgtp_plan
            "cgtp_resnorm_create", "cgtp_resnorm_destroy", "cgtp_resnorm_info", "cgtp_resnorm_device_bytes",
            "cgtp_resnorm_forward", "cgtp_resnorm_backward", "cgtp_adamw_create", "cgtp_adamw_destroy",
            "cgtp_adamw_info", "cgtp_adamw_device_bytes", "cgtp_adamw_step", "cgtp_grad_norm",
-           "cgtp_adamw_state_values"]
+           "cgtp_adamw_state_values",
+           "cgtp_graph_create_cross", "cgtp_attn_create", "cgtp_attn_destroy", "cgtp_attn_info", "cgtp_attn_device_bytes",
+           "cgtp_attn_workspace", "cgtp_attn_forward", "cgtp_attn_backward", "cgtp_attn_edges_forward",
+           "cgtp_attn_edges_backward"]
 
 
 class CgtpError(RuntimeError):
@@ -107,6 +114,18 @@ def lib():
         L.cgtp_mixed_conv_forward.argtypes = [vp] * 8 + [i64, vp]
         L.cgtp_mixed_conv_backward.argtypes = [vp] * 12 + [i64, vp]
         L.cgtp_mixed_conv_double_backward.argtypes = [vp] * 17 + [i64, vp]
+        L.cgtp_graph_create_cross.argtypes = [ctypes.POINTER(vp), vp, vp, i64, i64, i64, vp]
+        L.cgtp_attn_create.argtypes = [ctypes.POINTER(vp), ctypes.c_char_p, ctypes.c_char_p, i32, i32, i32, i32, dbl, i32,
+                                       ctypes.POINTER(dbl)]
+        L.cgtp_attn_destroy.argtypes = [vp]
+        L.cgtp_attn_destroy.restype = None
+        L.cgtp_attn_info.argtypes = [vp, ctypes.POINTER(i64), ctypes.POINTER(i64)]
+        L.cgtp_attn_device_bytes.argtypes = [vp, ctypes.POINTER(i64)]
+        L.cgtp_attn_workspace.argtypes = [vp, vp, i32, ctypes.POINTER(i64)]
+        L.cgtp_attn_forward.argtypes = [vp] * 2 + [vp, i64] * 3 + [vp] * 3 + [vp, i64, vp, vp, i64, vp]
+        L.cgtp_attn_backward.argtypes = [vp] * 2 + [vp, i64] * 4 + [vp] * 4 + [vp, i64] * 3 + [vp] * 3 + [i64, vp]
+        L.cgtp_attn_edges_forward.argtypes = [vp] * 2 + [vp, i64] * 3 + [vp] * 3 + [vp, i64, vp, vp, i64, vp]
+        L.cgtp_attn_edges_backward.argtypes = [vp] * 2 + [vp, i64] * 4 + [vp] * 2 + [vp, i64] * 3 + [vp] * 3 + [i64, vp]
         L.cgtp_plan_device_bytes.argtypes = [vp, ctypes.POINTER(i64)]
         L.cgtp_plan_set_wait_limit.argtypes = [vp, i64]
         L.cgtp_plan_set_node_chunk.argtypes = [vp, i64]
@@ -264,17 +283,23 @@ class Plan:
 
 
 class Graph:
-    """cgtp_graph_create: validated receiver-sorted CSR + device transpose."""
+    """cgtp_graph_create: validated receiver-sorted CSR + device transpose.
 
-    def __init__(self, rowptr, col, N, stream=None):
+    n_src: number of sources where they are another set than the N receivers (cgtp_graph_create_cross; attention
+    only, convolutions need one set of nodes)."""
+
+    def __init__(self, rowptr, col, N, stream=None, n_src=None):
         torch = _torch()
         self.rowptr, self.col, self.N = rowptr, col, int(N)
+        self.n_src = self.N if n_src is None else int(n_src)
         self.E = int(col.numel())
         h = ctypes.c_void_p()
-        _check(lib().cgtp_graph_create(ctypes.byref(h), _ptr(rowptr, "rowptr", torch.int32),
-                                       _ptr(col, "col", torch.int32) if self.E else None,
-                                       self.N, self.E, _stream(stream)))
+        _check(lib().cgtp_graph_create_cross(ctypes.byref(h), _ptr(rowptr, "rowptr", torch.int32),
+                                             _ptr(col, "col", torch.int32) if self.E else None,
+                                             self.N, self.n_src, self.E, _stream(stream)))
         self._h = h
+        self.device = torch.device("cuda", torch.cuda.current_device())
+        self._native = (h.value, self.N, self.n_src, self.E, self.device.index)
 
     @property
     def handle(self):
@@ -289,7 +314,7 @@ class Graph:
     def transpose(self, stream=None):
         torch = _torch()
         dev = self.rowptr.device
-        t_rowptr = torch.empty(self.N + 1, dtype=torch.int32, device=dev)
+        t_rowptr = torch.empty(self.n_src + 1, dtype=torch.int32, device=dev)
         t_eid = torch.empty(max(self.E, 1), dtype=torch.int32, device=dev)
         t_dst = torch.empty(max(self.E, 1), dtype=torch.int32, device=dev)
         _check(lib().cgtp_graph_transpose(self._h, _ptr(t_rowptr, "t_rowptr"), _ptr(t_eid, "t_eid"),
@@ -566,14 +591,18 @@ def cgtp_mixed_conv_double_backward(plan, graph, gout, x, Y, Wu, Ww, ggx, ggY, g
     return d_g, d_x, d_Y, d_Wu, d_Ww
 
 
-_TRAIN = ("AdamW", "ResNormPlan", "cgtp_adamw_state_values", "cgtp_adamw_step", "cgtp_grad_norm",
-          "cgtp_resnorm_backward", "cgtp_resnorm_forward")
+_LATER = dict(train=("AdamW", "ResNormPlan", "cgtp_adamw_state_values", "cgtp_adamw_step", "cgtp_grad_norm",
+                     "cgtp_resnorm_backward", "cgtp_resnorm_forward"),
+              attn=("AttentionPlan", "attention_borders", "attention_rows", "cgtp_attn_backward", "cgtp_attn_edges_backward",
+                    "cgtp_attn_edges_forward", "cgtp_attn_forward"))
 
 
 def __getattr__(name):
-    """The operators of train.py, which needs torch as soon as it is imported."""
-    if name in _TRAIN:
-        from . import train
-        globals().update({k: getattr(train, k) for k in _TRAIN})
-        return globals()[name]
+    """The operators of train.py and attn.py, which need torch as soon as they are imported."""
+    for module, names in _LATER.items():
+        if name in names:
+            import importlib
+            m = importlib.import_module("." + module, __name__)
+            globals().update({k: getattr(m, k) for k in names})
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

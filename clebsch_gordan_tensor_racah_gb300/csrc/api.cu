@@ -12,6 +12,7 @@
 #include <mutex>
 #include <new>
 
+#include "cgtp_attn.h"
 #include "internal.h"
 
 namespace cgtp {
@@ -300,7 +301,8 @@ cgtp_status cgtp_plan_device_bytes(cgtp_plan plan, int64_t* bytes) {
 cgtp_status cgtp_graph_device_bytes(cgtp_graph graph, int64_t* bytes) {
   clear_error();
   if (!graph || !bytes) return fail(CGTP_EINVAL, "null graph or bytes");
-  *bytes = static_cast<int64_t>(sizeof(int32_t)) * (graph->N + 1 + 2 * std::max<int64_t>(graph->E, 1));
+  *bytes = static_cast<int64_t>(sizeof(int32_t)) * (graph->N_src + 1 + 2 * std::max<int64_t>(graph->E, 1));
+  for (const GraphSplit* s : {&graph->split, &graph->split_t}) *bytes += int64_t(s->n_items + s->n_joins) * sizeof(Int4);
   return CGTP_OK;
 }
 
@@ -357,9 +359,15 @@ cgtp_status cgtp_backward(cgtp_plan plan, const void* gout, const void* x1, cons
 
 cgtp_status cgtp_graph_create(cgtp_graph* out, const int32_t* rowptr, const int32_t* col, int64_t N,
                               int64_t E, void* stream) {
+  return cgtp_graph_create_cross(out, rowptr, col, N, N, E, stream);
+}
+
+cgtp_status cgtp_graph_create_cross(cgtp_graph* out, const int32_t* rowptr, const int32_t* col, int64_t N,
+                                    int64_t N_src, int64_t E, void* stream) {
   clear_error();
   if (!out) return fail(CGTP_EINVAL, "null graph output pointer");
   *out = nullptr;
+  if (N_src < 1 || N_src >= (int64_t(1) << 31) - 1) return fail(CGTP_EINVAL, "N_src must be in [1, 2^31-1)");
   if (N < 1 || N >= (int64_t(1) << 31) - 1 || E < 0 || E >= (int64_t(1) << 31))
     return fail(CGTP_EINVAL, "N must be in [1, 2^31-1) and E in [0, 2^31)");
   if (!rowptr) return fail(CGTP_EINVAL, "null rowptr");
@@ -369,10 +377,11 @@ cgtp_status cgtp_graph_create(cgtp_graph* out, const int32_t* rowptr, const int3
   g->rowptr = rowptr;
   g->col = col;
   g->N = N;
+  g->N_src = N_src;
   g->E = E;
   cudaGetDevice(&g->device);
   const size_t eb = std::max<int64_t>(E, 1) * sizeof(int32_t);
-  if (cudaMalloc(&g->t_rowptr, (N + 1) * sizeof(int32_t)) != cudaSuccess ||
+  if (cudaMalloc(&g->t_rowptr, (N_src + 1) * sizeof(int32_t)) != cudaSuccess ||
       cudaMalloc(&g->t_eid, eb) != cudaSuccess || cudaMalloc(&g->t_dst, eb) != cudaSuccess) {
     cgtp_graph_destroy(g);
     return fail(CGTP_ENOMEM, "graph allocation failed");
@@ -391,6 +400,8 @@ void cgtp_graph_destroy(cgtp_graph g) {
   if (g->t_rowptr) cudaFree(g->t_rowptr);
   if (g->t_eid) cudaFree(g->t_eid);
   if (g->t_dst) cudaFree(g->t_dst);
+  for (const GraphSplit* s : {&g->split, &g->split_t})
+    if (s->items) cudaFree(const_cast<Int4*>(s->items));
   delete g;
 }
 
@@ -400,7 +411,7 @@ cgtp_status cgtp_graph_transpose(cgtp_graph g, int32_t* t_rowptr, int32_t* t_eid
   if (!g) return fail(CGTP_EINVAL, "null graph");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (t_rowptr) e = cudaMemcpyAsync(t_rowptr, g->t_rowptr, (g->N + 1) * sizeof(int32_t), cudaMemcpyDeviceToDevice, st);
+  if (t_rowptr) e = cudaMemcpyAsync(t_rowptr, g->t_rowptr, (g->N_src + 1) * sizeof(int32_t), cudaMemcpyDeviceToDevice, st);
   if (e == cudaSuccess && t_eid && g->E)
     e = cudaMemcpyAsync(t_eid, g->t_eid, g->E * sizeof(int32_t), cudaMemcpyDeviceToDevice, st);
   if (e == cudaSuccess && t_dst && g->E)
@@ -413,6 +424,7 @@ cgtp_status cgtp_conv_forward(cgtp_plan plan, cgtp_graph g, const void* x, const
                               const void* W_or_R, const void* M, void* out, void* stream) {
   clear_error();
   if (!plan || !g) return fail(CGTP_EINVAL, "null plan or graph");
+  if (const cgtp_status one = one_set(g)) return one;
   cgtp_status s;
   if ((s = need(x, "x")) || (s = need(out, "out"))) return s;
   if (g->E > 0 && ((s = need(Y, "Y")) || (s = need(W_or_R, plan->mode == CGTP_UVU ? "W" : "R")))) return s;
@@ -434,6 +446,7 @@ cgtp_status cgtp_conv_backward(cgtp_plan plan, cgtp_graph g, const void* gout, c
                                void* gW_or_gR, void* gM, void* stream) {
   clear_error();
   if (!plan || !g) return fail(CGTP_EINVAL, "null plan or graph");
+  if (const cgtp_status one = one_set(g)) return one;
   cgtp_status s;
   if ((s = need(gout, "gout")) || (s = need(x, "x")) || (s = need(gx, "gx"))) return s;
   if (g->E > 0 && ((s = need(Y, "Y")) || (s = need(W_or_R, "W_or_R")) || (s = need(gY, "gY")) ||

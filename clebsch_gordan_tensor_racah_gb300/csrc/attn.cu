@@ -1,0 +1,604 @@
+// attn.cu -- the attention's plan, argument checks and launches (declared in include/cgtp_attn.h; kernels in
+// attn_impl.cuh).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+#include <string>
+
+#include "attn.h"
+#include "cgtp_attn.h"
+
+namespace cgtp {
+namespace {
+
+int es_store(const cgtp_attn_s* p) { return p->dtype == CGTP_F64 ? 8 : p->dtype == CGTP_BF16 ? 2 : 4; }
+int es_acc(const cgtp_attn_s* p) { return p->dtype == CGTP_F64 ? 8 : 4; }
+int es_result(const cgtp_attn_s* p) { return p->flags & CGTP_ATTN_STORAGE ? 2 : es_acc(p); }
+
+int64_t align16(int64_t v) { return (v + 15) / 16 * 16; }
+
+// ---------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------
+
+struct Blocks {
+  std::vector<Irrep> ir;
+  int dim = 0;   // elements of one head
+};
+
+cgtp_status parse(const char* s, int heads, const char* name, Blocks* b) {
+  std::string err;
+  if (!s || !parse_irreps(s, &b->ir, &err)) return fail(CGTP_EINVAL, std::string(name) + ": " + (s ? err : "null irreps"));
+  int64_t dim = 0;
+  for (const Irrep& i : b->ir) {
+    if (i.mul < 1) return fail(CGTP_EINVAL, std::string(name) + ": irreps blocks of a head must have a channel");
+    dim += int64_t(i.mul) * (2 * i.l + 1);
+    if (dim * heads > kAtMaxRow) return fail(CGTP_EUNSUPPORTED, std::string(name) + ": rows of more than 8192 elements");
+  }
+  b->dim = static_cast<int>(dim);
+  return CGTP_OK;
+}
+
+// Tables for vectors of V elements, which divide every head's run of every block; offsets into *out until upload.
+AtTab make_tab(const Blocks& b, int heads, int kv, int V, std::vector<int>* out) {
+  const int group = heads / kv;
+  AtTab t;
+  t.vec = V;
+  t.pieces = b.dim / V;
+  // offset of vector c of head h in a row of `count` heads
+  const auto offsets = [&](int count) {
+    std::vector<int> off(size_t(count) * t.pieces);
+    int at = 0, c0 = 0;
+    for (const Irrep& i : b.ir) {
+      const int run = i.mul * (2 * i.l + 1);
+      for (int h = 0; h < count; ++h)
+        for (int c = 0; c < run / V; ++c) off[size_t(h) * t.pieces + c0 + c] = at + h * run + c * V;
+      at += count * run;
+      c0 += run / V;
+    }
+    return off;
+  };
+  const std::vector<int> full = offsets(heads), shared = offsets(kv);
+  std::vector<int> acc(full.size()), send(full.size());
+  for (int h = 0; h < heads; ++h)
+    for (int c = 0; c < t.pieces; ++c) {
+      const int f = full[size_t(h) * t.pieces + c], s = shared[size_t(h / group) * t.pieces + c];
+      acc[f / V] = s | h << kAtHeadShift;
+      send[size_t(s / V) * group + h % group] = f | h << kAtHeadShift;
+    }
+  const auto put = [&](const std::vector<int>& v) {
+    const size_t at = out->size();
+    out->insert(out->end(), v.begin(), v.end());
+    return reinterpret_cast<const int*>(at * sizeof(int));
+  };
+  t.dot_full = put(full);
+  t.dot_kv = put(shared);
+  t.acc = put(acc);
+  t.send = put(send);
+  return t;
+}
+
+cgtp_status create(cgtp_attn_s* p, const char* irreps_qk, const char* irreps_v, int n_borders, const double* borders) {
+  Blocks qk, v;
+  cgtp_status s = parse(irreps_qk, p->heads, "irreps_qk", &qk);
+  if (s == CGTP_OK) s = parse(irreps_v, p->heads, "irreps_v", &v);
+  if (s != CGTP_OK) return s;
+  p->dk = qk.dim;
+  p->dv = v.dim;
+  std::vector<int> table;
+  const int full = 16 / es_store(p);
+  const auto tabs = [&](const Blocks& b, AtTab* t, int* n) {
+    for (int V : {full, full == 8 ? 4 : 1, 1}) {
+      bool fits = true;
+      for (const Irrep& i : b.ir) fits &= i.mul * (2 * i.l + 1) % V == 0;
+      if (fits && (*n == 0 || t[*n - 1].vec != V)) t[(*n)++] = make_tab(b, p->heads, p->kv, V, &table);
+    }
+  };
+  tabs(qk, p->qk, &p->n_qk);
+  tabs(v, p->vv, &p->n_vv);
+  if (cudaGetDevice(&p->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&p->smem_cap, cudaDevAttrMaxSharedMemoryPerBlockOptin, p->device) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(CGTP_ECUDA, "no CUDA device");
+  }
+  const size_t ints = align16(table.size() * sizeof(int)), total = ints + align16(int64_t(std::max(n_borders, 1)) * es_acc(p));
+  std::vector<char> host(total, 0);
+  std::memcpy(host.data(), table.data(), table.size() * sizeof(int));
+  for (int i = 0; i < n_borders; ++i) {
+    if (es_acc(p) == 8) reinterpret_cast<double*>(host.data() + ints)[i] = borders[i];
+    else reinterpret_cast<float*>(host.data() + ints)[i] = static_cast<float>(borders[i]);
+  }
+  if (cudaMalloc(&p->base, total) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(CGTP_ENOMEM, "attention table allocation failed");
+  }
+  p->device_bytes = total;
+  if (!upload(p->base, host.data(), total)) {
+    cudaGetLastError();
+    return fail(CGTP_ECUDA, "attention table upload failed");
+  }
+  const auto place = [&](const int** x) { *x = reinterpret_cast<const int*>(static_cast<char*>(p->base) + reinterpret_cast<size_t>(*x)); };
+  for (AtTab* t : {p->qk, p->vv})
+    for (int i = 0; i < (t == p->qk ? p->n_qk : p->n_vv); ++i)
+      place(&t[i].dot_full), place(&t[i].dot_kv), place(&t[i].acc), place(&t[i].send);
+  p->borders = static_cast<char*>(p->base) + ints;
+  return CGTP_OK;
+}
+
+// ---------------------------------------------------------------------------
+// arguments
+// ---------------------------------------------------------------------------
+
+struct Tensor {
+  const void* p;
+  int64_t ld, rows, width;
+  int es;
+  const char* name;
+};
+
+cgtp_status check(Tensor* t, AtRows* out) {
+  if (t->rows > 0 && !t->p) return fail(CGTP_EINVAL, std::string("null pointer: ") + t->name);
+  if (reinterpret_cast<uintptr_t>(t->p) % t->es) return fail(CGTP_EINVAL, std::string("pointer not aligned to its element: ") + t->name);
+  if (t->ld == 0) t->ld = t->width;
+  if (t->ld < t->width) return fail(CGTP_EINVAL, std::string("rows overlap (row distance below the row length): ") + t->name);
+  out->p = const_cast<char*>(static_cast<const char*>(t->p));
+  out->ld = t->ld;
+  return CGTP_OK;
+}
+
+cgtp_status check_vector(const void* p, int es, bool needed, const char* name) {
+  if (needed && !p) return fail(CGTP_EINVAL, std::string("null pointer: ") + name);
+  if (reinterpret_cast<uintptr_t>(p) % es) return fail(CGTP_EINVAL, std::string("pointer not aligned to its element: ") + name);
+  return CGTP_OK;
+}
+
+bool fits(const Tensor& t, int vec) {
+  const int bytes = std::min(16, vec * t.es);
+  return reinterpret_cast<uintptr_t>(t.p) % bytes == 0 && (t.rows <= 1 || t.ld * t.es % bytes == 0);
+}
+
+// widest vectors that every tensor allows
+const AtTab& choose(const AtTab* tabs, int n, std::initializer_list<const Tensor*> list) {
+  int i = 0;
+  for (; i < n - 1; ++i) {
+    bool ok = true;
+    for (const Tensor* t : list) ok &= fits(*t, tabs[i].vec);
+    if (ok) break;
+  }
+  return tabs[i];
+}
+
+AtArgs base_args(const cgtp_attn_s* p, const cgtp_graph_s* g) {
+  AtArgs a;
+  a.heads = p->heads;
+  a.kv = p->kv;
+  a.group = p->heads / p->kv;
+  a.heads_magic = static_cast<uint32_t>((((uint64_t(1)) << 32) + p->heads - 1) / p->heads);
+  a.dk = p->dk;
+  a.dv = p->dv;
+  a.scale = p->scale;
+  a.n_borders = p->n_borders;
+  a.borders = p->borders;
+  a.n_edges = g->E;
+  return a;
+}
+
+// the receivers' side of the graph, or the sources'
+void side(AtArgs* a, const cgtp_graph_s* g, bool send) {
+  const GraphSplit& s = send ? g->split_t : g->split;
+  a->rowptr = send ? g->t_rowptr : g->rowptr;
+  a->col = send ? g->t_dst : g->col;
+  a->eid = send ? g->t_eid : nullptr;
+  a->n_rows = send ? g->N_src : g->N;
+  a->items = s.items;
+  a->joins = s.joins;
+  a->n_items = s.n_items;
+  a->n_joins = s.n_joins;
+  a->chunk = g->chunk;
+}
+
+enum Kernel { kForward, kEdgesForward, kReceive, kEdgesReceive, kSendKeys, kSendAll };
+
+int pow2_at_most(int x) {
+  int r = 1;
+  while (2 * r <= x) r *= 2;
+  return r;
+}
+
+// Threads of a row, edges held at once and shared memory.
+cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* a) {
+  const bool send = k == kSendKeys || k == kSendAll, edges = k == kEdgesForward || k == kEdgesReceive;
+  const int es = es_acc(p);
+  // vectors of the results' rows (of the edges' rows, which are most of the work)
+  const int out = k == kForward || edges ? a->heads * a->vv.pieces
+                  : k == kReceive        ? a->heads * std::max(a->qk.pieces, a->vv.pieces)
+                                         : a->kv * std::max(a->qk.pieces, k == kSendAll ? a->vv.pieces : 0);
+  const int64_t longest = std::max(1, std::min(send ? g->max_out : g->max_in, a->n_items ? a->chunk : INT32_MAX));
+  const int64_t rows = a->n_rows, mean = a->n_edges / std::max<int64_t>(rows, 1);
+  a->warp_rows = out <= 64 && mean * out <= 2048;
+  int threads = 32;
+  if (!a->warp_rows) {
+    const int turns = (out + 383) / 384;
+    threads = (out + turns - 1) / turns;
+    // several streams of edges where rows are long beside their width
+    threads *= static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(256 / threads, mean / 8)));
+    threads = std::max(64, (threads + 31) / 32 * 32);
+    if (edges) threads = std::max(threads, 256);
+  }
+  const int pairs = k == kReceive || k == kEdgesReceive || k == kSendAll ? 2 : 1;   // z and p
+  const int64_t budget = a->warp_rows ? 6 * 1024 : 16 * 1024;
+  int64_t sub = std::min<int64_t>((longest + 7) / 8 * 8, budget / (int64_t(a->heads) * es * pairs) / 8 * 8);
+  sub = std::max<int64_t>(sub, 8);
+  const int vmax = std::max(a->qk.vec, a->vv.vec);
+  const int64_t acc = longest <= sub ? 0
+                      : k == kForward                       ? a->heads * a->dv
+                      : k == kReceive || k == kEdgesReceive ? a->heads * a->dk
+                      : k == kSendKeys                      ? a->kv * a->dk
+                      : k == kSendAll                       ? a->kv * (a->dk + a->dv)
+                                                            : 0;
+  int64_t at = send || k == kEdgesReceive ? 0 : align16(int64_t(a->heads) * a->dk * es);
+  const auto region = [&](int* place, int64_t bytes) {
+    *place = static_cast<int>(at);
+    at += align16(bytes);
+  };
+  region(&a->at_g, k == kReceive ? int64_t(a->heads) * a->dv * es : 0);
+  region(&a->at_z, sub * a->heads * es);
+  region(&a->at_p, pairs == 2 ? sub * a->heads * es : 0);
+  region(&a->at_idx, 2 * sub * sizeof(int));
+  region(&a->at_stat, int64_t(3) * a->heads * es);
+  region(&a->at_acc, acc * es);
+  region(&a->at_red, int64_t(threads) * vmax * es);
+  a->sub = static_cast<int>(sub);
+  a->group_smem = static_cast<int>(at);
+  const int64_t items = a->n_items + rows;
+  if (a->warp_rows) {
+    int groups = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, items / p->num_sms)));
+    while (groups > 1 && groups * at > p->smem_cap) groups /= 2;
+    a->block = 32 * groups;
+    a->smem = static_cast<size_t>(groups) * at;
+    a->grid = static_cast<unsigned>(std::min<int64_t>((items + groups - 1) / groups, int64_t(p->num_sms) * 64));
+  } else {
+    a->block = threads;
+    a->smem = static_cast<size_t>(at);
+    a->grid = static_cast<unsigned>(items);
+  }
+  if (a->smem > static_cast<size_t>(p->smem_cap)) return fail(CGTP_EUNSUPPORTED, "attention rows too long for shared memory");
+  // threads of a dot product: two vectors a thread
+  a->team_qk = std::min(32, pow2_at_most(std::max(1, a->qk.pieces / 2)));
+  a->team_vv = std::min(32, k == kEdgesReceive ? std::min(pow2_at_most(std::max(1, 32 / a->heads)), pow2_at_most(a->vv.pieces))
+                                               : pow2_at_most(std::max(1, a->vv.pieces / 2)));
+  return CGTP_OK;
+}
+
+// ---------------------------------------------------------------------------
+// workspace
+// ---------------------------------------------------------------------------
+
+struct Space {
+  int64_t alpha = 0, ds = 0, part = 0, part_sum = 0, hist = 0, total = 0;
+};
+
+constexpr int kHistCtas = 152;
+
+Space space(const cgtp_attn_s* p, const cgtp_graph_s* g, int call) {
+  Space s;
+  const int64_t es = es_acc(p), heads = p->heads;
+  const auto region = [&](int64_t* at, int64_t bytes) {
+    *at = s.total;
+    s.total += align16(bytes);
+  };
+  const int64_t in = g->split.n_items, out = g->split_t.n_items;
+  if (call == CGTP_ATTN_FORWARD) {
+    region(&s.part, in * (heads * p->dv + 2 * heads) * es);
+  } else if (call == CGTP_ATTN_EDGES_FORWARD) {
+    region(&s.part, in * 2 * heads * es);
+  } else {
+    const bool values = call == CGTP_ATTN_BACKWARD;
+    region(&s.alpha, values ? g->E * heads * es : 0);
+    region(&s.ds, g->E * heads * es);
+    region(&s.part, std::max(in * heads * p->dk, out * p->kv * (p->dk + (values ? p->dv : 0))) * es);
+    region(&s.part_sum, in * heads * es);
+    region(&s.hist, p->n_borders ? int64_t(kHistCtas) * (p->n_borders + 1) * heads * sizeof(double) : 0);
+  }
+  return s;
+}
+
+cgtp_status take_space(const Space& s, void* workspace, int64_t bytes) {
+  if (s.total == 0) return CGTP_OK;
+  if (!workspace || bytes < s.total)
+    return fail(CGTP_EINVAL, "workspace too small: " + std::to_string(s.total) + " bytes needed (cgtp_attn_workspace)");
+  if (reinterpret_cast<uintptr_t>(workspace) % 16) return fail(CGTP_EINVAL, "workspace not 16-byte aligned");
+  return CGTP_OK;
+}
+
+#define CGTP_AT_PICK(p, name)                                \
+  ((p)->dtype == CGTP_F64                  ? at_##name##_f64 \
+   : (p)->dtype == CGTP_F32                ? at_##name##_f32 \
+   : (p)->flags & CGTP_ATTN_STORAGE ? at_##name##_bf16s      \
+                                           : at_##name##_bf16)
+
+cgtp_status done(cudaError_t e) {
+  return e == cudaSuccess ? CGTP_OK : fail(CGTP_ECUDA, std::string("attention: ") + cudaGetErrorString(e));
+}
+
+cgtp_status common(const cgtp_attn_s* p, const cgtp_graph_s* g) {
+  if (!p || !g) return fail(CGTP_EINVAL, "null plan or graph");
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(CGTP_ECUDA, "no current CUDA device");
+  }
+  if (p->device != dev || g->device != dev) return fail(CGTP_EINVAL, "plan, graph and current device differ");
+  return CGTP_OK;
+}
+
+cgtp_status logit_terms(const cgtp_attn_s* p, const cgtp_graph_s* g, const void* lengths, const void* table, const void* bias, AtArgs* a) {
+  const int es = es_acc(p);
+  if (table && p->n_borders == 0) return fail(CGTP_EINVAL, "a table needs a plan with borders");
+  if (g->E > 0 && (table != nullptr) != (lengths != nullptr)) return fail(CGTP_EINVAL, "table and lengths: both or neither");
+  cgtp_status s;
+  if ((s = check_vector(lengths, es, false, "lengths")) || (s = check_vector(table, es, false, "table")) ||
+      (s = check_vector(bias, es, false, "bias")))
+    return s;
+  a->lengths = lengths;
+  a->table = table;
+  a->bias = bias;
+  return CGTP_OK;
+}
+
+// gradients of keys (and values), and of the table, from a and ds
+cgtp_status finish_backward(const cgtp_attn_s* p, const cgtp_graph_s* g, AtArgs a, bool values, cudaStream_t st) {
+  cgtp_status s;
+  side(&a, g, true);
+  if ((s = deal(p, g, values ? kSendAll : kSendKeys, &a))) return s;
+  if ((s = done(CGTP_AT_PICK(p, send)(a, values, st)))) return s;
+  if (a.n_joins) {
+    const int wk = p->kv * p->dk, wv = values ? p->kv * p->dv : 0;
+    if ((s = done(CGTP_AT_PICK(p, join_sum)(a, a.gk, wk, 0, wk + wv, st)))) return s;
+    if (values && (s = done(CGTP_AT_PICK(p, join_sum)(a, a.gv, wv, wk, wk + wv, st)))) return s;
+  }
+  if (!a.gtable) return CGTP_OK;
+  const int64_t cells = int64_t(p->n_borders + 1) * p->heads;
+  if (g->E == 0) {
+    return done(cudaMemsetAsync(a.gtable, 0, cells * es_acc(p), st));
+  }
+  // four warps a CTA where their histograms fit; a CTA for each 4096 values, one where that saves the second launch
+  a.hist_cols = p->heads <= 32 ? 32 : 64;
+  const int64_t one = int64_t(p->n_borders + 1) * a.hist_cols * es_acc(p);
+  a.hist_warps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, (p->smem_cap - 1024) / one)));
+  if (a.hist_warps * one > p->smem_cap - 1024) return fail(CGTP_EUNSUPPORTED, "bias table too large for shared memory");
+  a.hist_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(kHistCtas, p->num_sms), g->E * p->heads / 4096)));
+  return done(CGTP_AT_PICK(p, table)(a, st));
+}
+
+// receivers' kernel of the backward, with the launches that split rows need
+cgtp_status receive(const cgtp_attn_s* p, const cgtp_graph_s* g, AtArgs* a, bool edges, cudaStream_t st) {
+  side(a, g, false);
+  cgtp_status s = deal(p, g, edges ? kEdgesReceive : kReceive, a);
+  if (s) return s;
+  const auto run = edges ? CGTP_AT_PICK(p, edges_receive) : CGTP_AT_PICK(p, receive);
+  a->phase = a->n_items ? kAtFirst : kAtWhole;
+  if ((s = done(run(*a, st)))) return s;
+  if (a->n_items) {
+    a->phase = kAtSecond;
+    AtArgs b = *a;
+    const int64_t groups = b.block / 32;
+    b.grid = static_cast<unsigned>(b.warp_rows ? (b.n_items + groups - 1) / groups : b.n_items);
+    if ((s = done(run(b, st)))) return s;
+    if ((s = done(CGTP_AT_PICK(p, join_sum)(b, b.gq, p->heads * p->dk, 0, p->heads * p->dk, st)))) return s;
+  }
+  a->phase = kAtWhole;
+  return CGTP_OK;
+}
+
+}  // namespace
+}  // namespace cgtp
+
+using namespace cgtp;
+
+extern "C" {
+
+cgtp_status cgtp_attn_create(cgtp_attn* out, const char* irreps_qk, const char* irreps_v, int heads, int kv_heads, int dtype, int flags,
+                             double scale, int n_borders, const double* borders) {
+  clear_error();
+  if (!out) return fail(CGTP_EINVAL, "null plan output pointer");
+  *out = nullptr;
+  if (dtype != CGTP_F32 && dtype != CGTP_F64 && dtype != CGTP_BF16)
+    return fail(CGTP_EINVAL, "dtype must be CGTP_F32, CGTP_F64 or CGTP_BF16");
+  if (flags & ~CGTP_ATTN_STORAGE) return fail(CGTP_EINVAL, "unknown flag");
+  if ((flags & CGTP_ATTN_STORAGE) && dtype != CGTP_BF16) return fail(CGTP_EINVAL, "CGTP_ATTN_STORAGE needs CGTP_BF16");
+  if (heads < 1 || heads > kAtMaxHeads) return fail(CGTP_EINVAL, "heads must be in [1, 64]");
+  if (kv_heads < 1 || kv_heads > heads || heads % kv_heads) return fail(CGTP_EINVAL, "heads must be a multiple of kv_heads");
+  if (!std::isfinite(scale)) return fail(CGTP_EINVAL, "scale must be finite");
+  if (n_borders < 0 || n_borders > kAtMaxBorders) return fail(CGTP_EINVAL, "n_borders must be in [0, 511]");
+  if (n_borders > 0 && !borders) return fail(CGTP_EINVAL, "null borders");
+  for (int i = 0; i < n_borders; ++i)
+    if (!std::isfinite(borders[i]) || (i > 0 && borders[i] < borders[i - 1])) return fail(CGTP_EINVAL, "borders must be finite and ascending");
+  cgtp_attn_s* p = new (std::nothrow) cgtp_attn_s();
+  if (!p) return fail(CGTP_ENOMEM, "host allocation failed");
+  p->dtype = dtype;
+  p->flags = flags;
+  p->heads = heads;
+  p->kv = kv_heads;
+  p->scale = scale;
+  p->n_borders = n_borders;
+  cgtp_status s;
+  try {
+    s = create(p, irreps_qk, irreps_v, n_borders, borders);
+  } catch (const std::bad_alloc&) {
+    s = fail(CGTP_ENOMEM, "host allocation failed");
+  }
+  if (s != CGTP_OK) {
+    cgtp_attn_destroy(p);
+    return s;
+  }
+  *out = p;
+  return CGTP_OK;
+}
+
+void cgtp_attn_destroy(cgtp_attn p) {
+  if (!p) return;
+  if (p->base) cudaFree(p->base);
+  delete p;
+}
+
+cgtp_status cgtp_attn_info(cgtp_attn p, int64_t* dim_qk, int64_t* dim_v) {
+  clear_error();
+  if (!p) return fail(CGTP_EINVAL, "null plan");
+  if (dim_qk) *dim_qk = p->dk;
+  if (dim_v) *dim_v = p->dv;
+  return CGTP_OK;
+}
+
+cgtp_status cgtp_attn_device_bytes(cgtp_attn p, int64_t* bytes) {
+  clear_error();
+  if (!p || !bytes) return fail(CGTP_EINVAL, "null argument");
+  *bytes = static_cast<int64_t>(p->device_bytes);
+  return CGTP_OK;
+}
+
+cgtp_status cgtp_attn_workspace(cgtp_attn p, cgtp_graph g, int call, int64_t* bytes) {
+  clear_error();
+  if (!p || !g || !bytes) return fail(CGTP_EINVAL, "null argument");
+  if (call < CGTP_ATTN_FORWARD || call > CGTP_ATTN_EDGES_BACKWARD) return fail(CGTP_EINVAL, "unknown call");
+  *bytes = space(p, g, call).total;
+  return CGTP_OK;
+}
+
+cgtp_status cgtp_attn_forward(cgtp_attn p, cgtp_graph g, const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                              const void* lengths, const void* table, const void* bias, void* out, int64_t ld_out, void* lse, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
+  clear_error();
+  cgtp_status s = common(p, g);
+  if (s) return s;
+  AtArgs a = base_args(p, g);
+  const int es = es_store(p), er = es_result(p);
+  Tensor tq{q, ld_q, g->N, p->heads * p->dk, es, "q"}, tk{k, ld_k, g->N_src, p->kv * p->dk, es, "k"},
+      tv{v, ld_v, g->N_src, p->kv * p->dv, es, "v"}, to{out, ld_out, g->N, p->heads * p->dv, er, "out"};
+  if ((s = check(&tq, &a.q)) || (s = check(&tk, &a.k)) || (s = check(&tv, &a.v)) || (s = check(&to, &a.out)) ||
+      (s = check_vector(lse, es_acc(p), true, "lse")) || (s = logit_terms(p, g, lengths, table, bias, &a)))
+    return s;
+  const Space sp = space(p, g, CGTP_ATTN_FORWARD);
+  if ((s = take_space(sp, workspace, workspace_bytes))) return s;
+  a.part = static_cast<char*>(workspace) + sp.part;
+  a.lse = lse;
+  a.qk = choose(p->qk, p->n_qk, {&tq, &tk});
+  a.vv = choose(p->vv, p->n_vv, {&tv, &to});
+  side(&a, g, false);
+  if ((s = deal(p, g, kForward, &a))) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((s = done(CGTP_AT_PICK(p, forward)(a, st)))) return s;
+  return a.n_joins ? done(CGTP_AT_PICK(p, join_forward)(a, st)) : CGTP_OK;
+}
+
+cgtp_status cgtp_attn_backward(cgtp_attn p, cgtp_graph g, const void* gout, int64_t ld_gout, const void* q, int64_t ld_q, const void* k,
+                               int64_t ld_k, const void* v, int64_t ld_v, const void* lengths, const void* table, const void* bias,
+                               const void* lse, void* gq, int64_t ld_gq, void* gk, int64_t ld_gk, void* gv, int64_t ld_gv, void* gtable,
+                               void* gbias, void* workspace, int64_t workspace_bytes, void* stream) {
+  clear_error();
+  cgtp_status s = common(p, g);
+  if (s) return s;
+  AtArgs a = base_args(p, g);
+  const int es = es_store(p), er = es_result(p), ea = es_acc(p);
+  Tensor tq{q, ld_q, g->N, p->heads * p->dk, es, "q"}, tk{k, ld_k, g->N_src, p->kv * p->dk, es, "k"},
+      tv{v, ld_v, g->N_src, p->kv * p->dv, es, "v"}, tg{gout, ld_gout, g->N, p->heads * p->dv, es, "gout"},
+      tgq{gq, ld_gq, g->N, p->heads * p->dk, er, "gq"}, tgk{gk, ld_gk, g->N_src, p->kv * p->dk, er, "gk"},
+      tgv{gv, ld_gv, g->N_src, p->kv * p->dv, er, "gv"};
+  if ((s = check(&tq, &a.q)) || (s = check(&tk, &a.k)) || (s = check(&tv, &a.v)) || (s = check(&tg, &a.gout)) || (s = check(&tgq, &a.gq)) ||
+      (s = check(&tgk, &a.gk)) || (s = check(&tgv, &a.gv)) || (s = check_vector(lse, ea, true, "lse")) ||
+      (s = check_vector(gtable, ea, false, "gtable")) || (s = check_vector(gbias, ea, false, "gbias")) ||
+      (s = logit_terms(p, g, lengths, table, bias, &a)))
+    return s;
+  if (gtable && !table) return fail(CGTP_EINVAL, "gtable needs table");
+  const Space sp = space(p, g, CGTP_ATTN_BACKWARD);
+  if ((s = take_space(sp, workspace, workspace_bytes))) return s;
+  char* w = static_cast<char*>(workspace);
+  a.alpha = w + sp.alpha;
+  a.ds = gbias ? gbias : w + sp.ds;
+  a.part = w + sp.part;
+  a.part_sum = w + sp.part_sum;
+  a.hist = w + sp.hist;
+  a.lse = const_cast<void*>(lse);
+  a.gtable = gtable;
+  a.qk = choose(p->qk, p->n_qk, {&tq, &tk, &tgq, &tgk});
+  a.vv = choose(p->vv, p->n_vv, {&tv, &tg, &tgv});
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((s = receive(p, g, &a, false, st))) return s;
+  return finish_backward(p, g, a, true, st);
+}
+
+cgtp_status cgtp_attn_edges_forward(cgtp_attn p, cgtp_graph g, const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* w,
+                                    int64_t ld_w, const void* lengths, const void* table, const void* bias, void* out, int64_t ld_out,
+                                    void* alpha, void* workspace, int64_t workspace_bytes, void* stream) {
+  clear_error();
+  cgtp_status s = common(p, g);
+  if (s) return s;
+  if (p->flags & CGTP_ATTN_STORAGE) return fail(CGTP_EUNSUPPORTED, "edge rows take their gradient in FP32: no CGTP_ATTN_STORAGE");
+  AtArgs a = base_args(p, g);
+  const int es = es_store(p);
+  Tensor tq{q, ld_q, g->N, p->heads * p->dk, es, "q"}, tk{k, ld_k, g->N_src, p->kv * p->dk, es, "k"},
+      tw{w, ld_w, g->E, p->heads * p->dv, es, "w"}, to{out, ld_out, g->E, p->heads * p->dv, es, "out"};
+  if ((s = check(&tq, &a.q)) || (s = check(&tk, &a.k)) || (s = check(&tw, &a.v)) || (s = check(&to, &a.out)) ||
+      (s = check_vector(alpha, es_acc(p), g->E > 0, "alpha")) || (s = logit_terms(p, g, lengths, table, bias, &a)))
+    return s;
+  const Space sp = space(p, g, CGTP_ATTN_EDGES_FORWARD);
+  if ((s = take_space(sp, workspace, workspace_bytes))) return s;
+  if (g->E == 0) return CGTP_OK;
+  a.part = static_cast<char*>(workspace) + sp.part;
+  a.alpha = alpha;
+  a.qk = choose(p->qk, p->n_qk, {&tq, &tk});
+  a.vv = choose(p->vv, p->n_vv, {&tw, &to});
+  side(&a, g, false);
+  if ((s = deal(p, g, kEdgesForward, &a))) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  a.phase = a.n_items ? kAtFirst : kAtWhole;
+  if ((s = done(CGTP_AT_PICK(p, edges_forward)(a, st)))) return s;
+  if (!a.n_items) return CGTP_OK;
+  a.phase = kAtSecond;
+  const unsigned groups = a.block / 32;
+  a.grid = a.warp_rows ? (a.n_items + groups - 1) / groups : a.n_items;
+  return done(CGTP_AT_PICK(p, edges_forward)(a, st));
+}
+
+cgtp_status cgtp_attn_edges_backward(cgtp_attn p, cgtp_graph g, const void* gout, int64_t ld_gout, const void* q, int64_t ld_q, const void* k,
+                                     int64_t ld_k, const void* w, int64_t ld_w, const void* lengths, const void* alpha, void* gq,
+                                     int64_t ld_gq, void* gk, int64_t ld_gk, void* gw, int64_t ld_gw, void* gtable, void* gbias,
+                                     void* workspace, int64_t workspace_bytes, void* stream) {
+  clear_error();
+  cgtp_status s = common(p, g);
+  if (s) return s;
+  if (p->flags & CGTP_ATTN_STORAGE) return fail(CGTP_EUNSUPPORTED, "edge rows take their gradient in FP32: no CGTP_ATTN_STORAGE");
+  AtArgs a = base_args(p, g);
+  const int es = es_store(p), ea = es_acc(p);
+  Tensor tq{q, ld_q, g->N, p->heads * p->dk, es, "q"}, tk{k, ld_k, g->N_src, p->kv * p->dk, es, "k"},
+      tw{w, ld_w, g->E, p->heads * p->dv, es, "w"}, tg{gout, ld_gout, g->E, p->heads * p->dv, ea, "gout"},
+      tgq{gq, ld_gq, g->N, p->heads * p->dk, ea, "gq"}, tgk{gk, ld_gk, g->N_src, p->kv * p->dk, ea, "gk"},
+      tgw{gw, ld_gw, g->E, p->heads * p->dv, ea, "gw"};
+  if ((s = check(&tq, &a.q)) || (s = check(&tk, &a.k)) || (s = check(&tw, &a.v)) || (s = check(&tg, &a.gout)) || (s = check(&tgq, &a.gq)) ||
+      (s = check(&tgk, &a.gk)) || (s = check(&tgw, &a.gv)) || (s = check_vector(alpha, ea, g->E > 0, "alpha")) ||
+      (s = check_vector(lengths, ea, gtable && g->E > 0, "lengths")) || (s = check_vector(gtable, ea, false, "gtable")) ||
+      (s = check_vector(gbias, ea, false, "gbias")))
+    return s;
+  if (gtable && p->n_borders == 0) return fail(CGTP_EINVAL, "gtable needs a plan with borders");
+  const Space sp = space(p, g, CGTP_ATTN_EDGES_BACKWARD);
+  if ((s = take_space(sp, workspace, workspace_bytes))) return s;
+  char* ws = static_cast<char*>(workspace);
+  a.lengths = lengths;
+  a.alpha = const_cast<void*>(alpha);
+  a.ds = gbias ? gbias : ws + sp.ds;
+  a.part = ws + sp.part;
+  a.part_sum = ws + sp.part_sum;
+  a.hist = ws + sp.hist;
+  a.gtable = gtable;
+  a.qk = choose(p->qk, p->n_qk, {&tq, &tk, &tgq, &tgk});
+  a.vv = choose(p->vv, p->n_vv, {&tw, &tg, &tgw});
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((s = receive(p, g, &a, true, st))) return s;
+  return finish_backward(p, g, a, false, st);
+}
+
+}  // extern "C"

@@ -1,13 +1,13 @@
-// binding.cpp -- the Python binding's per-step calls in native code: the checks of train.py on tensors
-// and lists of tensors, the results' allocation and the call into libcgtp (include/cgtp_train.h), whose
-// entry points train.py hands over by address.
+// binding.cpp -- the Python binding's per-step calls in native code: the checks of train.py and attn.py on tensors
+// and lists of tensors, the results' allocation and the call into libcgtp (include/cgtp_train.h, include/cgtp_attn.h),
+// whose entry points these modules hand over by address.
 //
 // A training step of a small model is bound by such marshalling: reading type, size, strides and address
 // of one tensor costs about 0.4 us through the interpreter and a few ns here, and a step passes three lists
 // of all parameters.
 //
 // Every function returns its results; the library's status (an int) where that is not CGTP_OK; or
-// NotImplemented where an argument does not fit, and train.py then says which.
+// NotImplemented where an argument does not fit, and the Python module then says which.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -20,6 +20,7 @@
 #include <exception>
 #include <vector>
 
+#include "cgtp_attn.h"
 #include "cgtp_train.h"
 
 namespace {
@@ -29,8 +30,13 @@ decltype(&cgtp_resnorm_backward) lib_backward = nullptr;
 decltype(&cgtp_adamw_step) lib_step = nullptr;
 decltype(&cgtp_grad_norm) lib_norm = nullptr;
 decltype(&cgtp_adamw_state_values) lib_values = nullptr;
+decltype(&cgtp_attn_workspace) lib_attn_workspace = nullptr;
+decltype(&cgtp_attn_forward) lib_attn_forward = nullptr;
+decltype(&cgtp_attn_backward) lib_attn_backward = nullptr;
+decltype(&cgtp_attn_edges_forward) lib_attn_edges_forward = nullptr;
+decltype(&cgtp_attn_edges_backward) lib_attn_edges_backward = nullptr;
 
-// an argument that train.py has to explain
+// an argument that the Python module has to explain
 struct Misfit {};
 
 at::ScalarType type_of(int64_t code) {
@@ -359,7 +365,184 @@ PyObject* state_values(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
+// AttentionPlan._native, and Graph._native of the same device
+struct Attention {
+  cgtp_attn handle;
+  cgtp_graph graph;
+  at::ScalarType store, result, param;
+  int64_t heads, kv, dk, dv, buckets, n, n_src, e;
+  Device device;
+  Attention(PyObject* t, PyObject* g) : device(field(t, 10, 9)) {
+    const auto at_ = [&](int i) { return PyTuple_GET_ITEM(t, i); };
+    handle = static_cast<cgtp_attn>(address(at_(0)));
+    store = type_of(number(at_(1))), result = type_of(number(at_(2))), param = type_of(number(at_(3)));
+    heads = number(at_(4)), kv = number(at_(5)), dk = number(at_(6)), dv = number(at_(7)), buckets = number(at_(8));
+    if (number(field(g, 5, 4)) != device.index) throw Misfit();
+    graph = static_cast<cgtp_graph>(address(PyTuple_GET_ITEM(g, 0)));
+    n = number(PyTuple_GET_ITEM(g, 1)), n_src = number(PyTuple_GET_ITEM(g, 2)), e = number(PyTuple_GET_ITEM(g, 3));
+  }
+  Rows q(PyObject* o) const { return given(rows(o, store, device, n, heads * dk), n); }
+  Rows k(PyObject* o) const { return given(rows(o, store, device, n_src, kv * dk), n_src); }
+  Rows v(PyObject* o) const { return given(rows(o, store, device, n_src, kv * dv), n_src); }
+  Rows w(PyObject* o, at::ScalarType type) const { return given(rows(o, type, device, e, heads * dv), e); }
+  static Rows given(Rows r, int64_t count) {
+    if (!r.p && count) throw Misfit();
+    return r;
+  }
+  void* lengths(PyObject* o) const { return vector(o, param, device, e); }
+  void* grid(PyObject* o, int64_t rows_, int64_t cols) const {   // a contiguous [rows, cols]
+    if (o == Py_None) return nullptr;
+    const at::Tensor& t = tensor(o, param, device);
+    if (t.dim() != 2 || t.size(0) != rows_ || t.size(1) != cols || !t.is_contiguous()) throw Misfit();
+    return t.data_ptr();
+  }
+  void* table(PyObject* o) const {
+    if (o != Py_None && buckets == 0) throw Misfit();
+    return grid(o, buckets, heads);
+  }
+  void* edges(PyObject* o) const { return grid(o, e, heads); }
+};
+
+// results in the order of the tuple that a call returns: `given` (a tensor) or a new one
+struct Results {
+  Held held;
+  const at::Tensor& like;
+  Rows rows_(PyObject* given, const Device& device, int64_t n, int64_t width, at::ScalarType type) {
+    if (given != Py_None) {
+      const Rows r = rows(given, type, device, n, width);
+      held.same(given);
+      return r;
+    }
+    const Result r = fresh({n, width}, type, like);
+    held.keep(r.object);
+    return {r.p, 0};
+  }
+  void* grid(int64_t n, int64_t width, at::ScalarType type) {
+    const Result r = fresh({n, width}, type, like);
+    held.keep(r.object);
+    return r.p;
+  }
+};
+
+// the call's workspace, from torch's allocator on the current stream
+struct Workspace {
+  at::Tensor t;
+  void* p = nullptr;
+  int64_t bytes = 0;
+  cgtp_status status;
+  Workspace(const Attention& a, int call, const at::Tensor& like) {
+    status = lib_attn_workspace(a.handle, a.graph, call, &bytes);
+    if (status == CGTP_OK && bytes > 0) {
+      t = at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(like.device()));
+      p = t.data_ptr();
+    }
+  }
+};
+
+// (plan, graph, q, k, v, lengths, table, bias, out, stream) -> (out, lse)
+PyObject* attn_forward(PyObject*, PyObject* const* x, Py_ssize_t n_args) {
+  return guarded([&]() -> PyObject* {
+    if (n_args != 10) throw Misfit();
+    const Attention a(x[0], x[1]);
+    const Rows q = a.q(x[2]), k = a.k(x[3]), v = a.v(x[4]);
+    const void *lengths = a.lengths(x[5]), *table = a.table(x[6]), *bias = a.edges(x[7]);
+    if ((x[5] == Py_None) != (x[6] == Py_None)) throw Misfit();
+    Results r{{}, THPVariable_Unpack(x[2])};
+    const Rows out = r.rows_(x[8], a.device, a.n, a.heads * a.dv, a.result);
+    void* lse = r.grid(a.n, a.heads, a.param);
+    const Workspace ws(a, CGTP_ATTN_FORWARD, r.like);
+    if (ws.status != CGTP_OK) return PyLong_FromLong(ws.status);
+    const cgtp_status s = lib_attn_forward(a.handle, a.graph, q.p, q.ld, k.p, k.ld, v.p, v.ld, lengths, table, bias, out.p, out.ld, lse, ws.p,
+                                           ws.bytes, address(x[9]));
+    return s == CGTP_OK ? r.held.tuple() : PyLong_FromLong(s);
+  });
+}
+
+// (plan, graph, gout, q, k, v, lse, lengths, table, bias, need_gbias, stream) -> (gq, gk, gv, gtable, gbias)
+PyObject* attn_backward(PyObject*, PyObject* const* x, Py_ssize_t n_args) {
+  return guarded([&]() -> PyObject* {
+    if (n_args != 12) throw Misfit();
+    const Attention a(x[0], x[1]);
+    const Rows gout = Attention::given(rows(x[2], a.store, a.device, a.n, a.heads * a.dv), a.n);
+    const Rows q = a.q(x[3]), k = a.k(x[4]), v = a.v(x[5]);
+    if (x[6] == Py_None) throw Misfit();
+    const void *lse = a.grid(x[6], a.n, a.heads), *lengths = a.lengths(x[7]), *table = a.table(x[8]), *bias = a.edges(x[9]);
+    if ((x[7] == Py_None) != (x[8] == Py_None)) throw Misfit();
+    Results r{{}, THPVariable_Unpack(x[3])};
+    void* gq = r.grid(a.n, a.heads * a.dk, a.result);
+    void* gk = r.grid(a.n_src, a.kv * a.dk, a.result);
+    void* gv = r.grid(a.n_src, a.kv * a.dv, a.result);
+    void *gtable = nullptr, *gbias = nullptr;
+    if (table) gtable = r.grid(a.buckets, a.heads, a.param);
+    else r.held.none();
+    if (PyObject_IsTrue(x[10]) == 1) gbias = r.grid(a.e, a.heads, a.param);
+    else r.held.none();
+    const Workspace ws(a, CGTP_ATTN_BACKWARD, r.like);
+    if (ws.status != CGTP_OK) return PyLong_FromLong(ws.status);
+    const cgtp_status s = lib_attn_backward(a.handle, a.graph, gout.p, gout.ld, q.p, q.ld, k.p, k.ld, v.p, v.ld, lengths, table, bias, lse, gq, 0,
+                                            gk, 0, gv, 0, gtable, gbias, ws.p, ws.bytes, address(x[11]));
+    return s == CGTP_OK ? r.held.tuple() : PyLong_FromLong(s);
+  });
+}
+
+// (plan, graph, q, k, w, lengths, table, bias, out, stream) -> (w', alpha)
+PyObject* attn_edges_forward(PyObject*, PyObject* const* x, Py_ssize_t n_args) {
+  return guarded([&]() -> PyObject* {
+    if (n_args != 10) throw Misfit();
+    const Attention a(x[0], x[1]);
+    const Rows q = a.q(x[2]), k = a.k(x[3]), w = a.w(x[4], a.store);
+    const void *lengths = a.lengths(x[5]), *table = a.table(x[6]), *bias = a.edges(x[7]);
+    if ((x[5] == Py_None) != (x[6] == Py_None)) throw Misfit();
+    Results r{{}, THPVariable_Unpack(x[2])};
+    const Rows out = r.rows_(x[8], a.device, a.e, a.heads * a.dv, a.store);
+    void* alpha = r.grid(a.e, a.heads, a.param);
+    const Workspace ws(a, CGTP_ATTN_EDGES_FORWARD, r.like);
+    if (ws.status != CGTP_OK) return PyLong_FromLong(ws.status);
+    const cgtp_status s = lib_attn_edges_forward(a.handle, a.graph, q.p, q.ld, k.p, k.ld, w.p, w.ld, lengths, table, bias, out.p, out.ld, alpha,
+                                                 ws.p, ws.bytes, address(x[9]));
+    return s == CGTP_OK ? r.held.tuple() : PyLong_FromLong(s);
+  });
+}
+
+// (plan, graph, gout, q, k, w, alpha, lengths, need_gbias, gw, stream) -> (gq, gk, gw, gtable, gbias)
+PyObject* attn_edges_backward(PyObject*, PyObject* const* x, Py_ssize_t n_args) {
+  return guarded([&]() -> PyObject* {
+    if (n_args != 11) throw Misfit();
+    const Attention a(x[0], x[1]);
+    const Rows gout = a.w(x[2], a.param), q = a.q(x[3]), k = a.k(x[4]), w = a.w(x[5], a.store);
+    if (x[6] == Py_None) throw Misfit();
+    const void *alpha = a.edges(x[6]), *lengths = a.lengths(x[7]);
+    if (x[7] != Py_None && a.buckets == 0) throw Misfit();
+    Results r{{}, THPVariable_Unpack(x[3])};
+    void* gq = r.grid(a.n, a.heads * a.dk, a.param);
+    void* gk = r.grid(a.n_src, a.kv * a.dk, a.param);
+    const Rows gw = r.rows_(x[9], a.device, a.e, a.heads * a.dv, a.param);
+    void *gtable = nullptr, *gbias = nullptr;
+    if (x[7] != Py_None) gtable = r.grid(a.buckets, a.heads, a.param);
+    else r.held.none();
+    if (PyObject_IsTrue(x[8]) == 1) gbias = r.grid(a.e, a.heads, a.param);
+    else r.held.none();
+    const Workspace ws(a, CGTP_ATTN_EDGES_BACKWARD, r.like);
+    if (ws.status != CGTP_OK) return PyLong_FromLong(ws.status);
+    const cgtp_status s = lib_attn_edges_backward(a.handle, a.graph, gout.p, gout.ld, q.p, q.ld, k.p, k.ld, w.p, w.ld, lengths, alpha, gq, 0, gk,
+                                                  0, gw.p, gw.ld, gtable, gbias, ws.p, ws.bytes, address(x[10]));
+    return s == CGTP_OK ? r.held.tuple() : PyLong_FromLong(s);
+  });
+}
+
 // addresses of the library's entry points
+PyObject* connect_attn(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return guarded([&]() -> PyObject* {
+    if (n_args != 5) throw Misfit();
+    lib_attn_workspace = reinterpret_cast<decltype(lib_attn_workspace)>(address(a[0]));
+    lib_attn_forward = reinterpret_cast<decltype(lib_attn_forward)>(address(a[1]));
+    lib_attn_backward = reinterpret_cast<decltype(lib_attn_backward)>(address(a[2]));
+    lib_attn_edges_forward = reinterpret_cast<decltype(lib_attn_edges_forward)>(address(a[3]));
+    lib_attn_edges_backward = reinterpret_cast<decltype(lib_attn_edges_backward)>(address(a[4]));
+    Py_RETURN_NONE;
+  });
+}
+
 PyObject* connect(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
     if (n_args != 5) throw Misfit();
@@ -383,6 +566,11 @@ PyMethodDef methods[] = {{"connect", fast<connect>(), METH_FASTCALL, nullptr},
                          {"adamw_step", fast<adamw_step>(), METH_FASTCALL, nullptr},
                          {"grad_norm", fast<grad_norm>(), METH_FASTCALL, nullptr},
                          {"state_values", fast<state_values>(), METH_FASTCALL, nullptr},
+                         {"connect_attn", fast<connect_attn>(), METH_FASTCALL, nullptr},
+                         {"attn_forward", fast<attn_forward>(), METH_FASTCALL, nullptr},
+                         {"attn_backward", fast<attn_backward>(), METH_FASTCALL, nullptr},
+                         {"attn_edges_forward", fast<attn_edges_forward>(), METH_FASTCALL, nullptr},
+                         {"attn_edges_backward", fast<attn_edges_backward>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -153,6 +153,7 @@ extern "C" {
 cgtp_status cgtp_conv_double_backward_workspace(cgtp_plan plan, cgtp_graph graph, int64_t* bytes) {
   clear_error();
   if (!plan || !graph || !bytes) return fail(CGTP_EINVAL, "null plan, graph or bytes");
+  if (const cgtp_status one = one_set(graph)) return one;
   *bytes = workspace_bytes(plan, graph->N, graph->E);
   return CGTP_OK;
 }
@@ -164,6 +165,7 @@ cgtp_status cgtp_conv_double_backward(cgtp_plan plan, cgtp_graph graph, const vo
                                       int64_t workspace_size, void* stream) {
   clear_error();
   if (!plan || !graph) return fail(CGTP_EINVAL, "null plan or graph");
+  if (const cgtp_status one = one_set(graph)) return one;
   if (plan->radial_k == 0 && (M || ggM || d_M))
     return fail(CGTP_EINVAL, "M, ggM and d_M must be NULL for per-edge weights");
   const void* a[4] = {x, Y, W_or_R, M};

@@ -8,18 +8,20 @@
 // grouped by sender, ascending inside each sender -- a stable sort by sender)
 // and t_dst (receiver of each such edge).
 //
-// Steps: (1) check rowptr[0] = 0, rowptr[N] = E, rowptr monotone, 0 <= col < N;
+// Steps: (1) check rowptr[0] = 0, rowptr[N] = E, rowptr monotone, 0 <= col < N_src;
 // (2) out-degree histogram (integer atomics: the counts are exact);
 // (3) exclusive scan -> t_rowptr; (4) scatter positions into their sender
 // segment (integer atomics pick slots in arbitrary order); (5) sort each
 // segment ascending, which makes the result unique and bit-exact; (6) t_dst by
-// binary search of rowptr.
+// binary search of rowptr; (7) cut the rows of more than `chunk` edges, of either side, into pieces.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <climits>
 #include <mutex>
+#include <new>
 #include <string>
+#include <vector>
 
 #include "internal.h"
 
@@ -33,7 +35,7 @@ constexpr int kScanTile = 1024;
 
 enum : int { kBadRow0 = 1, kBadRowN = 2, kNotMonotone = 4, kBadCol = 8, kTooLong = 16 };
 
-__global__ void csr_check_kernel(const int* rowptr, const int* col, int N, int E, int* flag) {
+__global__ void csr_check_kernel(const int* rowptr, const int* col, int N, int N_src, int E, int* flag) {
   int bits = 0;
   const int total = max(N + 1, E);
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < total; i += gridDim.x * blockDim.x) {
@@ -45,7 +47,7 @@ __global__ void csr_check_kernel(const int* rowptr, const int* col, int N, int E
     }
     if (i < E) {
       const int c = col[i];
-      if (c < 0 || c >= N) bits |= kBadCol;
+      if (c < 0 || c >= N_src) bits |= kBadCol;
     }
   }
   if (bits) atomicOr(flag, bits);
@@ -172,24 +174,87 @@ __global__ void dst_kernel(const int* rowptr, int N, const int* t_eid, int E, in
   }
 }
 
+// Most edges of a row, and the rows of more than `chunk` edges (row, first edge, last edge; in any order).
+__global__ void long_rows_kernel(const int* rowptr, int n, int chunk, int* most, int* count, int* list) {
+  int top = 0;
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) {
+    const int b = rowptr[i], e = rowptr[i + 1];
+    top = max(top, e - b);
+    if (e - b > chunk) {
+      int* at = list + 3 * static_cast<size_t>(atomicAdd(count, 1));
+      at[0] = i;
+      at[1] = b;
+      at[2] = e;
+    }
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((threadIdx.x & 31) == 0 && top > 0) atomicMax(most, top);
+}
+
+// Edges of the longest row that is not split: a few pieces an SM where all edges belong to long rows, and no fewer
+// than 64, so that the joining of partial results stays small beside a piece.
+int chunk_of(int64_t E) {
+  int c = 64;
+  while (c < 512 && E / (4 * 152) >= 2 * c) c *= 2;
+  return c;
+}
+
+// The pieces of the listed rows, on the device.
+cgtp_status split_rows(GraphSplit* s, const int* list_dev, int count, int chunk, cudaStream_t st) {
+  if (count == 0) return CGTP_OK;
+  struct Row {
+    int row, e0, e1;
+  };
+  std::vector<Row> rows(count);
+  if (cudaMemcpyAsync(rows.data(), list_dev, count * sizeof(Row), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
+    return fail(CGTP_ECUDA, "reading the long rows failed");
+  std::sort(rows.begin(), rows.end(), [](const Row& a, const Row& b) { return a.row < b.row; });
+  std::vector<Int4> items, joins;
+  for (const Row& r : rows) {
+    const int64_t len = r.e1 - r.e0, n = (len + chunk - 1) / chunk;
+    joins.push_back({r.row, static_cast<int>(items.size()), static_cast<int>(n), 0});
+    for (int64_t i = 0; i < n; ++i)
+      items.push_back({r.row, r.e0 + static_cast<int>(len * i / n), r.e0 + static_cast<int>(len * (i + 1) / n),
+                       static_cast<int>(joins.size()) - 1});
+  }
+  s->n_items = static_cast<int>(items.size());
+  s->n_joins = static_cast<int>(joins.size());
+  items.insert(items.end(), joins.begin(), joins.end());
+  void* dev = nullptr;
+  if (cudaMalloc(&dev, items.size() * sizeof(Int4)) != cudaSuccess) {
+    cudaGetLastError();
+    s->n_items = s->n_joins = 0;
+    return fail(CGTP_ENOMEM, "graph allocation failed");
+  }
+  s->items = static_cast<Int4*>(dev);
+  s->joins = s->items + s->n_items;
+  return upload(dev, items.data(), items.size() * sizeof(Int4)) ? CGTP_OK : fail(CGTP_ECUDA, "graph upload failed");
+}
+
 }  // namespace
 
 cgtp_status graph_build(cgtp_graph_s* g, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int N = static_cast<int>(g->N), E = static_cast<int>(g->E);
-  int* scratch = nullptr;  // flag | total | counts/cursor [N+1] | tile sums
-  const int ntiles = (N + 1 + kScanTile - 1) / kScanTile;
-  const size_t words = 2 + static_cast<size_t>(N + 1) + ntiles;
-  if (cudaMalloc(&scratch, words * sizeof(int)) != cudaSuccess)
+  const int N = static_cast<int>(g->N), M = static_cast<int>(g->N_src), E = static_cast<int>(g->E);
+  g->chunk = chunk_of(E);
+  // flag | total | most edges and long rows of either side [4] | counts/cursor [M+1] | tile sums | long rows [2][3 cap]
+  int* scratch = nullptr;
+  const int ntiles = (M + 1 + kScanTile - 1) / kScanTile;
+  const size_t cap = static_cast<size_t>(E / g->chunk) + 1;
+  const size_t words = 6 + static_cast<size_t>(M + 1) + ntiles, all = words + 6 * cap;
+  if (cudaMalloc(&scratch, all * sizeof(int)) != cudaSuccess)
     return fail(CGTP_ENOMEM, "graph scratch allocation failed");
   int* flag = scratch;
   int* total = scratch + 1;
-  int* counts = scratch + 2;
-  int* sums = counts + (N + 1);
+  int* found = scratch + 2;   // most edges and number of long rows: receivers, sources
+  int* counts = scratch + 6;
+  int* sums = counts + (M + 1);
+  int* list = scratch + words;
   cudaMemsetAsync(scratch, 0, words * sizeof(int), st);
   const int threads = 256;
   auto blocks = [](int64_t n) { return static_cast<int>(std::min<int64_t>((n + 255) / 256, 4096)); };
-  csr_check_kernel<<<std::max(1, blocks(std::max(N + 1, E))), threads, 0, st>>>(g->rowptr, g->col, N, E, flag);
+  csr_check_kernel<<<std::max(1, blocks(std::max(N + 1, E))), threads, 0, st>>>(g->rowptr, g->col, N, M, E, flag);
   int hflag = 0;
   cudaMemcpyAsync(&hflag, flag, sizeof(int), cudaMemcpyDeviceToHost, st);
   cudaError_t err = cudaStreamSynchronize(st);
@@ -203,18 +268,18 @@ cgtp_status graph_build(cgtp_graph_s* g, void* stream) {
     if (hflag & kBadRow0) why += " rowptr[0] != 0;";
     if (hflag & kBadRowN) why += " rowptr[N] != E;";
     if (hflag & kNotMonotone) why += " rowptr not monotone;";
-    if (hflag & kBadCol) why += " col out of [0, N);";
+    if (hflag & kBadCol) why += " col out of [0, N_src);";
     return fail(CGTP_EGRAPH, "invalid CSR:" + why);
   }
   if (E > 0) histogram_kernel<<<blocks(E), threads, 0, st>>>(g->col, E, counts);
-  // counts[N] = 0 -> exclusive scan over N+1 entries gives t_rowptr with t_rowptr[N] = E
-  scan_tiles_kernel<<<ntiles, 256, 0, st>>>(counts, N + 1, g->t_rowptr, sums);
+  // counts[M] = 0 -> exclusive scan over M+1 entries gives t_rowptr with t_rowptr[M] = E
+  scan_tiles_kernel<<<ntiles, 256, 0, st>>>(counts, M + 1, g->t_rowptr, sums);
   scan_sums_kernel<<<1, 32, 0, st>>>(sums, ntiles, total);
-  add_offsets_kernel<<<blocks(N + 1), threads, 0, st>>>(g->t_rowptr, N + 1, sums);
+  add_offsets_kernel<<<blocks(M + 1), threads, 0, st>>>(g->t_rowptr, M + 1, sums);
   if (E > 0) {
-    cudaMemcpyAsync(counts, g->t_rowptr, sizeof(int) * (N + 1), cudaMemcpyDeviceToDevice, st);
+    cudaMemcpyAsync(counts, g->t_rowptr, sizeof(int) * (M + 1), cudaMemcpyDeviceToDevice, st);
     scatter_kernel<<<blocks(E), threads, 0, st>>>(g->col, E, counts, g->t_eid);
-    sort_short_kernel<<<std::max(1, std::min((N + 3) / 4, 4096)), 128, 0, st>>>(g->t_rowptr, N, g->t_eid, flag);
+    sort_short_kernel<<<std::max(1, std::min((M + 3) / 4, 4096)), 128, 0, st>>>(g->t_rowptr, M, g->t_eid, flag);
     const size_t lsm = kSortBlock * sizeof(int);
     err = cudaFuncSetAttribute(sort_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)lsm);
     if (err != cudaSuccess) {
@@ -222,18 +287,30 @@ cgtp_status graph_build(cgtp_graph_s* g, void* stream) {
       cudaFree(scratch);
       return fail(CGTP_ECUDA, std::string("graph build (sort shared memory): ") + cudaGetErrorString(err));
     }
-    sort_long_kernel<<<std::max(1, std::min(N, 1024)), 1024, lsm, st>>>(g->t_rowptr, N, g->t_eid);
+    sort_long_kernel<<<std::max(1, std::min(M, 1024)), 1024, lsm, st>>>(g->t_rowptr, M, g->t_eid);
     dst_kernel<<<blocks(E), threads, 0, st>>>(g->rowptr, N, g->t_eid, E, g->t_dst);
+    long_rows_kernel<<<blocks(N), threads, 0, st>>>(g->rowptr, N, g->chunk, found, found + 1, list);
+    long_rows_kernel<<<blocks(M), threads, 0, st>>>(g->t_rowptr, M, g->chunk, found + 2, found + 3, list + 3 * cap);
   }
   // a launch refused for its configuration is reported here, not by the synchronisation
   const cudaError_t lerr = cudaGetLastError();
-  cudaMemcpyAsync(&hflag, flag, sizeof(int), cudaMemcpyDeviceToHost, st);
+  int head[6] = {};
+  cudaMemcpyAsync(head, scratch, sizeof(head), cudaMemcpyDeviceToHost, st);
   err = cudaStreamSynchronize(st);
+  cgtp_status s = CGTP_OK;
+  if (lerr != cudaSuccess) s = fail(CGTP_ECUDA, std::string("graph build launch: ") + cudaGetErrorString(lerr));
+  else if (err != cudaSuccess) s = fail(CGTP_ECUDA, std::string("graph build: ") + cudaGetErrorString(err));
+  else if (head[0] & kTooLong) s = fail(CGTP_EUNSUPPORTED, "a sender has more than 32768 out-edges");
+  g->max_in = head[2];
+  g->max_out = head[4];
+  try {
+    if (s == CGTP_OK) s = split_rows(&g->split, list, head[3], g->chunk, st);
+    if (s == CGTP_OK) s = split_rows(&g->split_t, list + 3 * cap, head[5], g->chunk, st);
+  } catch (const std::bad_alloc&) {
+    s = fail(CGTP_ENOMEM, "host allocation failed");
+  }
   cudaFree(scratch);
-  if (lerr != cudaSuccess) return fail(CGTP_ECUDA, std::string("graph build launch: ") + cudaGetErrorString(lerr));
-  if (err != cudaSuccess) return fail(CGTP_ECUDA, std::string("graph build: ") + cudaGetErrorString(err));
-  if (hflag & kTooLong) return fail(CGTP_EUNSUPPORTED, "a sender has more than 32768 out-edges");
-  return CGTP_OK;
+  return s;
 }
 
 }  // namespace cgtp
@@ -313,7 +390,7 @@ extern "C" cgtp_status cgtp_graph_transpose_noalloc(const int32_t* rowptr, const
     return fail(CGTP_ECUDA, "clearing the transpose scratch failed");
   const int threads = 256;
   auto blocks = [](int64_t k) { return static_cast<int>(std::min<int64_t>((k + 255) / 256, 4096)); };
-  csr_check_kernel<<<std::max(1, blocks(std::max(n + 1, e))), threads, 0, st>>>(rowptr, col, n, e, flag);
+  csr_check_kernel<<<std::max(1, blocks(std::max(n + 1, e))), threads, 0, st>>>(rowptr, col, n, n, e, flag);
   int hflag = 0;
   cudaMemcpyAsync(&hflag, flag, sizeof(int), cudaMemcpyDeviceToHost, st);
   cudaError_t err = cudaStreamSynchronize(st);

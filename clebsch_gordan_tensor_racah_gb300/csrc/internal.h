@@ -160,10 +160,28 @@ struct cgtp_plan_s {
   long long wait_limit = 1ll << 22;
 };
 
+namespace cgtp {
+
+struct alignas(16) Int4 {
+  int x, y, z, w;
+};
+
+// Rows of more than `chunk` edges cut into pieces of like length, for kernels that deal rows out one at a time
+// (attn.cu).  items: row, first edge, last edge, its place in joins; joins: row, first item, number of items.
+struct GraphSplit {
+  const Int4 *items = nullptr, *joins = nullptr;   // one device allocation, at items
+  int n_items = 0, n_joins = 0;
+};
+
+}  // namespace cgtp
+
 struct cgtp_graph_s {
   const int32_t* rowptr = nullptr;
   const int32_t* col = nullptr;
-  int64_t N = 0, E = 0;
+  int64_t N = 0, N_src = 0, E = 0;   // receivers, sources (the same nodes where equal), edges
+  int chunk = 0;                     // longest run of edges of one row that is not split
+  int max_in = 0, max_out = 0;       // most edges of a receiver, of a source
+  cgtp::GraphSplit split, split_t;   // receivers, sources
   int32_t* t_rowptr = nullptr;
   int32_t* t_eid = nullptr;
   int32_t* t_dst = nullptr;
@@ -237,6 +255,10 @@ bool bt_backward(const cgtp_plan_s* plan, const void* gout, const void* x1, cons
 
 // graph.cu
 cgtp_status graph_build(cgtp_graph_s* g, void* stream);
+// CGTP_EGRAPH for a graph whose sources are not its receivers: convolutions need one set of nodes.
+inline cgtp_status one_set(const cgtp_graph_s* g) {
+  return g->N == g->N_src ? CGTP_OK : fail(CGTP_EGRAPH, "the graph's sources are another set than its receivers");
+}
 
 // uvw.cu
 cgtp_status uvw_create(cgtp_plan_s* plan);

@@ -285,6 +285,7 @@ cgtp_status cgtp_mixed_plan_info(cgtp_mixed_plan plan, int64_t* d1, int64_t* d2,
 cgtp_status cgtp_mixed_conv_workspace(cgtp_mixed_plan plan, cgtp_graph graph, int64_t* bytes) {
   clear_error();
   if (!plan || !graph || !bytes) return fail(CGTP_EINVAL, "null plan, graph or bytes");
+  if (const cgtp_status one = one_set(graph)) return one;
   Carve c;
   cgtp_status s = carve(plan, graph, &c);
   if (!s) *bytes = c.total;
@@ -296,6 +297,7 @@ cgtp_status cgtp_mixed_conv_forward(cgtp_mixed_plan plan, cgtp_graph graph, cons
                                     int64_t workspace_size, void* stream) {
   clear_error();
   if (!plan || !graph) return fail(CGTP_EINVAL, "null plan or graph");
+  if (const cgtp_status one = one_set(graph)) return one;
   if (graph->N == 0) return CGTP_OK;
   Carve c;
   cgtp_status s;
@@ -315,6 +317,7 @@ cgtp_status cgtp_mixed_conv_backward(cgtp_mixed_plan plan, cgtp_graph graph, con
                                      void* gWw, void* workspace, int64_t workspace_size, void* stream) {
   clear_error();
   if (!plan || !graph) return fail(CGTP_EINVAL, "null plan or graph");
+  if (const cgtp_status one = one_set(graph)) return one;
   Carve c;
   cgtp_status s;
   if ((s = check_ws(plan, graph, workspace, workspace_size, &c))) return s;
@@ -345,6 +348,7 @@ cgtp_status cgtp_mixed_conv_double_backward(cgtp_mixed_plan plan, cgtp_graph gra
                                             int64_t workspace_size, void* stream) {
   clear_error();
   if (!plan || !graph) return fail(CGTP_EINVAL, "null plan or graph");
+  if (const cgtp_status one = one_set(graph)) return one;
   Carve c;
   cgtp_status s;
   if ((s = check_ws(plan, graph, workspace, workspace_size, &c))) return s;

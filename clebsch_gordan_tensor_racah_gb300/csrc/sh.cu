@@ -164,6 +164,7 @@ cgtp_status cgtp_conv_forward_sh(cgtp_plan plan, cgtp_graph g, const void* x, co
                                  void* out, void* stream) {
   clear_error();
   if (!plan || !g) return fail(CGTP_EINVAL, "null plan or graph");
+  if (const cgtp_status one = one_set(g)) return one;
   cgtp_status s;
   if ((s = sh_check(plan))) return s;
   if (!x || !out || (g->E > 0 && (!rvec || !W))) return fail(CGTP_EINVAL, "null x, rvec, W or out");
@@ -181,6 +182,7 @@ cgtp_status cgtp_conv_backward_sh(cgtp_plan plan, cgtp_graph g, const void* gout
                                   const void* W, void* gx, void* gY, void* grvec, void* gW, void* stream) {
   clear_error();
   if (!plan || !g) return fail(CGTP_EINVAL, "null plan or graph");
+  if (const cgtp_status one = one_set(g)) return one;
   cgtp_status s;
   if ((s = sh_check(plan))) return s;
   if (!gout || !x || !gx || (g->E > 0 && (!rvec || !W || !gY || !grvec || !gW)))
@@ -211,6 +213,7 @@ cgtp_status cgtp_conv_forward_sh_radial(cgtp_plan plan, cgtp_graph g, const void
                                         const void* M, double rbf_lo, double rbf_hi, void* out, void* stream) {
   clear_error();
   if (!plan || !g) return fail(CGTP_EINVAL, "null plan or graph");
+  if (const cgtp_status one = one_set(g)) return one;
   cgtp_status s;
   if ((s = sh_radial_check(plan, rbf_lo, rbf_hi))) return s;
   if (!x || !M || !out || (g->E > 0 && !rvec)) return fail(CGTP_EINVAL, "null x, rvec, M or out");
@@ -224,6 +227,7 @@ cgtp_status cgtp_conv_backward_sh_radial(cgtp_plan plan, cgtp_graph g, const voi
                                          void* gx, void* gY, void* gR, void* grvec, void* gM, void* stream) {
   clear_error();
   if (!plan || !g) return fail(CGTP_EINVAL, "null plan or graph");
+  if (const cgtp_status one = one_set(g)) return one;
   cgtp_status s;
   if ((s = sh_radial_check(plan, rbf_lo, rbf_hi))) return s;
   if (!gout || !x || !M || !gx || !gM || (g->E > 0 && (!rvec || !gY || !gR || !grvec)))

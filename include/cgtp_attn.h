@@ -1,0 +1,119 @@
+/*
+ * cgtp_attn.h -- C ABI of the attention along a graph's edges: receivers attend to the states of
+ * their sources (the same nodes, or another set of another size), with a learned bias by distance
+ * buckets; and the same attention applied to the rows of per-edge weights that a convolution of cgtp.h
+ * reads, so that its messages are what the attention sums.  Same library, status codes, element types
+ * and stream rules as cgtp.h.  The paper pages have no counterpart: "An Efficient Sparse Kernel
+ * Generator ...", "Sobek ..." and "LunaTP ..." leave the weighing of messages to the user's model.
+ */
+#ifndef CGTP_ATTN_H
+#define CGTP_ATTN_H
+
+#include "cgtp.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct cgtp_attn_s* cgtp_attn;
+
+/*
+ * cgtp_graph_create_cross -- cgtp_graph_create for sources that are a set of their own: col[e] in
+ * [0, N_src), N_src in [1, 2^31-1).  For the attention only where N_src differs from N; convolutions refuse
+ * such a graph (CGTP_EGRAPH).  t_rowptr of its transpose has N_src + 1 entries.
+ */
+cgtp_status cgtp_graph_create_cross(cgtp_graph* graph, const int32_t* rowptr, const int32_t* col, int64_t N,
+                                    int64_t N_src, int64_t E, void* stream);
+
+/*
+ * Attention.  For an edge e of receiver n, s = col[e], heads h < heads, shared heads g = h / (heads / kv_heads):
+ *
+ *   z[e,h]   = scale <q[n,h], k[s,g]> + table[bucket(lengths[e]), h] + bias[e,h]
+ *   a[e,h]   = exp(z[e,h]) / (sum of exp(z[.,h]) over the edges of n)
+ *   out[n,h] = sum over the edges of n of a[e,h] v[s,g]
+ *
+ * bucket(r) = number of borders <= r (0 for a NaN).  An edge whose logit is -infinity for a head (a mask
+ * put into bias or table) is left out for that head, and a weight of zero takes nothing from its edge,
+ * whatever the rows hold; a receiver without edges left has a row of zeros and lse = -infinity.
+ * The inner product of irreps rows is invariant under rotations, so are the weights.
+ *
+ *  irreps_qk, irreps_v : irreps of ONE head's queries and keys, and values.  A row holds the heads side by
+ *      side in every block: block b of "MULxLP" has heads * MUL channels of 2L+1 components (kv_heads * MUL
+ *      for k and v), head h the channels [h MUL, (h+1) MUL).  A block of scalars "Dx0e" alone gives rows
+ *      [heads, D].  Rows of up to 8192 elements, heads <= 64, a multiple of kv_heads.
+ *  dtype : CGTP_F32, CGTP_F64: every tensor in that type.  CGTP_BF16: q, k, v, gout and edge rows in bfloat16,
+ *      results and gradients in FP32, as CGTP_BF16 plans of cgtp.h have it; with CGTP_ATTN_STORAGE
+ *      out, gq, gk, gv in bfloat16 too.  lengths, table, bias, lse, alpha and their gradients are FP32 (FP64
+ *      for CGTP_F64), arithmetic and sums too.
+ *  borders [n_borders] : HOST array, ascending, at most 511, rounded to the type of the lengths; n_borders = 0: no table.
+ * The plan owns its tables only: calls of the same plan may overlap, each with a workspace of its own.
+ */
+#define CGTP_ATTN_STORAGE 1
+cgtp_status cgtp_attn_create(cgtp_attn* plan, const char* irreps_qk, const char* irreps_v, int heads, int kv_heads,
+                             int dtype, int flags, double scale, int n_borders, const double* borders);
+void cgtp_attn_destroy(cgtp_attn plan);
+/* Elements of one head's queries and values.  Any pointer may be NULL. */
+cgtp_status cgtp_attn_info(cgtp_attn plan, int64_t* dim_qk, int64_t* dim_v);
+/* Device memory of the plan, as cgtp_plan_device_bytes. */
+cgtp_status cgtp_attn_device_bytes(cgtp_attn plan, int64_t* bytes);
+
+/* Bytes of DEVICE workspace (16-byte aligned) of a call on that graph; 0 where none is needed. */
+typedef enum {
+  CGTP_ATTN_FORWARD = 0, CGTP_ATTN_BACKWARD = 1, CGTP_ATTN_EDGES_FORWARD = 2, CGTP_ATTN_EDGES_BACKWARD = 3
+} cgtp_attn_call;
+cgtp_status cgtp_attn_workspace(cgtp_attn plan, cgtp_graph graph, int call, int64_t* bytes);
+
+/*
+ * cgtp_attn_forward
+ *  q [N, heads*dim_qk], k [N_src, kv_heads*dim_qk], v [N_src, kv_heads*dim_v] -> out [N, heads*dim_v],
+ *  lse [N, heads] = log of the sums of exponentials (for the backward).
+ *  lengths [E], table [n_borders+1, heads] : both or neither.  bias [E, heads] or NULL.
+ *  ld_* : distance between rows in elements (0: rows are contiguous), so that q, k and v may be column
+ *      ranges of one product's output.  Row tensors need the alignment of their element only; 16-byte aligned
+ *      rows are faster.
+ *  Outputs may not overlap inputs.
+ */
+cgtp_status cgtp_attn_forward(cgtp_attn plan, cgtp_graph graph, const void* q, int64_t ld_q, const void* k,
+                              int64_t ld_k, const void* v, int64_t ld_v, const void* lengths, const void* table,
+                              const void* bias, void* out, int64_t ld_out, void* lse, void* workspace,
+                              int64_t workspace_bytes, void* stream);
+
+/*
+ * cgtp_attn_backward -- adjoint for gout [N, heads*dim_v], from the inputs and lse of the forward.
+ *  gq, gk, gv as q, k, v (every row is written: zeros for nodes without edges).
+ *  gtable [n_borders+1, heads] : NULL, or wanted (needs table).  gbias [E, heads] : NULL, or wanted (bias need not
+ *      be given: it is the gradient of the logits).
+ *  Lengths have no gradient: the table is constant within a bucket.  All sums are taken in a fixed order.
+ */
+cgtp_status cgtp_attn_backward(cgtp_attn plan, cgtp_graph graph, const void* gout, int64_t ld_gout, const void* q,
+                               int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                               const void* lengths, const void* table, const void* bias, const void* lse, void* gq,
+                               int64_t ld_gq, void* gk, int64_t ld_gk, void* gv, int64_t ld_gv, void* gtable,
+                               void* gbias, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * cgtp_attn_edges_forward -- w [E, heads*dim_v] -> out [E, heads*dim_v] with out[e,h] = a[e,h] w[e,h] in the type of
+ *  w, and alpha [E, heads] = a.  irreps_v describes one head's share of w; for the weights of a uvu convolution it is
+ *  "MULx0e" for every path, MUL = channels of the path / heads.  kv_heads applies to k alone.  Not for plans with
+ *  CGTP_ATTN_STORAGE: convolutions give the gradient of their weights in FP32.
+ */
+cgtp_status cgtp_attn_edges_forward(cgtp_attn plan, cgtp_graph graph, const void* q, int64_t ld_q, const void* k,
+                                    int64_t ld_k, const void* w, int64_t ld_w, const void* lengths,
+                                    const void* table, const void* bias, void* out, int64_t ld_out, void* alpha,
+                                    void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * cgtp_attn_edges_backward -- adjoint for gout [E, heads*dim_v] in the type of results (FP32 with CGTP_BF16, as
+ *  convolutions give it), from w and the forward's alpha.  gq, gk, and gw in the type of gout.
+ *  lengths [E] are read for gtable only (NULL: not wanted); gbias as above.
+ */
+cgtp_status cgtp_attn_edges_backward(cgtp_attn plan, cgtp_graph graph, const void* gout, int64_t ld_gout,
+                                     const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* w,
+                                     int64_t ld_w, const void* lengths, const void* alpha, void* gq, int64_t ld_gq,
+                                     void* gk, int64_t ld_gk, void* gw, int64_t ld_gw, void* gtable, void* gbias,
+                                     void* workspace, int64_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* CGTP_ATTN_H */
