@@ -27,7 +27,8 @@ CU_SOURCES = ["api.cu", "graph.cu", "uvu.cu", "uvu_f32.cu", "uvu_f32_l7.cu", "uv
               "uvu3_sh_f64_8.cu", "uvu3_sh_f64_32.cu", "uvwe.cu", "mixed.cu", "measure.cu",
               "resnorm.cu", "resnorm_f32_fwd.cu", "resnorm_f32_bwd.cu", "resnorm_f64_fwd.cu", "resnorm_f64_bwd.cu",
               "resnorm_bf16_fwd.cu", "resnorm_bf16_bwd.cu", "resnorm_bf16s_fwd.cu", "resnorm_bf16s_bwd.cu", "adamw.cu",
-              "attn.cu", "attn_f32.cu", "attn_f64.cu", "attn_bf16.cu", "attn_bf16s.cu"]
+              "attn.cu", "attn_f32_fwd.cu", "attn_f32_bwd.cu", "attn_f64_fwd.cu", "attn_f64_bwd.cu",
+              "attn_bf16_fwd.cu", "attn_bf16_bwd.cu", "attn_bf16s_fwd.cu", "attn_bf16s_bwd.cu"]
 CPP_SOURCES = ["planner.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -136,7 +137,7 @@ def build(verbose=False, jobs=None):
     jobs = jobs or max(1, min(len(cmds), os.cpu_count() or 4))
     if cmds:
         # longest translation units first
-        cmds.sort(key=lambda c: (not any(k in c[-3] for k in ("_l7", "uvu3_", "_bwd", "_fwd", "attn_", "torch")), c[-3]))
+        cmds.sort(key=lambda c: (not any(k in c[-3] for k in ("_l7", "uvu3_", "_bwd", "_fwd", "torch")), c[-3]))
         with cf.ThreadPoolExecutor(jobs) as ex:
             for out in ex.map(_run, cmds):
                 if verbose and out.strip():

@@ -44,7 +44,6 @@ cgtp_status parse(const char* s, int heads, const char* name, Blocks* b) {
 
 // Tables for vectors of V elements, which divide every head's run of every block; offsets into *out until upload.
 AtTab make_tab(const Blocks& b, int heads, int kv, int V, std::vector<int>* out) {
-  const int group = heads / kv;
   AtTab t;
   t.vec = V;
   t.pieces = b.dim / V;
@@ -62,13 +61,8 @@ AtTab make_tab(const Blocks& b, int heads, int kv, int V, std::vector<int>* out)
     return off;
   };
   const std::vector<int> full = offsets(heads), shared = offsets(kv);
-  std::vector<int> acc(full.size()), send(full.size());
-  for (int h = 0; h < heads; ++h)
-    for (int c = 0; c < t.pieces; ++c) {
-      const int f = full[size_t(h) * t.pieces + c], s = shared[size_t(h / group) * t.pieces + c];
-      acc[f / V] = s | h << kAtHeadShift;
-      send[size_t(s / V) * group + h % group] = f | h << kAtHeadShift;
-    }
+  std::vector<int> acc(full.size());
+  for (size_t i = 0; i < full.size(); ++i) acc[full[i] / V] = static_cast<int>(i) / t.pieces << kAtHeadShift;
   const auto put = [&](const std::vector<int>& v) {
     const size_t at = out->size();
     out->insert(out->end(), v.begin(), v.end());
@@ -77,7 +71,6 @@ AtTab make_tab(const Blocks& b, int heads, int kv, int V, std::vector<int>* out)
   t.dot_full = put(full);
   t.dot_kv = put(shared);
   t.acc = put(acc);
-  t.send = put(send);
   return t;
 }
 
@@ -124,7 +117,7 @@ cgtp_status create(cgtp_attn_s* p, const char* irreps_qk, const char* irreps_v, 
   const auto place = [&](const int** x) { *x = reinterpret_cast<const int*>(static_cast<char*>(p->base) + reinterpret_cast<size_t>(*x)); };
   for (AtTab* t : {p->qk, p->vv})
     for (int i = 0; i < (t == p->qk ? p->n_qk : p->n_vv); ++i)
-      place(&t[i].dot_full), place(&t[i].dot_kv), place(&t[i].acc), place(&t[i].send);
+      place(&t[i].dot_full), place(&t[i].dot_kv), place(&t[i].acc);
   p->borders = static_cast<char*>(p->base) + ints;
   return CGTP_OK;
 }
@@ -145,8 +138,10 @@ cgtp_status check(Tensor* t, AtRows* out) {
   if (reinterpret_cast<uintptr_t>(t->p) % t->es) return fail(CGTP_EINVAL, std::string("pointer not aligned to its element: ") + t->name);
   if (t->ld == 0) t->ld = t->width;
   if (t->ld < t->width) return fail(CGTP_EINVAL, std::string("rows overlap (row distance below the row length): ") + t->name);
+  if (t->ld > (int64_t(1) << 31) / t->es) return fail(CGTP_EUNSUPPORTED, std::string("rows more than 2 GB apart: ") + t->name);
   out->p = const_cast<char*>(static_cast<const char*>(t->p));
   out->ld = t->ld;
+  out->ld_bytes = static_cast<uint32_t>(t->ld * t->es);
   return CGTP_OK;
 }
 
@@ -161,9 +156,10 @@ bool fits(const Tensor& t, int vec) {
   return reinterpret_cast<uintptr_t>(t.p) % bytes == 0 && (t.rows <= 1 || t.ld * t.es % bytes == 0);
 }
 
-// widest vectors that every tensor allows
-const AtTab& choose(const AtTab* tabs, int n, std::initializer_list<const Tensor*> list) {
+// widest vectors that every tensor allows, of at most `most` elements
+const AtTab& choose(const AtTab* tabs, int n, std::initializer_list<const Tensor*> list, int most = 4) {
   int i = 0;
+  while (i < n - 1 && tabs[i].vec > most) ++i;
   for (; i < n - 1; ++i) {
     bool ok = true;
     for (const Tensor* t : list) ok &= fits(*t, tabs[i].vec);
@@ -201,77 +197,108 @@ void side(AtArgs* a, const cgtp_graph_s* g, bool send) {
   a->chunk = g->chunk;
 }
 
-enum Kernel { kForward, kEdgesForward, kReceive, kEdgesReceive, kSendKeys, kSendAll };
+enum Kernel { kForward, kWeights, kReceive, kEdgesReceive, kSendKeys, kSendAll };
 
-int pow2_at_most(int x) {
+int pow2_at_most(int64_t x) {
   int r = 1;
-  while (2 * r <= x) r *= 2;
+  while (r < 1024 && 2 * r <= x) r *= 2;
   return r;
 }
 
-// Threads of a row, edges held at once and shared memory.
-cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* a) {
-  const bool send = k == kSendKeys || k == kSendAll, edges = k == kEdgesForward || k == kEdgesReceive;
-  const int es = es_acc(p);
-  // vectors of the results' rows (of the edges' rows, which are most of the work)
-  const int out = k == kForward || edges ? a->heads * a->vv.pieces
-                  : k == kReceive        ? a->heads * std::max(a->qk.pieces, a->vv.pieces)
-                                         : a->kv * std::max(a->qk.pieces, k == kSendAll ? a->vv.pieces : 0);
-  const int64_t longest = std::max(1, std::min(send ? g->max_out : g->max_in, a->n_items ? a->chunk : INT32_MAX));
-  const int64_t rows = a->n_rows, mean = a->n_edges / std::max<int64_t>(rows, 1);
-  a->warp_rows = out <= 64 && mean * out <= 2048;
-  int threads = 32;
-  if (!a->warp_rows) {
-    const int turns = (out + 383) / 384;
-    threads = (out + turns - 1) / turns;
-    // several streams of edges where rows are long beside their width
-    threads *= static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(256 / threads, mean / 8)));
-    threads = std::max(64, (threads + 31) / 32 * 32);
-    if (edges) threads = std::max(threads, 256);
+int log2_up(int x) {
+  int r = 0;
+  while (1 << r < x) ++r;
+  return r;
+}
+
+// Lanes for `units` heads of t->pieces vectors, and how many of a lane's vectors are held at once: as few turns as
+// possible with few idle lanes, for a turn costs about as much as one and a half vectors (addresses, weights, the
+// sums over lanes).  Returns the edges that the loops take at a time.
+int arrange(AtTab* t, int units, bool four) {
+  AtLanes& l = t->lanes;
+  l.units = log2_up(std::min(units, 32));
+  l.width = 0;
+  while (2 << l.width < t->pieces && l.width + l.units < 5) ++l.width;   // two vectors a lane where there are two
+  if (four && l.width + l.units == 0) l.width = 1;                       // (no more than 64 edges at a time)
+  const int each = (t->pieces + (1 << l.width) - 1) >> l.width;
+  double best = 0;
+  for (int turn : {2, 4, 5}) {
+    const int turns = (each + turn - 1) / turn;
+    const double cost = turns * (turn + 1.5);
+    if (best == 0 || cost < best) {
+      best = cost;
+      t->turn = turn;
+    }
   }
-  const int pairs = k == kReceive || k == kEdgesReceive || k == kSendAll ? 2 : 1;   // z and p
-  const int64_t budget = a->warp_rows ? 6 * 1024 : 16 * 1024;
-  int64_t sub = std::min<int64_t>((longest + 7) / 8 * 8, budget / (int64_t(a->heads) * es * pairs) / 8 * 8);
-  sub = std::max<int64_t>(sub, 8);
-  const int vmax = std::max(a->qk.vec, a->vv.vec);
-  const int64_t acc = longest <= sub ? 0
-                      : k == kForward                       ? a->heads * a->dv
-                      : k == kReceive || k == kEdgesReceive ? a->heads * a->dk
-                      : k == kSendKeys                      ? a->kv * a->dk
-                      : k == kSendAll                       ? a->kv * (a->dk + a->dv)
-                                                            : 0;
-  int64_t at = send || k == kEdgesReceive ? 0 : align16(int64_t(a->heads) * a->dk * es);
-  const auto region = [&](int* place, int64_t bytes) {
-    *place = static_cast<int>(at);
-    at += align16(bytes);
+  const int slots = 32 >> (l.width + l.units);
+  return slots * (four ? 4 : 2);
+}
+
+// Warps of a row, edges held at once and shared memory.
+cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* a) {
+  const bool send = k == kSendKeys || k == kSendAll;
+  const int es = es_acc(p), pairs = k == kForward || k == kWeights || k == kSendKeys ? 1 : 2;   // z, or z and p
+  const int64_t items = a->n_items + a->n_rows;
+  const int64_t longest = std::max(1, std::min(send ? g->max_out : g->max_in, a->n_items ? a->chunk : INT32_MAX));
+  // A warp a row where the rows give every SM sixteen warps; otherwise more, as long as each has eight edges.
+  int warps = pow2_at_most((p->num_sms * 16 + items - 1) / items);
+  warps = std::min(std::min(warps, 8), pow2_at_most(longest / 8));
+  const int64_t width = k == kForward                         ? a->heads * a->dv
+                        : k == kReceive || k == kEdgesReceive ? a->heads * a->dk
+                        : k == kSendKeys                      ? a->kv * a->dk
+                        : k == kSendAll                       ? a->kv * (a->dk + a->dv)
+                                                              : 0;
+  // (edge rows have a kernel of their own)
+  const bool values = k == kForward || k == kReceive;
+  a->four = !send && a->group % 4 == 0 && a->qk.vec > 1 && (!values || a->vv.vec > 1);
+  a->head_lanes = log2_up(std::min(a->heads, 32));
+  const int units = send ? a->kv : a->four ? a->heads / 4 : a->heads;
+  a->pad = arrange(&a->qk, units, a->four) - 1;
+  a->pad = std::max(a->pad, arrange(&a->vv, units, a->four) - 1);
+  int64_t at = 0;
+  const auto lay_out = [&] {
+    at = 0;
+    const auto region = [&](int64_t bytes) {
+      const int64_t place = at;
+      at += align16(bytes);
+      return static_cast<int>(place);
+    };
+    const int64_t run = (longest + warps - 1) / warps;
+    a->sub = static_cast<int>(std::max<int64_t>(8, std::min<int64_t>((run + 7) / 8 * 8, 4096 / (int64_t(a->heads) * es * pairs) / 8 * 8)));
+    const int64_t held = a->sub + a->pad;
+    region(held * a->heads * es);
+    a->at_p = region(pairs == 2 ? held * a->heads * es : 0);
+    a->at_idx = region((held + a->sub) * int64_t(sizeof(int)));
+    a->at_stat = region(int64_t(3) * a->heads * es);
+    a->at_acc = region(warps > 1 || run > a->sub ? width * es : 0);
+    a->warp_smem = static_cast<int>(at);
   };
-  region(&a->at_g, k == kReceive ? int64_t(a->heads) * a->dv * es : 0);
-  region(&a->at_z, sub * a->heads * es);
-  region(&a->at_p, pairs == 2 ? sub * a->heads * es : 0);
-  region(&a->at_idx, 2 * sub * sizeof(int));
-  region(&a->at_stat, int64_t(3) * a->heads * es);
-  region(&a->at_acc, acc * es);
-  region(&a->at_red, int64_t(threads) * vmax * es);
-  a->sub = static_cast<int>(sub);
-  a->group_smem = static_cast<int>(at);
-  const int64_t items = a->n_items + rows;
-  if (a->warp_rows) {
-    int groups = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, items / p->num_sms)));
-    while (groups > 1 && groups * at > p->smem_cap) groups /= 2;
-    a->block = 32 * groups;
-    a->smem = static_cast<size_t>(groups) * at;
-    a->grid = static_cast<unsigned>(std::min<int64_t>((items + groups - 1) / groups, int64_t(p->num_sms) * 64));
+  lay_out();
+  while (warps > 1 && warps * at > p->smem_cap) {
+    warps /= 2;
+    lay_out();
+  }
+  a->one = warps == 1;
+  if (a->one) {
+    warps = 4;
+    while (warps > 1 && warps * at > p->smem_cap) warps /= 2;
+    a->grid = static_cast<unsigned>(std::min<int64_t>((items + warps - 1) / warps, int64_t(p->num_sms) * 64));
   } else {
-    a->block = threads;
-    a->smem = static_cast<size_t>(at);
     a->grid = static_cast<unsigned>(items);
   }
+  a->block = 32 * warps;
+  a->smem = static_cast<size_t>(warps) * at;
   if (a->smem > static_cast<size_t>(p->smem_cap)) return fail(CGTP_EUNSUPPORTED, "attention rows too long for shared memory");
-  // threads of a dot product: two vectors a thread
-  a->team_qk = std::min(32, pow2_at_most(std::max(1, a->qk.pieces / 2)));
-  a->team_vv = std::min(32, k == kEdgesReceive ? std::min(pow2_at_most(std::max(1, 32 / a->heads)), pow2_at_most(a->vv.pieces))
-                                               : pow2_at_most(std::max(1, a->vv.pieces / 2)));
   return CGTP_OK;
+}
+
+// the launch of a kernel's second phase: items of split rows only
+AtArgs second_phase(const AtArgs& a) {
+  AtArgs b = a;
+  const unsigned teams = a.one ? a.block / 32 : 1;
+  b.phase = kAtSecond;
+  b.grid = (a.n_items + teams - 1) / teams;
+  return b;
 }
 
 // ---------------------------------------------------------------------------
@@ -279,10 +306,10 @@ cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* 
 // ---------------------------------------------------------------------------
 
 struct Space {
-  int64_t alpha = 0, ds = 0, part = 0, part_sum = 0, hist = 0, total = 0;
+  int64_t pairs = 0, ds = 0, part = 0, part_sum = 0, hist = 0, total = 0;
 };
 
-constexpr int kHistCtas = 152;
+constexpr int kHistCtas = 608;
 
 Space space(const cgtp_attn_s* p, const cgtp_graph_s* g, int call) {
   Space s;
@@ -298,8 +325,8 @@ Space space(const cgtp_attn_s* p, const cgtp_graph_s* g, int call) {
     region(&s.part, in * 2 * heads * es);
   } else {
     const bool values = call == CGTP_ATTN_BACKWARD;
-    region(&s.alpha, values ? g->E * heads * es : 0);
-    region(&s.ds, g->E * heads * es);
+    region(&s.pairs, values ? 2 * g->E * heads * es : 0);
+    region(&s.ds, values ? 0 : g->E * heads * es);
     region(&s.part, std::max(in * heads * p->dk, out * p->kv * (p->dk + (values ? p->dv : 0))) * es);
     region(&s.part_sum, in * heads * es);
     region(&s.hist, p->n_borders ? int64_t(kHistCtas) * (p->n_borders + 1) * heads * sizeof(double) : 0);
@@ -368,10 +395,12 @@ cgtp_status finish_backward(const cgtp_attn_s* p, const cgtp_graph_s* g, AtArgs 
   }
   // four warps a CTA where their histograms fit; a CTA for each 4096 values, one where that saves the second launch
   a.hist_cols = p->heads <= 32 ? 32 : 64;
-  const int64_t one = int64_t(p->n_borders + 1) * a.hist_cols * es_acc(p);
-  a.hist_warps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, (p->smem_cap - 1024) / one)));
-  if (a.hist_warps * one > p->smem_cap - 1024) return fail(CGTP_EUNSUPPORTED, "bias table too large for shared memory");
-  a.hist_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(kHistCtas, p->num_sms), g->E * p->heads / 4096)));
+  const int64_t one = int64_t(p->n_borders + 1) * a.hist_cols * es_acc(p), room = p->smem_cap - p->n_borders * es_acc(p);
+  a.hist_warps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, room / one)));
+  if (a.hist_warps * one > room) return fail(CGTP_EUNSUPPORTED, "bias table too large for shared memory");
+  a.hist_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(kHistCtas, 4 * p->num_sms), g->E * p->heads / 2048)));
+  a.hist_from = values ? a.pairs : a.ds;
+  a.hist_step = values ? 2 : 1;
   return done(CGTP_AT_PICK(p, table)(a, st));
 }
 
@@ -380,16 +409,11 @@ cgtp_status receive(const cgtp_attn_s* p, const cgtp_graph_s* g, AtArgs* a, bool
   side(a, g, false);
   cgtp_status s = deal(p, g, edges ? kEdgesReceive : kReceive, a);
   if (s) return s;
-  const auto run = edges ? CGTP_AT_PICK(p, edges_receive) : CGTP_AT_PICK(p, receive);
   a->phase = a->n_items ? kAtFirst : kAtWhole;
-  if ((s = done(run(*a, st)))) return s;
+  if ((s = done(CGTP_AT_PICK(p, receive)(*a, edges, st)))) return s;
   if (a->n_items) {
-    a->phase = kAtSecond;
-    AtArgs b = *a;
-    const int64_t groups = b.block / 32;
-    b.grid = static_cast<unsigned>(b.warp_rows ? (b.n_items + groups - 1) / groups : b.n_items);
-    if ((s = done(run(b, st)))) return s;
-    if ((s = done(CGTP_AT_PICK(p, join_sum)(b, b.gq, p->heads * p->dk, 0, p->heads * p->dk, st)))) return s;
+    if ((s = done(CGTP_AT_PICK(p, receive)(second_phase(*a), edges, st)))) return s;
+    if ((s = done(CGTP_AT_PICK(p, join_sum)(*a, a->gq, p->heads * p->dk, 0, p->heads * p->dk, st)))) return s;
   }
   a->phase = kAtWhole;
   return CGTP_OK;
@@ -517,8 +541,8 @@ cgtp_status cgtp_attn_backward(cgtp_attn p, cgtp_graph g, const void* gout, int6
   const Space sp = space(p, g, CGTP_ATTN_BACKWARD);
   if ((s = take_space(sp, workspace, workspace_bytes))) return s;
   char* w = static_cast<char*>(workspace);
-  a.alpha = w + sp.alpha;
-  a.ds = gbias ? gbias : w + sp.ds;
+  a.pairs = w + sp.pairs;
+  a.ds = gbias;
   a.part = w + sp.part;
   a.part_sum = w + sp.part_sum;
   a.hist = w + sp.hist;
@@ -551,17 +575,17 @@ cgtp_status cgtp_attn_edges_forward(cgtp_attn p, cgtp_graph g, const void* q, in
   a.part = static_cast<char*>(workspace) + sp.part;
   a.alpha = alpha;
   a.qk = choose(p->qk, p->n_qk, {&tq, &tk});
-  a.vv = choose(p->vv, p->n_vv, {&tw, &to});
+  a.vv = choose(p->vv, p->n_vv, {&tw, &to}, 8);
   side(&a, g, false);
-  if ((s = deal(p, g, kEdgesForward, &a))) return s;
+  if ((s = deal(p, g, kWeights, &a))) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   a.phase = a.n_items ? kAtFirst : kAtWhole;
-  if ((s = done(CGTP_AT_PICK(p, edges_forward)(a, st)))) return s;
-  if (!a.n_items) return CGTP_OK;
-  a.phase = kAtSecond;
-  const unsigned groups = a.block / 32;
-  a.grid = a.warp_rows ? (a.n_items + groups - 1) / groups : a.n_items;
-  return done(CGTP_AT_PICK(p, edges_forward)(a, st));
+  if ((s = done(CGTP_AT_PICK(p, weights)(a, st)))) return s;
+  if (a.n_items && (s = done(CGTP_AT_PICK(p, weights)(second_phase(a), st)))) return s;
+  const int64_t pieces = int64_t(a.heads) * a.vv.pieces;
+  a.pieces_magic = static_cast<uint32_t>(((uint64_t(1) << 32) + pieces - 1) / pieces);
+  a.grid = static_cast<unsigned>(std::min<int64_t>((g->E * pieces + 1023) / 1024, int64_t(p->num_sms) * 8));
+  return done(CGTP_AT_PICK(p, scale_rows)(a, st));
 }
 
 cgtp_status cgtp_attn_edges_backward(cgtp_attn p, cgtp_graph g, const void* gout, int64_t ld_gout, const void* q, int64_t ld_q, const void* k,
@@ -595,8 +619,13 @@ cgtp_status cgtp_attn_edges_backward(cgtp_attn p, cgtp_graph g, const void* gout
   a.hist = ws + sp.hist;
   a.gtable = gtable;
   a.qk = choose(p->qk, p->n_qk, {&tq, &tk, &tgq, &tgk});
-  a.vv = choose(p->vv, p->n_vv, {&tw, &tg, &tgw});
+  a.vv = choose(p->vv, p->n_vv, {&tw, &tg, &tgw}, 8);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (g->E > 0) {
+    a.grid = static_cast<unsigned>(std::min<int64_t>((g->E + 7) / 8, int64_t(p->num_sms) * 8));
+    arrange(&a.vv, a.heads, false);
+    if ((s = done(CGTP_AT_PICK(p, edge_rows)(a, st)))) return s;
+  }
   if ((s = receive(p, g, &a, true, st))) return s;
   return finish_backward(p, g, a, false, st);
 }

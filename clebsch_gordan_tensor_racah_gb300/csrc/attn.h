@@ -15,20 +15,27 @@ constexpr int kAtMaxRow = 8192;       // elements of a row of all heads
 constexpr int kAtMaxBorders = 511;
 constexpr int kAtHeadShift = 24;      // table entries: element offset | head << 24
 
-// Tables of one irreps string for vectors of V elements (see attn.cu): per head ("dot", head-major) and in the
-// order of memory ("acc").
+// Lanes of a warp for heads (or groups of heads, or shared heads) of some vectors: logarithms of the lanes of a head
+// and of the heads abreast; the rest of the 32 lanes are edges abreast.
+struct AtLanes {
+  int width = 0, units = 0;
+};
+
+// Tables of one irreps string for vectors of V elements (see attn.cu).
 struct AtTab {
   int vec = 1;                   // elements of a vector
   int pieces = 0;                // vectors of one head
-  const int* dot_full = nullptr; // [heads * pieces] offsets in rows of all heads
-  const int* dot_kv = nullptr;   // [kv * pieces] offsets in rows of the shared heads
-  const int* acc = nullptr;      // [heads * pieces] by place in a full row: offset in the shared row | head
-  const int* send = nullptr;     // [kv * pieces][group] by place in a shared row: offset in the full row | head
+  const int* dot_full = nullptr; // [heads * pieces] head by head: offsets in rows of all heads
+  const int* dot_kv = nullptr;   // [kv * pieces] head by head: offsets in rows of the shared heads
+  const int* acc = nullptr;      // [heads * pieces] by place in a row of all heads: head << 24
+  AtLanes lanes;                 // of a launch
+  int turn = 2;                  // vectors of a lane that are held at once
 };
 
 struct AtRows {
   char* p = nullptr;
-  int64_t ld = 0;   // elements
+  int64_t ld = 0;          // elements
+  uint32_t ld_bytes = 0;
 };
 
 struct AtArgs {
@@ -51,16 +58,21 @@ struct AtArgs {
   AtRows q, k, v, out, gout, gq, gk, gv;
   const void *lengths = nullptr, *table = nullptr, *bias = nullptr;
   void *lse = nullptr, *alpha = nullptr, *ds = nullptr, *gtable = nullptr;
+  void* pairs = nullptr;           // ds and a of every edge and head, between the backward's kernels
   void* part = nullptr;            // partial results of split rows
-  void* part_sum = nullptr;        // edge rows, backward: partial sums of split rows [parts][heads]
+  void* part_sum = nullptr;        // backward: partial sums of a dp of split rows [items][heads]
   void* hist = nullptr;            // partial sums of the bias table [ctas][buckets * heads]
+  const void* hist_from = nullptr; // ds of the edges, hist_step values apart
+  int hist_step = 1;
   // launch
   int phase = 0;
-  int sub = 0;                     // edges held at once
-  int team_qk = 1, team_vv = 1;    // threads of one dot product
-  int warp_rows = 0;               // a warp a row; otherwise a CTA a row
-  int group_smem = 0;              // bytes of shared memory of a row's threads
-  int at_g = 0, at_z = 0, at_p = 0, at_idx = 0, at_stat = 0, at_acc = 0, at_red = 0;  // regions, in bytes
+  int sub = 0;                     // edges that a warp holds at once
+  int pad = 0;                     // places behind a list of edges that the loops may read
+  int four = 0;                    // four heads that share keys and values are taken together
+  int head_lanes = 0;              // logarithm of the heads abreast where a lane takes a head's edges
+  int one = 1;                     // a warp a row; otherwise a CTA a row
+  int warp_smem = 0, at_p = 0, at_idx = 0, at_stat = 0, at_acc = 0;   // a warp's shared memory and its regions, in bytes
+  uint32_t pieces_magic = 0;       // ceil(2^32 / vectors of an edge's row)
   unsigned grid = 0, block = 0;
   size_t smem = 0;
   int hist_ctas = 0, hist_warps = 0, hist_cols = 0;
@@ -71,9 +83,10 @@ enum : int { kAtWhole = 0, kAtFirst = 1, kAtSecond = 2 };
 
 #define CGTP_AT_DECLARE(suffix)                                              \
   cudaError_t at_forward_##suffix(const AtArgs&, cudaStream_t);              \
-  cudaError_t at_edges_forward_##suffix(const AtArgs&, cudaStream_t);        \
-  cudaError_t at_receive_##suffix(const AtArgs&, cudaStream_t);              \
-  cudaError_t at_edges_receive_##suffix(const AtArgs&, cudaStream_t);        \
+  cudaError_t at_weights_##suffix(const AtArgs&, cudaStream_t);              \
+  cudaError_t at_scale_rows_##suffix(const AtArgs&, cudaStream_t);           \
+  cudaError_t at_edge_rows_##suffix(const AtArgs&, cudaStream_t);            \
+  cudaError_t at_receive_##suffix(const AtArgs&, bool edges, cudaStream_t);  \
   cudaError_t at_send_##suffix(const AtArgs&, bool values, cudaStream_t);    \
   cudaError_t at_join_forward_##suffix(const AtArgs&, cudaStream_t);         \
   cudaError_t at_join_sum_##suffix(const AtArgs&, const AtRows&, int width, int at, int stride, cudaStream_t); \
