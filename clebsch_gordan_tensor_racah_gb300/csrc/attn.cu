@@ -61,8 +61,14 @@ AtTab make_tab(const Blocks& b, int heads, int kv, int V, std::vector<int>* out)
     return off;
   };
   const std::vector<int> full = offsets(heads), shared = offsets(kv);
-  std::vector<int> acc(full.size());
-  for (size_t i = 0; i < full.size(); ++i) acc[full[i] / V] = static_cast<int>(i) / t.pieces << kAtHeadShift;
+  const int group = heads / kv;
+  std::vector<int> acc(full.size()), rows(full.size());
+  for (int h = 0; h < heads; ++h)
+    for (int c = 0; c < t.pieces; ++c) {
+      const int f = full[size_t(h) * t.pieces + c];
+      acc[f / V] = h << kAtHeadShift;
+      rows[size_t(shared[size_t(h / group) * t.pieces + c] / V) * group + h % group] = f | h << kAtHeadShift;
+    }
   const auto put = [&](const std::vector<int>& v) {
     const size_t at = out->size();
     out->insert(out->end(), v.begin(), v.end());
@@ -71,6 +77,7 @@ AtTab make_tab(const Blocks& b, int heads, int kv, int V, std::vector<int>* out)
   t.dot_full = put(full);
   t.dot_kv = put(shared);
   t.acc = put(acc);
+  t.rows = put(rows);
   return t;
 }
 
@@ -117,7 +124,7 @@ cgtp_status create(cgtp_attn_s* p, const char* irreps_qk, const char* irreps_v, 
   const auto place = [&](const int** x) { *x = reinterpret_cast<const int*>(static_cast<char*>(p->base) + reinterpret_cast<size_t>(*x)); };
   for (AtTab* t : {p->qk, p->vv})
     for (int i = 0; i < (t == p->qk ? p->n_qk : p->n_vv); ++i)
-      place(&t[i].dot_full), place(&t[i].dot_kv), place(&t[i].acc);
+      place(&t[i].dot_full), place(&t[i].dot_kv), place(&t[i].acc), place(&t[i].rows);
   p->borders = static_cast<char*>(p->base) + ints;
   return CGTP_OK;
 }
@@ -156,16 +163,25 @@ bool fits(const Tensor& t, int vec) {
   return reinterpret_cast<uintptr_t>(t.p) % bytes == 0 && (t.rows <= 1 || t.ld * t.es % bytes == 0);
 }
 
-// widest vectors that every tensor allows, of at most `most` elements
-const AtTab& choose(const AtTab* tabs, int n, std::initializer_list<const Tensor*> list, int most = 4) {
-  int i = 0;
-  while (i < n - 1 && tabs[i].vec > most) ++i;
-  for (; i < n - 1; ++i) {
+// widest vectors that every tensor allows
+const AtTab& choose(const AtTab* tabs, int n, std::initializer_list<const Tensor*> list) {
+  for (int i = 0; i < n - 1; ++i) {
     bool ok = true;
     for (const Tensor* t : list) ok &= fits(*t, tabs[i].vec);
-    if (ok) break;
+    if (ok) return tabs[i];
   }
-  return tabs[i];
+  return tabs[n - 1];
+}
+
+// queries and values in the same vectors: the widest that a head's runs and the tensors that lanes read and write allow
+void choose_both(const cgtp_attn_s* p, AtArgs* a, std::initializer_list<const Tensor*> list) {
+  a->qk = choose(p->qk, p->n_qk, list);
+  a->vv = choose(p->vv, p->n_vv, list);
+  const int vec = std::min(a->qk.vec, a->vv.vec);
+  for (int i = 0; i < p->n_qk; ++i)
+    if (p->qk[i].vec == vec) a->qk = p->qk[i];
+  for (int i = 0; i < p->n_vv; ++i)
+    if (p->vv[i].vec == vec) a->vv = p->vv[i];
 }
 
 AtArgs base_args(const cgtp_attn_s* p, const cgtp_graph_s* g) {
@@ -211,28 +227,29 @@ int log2_up(int x) {
   return r;
 }
 
-// Lanes for `units` heads of t->pieces vectors, and how many of a lane's vectors are held at once: as few turns as
-// possible with few idle lanes, for a turn costs about as much as one and a half vectors (addresses, weights, the
-// sums over lanes).  Returns the edges that the loops take at a time.
-int arrange(AtTab* t, int units, bool four) {
+// Lanes for the dot products of `units` heads of t->pieces vectors and for sums over rows of `kv` heads, whose vectors are
+// taken in as few turns of at most `most` a lane as there can be, of even length.  Returns the most edges that a loop
+// takes at a time.
+int arrange(AtTab* t, int units, int kv, int most) {
+  const auto turn = [&](int each) {
+    const int turns = (each + most - 1) / most;
+    return (each + turns - 1) / turns;
+  };
   AtLanes& l = t->lanes;
   l.units = log2_up(std::min(units, 32));
   l.width = 0;
   while (2 << l.width < t->pieces && l.width + l.units < 5) ++l.width;   // two vectors a lane where there are two
-  if (four && l.width + l.units == 0) l.width = 1;                       // (no more than 64 edges at a time)
-  const int each = (t->pieces + (1 << l.width) - 1) >> l.width;
-  double best = 0;
-  for (int turn : {2, 4, 5}) {
-    const int turns = (each + turn - 1) / turn;
-    const double cost = turns * (turn + 1.5);
-    if (best == 0 || cost < best) {
-      best = cost;
-      t->turn = turn;
-    }
-  }
-  const int slots = 32 >> (l.width + l.units);
-  return slots * (four ? 4 : 2);
+  t->dot_turn = turn((t->pieces + (1 << l.width) - 1) >> l.width);
+  const int total = kv * t->pieces;
+  t->abreast = 2;   // (no more than 32 edges at a time)
+  while (1 << t->abreast < total && t->abreast < 5) ++t->abreast;
+  t->turn = turn((total + (1 << t->abreast) - 1) >> t->abreast);
+  return kAtQuad * std::max(32 >> t->abreast, 32 >> (l.width + l.units));
 }
+
+// Distance between the partial results of split rows: whole vectors.
+int part_ld(int64_t width) { return static_cast<int>((width + 3) / 4 * 4); }
+int send_ld(const cgtp_attn_s* p, bool values) { return part_ld(p->kv * p->dk) + (values ? part_ld(p->kv * p->dv) : 0); }
 
 // Warps of a row, edges held at once and shared memory.
 cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* a) {
@@ -245,16 +262,17 @@ cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* 
   warps = std::min(std::min(warps, 8), pow2_at_most(longest / 8));
   const int64_t width = k == kForward                         ? a->heads * a->dv
                         : k == kReceive || k == kEdgesReceive ? a->heads * a->dk
-                        : k == kSendKeys                      ? a->kv * a->dk
-                        : k == kSendAll                       ? a->kv * (a->dk + a->dv)
+                        : k == kSendKeys                      ? send_ld(p, false)
+                        : k == kSendAll                       ? send_ld(p, true)
                                                               : 0;
   // (edge rows have a kernel of their own)
   const bool values = k == kForward || k == kReceive;
   a->four = !send && a->group % 4 == 0 && a->qk.vec > 1 && (!values || a->vv.vec > 1);
   a->head_lanes = log2_up(std::min(a->heads, 32));
   const int units = send ? a->kv : a->four ? a->heads / 4 : a->heads;
-  a->pad = arrange(&a->qk, units, a->four) - 1;
-  a->pad = std::max(a->pad, arrange(&a->vv, units, a->four) - 1);
+  const auto most = [&](int vec, int plain) { return vec == 1 ? 4 : a->four ? (vec == 8 ? 1 : 2) : plain; };
+  a->pad = arrange(&a->qk, units, a->kv, a->qk.vec == 1 ? 2 : most(a->qk.vec, 2));
+  a->pad = std::max(a->pad, arrange(&a->vv, units, a->kv, most(a->vv.vec, kAtTurn)));
   int64_t at = 0;
   const auto lay_out = [&] {
     at = 0;
@@ -265,9 +283,12 @@ cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* 
     };
     const int64_t run = (longest + warps - 1) / warps;
     a->sub = static_cast<int>(std::max<int64_t>(8, std::min<int64_t>((run + 7) / 8 * 8, 4096 / (int64_t(a->heads) * es * pairs) / 8 * 8)));
-    const int64_t held = a->sub + a->pad;
-    region(held * a->heads * es);
-    a->at_p = region(pairs == 2 ? held * a->heads * es : 0);
+    // weights of a head: a multiple of 32 and the edges abreast where a lane takes a head's edges, so that heads lie
+    // in different banks; whole quads
+    const int64_t held = align16(a->sub + a->pad);
+    a->stride = static_cast<int>((held + 31) / 32 * 32 + std::max(4, 32 >> a->head_lanes) % 32);
+    region(int64_t(a->stride) * a->heads * es);
+    a->at_p = region(pairs == 2 ? int64_t(a->stride) * a->heads * es : 0);
     a->at_idx = region((held + a->sub) * int64_t(sizeof(int)));
     a->at_stat = region(int64_t(3) * a->heads * es);
     a->at_acc = region(warps > 1 || run > a->sub ? width * es : 0);
@@ -282,7 +303,7 @@ cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* 
   if (a->one) {
     warps = 4;
     while (warps > 1 && warps * at > p->smem_cap) warps /= 2;
-    a->grid = static_cast<unsigned>(std::min<int64_t>((items + warps - 1) / warps, int64_t(p->num_sms) * 64));
+    a->grid = static_cast<unsigned>((items + warps - 1) / warps);
   } else {
     a->grid = static_cast<unsigned>(items);
   }
@@ -320,14 +341,14 @@ Space space(const cgtp_attn_s* p, const cgtp_graph_s* g, int call) {
   };
   const int64_t in = g->split.n_items, out = g->split_t.n_items;
   if (call == CGTP_ATTN_FORWARD) {
-    region(&s.part, in * (heads * p->dv + 2 * heads) * es);
+    region(&s.part, in * part_ld(heads * p->dv + 2 * heads) * es);
   } else if (call == CGTP_ATTN_EDGES_FORWARD) {
     region(&s.part, in * 2 * heads * es);
   } else {
     const bool values = call == CGTP_ATTN_BACKWARD;
     region(&s.pairs, values ? 2 * g->E * heads * es : 0);
     region(&s.ds, values ? 0 : g->E * heads * es);
-    region(&s.part, std::max(in * heads * p->dk, out * p->kv * (p->dk + (values ? p->dv : 0))) * es);
+    region(&s.part, std::max(in * part_ld(heads * p->dk), out * send_ld(p, values)) * es);
     region(&s.part_sum, in * heads * es);
     region(&s.hist, p->n_borders ? int64_t(kHistCtas) * (p->n_borders + 1) * heads * sizeof(double) : 0);
   }
@@ -382,11 +403,12 @@ cgtp_status finish_backward(const cgtp_attn_s* p, const cgtp_graph_s* g, AtArgs 
   cgtp_status s;
   side(&a, g, true);
   if ((s = deal(p, g, values ? kSendAll : kSendKeys, &a))) return s;
+  a.part_ld = send_ld(p, values);
   if ((s = done(CGTP_AT_PICK(p, send)(a, values, st)))) return s;
   if (a.n_joins) {
     const int wk = p->kv * p->dk, wv = values ? p->kv * p->dv : 0;
-    if ((s = done(CGTP_AT_PICK(p, join_sum)(a, a.gk, wk, 0, wk + wv, st)))) return s;
-    if (values && (s = done(CGTP_AT_PICK(p, join_sum)(a, a.gv, wv, wk, wk + wv, st)))) return s;
+    if ((s = done(CGTP_AT_PICK(p, join_sum)(a, a.gk, wk, 0, a.part_ld, st)))) return s;
+    if (values && (s = done(CGTP_AT_PICK(p, join_sum)(a, a.gv, wv, part_ld(wk), a.part_ld, st)))) return s;
   }
   if (!a.gtable) return CGTP_OK;
   const int64_t cells = int64_t(p->n_borders + 1) * p->heads;
@@ -409,11 +431,12 @@ cgtp_status receive(const cgtp_attn_s* p, const cgtp_graph_s* g, AtArgs* a, bool
   side(a, g, false);
   cgtp_status s = deal(p, g, edges ? kEdgesReceive : kReceive, a);
   if (s) return s;
+  a->part_ld = part_ld(p->heads * p->dk);
   a->phase = a->n_items ? kAtFirst : kAtWhole;
   if ((s = done(CGTP_AT_PICK(p, receive)(*a, edges, st)))) return s;
   if (a->n_items) {
     if ((s = done(CGTP_AT_PICK(p, receive)(second_phase(*a), edges, st)))) return s;
-    if ((s = done(CGTP_AT_PICK(p, join_sum)(*a, a->gq, p->heads * p->dk, 0, p->heads * p->dk, st)))) return s;
+    if ((s = done(CGTP_AT_PICK(p, join_sum)(*a, a->gq, p->heads * p->dk, 0, a->part_ld, st)))) return s;
   }
   a->phase = kAtWhole;
   return CGTP_OK;
@@ -510,10 +533,10 @@ cgtp_status cgtp_attn_forward(cgtp_attn p, cgtp_graph g, const void* q, int64_t 
   if ((s = take_space(sp, workspace, workspace_bytes))) return s;
   a.part = static_cast<char*>(workspace) + sp.part;
   a.lse = lse;
-  a.qk = choose(p->qk, p->n_qk, {&tq, &tk});
-  a.vv = choose(p->vv, p->n_vv, {&tv, &to});
+  choose_both(p, &a, {&tq, &tk, &tv, &to});
   side(&a, g, false);
   if ((s = deal(p, g, kForward, &a))) return s;
+  a.part_ld = part_ld(p->heads * p->dv + 2 * p->heads);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((s = done(CGTP_AT_PICK(p, forward)(a, st)))) return s;
   return a.n_joins ? done(CGTP_AT_PICK(p, join_forward)(a, st)) : CGTP_OK;
@@ -548,8 +571,7 @@ cgtp_status cgtp_attn_backward(cgtp_attn p, cgtp_graph g, const void* gout, int6
   a.hist = w + sp.hist;
   a.lse = const_cast<void*>(lse);
   a.gtable = gtable;
-  a.qk = choose(p->qk, p->n_qk, {&tq, &tk, &tgq, &tgk});
-  a.vv = choose(p->vv, p->n_vv, {&tv, &tg, &tgv});
+  choose_both(p, &a, {&tq, &tk, &tv, &tg, &tgq, &tgk, &tgv});
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((s = receive(p, g, &a, false, st))) return s;
   return finish_backward(p, g, a, true, st);
@@ -575,7 +597,7 @@ cgtp_status cgtp_attn_edges_forward(cgtp_attn p, cgtp_graph g, const void* q, in
   a.part = static_cast<char*>(workspace) + sp.part;
   a.alpha = alpha;
   a.qk = choose(p->qk, p->n_qk, {&tq, &tk});
-  a.vv = choose(p->vv, p->n_vv, {&tw, &to}, 8);
+  a.vv = choose(p->vv, p->n_vv, {&tw, &to});
   side(&a, g, false);
   if ((s = deal(p, g, kWeights, &a))) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -619,11 +641,11 @@ cgtp_status cgtp_attn_edges_backward(cgtp_attn p, cgtp_graph g, const void* gout
   a.hist = ws + sp.hist;
   a.gtable = gtable;
   a.qk = choose(p->qk, p->n_qk, {&tq, &tk, &tgq, &tgk});
-  a.vv = choose(p->vv, p->n_vv, {&tw, &tg, &tgw}, 8);
+  a.vv = choose(p->vv, p->n_vv, {&tw, &tg, &tgw});
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (g->E > 0) {
     a.grid = static_cast<unsigned>(std::min<int64_t>((g->E + 7) / 8, int64_t(p->num_sms) * 8));
-    arrange(&a.vv, a.heads, false);
+    arrange(&a.vv, a.heads, a.kv, kAtTurn);
     if ((s = done(CGTP_AT_PICK(p, edge_rows)(a, st)))) return s;
   }
   if ((s = receive(p, g, &a, true, st))) return s;

@@ -15,6 +15,9 @@ constexpr int kAtMaxRow = 8192;       // elements of a row of all heads
 constexpr int kAtMaxBorders = 511;
 constexpr int kAtHeadShift = 24;      // table entries: element offset | head << 24
 
+constexpr int kAtTurn = 4;            // most vectors of a lane that a loop holds at once
+constexpr int kAtQuad = 4;            // edges that a lane's sums take at a time
+
 // Lanes of a warp for heads (or groups of heads, or shared heads) of some vectors: logarithms of the lanes of a head
 // and of the heads abreast; the rest of the 32 lanes are edges abreast.
 struct AtLanes {
@@ -28,8 +31,11 @@ struct AtTab {
   const int* dot_full = nullptr; // [heads * pieces] head by head: offsets in rows of all heads
   const int* dot_kv = nullptr;   // [kv * pieces] head by head: offsets in rows of the shared heads
   const int* acc = nullptr;      // [heads * pieces] by place in a row of all heads: head << 24
-  AtLanes lanes;                 // of a launch
-  int turn = 2;                  // vectors of a lane that are held at once
+  const int* rows = nullptr;     // [kv * pieces][group] by place in a shared row: offset in the full row | head << 24
+  AtLanes lanes;                 // of a launch, for dot products
+  int abreast = 0;               // of a launch, for sums: logarithm of a row's vectors abreast; the rest are edges abreast
+  int dot_turn = 1;              // of a launch, for dot products: vectors of a lane that are held at once
+  int turn = 1;                  // of a launch, for sums: vectors of a lane that are held at once
 };
 
 struct AtRows {
@@ -59,7 +65,8 @@ struct AtArgs {
   const void *lengths = nullptr, *table = nullptr, *bias = nullptr;
   void *lse = nullptr, *alpha = nullptr, *ds = nullptr, *gtable = nullptr;
   void* pairs = nullptr;           // ds and a of every edge and head, between the backward's kernels
-  void* part = nullptr;            // partial results of split rows
+  void* part = nullptr;            // partial results of split rows, part_ld values apart
+  int part_ld = 0;
   void* part_sum = nullptr;        // backward: partial sums of a dp of split rows [items][heads]
   void* hist = nullptr;            // partial sums of the bias table [ctas][buckets * heads]
   const void* hist_from = nullptr; // ds of the edges, hist_step values apart
@@ -67,6 +74,7 @@ struct AtArgs {
   // launch
   int phase = 0;
   int sub = 0;                     // edges that a warp holds at once
+  int stride = 0;                  // weights of a head
   int pad = 0;                     // places behind a list of edges that the loops may read
   int four = 0;                    // four heads that share keys and values are taken together
   int head_lanes = 0;              // logarithm of the heads abreast where a lane takes a head's edges

@@ -88,6 +88,15 @@ __device__ __forceinline__ T to(A x) {
   else return narrow<T>(x);
 }
 
+// V numbers of the arithmetic, to places that are aligned for them
+template <int V, typename A>
+__device__ __forceinline__ void store_as(A* p, const A* r) {
+  Pack<A, V> y;
+#pragma unroll
+  for (int k = 0; k < V; ++k) y.e[k] = r[k];
+  y.store(p);
+}
+
 template <typename A>
 __device__ __forceinline__ A lowest() { return -static_cast<A>(INFINITY); }
 __device__ __forceinline__ float expo(float x) { return expf(x); }
@@ -97,67 +106,51 @@ __device__ __forceinline__ double loga(double x) { return log(x); }
 __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
 
-// V numbers of the arithmetic.  Pairs of FP32 numbers are multiplied and added together.
+// V numbers of the arithmetic: pairs of FP32 numbers, which are multiplied and added together, else single ones.
 template <typename A, int V>
+constexpr bool kPairs = std::is_same<A, float>::value && V % 2 == 0;
+template <typename A, int V, bool = kPairs<A, V>>
 struct Nums {
   A e[V];
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int k = 0; k < V; ++k) e[k] = 0;
   }
-  __device__ __forceinline__ A get(int k) const { return e[k]; }
-  __device__ __forceinline__ void set(int k, A x) { e[k] = x; }
+  __device__ __forceinline__ void get(A* r) const {
+#pragma unroll
+    for (int k = 0; k < V; ++k) r[k] = e[k];
+  }
   // += f y; a weight of zero takes nothing, whatever y holds
-  __device__ __forceinline__ void add(A f, const Nums& y) {
-    if (f != 0) {
+  __device__ __forceinline__ void add_weighed(A f, const Nums& y) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) e[k] += f * y.e[k];
-    }
-  }
-  __device__ __forceinline__ void add_product(const Nums& x, const Nums& y) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) e[k] += x.e[k] * y.e[k];
-  }
-  __device__ __forceinline__ A total() const {
-    A s = e[0];
-#pragma unroll
-    for (int k = 1; k < V; ++k) s += e[k];
-    return s;
+    for (int k = 0; k < V; ++k) e[k] = f != 0 ? e[k] + f * y.e[k] : e[k];
   }
 };
-template <>
-struct Nums<float, 4> {
-  uint64_t p[2];
-  static __device__ __forceinline__ uint64_t pair(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
+template <int V>
+struct Nums<float, V, true> {
+  uint64_t p[V / 2];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) p[k] = 0;
   }
-  __device__ __forceinline__ void clear() { p[0] = p[1] = 0; }
-  __device__ __forceinline__ float get(int k) const {
-    float a, b;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p[k / 2]));
-    return k & 1 ? b : a;
+  __device__ __forceinline__ void get(float* r) const {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) asm("mov.b64 {%0, %1}, %2;" : "=f"(r[2 * k]), "=f"(r[2 * k + 1]) : "l"(p[k]));
   }
-  __device__ __forceinline__ void set(int k, float x) { p[k / 2] = k & 1 ? pair(get(k - 1), x) : pair(x, get(k + 1)); }
-  __device__ __forceinline__ void add(float f, const Nums& y) {
-    asm("{\n\t.reg .pred q;\n\t.reg .b64 ff;\n\tsetp.neu.f32 q, %2, 0f00000000;\n\tmov.b64 ff, {%2, %2};\n\t"
-        "@q fma.rn.f32x2 %0, ff, %3, %0;\n\t@q fma.rn.f32x2 %1, ff, %4, %1;\n\t}"
-        : "+l"(p[0]), "+l"(p[1])
-        : "f"(f), "l"(y.p[0]), "l"(y.p[1]));
+  __device__ __forceinline__ void add_weighed(float f, const Nums& y) {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k)
+      asm("{\n\t.reg .pred q;\n\t.reg .b64 w;\n\tsetp.neu.f32 q, %1, 0f00000000;\n\tmov.b64 w, {%1, %1};\n\t@q fma.rn.f32x2 %0, w, %2, %0;\n\t}"
+          : "+l"(p[k])
+          : "f"(f), "l"(y.p[k]));
   }
-  __device__ __forceinline__ void add_product(const Nums& x, const Nums& y) {
-    asm("fma.rn.f32x2 %0, %2, %4, %0;\n\tfma.rn.f32x2 %1, %3, %5, %1;" : "+l"(p[0]), "+l"(p[1]) : "l"(x.p[0]), "l"(x.p[1]), "l"(y.p[0]), "l"(y.p[1]));
-  }
-  __device__ __forceinline__ float total() const { return (get(0) + get(2)) + (get(1) + get(3)); }
 };
-
 template <typename A, typename S, int V>
 __device__ __forceinline__ Nums<A, V> widened(const Pack<S, V>& y) {
   Nums<A, V> r;
-  if constexpr (std::is_same<A, float>::value && V == 4) {
-    r.p[0] = r.pair(wide(y.e[0]), wide(y.e[1]));
-    r.p[1] = r.pair(wide(y.e[2]), wide(y.e[3]));
+  if constexpr (kPairs<A, V>) {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) asm("mov.b64 %0, {%1, %2};" : "=l"(r.p[k]) : "f"(wide(y.e[2 * k])), "f"(wide(y.e[2 * k + 1])));
   } else {
 #pragma unroll
     for (int k = 0; k < V; ++k) r.e[k] = wide(y.e[k]);
@@ -165,14 +158,38 @@ __device__ __forceinline__ Nums<A, V> widened(const Pack<S, V>& y) {
   return r;
 }
 
-// Widths of vectors of a storage type: 16 bytes (8 for bfloat16, whose elements cost more to widen than to load), or
-// one element.  Rows of edges, which are read in the order of memory, take 16 bytes of bfloat16 too.
+// Sum of products of V numbers.
+template <typename A, int V, bool = kPairs<A, V>>
+struct Dot {
+  A s = 0;
+  __device__ __forceinline__ void add(const Nums<A, V>& x, const Nums<A, V>& y, bool on) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) s = on ? s + x.e[k] * y.e[k] : s;
+  }
+  __device__ __forceinline__ A total() const { return s; }
+};
+template <int V>
+struct Dot<float, V, true> {
+  uint64_t s = 0;
+  __device__ __forceinline__ void add(const Nums<float, V>& x, const Nums<float, V>& y, bool on) {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k)
+      asm("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q fma.rn.f32x2 %0, %1, %2, %0;\n\t}" : "+l"(s) : "l"(x.p[k]), "l"(y.p[k]), "r"(unsigned(on)));
+  }
+  __device__ __forceinline__ float total() const {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(s));
+    return a + b;
+  }
+};
+
+// Widths of vectors of a storage type: 16 bytes, 8 of bfloat16 where a head's runs allow no more, or one element.
 template <typename S>
-constexpr int kWide = sizeof(S) == 8 ? 2 : 4;
+constexpr int kWide = 16 / sizeof(S);
 template <typename S, typename F>
 __device__ __forceinline__ void with_width(int v, F&& f) {
-  if (sizeof(S) == 2 && v == 8) f(std::integral_constant<int, 8>());
-  else if (v == kWide<S>) f(std::integral_constant<int, kWide<S>>());
+  if (v == kWide<S>) f(std::integral_constant<int, kWide<S>>());
+  else if (sizeof(S) == 2 && v == 4) f(std::integral_constant<int, 4>());
   else f(std::integral_constant<int, 1>());
 }
 
@@ -197,37 +214,33 @@ struct Team {
 };
 
 struct Item {
-  int64_t row;
-  int64_t e0, e1;   // this warp's edges
-  int index;        // item of a split row, or -1
+  int row = 0;
+  int e0 = 0, e1 = 0;   // this warp's edges
+  int index = -1;       // item of a split row, or -1
+  bool some = false;
 };
 
-// f(item) for every piece of work of this team.  First come the items of split rows, the longest work.
-template <typename F>
-__device__ __forceinline__ void each_item(const AtArgs& a, const Team& t, F&& f) {
-  const int64_t teams = t.one ? int64_t(gridDim.x) * (blockDim.x / 32) : gridDim.x;
-  const int64_t first = t.one ? int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
-  const int64_t total = a.n_items + (a.phase == kAtSecond ? 0 : a.n_rows);
-  for (int64_t i = first; i < total; i += teams) {
-    Item it;
-    if (i < a.n_items) {
-      const Int4 v = a.items[i];
-      it = {v.x, v.y, v.z, static_cast<int>(i)};
-    } else {
-      it.row = i - a.n_items;
-      it.e0 = a.rowptr[it.row];
-      it.e1 = a.rowptr[it.row + 1];
-      it.index = -1;
-      if (a.n_items && it.e1 - it.e0 > a.chunk) continue;
-    }
-    if (!t.one) {
-      const int64_t b = it.e0, len = it.e1 - b;
-      it.e0 = b + len * t.w / t.warps;
-      it.e1 = b + len * (t.w + 1) / t.warps;
-    }
-    f(it);
-    t.sync();
+// This team's piece of work.  First come the items of split rows, the longest work.
+__device__ __forceinline__ Item item_of(const AtArgs& a, const Team& t) {
+  const int64_t i = t.one ? int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+  Item it;
+  if (i < a.n_items) {
+    const Int4 v = a.items[i];
+    it.row = v.x, it.e0 = v.y, it.e1 = v.z;
+    it.index = static_cast<int>(i);
+    it.some = true;
+  } else if (a.phase != kAtSecond && i < a.n_items + a.n_rows) {
+    it.row = static_cast<int>(i - a.n_items);
+    it.e0 = a.rowptr[it.row];
+    it.e1 = a.rowptr[it.row + 1];
+    it.some = !(a.n_items && it.e1 - it.e0 > a.chunk);
   }
+  if (!t.one) {
+    const int b = it.e0, len = it.e1 - b;
+    it.e0 = b + static_cast<int>(int64_t(len) * t.w / t.warps);
+    it.e1 = b + static_cast<int>(int64_t(len) * (t.w + 1) / t.warps);
+  }
+  return it;
 }
 
 // pair / heads for pairs below 2^24 (heads <= 64: the error of the multiplier is below 2^-32 a unit)
@@ -246,20 +259,80 @@ struct Place {
   }
 };
 
-// The edges of a run are taken U times the edge slots at a time: the lists of edges and weights are filled up to that
-// (with the first edge and zeros), so that the loops need no bounds.
-__device__ __forceinline__ int filled(int cnt, int step) { return (cnt + step - 1) & -step; }
+// A warp's regions of shared memory
+template <typename A>
+struct Smem {
+  A *z, *p, *stat, *acc;
+  int *idx, *bucket;
+  __device__ __forceinline__ Smem(const AtArgs& a, int warp) {
+    extern __shared__ __align__(128) char at_smem[];
+    char* s = at_smem + warp * a.warp_smem;
+    z = reinterpret_cast<A*>(s);
+    p = reinterpret_cast<A*>(s + a.at_p);
+    idx = reinterpret_cast<int*>(s + a.at_idx);
+    bucket = idx + a.sub + a.pad;
+    stat = reinterpret_cast<A*>(s + a.at_stat);
+    acc = reinterpret_cast<A*>(s + a.at_acc);
+  }
+};
 
-// z[i][h] = <x[h], rows[idx(i)][shared head]>.  G heads that share a row's vectors are taken together; CB vectors a
-// lane stay in registers while the edges pass, U edges in flight.
-template <int V, int CB, int U, int G, typename S, typename A>
+// Most vectors of queries and keys that a lane holds at once (see attn.cu for values)
+template <int V, int G>
+constexpr int kShort = G == 4 && V == 8 ? 1 : 2;
+
+// Edges in flight of `elements` elements a lane: as many, up to `most`, as take 32 registers.
+template <typename S, int elements, int most>
+constexpr int kFlight = most > 1 && most * elements * int(sizeof(S)) > 128 ? kFlight<S, elements, most / 2> : most;
+template <typename S, int elements>
+constexpr int kFlight<S, elements, 1> = 1;
+
+// Sums of v[u] (u < U <= 4) over the 2^width lanes side by side.  The lanes share the sums out as they halve them: in the
+// end lane x of them holds those of v[u] with `mine(u)`, U / min(U, 2^width) of them, in v[0..].
+template <int U, typename A>
+__device__ __forceinline__ int lane_sums(A (&v)[U], int width, int x) {
+  int held = U, first = 0, o = 1;
+  if constexpr (U >= 2) {
+    if (width >= 1) {
+      const bool up = x & 1;
+#pragma unroll
+      for (int u = 0; u < U / 2; ++u) {
+        const A keep = up ? v[U / 2 + u] : v[u], give = up ? v[u] : v[U / 2 + u];
+        v[u] = keep + __shfl_xor_sync(kAll, give, 1);
+      }
+      held = U / 2, first = up ? U / 2 : 0, o = 2;
+    }
+  }
+  if constexpr (U >= 4) {
+    if (width >= 2) {
+      const bool up = x & 2;
+#pragma unroll
+      for (int u = 0; u < U / 4; ++u) {
+        const A keep = up ? v[U / 4 + u] : v[u], give = up ? v[u] : v[U / 4 + u];
+        v[u] = keep + __shfl_xor_sync(kAll, give, 2);
+      }
+      held = U / 4, first += up ? U / 4 : 0, o = 4;
+    }
+  }
+#pragma unroll 1
+  for (; o < 1 << width; o *= 2)
+#pragma unroll
+    for (int u = 0; u < (U >= 4 ? U / 4 : 1); ++u) v[u] += __shfl_xor_sync(kAll, v[u], o);
+  return first | held << 8;
+}
+
+// z[h][i] = <x[h], rows[idx(i)][shared head]> (weights lie head by head, a.stride apart: see sums).  G heads that share a
+// row's vectors are taken together; CB vectors of x a lane stay in registers while the edges pass.  LOGITS: z holds what is
+// added to the product times the scale; -infinity stays.
+template <int V, int CB, int G, bool LOGITS, typename S, typename A>
 __device__ __forceinline__ void dots(const AtArgs& a, const AtTab& tab, int cnt, const S* x, const AtRows& rows, const int* idx, A* z) {
+  constexpr int U = kFlight<S, V * CB, 4>;
   const AtLanes& l = tab.lanes;
   const Place at(l);
-  const int units = a.heads / G, pieces = tab.pieces, slots = 32 >> (l.width + l.units), end = filled(cnt, U * slots);
+  const int units = a.heads / G, pieces = tab.pieces, slots = 32 >> (l.width + l.units);
+#pragma unroll 1
   for (int ub = 0; ub < units; ub += 32) {
     const int h0 = min(ub + at.u, units - 1) * G;
-    const bool writes = at.x == 0 && ub + at.u < units;
+    const bool mine = ub + at.u < units;
     const int* full = tab.dot_full + h0 * pieces;
     const int* shared = tab.dot_kv + (a.group == 1 ? h0 : h0 / a.group) * pieces;
 #pragma unroll 1
@@ -267,7 +340,6 @@ __device__ __forceinline__ void dots(const AtArgs& a, const AtTab& tab, int cnt,
       Nums<A, V> xr[G][CB];
       const char* base[CB];
       bool ok[CB];
-      Pack<S, V> y[U][CB];
 #pragma unroll
       for (int j = 0; j < CB; ++j) {
         const int c = c0 + (j << l.width) + at.x;
@@ -280,72 +352,80 @@ __device__ __forceinline__ void dots(const AtArgs& a, const AtTab& tab, int cnt,
           if (ok[j]) v.load(x + full[q * pieces + c]);
           xr[q][j] = widened<A>(v);
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) y[u][j].clear();   // what lanes without a vector multiply by zero
       }
       const int* ip = idx + at.s;
-      A* to_ = z + at.s * a.heads + h0;
+      A* to_ = z + h0 * a.stride + at.s;
 #pragma unroll 1
-      for (int b = 0; b < end; b += U * slots, ip += U * slots, to_ += U * slots * a.heads) {
+      for (int b = 0; b < cnt; b += U * slots, ip += U * slots, to_ += U * slots) {
+        // (the list of edges is filled up with the last one's end; lanes without a vector read the row's first)
+        Pack<S, V> y[U][CB];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const uint64_t off = uint64_t(static_cast<unsigned>(ip[u * slots])) * rows.ld_bytes;
 #pragma unroll
-          for (int j = 0; j < CB; ++j)
-            if (ok[j]) y[u][j].load(reinterpret_cast<const S*>(base[j] + off));
+          for (int j = 0; j < CB; ++j) y[u][j].load(reinterpret_cast<const S*>(base[j] + off));
         }
-        A sum[U][G];
+        A sum[G][U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          Nums<A, V> s[G];
-#pragma unroll
-          for (int q = 0; q < G; ++q) s[q].clear();
+          Dot<A, V> s[G];
 #pragma unroll
           for (int j = 0; j < CB; ++j) {
             const Nums<A, V> w = widened<A>(y[u][j]);
 #pragma unroll
-            for (int q = 0; q < G; ++q) s[q].add_product(xr[q][j], w);
+            for (int q = 0; q < G; ++q) s[q].add(xr[q][j], w, ok[j]);
           }
 #pragma unroll
-          for (int q = 0; q < G; ++q) sum[u][q] = s[q].total();
+          for (int q = 0; q < G; ++q) sum[q][u] = s[q].total();
         }
-#pragma unroll 1
-        for (int o = 1 << l.width >> 1; o > 0; o >>= 1)
 #pragma unroll
-          for (int u = 0; u < U; ++u)
+        for (int q = 0; q < G; ++q) {
+          const int r = lane_sums<U>(sum[q], l.width, at.x), first = r & 255, held = r >> 8;
+          // (of the lanes that hold the same sums the first writes them)
+          if (mine && at.x < (held == U ? 1 : 2 * held == U ? 2 : 4))
 #pragma unroll
-            for (int q = 0; q < G; ++q) sum[u][q] += __shfl_xor_sync(kAll, sum[u][q], o);
-        if (writes)
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int q = 0; q < G; ++q) {
-              A* r = to_ + u * slots * a.heads + q;
-              *r = c0 == 0 ? sum[u][q] : *r + sum[u][q];
+            for (int u = 0; u < U; ++u) {
+              const int i = (first + u) * slots;
+              if (u >= held || b + i + at.s >= cnt) continue;
+              A* to = to_ + q * a.stride + i;
+              if (LOGITS) {
+                const A before = *to;
+                if (before != lowest<A>()) *to = sum[q][u] * static_cast<A>(a.scale) + before;
+              } else {
+                *to = c0 == 0 ? sum[q][u] : *to + sum[q][u];
+              }
             }
+        }
       }
     }
   }
   __syncwarp();
 }
 
-// Sums over edges: r = sum_i coef[i][h] rows[idx(i)][offset of a vector], plus, where this is not the first part of a run,
-// what the parts before left in `keep`, times rescale[head].  emit(head, vector's offset, r) by one lane where this is
-// the last part.  SEND: the units are shared heads, whose result sums over the heads of their group; otherwise G heads
-// that share a row's vectors are taken together.
-template <int V, int CB, int U, int G, bool SEND, typename S, typename A, typename F>
+// Sums over edges: r = sum_i coef[h][i] rows[idx(i)][vector], plus, where this is not the first part of a run, what the
+// parts before left in `keep`, times rescale[head].  emit(head, vector's offset, r) by one lane where this is the last
+// part.  The vectors of a row of the shared heads are dealt out to the lanes in the order of memory, so that a row is
+// read in whole lines, and a lane takes four edges at a time: their ends in one load, their weights, which lie side by
+// side, in one or two, and one address a row.  SEND: results are rows of the shared heads, which sum over the heads of
+// their group; otherwise rows of all heads, G that share a vector at a time.  APART: rows of all heads, in which the
+// vectors of a shared head's group lie apart.
+template <int V, int CB, int G, bool SEND, bool APART, typename S, typename A, typename F>
 __device__ __forceinline__ void sums(const AtArgs& a, const AtTab& tab, int cnt, A* coef, const AtRows& rows, const int* idx, A* keep,
                                      const A* rescale, bool first, bool last, F&& emit) {
-  const AtLanes& l = tab.lanes;
-  const Place at(l);
-  const int units = SEND ? a.kv : a.heads / G, pieces = tab.pieces, slots = 32 >> (l.width + l.units), end = filled(cnt, U * slots);
-  for (int f = cnt * a.heads + (threadIdx.x & 31); f < end * a.heads; f += 32) coef[f] = 0;
-  __syncwarp();
-  for (int ub = 0; ub < units; ub += 32) {
-    const bool on = ub + at.u < units;
-    const int unit = min(ub + at.u, units - 1);
+  const int lane = threadIdx.x & 31, x = lane & ((1 << tab.abreast) - 1), s = lane >> tab.abreast;
+  const int step = (32 >> tab.abreast) * kAtQuad, end = (cnt + step - 1) & -step, total = a.kv * tab.pieces;
+  constexpr int kOffset = (1 << kAtHeadShift) - 1;
+  // weights of the places behind the last edge
 #pragma unroll 1
-    for (int c0 = 0; c0 < pieces; c0 += CB << l.width) {
+  for (int k = lane; k < (end - cnt) * a.heads; k += 32) {
+    const int i = pair_edge(a, k);
+    coef[(k - i * a.heads) * a.stride + cnt + i] = 0;
+  }
+  __syncwarp();
+#pragma unroll 1
+  for (int c0 = 0; c0 < total; c0 += CB << tab.abreast) {
+#pragma unroll 1
+    for (int g0 = 0; g0 < (SEND ? 1 : a.group); g0 += G) {
       Nums<A, V> acc[G][CB];
 #pragma unroll
       for (int q = 0; q < G; ++q)
@@ -353,73 +433,65 @@ __device__ __forceinline__ void sums(const AtArgs& a, const AtTab& tab, int cnt,
         for (int j = 0; j < CB; ++j) acc[q][j].clear();
 #pragma unroll 1
       for (int g = 0; g < (SEND ? a.group : 1); ++g) {
-        const int h0 = SEND ? unit * a.group + g : unit * G;
-        const int* from = SEND ? tab.dot_full + h0 * pieces : tab.dot_kv + (a.group == 1 ? h0 : h0 / a.group) * pieces;
         const char* base[CB];
-        bool ok[CB];
-        Pack<S, V> y[U][CB];
+        const A* fp[CB];
 #pragma unroll
         for (int j = 0; j < CB; ++j) {
-          const int c = c0 + (j << l.width) + at.x;
-          ok[j] = c < pieces;
-          base[j] = rows.p + (ok[j] ? from[c] : 0) * sizeof(S);
-#pragma unroll
-          for (int u = 0; u < U; ++u) y[u][j].clear();
+          // (lanes beyond the last vector take it too, for nothing)
+          const int c = min(c0 + (j << tab.abreast) + x, total - 1), entry = tab.rows[c * a.group + g0 + g];
+          fp[j] = coef + (entry >> kAtHeadShift) * a.stride + s * kAtQuad;
+          base[j] = rows.p + (APART ? entry & kOffset : c * V) * sizeof(S);
         }
-        const int* ip = idx + at.s;
-        const A* fp = coef + at.s * a.heads + h0;
+        const int* ip = idx + s * kAtQuad;
 #pragma unroll 1
-        for (int b = 0; b < end; b += U * slots, ip += U * slots, fp += U * slots * a.heads) {
-          A f[U][G];
+        for (int b = 0; b < end; b += step) {
+          Pack<int, 4> ends;
+          ends.load(ip + b);
+          constexpr int U = kFlight<S, V * CB, kAtQuad>;
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const uint64_t off = uint64_t(static_cast<unsigned>(ip[u * slots])) * rows.ld_bytes;
+          for (int part = 0; part < kAtQuad; part += U) {
+            Pack<S, V> y[U][CB];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const uint64_t off = uint64_t(static_cast<unsigned>(ends.e[part + u])) * rows.ld_bytes;
+#pragma unroll
+              for (int j = 0; j < CB; ++j) y[u][j].load(reinterpret_cast<const S*>(base[j] + off));
+            }
 #pragma unroll
             for (int j = 0; j < CB; ++j)
-              if (ok[j]) y[u][j].load(reinterpret_cast<const S*>(base[j] + off));
 #pragma unroll
-            for (int q = 0; q < G; ++q) f[u][q] = fp[u * slots * a.heads + q];
+              for (int q = 0; q < G; ++q) {
+                Pack<A, U> f;
+                f.load(fp[j] + q * a.stride + b + part);
+#pragma unroll
+                for (int u = 0; u < U; ++u) acc[q][j].add_weighed(f.e[u], widened<A>(y[u][j]));
+              }
           }
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < CB; ++j) {
-              const Nums<A, V> w = widened<A>(y[u][j]);
-#pragma unroll
-              for (int q = 0; q < G; ++q) acc[q][j].add(f[u][q], w);
-            }
         }
       }
-#pragma unroll 1
-      for (int o = 1 << (l.width + l.units); o < 32; o <<= 1)
 #pragma unroll
-        for (int q = 0; q < G; ++q)
-#pragma unroll
-          for (int j = 0; j < CB; ++j)
-#pragma unroll
-            for (int k = 0; k < V; ++k) acc[q][j].set(k, acc[q][j].get(k) + __shfl_xor_sync(kAll, acc[q][j].get(k), o));
-      if (at.s == 0 && on)
+      for (int q = 0; q < G; ++q)
 #pragma unroll
         for (int j = 0; j < CB; ++j) {
-          const int c = c0 + (j << l.width) + at.x;
-          if (c >= pieces) continue;
+          A r[V];
+          acc[q][j].get(r);
+#pragma unroll 1
+          for (int o = 1 << tab.abreast; o < 32; o <<= 1)
 #pragma unroll
-          for (int q = 0; q < G; ++q) {
-            const int h = SEND ? unit : unit * G + q, place = (SEND ? tab.dot_kv : tab.dot_full)[h * pieces + c];
-            A r[V];
+            for (int k = 0; k < V; ++k) r[k] += __shfl_xor_sync(kAll, r[k], o);
+          const int c = c0 + (j << tab.abreast) + x;
+          if (s != 0 || c >= total) continue;
+          const int entry = tab.rows[c * a.group + g0 + q], h = entry >> kAtHeadShift, place = SEND ? c * V : entry & kOffset;
+          if (!first) {
+            const A f = rescale ? rescale[h] : A(1);
 #pragma unroll
-            for (int k = 0; k < V; ++k) r[k] = acc[q][j].get(k);
-            if (!first) {
-              const A f = rescale ? rescale[h] : A(1);
+            for (int k = 0; k < V; ++k) r[k] += f == 0 ? A(0) : keep[place + k] * f;
+          }
+          if (last) {
+            emit(h, place, r);
+          } else {
 #pragma unroll
-              for (int k = 0; k < V; ++k) r[k] += f == 0 ? A(0) : keep[place + k] * f;
-            }
-            if (last) {
-              emit(h, place, r);
-            } else {
-#pragma unroll
-              for (int k = 0; k < V; ++k) keep[place + k] = r[k];
-            }
+            for (int k = 0; k < V; ++k) keep[place + k] = r[k];
           }
         }
     }
@@ -427,17 +499,21 @@ __device__ __forceinline__ void sums(const AtArgs& a, const AtTab& tab, int cnt,
   __syncwarp();
 }
 
+// dots and sums of queries and keys, whose heads are short: one or two vectors a lane
+template <int V, int G, bool LOGITS, typename... P>
+__device__ __forceinline__ void short_dots(const AtArgs& a, const AtTab& tab, P&&... x) {
+  if (tab.dot_turn == 1) dots<V, 1, G, LOGITS>(a, tab, x...);
+  else dots<V, kShort<V, G>, G, LOGITS>(a, tab, x...);
+}
+template <int V, int G, bool SEND, bool APART, typename S, typename... P>
+__device__ __forceinline__ void short_sums(const AtArgs& a, const AtTab& tab, P&&... x) {
+  if (tab.turn == 1) sums<V, 1, G, SEND, APART, S>(a, tab, x...);
+  else sums<V, kShort<V, G>, G, SEND, APART, S>(a, tab, x...);
+}
+
 // CTAs of 256 threads that an SM is to hold: registers bound the edges in flight.
 template <int G>
 constexpr int kResident = G == 1 ? 3 : 2;
-
-// Vectors of a lane that the loops hold at once, and edges in flight: two of each for queries and keys, whose rows are
-// short, and for values what the plan's rows fill best (CB, see attn.cu); single elements four at a time; where four
-// heads share a vector one, with four edges.
-template <int V, int G>
-constexpr int kTurn = G == 4 ? 1 : V == 1 ? 4 : 2;
-template <int CB, int G>
-constexpr int kFlight = G == 4 ? 4 : CB == 2 ? 2 : 1;
 
 // The heads of a warp's lanes for sums over edges x heads in shared memory: lane = (edge slot, head); lanes beyond the
 // last head have no edges.
@@ -482,75 +558,63 @@ __device__ __forceinline__ int bucket_of(const A* borders, int n, A r) {
   return lo;
 }
 
-// A warp's regions of shared memory
-template <typename A>
-struct Smem {
-  A *z, *p, *stat, *acc;
-  int *idx, *bucket;
-  __device__ __forceinline__ Smem(const AtArgs& a, int warp) {
-    extern __shared__ __align__(16) char at_smem[];
-    char* s = at_smem + warp * a.warp_smem;
-    z = reinterpret_cast<A*>(s);
-    p = reinterpret_cast<A*>(s + a.at_p);
-    idx = reinterpret_cast<int*>(s + a.at_idx);
-    bucket = idx + a.sub + a.pad;
-    stat = reinterpret_cast<A*>(s + a.at_stat);
-    acc = reinterpret_cast<A*>(s + a.at_acc);
-  }
-};
-
 // Ends of the edges [e, e + cnt), filled up to what the loops take at a time.
 template <typename A>
-__device__ __forceinline__ void load_ends(const AtArgs& a, const Smem<A>& sm, int64_t e, int cnt) {
+__device__ __forceinline__ void load_ends(const AtArgs& a, const Smem<A>& sm, int e, int cnt) {
   if (cnt == 0) return;
-  for (int i = threadIdx.x & 31; i < cnt + a.pad; i += 32) sm.idx[i] = a.col[e + (i < cnt ? i : 0)];
+  for (int i = threadIdx.x & 31; i < cnt + a.pad; i += 32) sm.idx[i] = a.col[e + min(i, cnt - 1)];
 }
 
-// Inner products of the queries of `row` and the keys of the edges [e, e + cnt), into z.
-template <int QV, int G, typename S, typename A>
-__device__ __forceinline__ void products(const AtArgs& a, const Smem<A>& sm, int64_t row, int64_t e, int cnt) {
+// f(place in z, edge, head, index from e * heads) for the cnt edges and the heads in the order of memory, four a lane at a
+// time, so that their loads overlap.
+template <typename F>
+__device__ __forceinline__ void each_pair(const AtArgs& a, int cnt, F&& f) {
+#pragma unroll 4
+  for (int k = threadIdx.x & 31; k < cnt * a.heads; k += 32) {
+    const int i = pair_edge(a, k), h = k - i * a.heads;
+    f(h * a.stride + i, i, h, k);
+  }
+}
+
+// Logits of the edges [e, e + cnt) of `row` into z.
+template <int V, int G, typename S, typename A>
+__device__ __forceinline__ void logits(const AtArgs& a, const Smem<A>& sm, int row, int e, int cnt) {
   load_ends(a, sm, e, cnt);
-  if (a.table)
+  if (a.table) {
     for (int i = threadIdx.x & 31; i < cnt; i += 32)
       sm.bucket[i] = bucket_of(static_cast<const A*>(a.borders), a.n_borders, static_cast<const A*>(a.lengths)[e + i]);
+    __syncwarp();
+  }
+  const A *table = static_cast<const A*>(a.table), *bias = static_cast<const A*>(a.bias) + int64_t(e) * a.heads;
+  each_pair(a, cnt, [&](int at, int i, int h, int k) {
+    A b = a.bias ? bias[k] : A(0);
+    if (table) b += table[sm.bucket[i] * a.heads + h];
+    sm.z[at] = b;
+  });
   __syncwarp();
-  constexpr int CB = kTurn<QV, G>;
-  dots<QV, CB, kFlight<CB, G>, G>(a, a.qk, cnt, reinterpret_cast<const S*>(a.q.p) + row * a.q.ld, a.k, sm.idx, sm.z);
-}
-
-// The logit of edge e + i and head h from its inner product.
-template <typename A>
-__device__ __forceinline__ A logit(const AtArgs& a, const Smem<A>& sm, int64_t e, int i, int h) {
-  A b = 0;
-  if (a.table) b = static_cast<const A*>(a.table)[sm.bucket[i] * a.heads + h];
-  if (a.bias) b += static_cast<const A*>(a.bias)[(e + i) * a.heads + h];
-  return b == lowest<A>() ? b : sm.z[i * a.heads + h] * static_cast<A>(a.scale) + b;
+  short_dots<V, G, true>(a, a.qk, cnt, reinterpret_cast<const S*>(a.q.p) + int64_t(row) * a.q.ld, a.k, sm.idx, sm.z);
 }
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
 
-// Turns the products in z into logits and, unless keep_z, those into exp(z - maximum), with the running maximum (stat[h])
-// and sum of exponentials (stat[heads + h]); stat[2 heads + h] = factor of what was summed before.
+// Running maximum (stat[h]) and sum of exponentials (stat[heads + h]) over the logits in z, which become exp(z - maximum)
+// unless keep_z; stat[2 heads + h] = factor of what was summed before.
 template <typename A>
-__device__ __forceinline__ void softmax_step(const AtArgs& a, const Smem<A>& sm, int64_t e, int cnt, bool first, bool keep_z) {
+__device__ __forceinline__ void softmax_step(const AtArgs& a, const Smem<A>& sm, int cnt, bool first, bool keep_z) {
   each_head(a, [&](const HeadLanes& l) {
     A top = lowest<A>();
-    for (int i = l.slot; i < cnt; i += l.slots) {
-      const A z = logit(a, sm, e, i, l.h);
-      sm.z[i * a.heads + l.h] = z;
-      top = larger(top, z);
-    }
+    for (int i = l.slot; i < cnt; i += l.slots) top = larger(top, sm.z[l.h * a.stride + i]);
     top = all_max(l, top);
     const A before = first || l.h >= a.heads ? lowest<A>() : sm.stat[l.h];
     top = larger(top, before);
     const A shift = top == lowest<A>() ? A(0) : top;
     A sum = 0;
     for (int i = l.slot; i < cnt; i += l.slots) {
-      const A p = expo(sm.z[i * a.heads + l.h] - shift);
+      const A p = expo(sm.z[l.h * a.stride + i] - shift);
       sum += p;
-      if (!keep_z) sm.z[i * a.heads + l.h] = p;
+      if (!keep_z) sm.z[l.h * a.stride + i] = p;
     }
     sum = all_sum(l, sum);
     __syncwarp();
@@ -587,29 +651,28 @@ __device__ __forceinline__ void join_warps(const AtArgs& a, const Team& t) {
   __syncthreads();
 }
 
-template <typename S, typename R, typename A, int QV, int VV, int G, int CB>
-__global__ void __launch_bounds__(256, kResident<G>) attn_forward_kernel(const AtArgs a) {
+template <typename S, typename R, typename A, int V, int G, int CB>
+__global__ void __launch_bounds__(256, kResident<G>) attn_forward_kernel(const __grid_constant__ AtArgs a) {
   chain_enter();
   const Team t(a);
   const Smem<A> sm(a, threadIdx.x / 32);
   const int width = a.heads * a.dv;
-  each_item(a, t, [&](const Item& it) {
+  const Item it = item_of(a, t);
+  if (!it.some) return;
+  {
     const bool part = it.index >= 0;
-    A* to_part = static_cast<A*>(a.part) + int64_t(it.index) * (width + 2 * a.heads);
-    R* out = reinterpret_cast<R*>(a.out.p) + it.row * a.out.ld;
-    int64_t e = it.e0;
+    A* to_part = static_cast<A*>(a.part) + int64_t(it.index) * a.part_ld;
+    R* out = reinterpret_cast<R*>(a.out.p) + int64_t(it.row) * a.out.ld;
+    int e = it.e0;
     do {
-      const int cnt = static_cast<int>(min(int64_t(a.sub), it.e1 - e));
-      products<QV, G, S>(a, sm, it.row, e, cnt);
-      softmax_step(a, sm, e, cnt, e == it.e0, false);
+      const int cnt = min(a.sub, it.e1 - e);
+      logits<V, G, S>(a, sm, it.row, e, cnt);
+      softmax_step(a, sm, cnt, e == it.e0, false);
       const bool last = e + cnt >= it.e1;
-      sums<VV, CB, kFlight<CB, G>, G, false, S>(
-          a, a.vv, cnt, sm.z, a.v, sm.idx, sm.acc, sm.stat + 2 * a.heads, e == it.e0, t.one && last,
+      sums<V, CB, G, false, false, S>(a, a.vv, cnt, sm.z, a.v, sm.idx, sm.acc, sm.stat + 2 * a.heads, e == it.e0, t.one && last,
                   [&](int h, int at, const A* r) {
-                    constexpr int V = VV;
                     if (part) {
-#pragma unroll
-                      for (int k = 0; k < V; ++k) to_part[at + k] = r[k];
+                      store_as<V>(to_part + at, r);
                     } else {
                       const A l = sm.stat[a.heads + h], f = l == 0 ? A(0) : A(1) / l;
                       Pack<R, V> y;
@@ -642,19 +705,19 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_forward_kernel(const A
         to_part[width + h] = top;
         to_part[width + a.heads + h] = l;
       } else {
-        static_cast<A*>(a.lse)[it.row * a.heads + h] = loga(l) + (top == lowest<A>() ? A(0) : top);
+        static_cast<A*>(a.lse)[int64_t(it.row) * a.heads + h] = loga(l) + (top == lowest<A>() ? A(0) : top);
       }
     }
-  });
+  }
 }
 
 // Joins the parts of a split row: grid (rows, columns / 32); 8 streams of parts a column.
 template <typename R, typename A>
-__global__ void attn_join_forward_kernel(const AtArgs a) {
+__global__ void attn_join_forward_kernel(const __grid_constant__ AtArgs a) {
   chain_enter();
   __shared__ A red[8][33], red_l[8][33];
   const Int4 j = a.joins[blockIdx.x];
-  const int width = a.heads * a.dv, stride = width + 2 * a.heads;
+  const int width = a.heads * a.dv, stride = a.part_ld;
   const int c = blockIdx.y * 32 + threadIdx.x, s = threadIdx.y;
   const A* part = static_cast<const A*>(a.part) + int64_t(j.y) * stride;
   // the columns' heads: those of the vectors in the order of memory, then the statistics'
@@ -703,22 +766,24 @@ __global__ void attn_join_sum_kernel(const AtArgs a, const AtRows out, int width
 
 // Weights of the edges of a row.  A run of edges that fits `sub` is done at once; a longer one writes its logits to alpha
 // and comes back for them; the items of a split row do so in two launches.
-template <typename S, typename A, int QV, int G>
-__global__ void __launch_bounds__(256, kResident<G>) attn_weights_kernel(const AtArgs a) {
+template <typename S, typename A, int V, int G>
+__global__ void __launch_bounds__(256, kResident<G>) attn_weights_kernel(const __grid_constant__ AtArgs a) {
   chain_enter();
   const Team t(a);
   const Smem<A> sm(a, threadIdx.x / 32), one(a, t.one ? threadIdx.x / 32 : 0);
   A* alpha = static_cast<A*>(a.alpha);
-  each_item(a, t, [&](const Item& it) {
+  const Item it = item_of(a, t);
+  if (!it.some) return;
+  {
     const bool held = t.one && it.index < 0 && it.e1 - it.e0 <= a.sub;
     if (a.phase != kAtSecond) {
-      int64_t e = it.e0;
+      int e = it.e0;
       do {
-        const int cnt = static_cast<int>(min(int64_t(a.sub), it.e1 - e));
-        products<QV, G, S>(a, sm, it.row, e, cnt);
-        softmax_step(a, sm, e, cnt, e == it.e0, !held);
+        const int cnt = min(a.sub, it.e1 - e);
+        logits<V, G, S>(a, sm, it.row, e, cnt);
+        softmax_step(a, sm, cnt, e == it.e0, !held);
         if (!held)
-          for (int f = t.lane; f < cnt * a.heads; f += 32) alpha[e * a.heads + f] = sm.z[f];
+          each_pair(a, cnt, [&](int at, int, int, int k) { alpha[int64_t(e) * a.heads + k] = sm.z[at]; });
         __syncwarp();
         e += cnt;
       } while (e < it.e1);
@@ -751,20 +816,19 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_weights_kernel(const A
       __syncwarp();
     }
     const A* stat = a.phase == kAtSecond ? sm.stat : one.stat;
-    const int64_t base = it.e0 * a.heads;
-    const int count = static_cast<int>(it.e1 - it.e0) * a.heads;   // no run is longer than the graph's chunk
-    for (int f = t.lane; f < count; f += 32) {
-      const int h = f - pair_edge(a, f) * a.heads;
+    const int64_t base = int64_t(it.e0) * a.heads;
+    const int count = it.e1 - it.e0;   // no run is longer than the graph's chunk
+    each_pair(a, count, [&](int at, int, int h, int k) {
       const A l = stat[a.heads + h], top = stat[h];
-      const A p = held ? sm.z[f] : expo(alpha[base + f] - (top == lowest<A>() ? A(0) : top));
-      alpha[base + f] = p == 0 ? A(0) : p / l;
-    }
-  });
+      const A p = held ? sm.z[at] : expo(alpha[base + k] - (top == lowest<A>() ? A(0) : top));
+      alpha[base + k] = p == 0 ? A(0) : p / l;
+    });
+  }
 }
 
 // w' = a w: vectors of all rows in the order of memory, four a thread and turn.
 template <typename S, typename A>
-__global__ void __launch_bounds__(256) attn_scale_rows_kernel(const AtArgs a) {
+__global__ void __launch_bounds__(256) attn_scale_rows_kernel(const __grid_constant__ AtArgs a) {
   chain_enter();
   with_width<S>(a.vv.vec, [&](auto v) {
     constexpr int V = decltype(v)::value, U = 4;
@@ -811,7 +875,7 @@ __global__ void __launch_bounds__(256) attn_scale_rows_kernel(const AtArgs a) {
 
 // gw = a gw' and dp = <gw', w> (into ds): a warp takes the heads of one or more edges at a time.
 template <typename S, typename A>
-__global__ void __launch_bounds__(256) attn_edge_rows_backward_kernel(const AtArgs a) {
+__global__ void __launch_bounds__(256) attn_edge_rows_backward_kernel(const __grid_constant__ AtArgs a) {
   chain_enter();
   const A* alpha = static_cast<const A*>(a.alpha);
   A* dp = static_cast<A*>(a.ds);
@@ -871,55 +935,56 @@ struct alignas(2 * sizeof(A)) Pair {
 
 // The receivers' kernel: ds of every edge, and gq.  EDGES: dp comes in ds and a in alpha; otherwise both are
 // computed here.
-template <typename S, typename R, typename A, int QV, int VV, int G, int CB, bool EDGES>
-__global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const AtArgs a) {
+template <typename S, typename R, typename A, int V, int G, int CB, bool EDGES>
+__global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const __grid_constant__ AtArgs a) {
   chain_enter();
   const Team t(a);
   const Smem<A> sm(a, threadIdx.x / 32);
   const A scale = static_cast<A>(a.scale);
   Pair<A>* pairs = static_cast<Pair<A>*>(a.pairs);
   const int width = a.heads * a.dk;
+  const Item it = item_of(a, t);
+  if (!it.some) return;
   // dp and a of the edges [e, e + cnt) into z and p: from memory where they are there
-  const auto fetch = [&](int64_t e, int cnt) {
+  const auto fetch = [&](int e, int cnt) {
     load_ends(a, sm, e, cnt);
-    for (int f = t.lane; f < cnt * a.heads; f += 32) {
+    each_pair(a, cnt, [&](int at, int, int, int k) {
       if (EDGES) {
-        sm.z[f] = static_cast<const A*>(a.ds)[e * a.heads + f];
-        sm.p[f] = static_cast<const A*>(a.alpha)[e * a.heads + f];
+        sm.z[at] = static_cast<const A*>(a.ds)[int64_t(e) * a.heads + k];
+        sm.p[at] = static_cast<const A*>(a.alpha)[int64_t(e) * a.heads + k];
       } else {
-        const Pair<A> x = pairs[e * a.heads + f];
-        sm.z[f] = x.ds;
-        sm.p[f] = x.p;
+        const Pair<A> x = pairs[int64_t(e) * a.heads + k];
+        sm.z[at] = x.ds;
+        sm.p[at] = x.p;
       }
-    }
+    });
     __syncwarp();
   };
-  each_item(a, t, [&](const Item& it) {
+  {
     const bool held = it.e1 - it.e0 <= a.sub && a.phase != kAtSecond;   // z, p and idx hold the whole run
     if (a.phase != kAtSecond) {
-      int64_t e = it.e0;
+      int e = it.e0;
       do {
-        const int cnt = static_cast<int>(min(int64_t(a.sub), it.e1 - e));
+        const int cnt = min(a.sub, it.e1 - e);
         if (EDGES) {
           fetch(e, cnt);
         } else {
-          products<QV, G, S>(a, sm, it.row, e, cnt);
-          const A* lse = static_cast<const A*>(a.lse) + it.row * a.heads;
-          for (int f = t.lane; f < cnt * a.heads; f += 32) {
-            const int i = pair_edge(a, f), h = f - i * a.heads;
-            const A z = logit(a, sm, e, i, h);
-            sm.p[f] = z == lowest<A>() ? A(0) : expo(z - lse[h]);
-          }
+          logits<V, G, S>(a, sm, it.row, e, cnt);
+          const A* lse = static_cast<const A*>(a.lse) + int64_t(it.row) * a.heads;
+          each_pair(a, cnt, [&](int at, int, int h, int) {
+            const A z = sm.z[at];
+            sm.p[at] = z == lowest<A>() ? A(0) : expo(z - lse[h]);
+          });
           __syncwarp();
-          dots<VV, CB, kFlight<CB, G>, G>(a, a.vv, cnt, reinterpret_cast<const S*>(a.gout.p) + it.row * a.gout.ld, a.v, sm.idx, sm.z);
+          dots<V, CB, G, false>(a, a.vv, cnt, reinterpret_cast<const S*>(a.gout.p) + int64_t(it.row) * a.gout.ld, a.v, sm.idx, sm.z);
           if (!held || it.index >= 0)
-            for (int f = t.lane; f < cnt * a.heads; f += 32) pairs[e * a.heads + f] = {sm.z[f], sm.p[f]};
+            each_pair(a, cnt, [&](int at, int, int, int k) { pairs[int64_t(e) * a.heads + k] = {sm.z[at], sm.p[at]}; });
         }
         each_head(a, [&](const HeadLanes& l) {
           A sum = 0;
           for (int i = l.slot; i < cnt; i += l.slots) {
-            const A p = sm.p[i * a.heads + l.h];
-            if (p != 0) sum += p * sm.z[i * a.heads + l.h];
+            const A p = sm.p[l.h * a.stride + i];
+            if (p != 0) sum += p * sm.z[l.h * a.stride + i];
           }
           sum = all_sum(l, sum);
           if (l.on) sm.stat[l.h] = (e == it.e0 ? A(0) : sm.stat[l.h]) + sum;
@@ -955,34 +1020,33 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const A
       __syncwarp();
     }
     const auto finish = [&](int at, A x) {   // one element of gq
-      if (it.index >= 0) static_cast<A*>(a.part)[int64_t(it.index) * width + at] = x * scale;
-      else (reinterpret_cast<R*>(a.gq.p) + it.row * a.gq.ld)[at] = to<R>(x * scale);
+      if (it.index >= 0) static_cast<A*>(a.part)[int64_t(it.index) * a.part_ld + at] = x * scale;
+      else (reinterpret_cast<R*>(a.gq.p) + int64_t(it.row) * a.gq.ld)[at] = to<R>(x * scale);
     };
-    int64_t e = it.e0;
+    int e = it.e0;
     do {
-      const int cnt = static_cast<int>(min(int64_t(a.sub), it.e1 - e));
+      const int cnt = min(a.sub, it.e1 - e);
       if (!held) fetch(e, cnt);
-      for (int f = t.lane; f < cnt * a.heads; f += 32) {
-        const int h = f - pair_edge(a, f) * a.heads;
-        const A p = sm.p[f], d = p == 0 ? A(0) : p * (sm.z[f] - sm.stat[h]);
-        sm.z[f] = d;
-        if (!EDGES) pairs[e * a.heads + f] = {d, p};
-        if (a.ds) static_cast<A*>(a.ds)[e * a.heads + f] = d;
-      }
+      each_pair(a, cnt, [&](int at, int, int h, int k) {
+        const A p = sm.p[at], d = p == 0 ? A(0) : p * (sm.z[at] - sm.stat[h]);
+        sm.z[at] = d;
+        if (!EDGES) pairs[int64_t(e) * a.heads + k] = {d, p};
+        if (a.ds) static_cast<A*>(a.ds)[int64_t(e) * a.heads + k] = d;
+      });
       __syncwarp();
       const bool last = e + cnt >= it.e1;
-      constexpr int QB = kTurn<QV, G>;
-      sums<QV, QB, kFlight<QB, G>, G, false, S>(
-          a, a.qk, cnt, sm.z, a.k, sm.idx, sm.acc, static_cast<const A*>(nullptr), e == it.e0, t.one && last, [&](int, int at, const A* r) {
-                    constexpr int V = QV;
+      short_sums<V, G, false, false, S>(a, a.qk, cnt, sm.z, a.k, sm.idx, sm.acc, static_cast<const A*>(nullptr), e == it.e0, t.one && last,
+                  [&](int, int at, const A* r) {
                     if (it.index >= 0) {
+                      A x[V];
 #pragma unroll
-                      for (int k = 0; k < V; ++k) finish(at + k, r[k]);
+                      for (int k = 0; k < V; ++k) x[k] = r[k] * scale;
+                      store_as<V>(static_cast<A*>(a.part) + int64_t(it.index) * a.part_ld + at, x);
                     } else {
                       Pack<R, V> y;
 #pragma unroll
                       for (int k = 0; k < V; ++k) y.e[k] = to<R>(r[k] * scale);
-                      y.store(reinterpret_cast<R*>(a.gq.p) + it.row * a.gq.ld + at);
+                      y.store(reinterpret_cast<R*>(a.gq.p) + int64_t(it.row) * a.gq.ld + at);
                     }
                   });
       __syncwarp();
@@ -996,50 +1060,49 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const A
         finish(c, r);
       }
     }
-  });
+  }
 }
 
 // The sources' kernel, over the transpose: gk, and gv where VALUES.
-template <typename S, typename R, typename A, int QV, int VV, int CB, bool VALUES>
-__global__ void __launch_bounds__(256, kResident<1>) attn_send_kernel(const AtArgs a) {
+template <typename S, typename R, typename A, int V, int CB, bool VALUES>
+__global__ void __launch_bounds__(256, kResident<1>) attn_send_kernel(const __grid_constant__ AtArgs a) {
   chain_enter();
   const Team t(a);
   const Smem<A> sm(a, threadIdx.x / 32);
   const A scale = static_cast<A>(a.scale);
-  const int wk = a.kv * a.dk, stride = wk + (VALUES ? a.kv * a.dv : 0);
-  each_item(a, t, [&](const Item& it) {
+  const int wk = (a.kv * a.dk + 3) & ~3, stride = wk + (VALUES ? a.kv * a.dv : 0);   // (aligned for vectors)
+  const Item it = item_of(a, t);
+  if (!it.some) return;
+  {
     const bool part = it.index >= 0;
-    A* to_part = static_cast<A*>(a.part) + int64_t(it.index) * stride;
+    A* to_part = static_cast<A*>(a.part) + int64_t(it.index) * a.part_ld;
     const auto finish = [&](int at, A x) {   // element `at` of (gk, gv)
       if (part) to_part[at] = x;
-      else if (at < wk) (reinterpret_cast<R*>(a.gk.p) + it.row * a.gk.ld)[at] = to<R>(x);
-      else (reinterpret_cast<R*>(a.gv.p) + it.row * a.gv.ld)[at - wk] = to<R>(x);
+      else if (at < a.kv * a.dk) (reinterpret_cast<R*>(a.gk.p) + int64_t(it.row) * a.gk.ld)[at] = to<R>(x);
+      else if (at >= wk) (reinterpret_cast<R*>(a.gv.p) + int64_t(it.row) * a.gv.ld)[at - wk] = to<R>(x);
     };
-    int64_t e = it.e0;
+    int e = it.e0;
     do {
-      const int cnt = static_cast<int>(min(int64_t(a.sub), it.e1 - e));
+      const int cnt = min(a.sub, it.e1 - e);
       load_ends(a, sm, e, cnt);
       for (int i = t.lane; i < cnt; i += 32) sm.bucket[i] = a.eid[e + i];
       __syncwarp();
-      for (int f = t.lane; f < cnt * a.heads; f += 32) {
-        const int i = pair_edge(a, f);
-        const int64_t at = int64_t(sm.bucket[i]) * a.heads + (f - i * a.heads);
+      each_pair(a, cnt, [&](int to_, int i, int h, int) {
+        const int64_t at = int64_t(sm.bucket[i]) * a.heads + h;
         if (VALUES) {
           const Pair<A> x = static_cast<const Pair<A>*>(a.pairs)[at];
-          sm.z[f] = x.ds * scale;
-          sm.p[f] = x.p;
+          sm.z[to_] = x.ds * scale;
+          sm.p[to_] = x.p;
         } else {
-          sm.z[f] = static_cast<const A*>(a.ds)[at] * scale;
+          sm.z[to_] = static_cast<const A*>(a.ds)[at] * scale;
         }
-      }
+      });
       __syncwarp();
       const bool first = e == it.e0, last = t.one && e + cnt >= it.e1;
-      const auto store = [&](auto v, R* row, int from) {
+      const auto store = [&](R* row, int from) {
         return [=](int, int at, const A* r) {
-          constexpr int V = decltype(v)::value;
           if (part) {
-#pragma unroll
-            for (int k = 0; k < V; ++k) to_part[from + at + k] = r[k];
+            store_as<V>(to_part + from + at, r);
           } else {
             Pack<R, V> y;
 #pragma unroll
@@ -1048,13 +1111,16 @@ __global__ void __launch_bounds__(256, kResident<1>) attn_send_kernel(const AtAr
           }
         };
       };
-      constexpr int QB = kTurn<QV, 1>;
       const A* none = nullptr;
-      sums<QV, QB, kFlight<QB, 1>, 1, true, S>(a, a.qk, cnt, sm.z, a.q, sm.idx, sm.acc, none, first, last,
-                                               store(std::integral_constant<int, QV>(), reinterpret_cast<R*>(a.gk.p) + it.row * a.gk.ld, 0));
-      if (VALUES)
-        sums<VV, CB, kFlight<CB, 1>, 1, true, S>(a, a.vv, cnt, sm.p, a.gout, sm.idx, sm.acc + wk, none, first, last,
-                                                 store(std::integral_constant<int, VV>(), reinterpret_cast<R*>(a.gv.p) + it.row * a.gv.ld, wk));
+      const auto to_k = store(reinterpret_cast<R*>(a.gk.p) + int64_t(it.row) * a.gk.ld, 0);
+      const auto to_v = store(reinterpret_cast<R*>(a.gv.p) + int64_t(it.row) * a.gv.ld, wk);
+      if (a.group == 1) {
+        short_sums<V, 1, true, false, S>(a, a.qk, cnt, sm.z, a.q, sm.idx, sm.acc, none, first, last, to_k);
+        if (VALUES) sums<V, CB, 1, true, false, S>(a, a.vv, cnt, sm.p, a.gout, sm.idx, sm.acc + wk, none, first, last, to_v);
+      } else {
+        short_sums<V, 1, true, true, S>(a, a.qk, cnt, sm.z, a.q, sm.idx, sm.acc, none, first, last, to_k);
+        if (VALUES) sums<V, CB, 1, true, true, S>(a, a.vv, cnt, sm.p, a.gout, sm.idx, sm.acc + wk, none, first, last, to_v);
+      }
       __syncwarp();
       e += cnt;
     } while (e < it.e1);
@@ -1066,13 +1132,13 @@ __global__ void __launch_bounds__(256, kResident<1>) attn_send_kernel(const AtAr
         finish(c, r);
       }
     }
-  });
+  }
 }
 
 // Gradient of the bias table: sums of ds by bucket.  A lane always adds to the same head's column of its warp's
 // histogram, one column a lane, so that nothing collides and the order is fixed.  ds lies ds_step values apart.
 template <typename A>
-__global__ void attn_table_kernel(const AtArgs a) {
+__global__ void attn_table_kernel(const __grid_constant__ AtArgs a) {
   chain_enter();
   extern __shared__ __align__(16) char at_smem[];
   const int buckets = a.n_borders + 1, cols = a.hist_cols, lane = threadIdx.x & 31, w = threadIdx.x / 32, warps_here = blockDim.x / 32;
@@ -1162,31 +1228,39 @@ cudaError_t at_run(void (*kernel)(P...), const AtArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// kernel(QV, VV, G, CB) for the call's vectors
+// kernel(V, G, CB) for the call's vectors; turn: those of values that a lane holds at once
 template <typename S, typename F>
-auto at_variant(const AtArgs& a, F&& f) {
-  using std::integral_constant;
-  constexpr int W = kWide<S>;
-  const integral_constant<int, 1> one{};
-  const integral_constant<int, W> w{};
-  const integral_constant<int, 2> two{};
-  const integral_constant<int, 4> four{};
-  const integral_constant<int, 5> five{};
-  if (a.four) return f(w, w, four, one);
-  if (a.vv.vec == 1) return a.qk.vec == 1 ? f(one, one, one, four) : f(w, one, one, four);
-  if (a.qk.vec == 1) return a.vv.turn == 2 ? f(one, w, one, two) : a.vv.turn == 4 ? f(one, w, one, four) : f(one, w, one, five);
-  return a.vv.turn == 2 ? f(w, w, one, two) : a.vv.turn == 4 ? f(w, w, one, four) : f(w, w, one, five);
+auto at_variant(const AtArgs& a, int turn, F&& f) {
+  const std::integral_constant<int, 1> one{};
+  const std::integral_constant<int, 2> two{};
+  const std::integral_constant<int, 3> three{};
+  const std::integral_constant<int, 4> four{};
+  const auto with = [&](auto v) {
+    if (a.four) {
+      if constexpr (kShort<decltype(v)::value, 4> == 2) {
+        if (turn == 2) return f(v, four, two);
+      }
+      return f(v, four, one);
+    }
+    return turn == 1 ? f(v, one, one) : turn == 2 ? f(v, one, two) : turn == 3 ? f(v, one, three) : f(v, one, four);
+  };
+  if (a.qk.vec == 1) return f(one, one, four);
+  if constexpr (kWide<S> == 8) {
+    if (a.qk.vec == 4) return with(four);
+  }
+  return with(std::integral_constant<int, kWide<S>>());
 }
 
 #define CGTP_AT_FORWARD(suffix, S, R, A)                                                                                     \
   cudaError_t at_forward_##suffix(const AtArgs& a, cudaStream_t st) {                                                        \
-    return at_variant<S>(a, [&](auto qv, auto vv, auto g, auto cb) {                                                         \
-      return at_run(attn_forward_kernel<S, R, A, decltype(qv)::value, decltype(vv)::value, decltype(g)::value, decltype(cb)::value>, a, st); \
+    return at_variant<S>(a, a.vv.turn, [&](auto v, auto g, auto cb) {                                                        \
+      return at_run(attn_forward_kernel<S, R, A, decltype(v)::value, decltype(g)::value, decltype(cb)::value>, a, st);       \
     });                                                                                                                      \
   }                                                                                                                          \
   cudaError_t at_weights_##suffix(const AtArgs& a, cudaStream_t st) {                                                        \
-    constexpr int W = kWide<S>;                                                                                              \
-    return at_run(a.four ? attn_weights_kernel<S, A, W, 4> : a.qk.vec == 1 ? attn_weights_kernel<S, A, 1, 1> : attn_weights_kernel<S, A, W, 1>, a, st); \
+    return at_variant<S>(a, 1, [&](auto v, auto g, auto) {                                                                   \
+      return at_run(attn_weights_kernel<S, A, decltype(v)::value, decltype(g)::value>, a, st);                               \
+    });                                                                                                                      \
   }                                                                                                                          \
   cudaError_t at_scale_rows_##suffix(const AtArgs& a, cudaStream_t st) {                                                     \
     return at_launch(attn_scale_rows_kernel<S, A>, dim3(a.grid), dim3(256), 0, st, a);                                       \
@@ -1201,22 +1275,15 @@ auto at_variant(const AtArgs& a, F&& f) {
     return at_launch(attn_edge_rows_backward_kernel<S, A>, dim3(a.grid), dim3(256), 0, st, a);                               \
   }                                                                                                                          \
   cudaError_t at_receive_##suffix(const AtArgs& a, bool edges, cudaStream_t st) {                                            \
-    constexpr int W = kWide<S>;                                                                                              \
-    if (edges)                                                                                                               \
-      return at_run(a.four             ? attn_receive_kernel<S, R, A, W, 1, 4, 1, true>                                      \
-                    : a.qk.vec == 1 ? attn_receive_kernel<S, R, A, 1, 1, 1, 1, true>                                         \
-                                       : attn_receive_kernel<S, R, A, W, 1, 1, 1, true>,                                     \
-                    a, st);                                                                                                  \
-    return at_variant<S>(a, [&](auto qv, auto vv, auto g, auto cb) {                                                         \
-      return at_run(attn_receive_kernel<S, R, A, decltype(qv)::value, decltype(vv)::value, decltype(g)::value, decltype(cb)::value, false>, a, st); \
+    return at_variant<S>(a, edges ? 1 : a.vv.dot_turn, [&](auto v, auto g, auto cb) {                                        \
+      constexpr int V = decltype(v)::value, G = decltype(g)::value, CB = decltype(cb)::value;                                \
+      return at_run(edges ? attn_receive_kernel<S, R, A, V, G, 1, true> : attn_receive_kernel<S, R, A, V, G, CB, false>, a, st); \
     });                                                                                                                      \
   }                                                                                                                          \
   cudaError_t at_send_##suffix(const AtArgs& a, bool values, cudaStream_t st) {                                              \
-    constexpr int W = kWide<S>;                                                                                              \
-    if (!values) return at_run(a.qk.vec > 1 ? attn_send_kernel<S, R, A, W, 1, 1, false> : attn_send_kernel<S, R, A, 1, 1, 1, false>, a, st); \
-    return at_variant<S>(a, [&](auto qv, auto vv, auto g, auto cb) {                                                         \
-      constexpr int CB = decltype(g)::value == 4 ? 2 : decltype(cb)::value;                                                  \
-      return at_run(attn_send_kernel<S, R, A, decltype(qv)::value, decltype(vv)::value, CB, true>, a, st);                   \
+    return at_variant<S>(a, values ? a.vv.turn : 1, [&](auto v, auto, auto cb) {                                             \
+      constexpr int V = decltype(v)::value, CB = decltype(cb)::value;                                                        \
+      return at_run(values ? attn_send_kernel<S, R, A, V, CB, true> : attn_send_kernel<S, R, A, V, 1, false>, a, st);        \
     });                                                                                                                      \
   }                                                                                                                          \
   cudaError_t at_join_sum_##suffix(const AtArgs& a, const AtRows& out, int width, int at, int stride, cudaStream_t st) {     \
