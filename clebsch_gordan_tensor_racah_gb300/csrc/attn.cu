@@ -105,7 +105,7 @@ cgtp_status create(cgtp_attn_s* p, const char* irreps_qk, const char* irreps_v, 
     cudaGetLastError();
     return fail(CGTP_ECUDA, "no CUDA device");
   }
-  const size_t ints = align16(table.size() * sizeof(int)), total = ints + align16(int64_t(std::max(n_borders, 1)) * es_acc(p));
+  const size_t ints = align16(table.size() * sizeof(int)), edges = align16(int64_t(n_borders) * es_acc(p)), total = ints + edges + 16;
   std::vector<char> host(total, 0);
   std::memcpy(host.data(), table.data(), table.size() * sizeof(int));
   for (int i = 0; i < n_borders; ++i) {
@@ -126,6 +126,7 @@ cgtp_status create(cgtp_attn_s* p, const char* irreps_qk, const char* irreps_v, 
     for (int i = 0; i < (t == p->qk ? p->n_qk : p->n_vv); ++i)
       place(&t[i].dot_full), place(&t[i].dot_kv), place(&t[i].acc), place(&t[i].rows);
   p->borders = static_cast<char*>(p->base) + ints;
+  p->zeros = static_cast<char*>(p->base) + ints + edges;
   return CGTP_OK;
 }
 
@@ -195,6 +196,7 @@ AtArgs base_args(const cgtp_attn_s* p, const cgtp_graph_s* g) {
   a.scale = p->scale;
   a.n_borders = p->n_borders;
   a.borders = p->borders;
+  a.zeros = p->zeros;
   a.n_edges = g->E;
   return a;
 }

@@ -52,6 +52,7 @@ struct AtArgs {
   AtTab qk, vv;
   int n_borders = 0;
   const void* borders = nullptr;
+  const void* zeros = nullptr;     // 16 bytes
   // graph: rows are receivers, or sources for the sender kernel
   const int32_t* rowptr = nullptr;
   const int32_t* col = nullptr;    // the other end of each edge
@@ -112,7 +113,7 @@ struct cgtp_attn_s {
   int heads = 0, kv = 0, dk = 0, dv = 0;
   double scale = 1.0;
   int n_borders = 0;
-  const void* borders = nullptr;
+  const void *borders = nullptr, *zeros = nullptr;
   cgtp::AtTab qk[3], vv[3];      // by width of a vector, widest first; the last is one element
   int n_qk = 0, n_vv = 0;
   void* base = nullptr;

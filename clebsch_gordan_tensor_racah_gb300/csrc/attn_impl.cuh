@@ -112,38 +112,10 @@ constexpr bool kPairs = std::is_same<A, float>::value && V % 2 == 0;
 template <typename A, int V, bool = kPairs<A, V>>
 struct Nums {
   A e[V];
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int k = 0; k < V; ++k) e[k] = 0;
-  }
-  __device__ __forceinline__ void get(A* r) const {
-#pragma unroll
-    for (int k = 0; k < V; ++k) r[k] = e[k];
-  }
-  // += f y; a weight of zero takes nothing, whatever y holds
-  __device__ __forceinline__ void add_weighed(A f, const Nums& y) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) e[k] = f != 0 ? e[k] + f * y.e[k] : e[k];
-  }
 };
 template <int V>
 struct Nums<float, V, true> {
   uint64_t p[V / 2];
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int k = 0; k < V / 2; ++k) p[k] = 0;
-  }
-  __device__ __forceinline__ void get(float* r) const {
-#pragma unroll
-    for (int k = 0; k < V / 2; ++k) asm("mov.b64 {%0, %1}, %2;" : "=f"(r[2 * k]), "=f"(r[2 * k + 1]) : "l"(p[k]));
-  }
-  __device__ __forceinline__ void add_weighed(float f, const Nums& y) {
-#pragma unroll
-    for (int k = 0; k < V / 2; ++k)
-      asm("{\n\t.reg .pred q;\n\t.reg .b64 w;\n\tsetp.neu.f32 q, %1, 0f00000000;\n\tmov.b64 w, {%1, %1};\n\t@q fma.rn.f32x2 %0, w, %2, %0;\n\t}"
-          : "+l"(p[k])
-          : "f"(f), "l"(y.p[k]));
-  }
 };
 template <typename A, typename S, int V>
 __device__ __forceinline__ Nums<A, V> widened(const Pack<S, V>& y) {
@@ -162,19 +134,18 @@ __device__ __forceinline__ Nums<A, V> widened(const Pack<S, V>& y) {
 template <typename A, int V, bool = kPairs<A, V>>
 struct Dot {
   A s = 0;
-  __device__ __forceinline__ void add(const Nums<A, V>& x, const Nums<A, V>& y, bool on) {
+  __device__ __forceinline__ void add(const Nums<A, V>& x, const Nums<A, V>& y) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) s = on ? s + x.e[k] * y.e[k] : s;
+    for (int k = 0; k < V; ++k) s += x.e[k] * y.e[k];
   }
   __device__ __forceinline__ A total() const { return s; }
 };
 template <int V>
 struct Dot<float, V, true> {
   uint64_t s = 0;
-  __device__ __forceinline__ void add(const Nums<float, V>& x, const Nums<float, V>& y, bool on) {
+  __device__ __forceinline__ void add(const Nums<float, V>& x, const Nums<float, V>& y) {
 #pragma unroll
-    for (int k = 0; k < V / 2; ++k)
-      asm("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q fma.rn.f32x2 %0, %1, %2, %0;\n\t}" : "+l"(s) : "l"(x.p[k]), "l"(y.p[k]), "r"(unsigned(on)));
+    for (int k = 0; k < V / 2; ++k) asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(s) : "l"(x.p[k]), "l"(y.p[k]));
   }
   __device__ __forceinline__ float total() const {
     float a, b;
@@ -182,6 +153,29 @@ struct Dot<float, V, true> {
     return a + b;
   }
 };
+
+// acc += f y; a weight of zero takes nothing, whatever y holds.  (One number at a time: an addition of pairs under a
+// condition takes two more instructions to select its result.)
+template <int V>
+__device__ __forceinline__ void add_weighed(float* acc, float f, const float* y) {
+  if constexpr (V == 8) {
+    add_weighed<4>(acc, f, y);
+    add_weighed<4>(acc + 4, f, y + 4);
+  } else if constexpr (V == 4) {
+    asm("{\n\t.reg .pred q;\n\tsetp.neu.f32 q, %4, 0f00000000;\n\t@q fma.rn.f32 %0, %4, %5, %0;\n\t@q fma.rn.f32 %1, %4, %6, %1;\n\t"
+        "@q fma.rn.f32 %2, %4, %7, %2;\n\t@q fma.rn.f32 %3, %4, %8, %3;\n\t}"
+        : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
+        : "f"(f), "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = f != 0 ? fmaf(f, y[k], acc[k]) : acc[k];
+  }
+}
+template <int V>
+__device__ __forceinline__ void add_weighed(double* acc, double f, const double* y) {
+#pragma unroll
+  for (int k = 0; k < V; ++k) acc[k] = f != 0 ? fma(f, y[k], acc[k]) : acc[k];
+}
 
 // Widths of vectors of a storage type: 16 bytes, 8 of bfloat16 where a head's runs allow no more, or one element.
 template <typename S>
@@ -280,11 +274,14 @@ struct Smem {
 template <int V, int G>
 constexpr int kShort = G == 4 && V == 8 ? 1 : 2;
 
-// Edges in flight of `elements` elements a lane: as many, up to `most`, as take 32 registers.
-template <typename S, int elements, int most>
-constexpr int kFlight = most > 1 && most * elements * int(sizeof(S)) > 128 ? kFlight<S, elements, most / 2> : most;
-template <typename S, int elements>
-constexpr int kFlight<S, elements, 1> = 1;
+// Edges in flight of `elements` elements a lane: as many, up to `most`, as leave them and G sets of results or queries
+// about 48 of the 80 registers (72 of 128 where G = 4).
+template <typename S, typename A, int elements, int G, int most>
+constexpr int kFlight = most > 1 && most * elements * int(sizeof(S)) / 4 + G * elements * int(sizeof(A)) / 4 > (G == 1 ? 48 : 72)
+                            ? kFlight<S, A, elements, G, most / 2>
+                            : most;
+template <typename S, typename A, int elements, int G>
+constexpr int kFlight<S, A, elements, G, 1> = 1;
 
 // Sums of v[u] (u < U <= 4) over the 2^width lanes side by side.  The lanes share the sums out as they halve them: in the
 // end lane x of them holds those of v[u] with `mine(u)`, U / min(U, 2^width) of them, in v[0..].
@@ -325,7 +322,7 @@ __device__ __forceinline__ int lane_sums(A (&v)[U], int width, int x) {
 // added to the product times the scale; -infinity stays.
 template <int V, int CB, int G, bool LOGITS, typename S, typename A>
 __device__ __forceinline__ void dots(const AtArgs& a, const AtTab& tab, int cnt, const S* x, const AtRows& rows, const int* idx, A* z) {
-  constexpr int U = kFlight<S, V * CB, 4>;
+  constexpr int U = kFlight<S, A, V * CB, G, 4>;
   const AtLanes& l = tab.lanes;
   const Place at(l);
   const int units = a.heads / G, pieces = tab.pieces, slots = 32 >> (l.width + l.units);
@@ -338,18 +335,20 @@ __device__ __forceinline__ void dots(const AtArgs& a, const AtTab& tab, int cnt,
 #pragma unroll 1
     for (int c0 = 0; c0 < pieces; c0 += CB << l.width) {
       Nums<A, V> xr[G][CB];
+      // lanes without a vector multiply zeros by zeros
       const char* base[CB];
-      bool ok[CB];
+      uint32_t ld[CB];
 #pragma unroll
       for (int j = 0; j < CB; ++j) {
         const int c = c0 + (j << l.width) + at.x;
-        ok[j] = c < pieces;
-        base[j] = rows.p + (ok[j] ? shared[c] : 0) * sizeof(S);
+        const bool ok = c < pieces;
+        base[j] = ok ? rows.p + shared[c] * sizeof(S) : static_cast<const char*>(a.zeros);
+        ld[j] = ok ? rows.ld_bytes : 0;
 #pragma unroll
         for (int q = 0; q < G; ++q) {
           Pack<S, V> v;
           v.clear();
-          if (ok[j]) v.load(x + full[q * pieces + c]);
+          if (ok) v.load(x + full[q * pieces + c]);
           xr[q][j] = widened<A>(v);
         }
       }
@@ -357,13 +356,13 @@ __device__ __forceinline__ void dots(const AtArgs& a, const AtTab& tab, int cnt,
       A* to_ = z + h0 * a.stride + at.s;
 #pragma unroll 1
       for (int b = 0; b < cnt; b += U * slots, ip += U * slots, to_ += U * slots) {
-        // (the list of edges is filled up with the last one's end; lanes without a vector read the row's first)
+        // (the list of edges is filled up with the last one's end)
         Pack<S, V> y[U][CB];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const uint64_t off = uint64_t(static_cast<unsigned>(ip[u * slots])) * rows.ld_bytes;
+          const unsigned end = ip[u * slots];
 #pragma unroll
-          for (int j = 0; j < CB; ++j) y[u][j].load(reinterpret_cast<const S*>(base[j] + off));
+          for (int j = 0; j < CB; ++j) y[u][j].load(reinterpret_cast<const S*>(base[j] + uint64_t(end) * ld[j]));
         }
         A sum[G][U];
 #pragma unroll
@@ -373,7 +372,7 @@ __device__ __forceinline__ void dots(const AtArgs& a, const AtTab& tab, int cnt,
           for (int j = 0; j < CB; ++j) {
             const Nums<A, V> w = widened<A>(y[u][j]);
 #pragma unroll
-            for (int q = 0; q < G; ++q) s[q].add(xr[q][j], w, ok[j]);
+            for (int q = 0; q < G; ++q) s[q].add(xr[q][j], w);
           }
 #pragma unroll
           for (int q = 0; q < G; ++q) sum[q][u] = s[q].total();
@@ -426,11 +425,13 @@ __device__ __forceinline__ void sums(const AtArgs& a, const AtTab& tab, int cnt,
   for (int c0 = 0; c0 < total; c0 += CB << tab.abreast) {
 #pragma unroll 1
     for (int g0 = 0; g0 < (SEND ? 1 : a.group); g0 += G) {
-      Nums<A, V> acc[G][CB];
+      A acc[G][CB][V];
 #pragma unroll
       for (int q = 0; q < G; ++q)
 #pragma unroll
-        for (int j = 0; j < CB; ++j) acc[q][j].clear();
+        for (int j = 0; j < CB; ++j)
+#pragma unroll
+          for (int k = 0; k < V; ++k) acc[q][j][k] = 0;
 #pragma unroll 1
       for (int g = 0; g < (SEND ? a.group : 1); ++g) {
         const char* base[CB];
@@ -447,25 +448,30 @@ __device__ __forceinline__ void sums(const AtArgs& a, const AtTab& tab, int cnt,
         for (int b = 0; b < end; b += step) {
           Pack<int, 4> ends;
           ends.load(ip + b);
-          constexpr int U = kFlight<S, V * CB, kAtQuad>;
+          constexpr int U = kFlight<S, A, V * CB, G, kAtQuad>;
 #pragma unroll
           for (int part = 0; part < kAtQuad; part += U) {
             Pack<S, V> y[U][CB];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-              const uint64_t off = uint64_t(static_cast<unsigned>(ends.e[part + u])) * rows.ld_bytes;
+              const unsigned end_ = ends.e[part + u];
 #pragma unroll
-              for (int j = 0; j < CB; ++j) y[u][j].load(reinterpret_cast<const S*>(base[j] + off));
+              for (int j = 0; j < CB; ++j) y[u][j].load(reinterpret_cast<const S*>(base[j] + uint64_t(end_) * rows.ld_bytes));
             }
 #pragma unroll
-            for (int j = 0; j < CB; ++j)
+            for (int j = 0; j < CB; ++j) {
+              Pack<A, U> f[G];
 #pragma unroll
-              for (int q = 0; q < G; ++q) {
-                Pack<A, U> f;
-                f.load(fp[j] + q * a.stride + b + part);
+              for (int q = 0; q < G; ++q) f[q].load(fp[j] + q * a.stride + b + part);
 #pragma unroll
-                for (int u = 0; u < U; ++u) acc[q][j].add_weighed(f.e[u], widened<A>(y[u][j]));
+              for (int u = 0; u < U; ++u) {
+                A w[V];
+#pragma unroll
+                for (int k = 0; k < V; ++k) w[k] = wide(y[u][j].e[k]);
+#pragma unroll
+                for (int q = 0; q < G; ++q) add_weighed<V>(acc[q][j], f[q].e[u], w);
               }
+            }
           }
         }
       }
@@ -473,8 +479,7 @@ __device__ __forceinline__ void sums(const AtArgs& a, const AtTab& tab, int cnt,
       for (int q = 0; q < G; ++q)
 #pragma unroll
         for (int j = 0; j < CB; ++j) {
-          A r[V];
-          acc[q][j].get(r);
+          A* r = acc[q][j];
 #pragma unroll 1
           for (int o = 1 << tab.abreast; o < 32; o <<= 1)
 #pragma unroll
