@@ -283,7 +283,8 @@ cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* 
       at += align16(bytes);
       return static_cast<int>(place);
     };
-    const int64_t run = (longest + warps - 1) / warps;
+    int64_t run = (longest + warps - 1) / warps;
+    if (send && warps == 1) run = std::max<int64_t>(run, 64);   // (several rows)
     a->sub = static_cast<int>(std::max<int64_t>(8, std::min<int64_t>((run + 7) / 8 * 8, 4096 / (int64_t(a->heads) * es * pairs) / 8 * 8)));
     // weights of a head: a multiple of 32 and the edges abreast where a lane takes a head's edges, so that heads lie
     // in different banks; whole quads
@@ -293,7 +294,7 @@ cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* 
     a->at_p = region(pairs == 2 ? int64_t(a->stride) * a->heads * es : 0);
     a->at_idx = region((held + a->sub) * int64_t(sizeof(int)));
     a->at_stat = region(int64_t(3) * a->heads * es);
-    a->at_acc = region(warps > 1 || run > a->sub ? width * es : 0);
+    a->at_acc = region(warps > 1 || longest > a->sub ? width * es : 0);
     a->warp_smem = static_cast<int>(at);
   };
   lay_out();
@@ -305,7 +306,13 @@ cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* 
   if (a->one) {
     warps = 4;
     while (warps > 1 && warps * at > p->smem_cap) warps /= 2;
-    a->grid = static_cast<unsigned>((items + warps - 1) / warps);
+    // Short rows of sources side by side: as many as a warp's lists hold, up to eight, as long as four warps for each
+    // place of an SM remain.
+    if (send) {
+      const int64_t mean = g->E / std::max<int64_t>(a->n_rows, 1) + kAtQuad;
+      a->batch = static_cast<int>(std::max<int64_t>(1, std::min({int64_t(8), a->sub / mean, a->n_rows / (int64_t(p->num_sms) * 96)})));
+    }
+    a->grid = static_cast<unsigned>((a->n_items + (a->n_rows + a->batch - 1) / a->batch + warps - 1) / warps);
   } else {
     a->grid = static_cast<unsigned>(items);
   }
@@ -332,7 +339,8 @@ struct Space {
   int64_t pairs = 0, ds = 0, part = 0, part_sum = 0, hist = 0, total = 0;
 };
 
-constexpr int kHistCtas = 608;
+// CTAs of the bias table's gradient
+int hist_ctas(const cgtp_attn_s* p) { return 2 * p->num_sms; }
 
 Space space(const cgtp_attn_s* p, const cgtp_graph_s* g, int call) {
   Space s;
@@ -352,7 +360,7 @@ Space space(const cgtp_attn_s* p, const cgtp_graph_s* g, int call) {
     region(&s.ds, values ? 0 : g->E * heads * es);
     region(&s.part, std::max(in * part_ld(heads * p->dk), out * send_ld(p, values)) * es);
     region(&s.part_sum, in * heads * es);
-    region(&s.hist, p->n_borders ? int64_t(kHistCtas) * (p->n_borders + 1) * heads * sizeof(double) : 0);
+    region(&s.hist, p->n_borders ? int64_t(hist_ctas(p)) * (p->n_borders + 1) * heads * es : 0);
   }
   return s;
 }
@@ -417,12 +425,13 @@ cgtp_status finish_backward(const cgtp_attn_s* p, const cgtp_graph_s* g, AtArgs 
   if (g->E == 0) {
     return done(cudaMemsetAsync(a.gtable, 0, cells * es_acc(p), st));
   }
-  // four warps a CTA where their histograms fit; a CTA for each 4096 values, one where that saves the second launch
+  // Two CTAs an SM, of up to sixteen warps where their histograms fit twice; a CTA for each 2048 values, one where that
+  // saves the second launch.
   a.hist_cols = p->heads <= 32 ? 32 : 64;
   const int64_t one = int64_t(p->n_borders + 1) * a.hist_cols * es_acc(p), room = p->smem_cap - p->n_borders * es_acc(p);
-  a.hist_warps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, room / one)));
-  if (a.hist_warps * one > room) return fail(CGTP_EUNSUPPORTED, "bias table too large for shared memory");
-  a.hist_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(kHistCtas, 4 * p->num_sms), g->E * p->heads / 2048)));
+  if (one > room) return fail(CGTP_EUNSUPPORTED, "bias table too large for shared memory");
+  a.hist_warps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, (p->smem_cap / 2 - 1024 - p->n_borders * es_acc(p)) / one)));
+  a.hist_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(hist_ctas(p), g->E * p->heads / 2048)));
   a.hist_from = values ? a.pairs : a.ds;
   a.hist_step = values ? 2 : 1;
   return done(CGTP_AT_PICK(p, table)(a, st));

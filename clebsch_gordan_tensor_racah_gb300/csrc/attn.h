@@ -69,13 +69,14 @@ struct AtArgs {
   void* part = nullptr;            // partial results of split rows, part_ld values apart
   int part_ld = 0;
   void* part_sum = nullptr;        // backward: partial sums of a dp of split rows [items][heads]
-  void* hist = nullptr;            // partial sums of the bias table [ctas][buckets * heads]
+  void* hist = nullptr;            // partial sums of the bias table [ctas][buckets * heads], in the arithmetic's type
   const void* hist_from = nullptr; // ds of the edges, hist_step values apart
   int hist_step = 1;
   // launch
   int phase = 0;
   int sub = 0;                     // edges that a warp holds at once
   int stride = 0;                  // weights of a head
+  int batch = 1;                   // sources' kernel: rows that a warp takes side by side
   int pad = 0;                     // places behind a list of edges that the loops may read
   int four = 0;                    // four heads that share keys and values are taken together
   int head_lanes = 0;              // logarithm of the heads abreast where a lane takes a head's edges

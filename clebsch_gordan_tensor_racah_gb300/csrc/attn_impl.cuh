@@ -66,8 +66,15 @@ struct Pack {
   union {
     W raw[kRaws];
     T e[V];
+    uint32_t words[(V * sizeof(T) + 3) / 4];
   };
   __device__ __forceinline__ Pack() {}
+  // Element k in the arithmetic's type.  bfloat16 numbers are taken out of their word in one instruction each: taken
+  // as 16 bits first, every other one costs two.
+  __device__ __forceinline__ auto number(int k) const {
+    if constexpr (std::is_same<T, bf16>::value && V % 2 == 0) return __uint_as_float(k & 1 ? words[k / 2] & 0xffff0000u : words[k / 2] << 16);
+    else return wide(e[k]);
+  }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < kRaws; ++i) raw[i] = W{};
@@ -122,10 +129,10 @@ __device__ __forceinline__ Nums<A, V> widened(const Pack<S, V>& y) {
   Nums<A, V> r;
   if constexpr (kPairs<A, V>) {
 #pragma unroll
-    for (int k = 0; k < V / 2; ++k) asm("mov.b64 %0, {%1, %2};" : "=l"(r.p[k]) : "f"(wide(y.e[2 * k])), "f"(wide(y.e[2 * k + 1])));
+    for (int k = 0; k < V / 2; ++k) asm("mov.b64 %0, {%1, %2};" : "=l"(r.p[k]) : "f"(y.number(2 * k)), "f"(y.number(2 * k + 1)));
   } else {
 #pragma unroll
-    for (int k = 0; k < V; ++k) r.e[k] = wide(y.e[k]);
+    for (int k = 0; k < V; ++k) r.e[k] = y.number(k);
   }
   return r;
 }
@@ -214,9 +221,8 @@ struct Item {
   bool some = false;
 };
 
-// This team's piece of work.  First come the items of split rows, the longest work.
-__device__ __forceinline__ Item item_of(const AtArgs& a, const Team& t) {
-  const int64_t i = t.one ? int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+// Piece i of the work.  First come the items of split rows, the longest work.
+__device__ __forceinline__ Item item_at(const AtArgs& a, const Team& t, int64_t i) {
   Item it;
   if (i < a.n_items) {
     const Int4 v = a.items[i];
@@ -235,6 +241,10 @@ __device__ __forceinline__ Item item_of(const AtArgs& a, const Team& t) {
     it.e1 = b + static_cast<int>(int64_t(len) * (t.w + 1) / t.warps);
   }
   return it;
+}
+
+__device__ __forceinline__ Item item_of(const AtArgs& a, const Team& t) {
+  return item_at(a, t, t.one ? int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x);
 }
 
 // pair / heads for pairs below 2^24 (heads <= 64: the error of the multiplier is below 2^-32 a unit)
@@ -283,38 +293,23 @@ constexpr int kFlight = most > 1 && most * elements * int(sizeof(S)) / 4 + G * e
 template <typename S, typename A, int elements, int G>
 constexpr int kFlight<S, A, elements, G, 1> = 1;
 
-// Sums of v[u] (u < U <= 4) over the 2^width lanes side by side.  The lanes share the sums out as they halve them: in the
-// end lane x of them holds those of v[u] with `mine(u)`, U / min(U, 2^width) of them, in v[0..].
-template <int U, typename A>
-__device__ __forceinline__ int lane_sums(A (&v)[U], int width, int x) {
-  int held = U, first = 0, o = 1;
-  if constexpr (U >= 2) {
-    if (width >= 1) {
-      const bool up = x & 1;
+// Sums of v[u] (u < 4) over the 2^width lanes side by side, which share them out as they halve them: in the end lane x holds
+// those of v[first], v[first + 1], ... in v[0..] (4, 2 or 1 of them for width 0, 1 and more).  Returns `first`.
+template <typename A>
+__device__ __forceinline__ int lane_sums(A (&v)[4], int width, int x) {
+  if (width == 0) return 0;
+  const bool up = x & 1, upper = x & 2;
 #pragma unroll
-      for (int u = 0; u < U / 2; ++u) {
-        const A keep = up ? v[U / 2 + u] : v[u], give = up ? v[u] : v[U / 2 + u];
-        v[u] = keep + __shfl_xor_sync(kAll, give, 1);
-      }
-      held = U / 2, first = up ? U / 2 : 0, o = 2;
-    }
+  for (int u = 0; u < 2; ++u) {
+    const A keep = up ? v[2 + u] : v[u], give = up ? v[u] : v[2 + u];
+    v[u] = keep + __shfl_xor_sync(kAll, give, 1);
   }
-  if constexpr (U >= 4) {
-    if (width >= 2) {
-      const bool up = x & 2;
-#pragma unroll
-      for (int u = 0; u < U / 4; ++u) {
-        const A keep = up ? v[U / 4 + u] : v[u], give = up ? v[u] : v[U / 4 + u];
-        v[u] = keep + __shfl_xor_sync(kAll, give, 2);
-      }
-      held = U / 4, first += up ? U / 4 : 0, o = 4;
-    }
-  }
+  if (width == 1) return up ? 2 : 0;
+  const A keep = upper ? v[1] : v[0], give = upper ? v[0] : v[1];
+  v[0] = keep + __shfl_xor_sync(kAll, give, 2);
 #pragma unroll 1
-  for (; o < 1 << width; o *= 2)
-#pragma unroll
-    for (int u = 0; u < (U >= 4 ? U / 4 : 1); ++u) v[u] += __shfl_xor_sync(kAll, v[u], o);
-  return first | held << 8;
+  for (int o = 4; o < 1 << width; o *= 2) v[0] += __shfl_xor_sync(kAll, v[0], o);
+  return (up ? 2 : 0) + (upper ? 1 : 0);
 }
 
 // z[h][i] = <x[h], rows[idx(i)][shared head]> (weights lie head by head, a.stride apart: see sums).  G heads that share a
@@ -354,36 +349,40 @@ __device__ __forceinline__ void dots(const AtArgs& a, const AtTab& tab, int cnt,
       }
       const int* ip = idx + at.s;
       A* to_ = z + h0 * a.stride + at.s;
+      // (four edges a slot: their sums over the lanes cost fewer exchanges together.  The list of edges is filled up with
+      // the last one's end.)
 #pragma unroll 1
-      for (int b = 0; b < cnt; b += U * slots, ip += U * slots, to_ += U * slots) {
-        // (the list of edges is filled up with the last one's end)
-        Pack<S, V> y[U][CB];
+      for (int b = 0; b < cnt; b += kAtQuad * slots, ip += kAtQuad * slots, to_ += kAtQuad * slots) {
+        A sum[G][kAtQuad];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const unsigned end = ip[u * slots];
+        for (int part = 0; part < kAtQuad; part += U) {
+          Pack<S, V> y[U][CB];
 #pragma unroll
-          for (int j = 0; j < CB; ++j) y[u][j].load(reinterpret_cast<const S*>(base[j] + uint64_t(end) * ld[j]));
-        }
-        A sum[G][U];
+          for (int u = 0; u < U; ++u) {
+            const unsigned end = ip[(part + u) * slots];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          Dot<A, V> s[G];
-#pragma unroll
-          for (int j = 0; j < CB; ++j) {
-            const Nums<A, V> w = widened<A>(y[u][j]);
-#pragma unroll
-            for (int q = 0; q < G; ++q) s[q].add(xr[q][j], w);
+            for (int j = 0; j < CB; ++j) y[u][j].load(reinterpret_cast<const S*>(base[j] + uint64_t(end) * ld[j]));
           }
 #pragma unroll
-          for (int q = 0; q < G; ++q) sum[q][u] = s[q].total();
+          for (int u = 0; u < U; ++u) {
+            Dot<A, V> s[G];
+#pragma unroll
+            for (int j = 0; j < CB; ++j) {
+              const Nums<A, V> w = widened<A>(y[u][j]);
+#pragma unroll
+              for (int q = 0; q < G; ++q) s[q].add(xr[q][j], w);
+            }
+#pragma unroll
+            for (int q = 0; q < G; ++q) sum[q][part + u] = s[q].total();
+          }
         }
 #pragma unroll
         for (int q = 0; q < G; ++q) {
-          const int r = lane_sums<U>(sum[q], l.width, at.x), first = r & 255, held = r >> 8;
+          const int first = lane_sums(sum[q], l.width, at.x), held = l.width == 0 ? 4 : l.width == 1 ? 2 : 1;
           // (of the lanes that hold the same sums the first writes them)
-          if (mine && at.x < (held == U ? 1 : 2 * held == U ? 2 : 4))
+          if (mine && at.x < 4)
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < kAtQuad; ++u) {
               const int i = (first + u) * slots;
               if (u >= held || b + i + at.s >= cnt) continue;
               A* to = to_ + q * a.stride + i;
@@ -467,7 +466,7 @@ __device__ __forceinline__ void sums(const AtArgs& a, const AtTab& tab, int cnt,
               for (int u = 0; u < U; ++u) {
                 A w[V];
 #pragma unroll
-                for (int k = 0; k < V; ++k) w[k] = wide(y[u][j].e[k]);
+                for (int k = 0; k < V; ++k) w[k] = y[u][j].number(k);
 #pragma unroll
                 for (int q = 0; q < G; ++q) add_weighed<V>(acc[q][j], f[q].e[u], w);
               }
@@ -584,12 +583,17 @@ __device__ __forceinline__ void each_pair(const AtArgs& a, int cnt, F&& f) {
 // Logits of the edges [e, e + cnt) of `row` into z.
 template <int V, int G, typename S, typename A>
 __device__ __forceinline__ void logits(const AtArgs& a, const Smem<A>& sm, int row, int e, int cnt) {
-  load_ends(a, sm, e, cnt);
-  if (a.table) {
-    for (int i = threadIdx.x & 31; i < cnt; i += 32)
-      sm.bucket[i] = bucket_of(static_cast<const A*>(a.borders), a.n_borders, static_cast<const A*>(a.lengths)[e + i]);
-    __syncwarp();
-  }
+  // (the biases of the run are on their way while the ends and lengths arrive)
+  const int far = (threadIdx.x & 31) * (128 / int(sizeof(A)));
+  if (a.bias && far < cnt * a.heads)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const A*>(a.bias) + int64_t(e) * a.heads + far));
+  if (cnt > 0)
+    for (int i = threadIdx.x & 31; i < cnt + a.pad; i += 32) {
+      const int at = e + min(i, cnt - 1), end = a.col[at];
+      if (a.table && i < cnt) sm.bucket[i] = bucket_of(static_cast<const A*>(a.borders), a.n_borders, static_cast<const A*>(a.lengths)[at]);
+      sm.idx[i] = end;
+    }
+  __syncwarp();
   const A *table = static_cast<const A*>(a.table), *bias = static_cast<const A*>(a.bias) + int64_t(e) * a.heads;
   each_pair(a, cnt, [&](int at, int i, int h, int k) {
     A b = a.bias ? bias[k] : A(0);
@@ -804,10 +808,12 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_weights_kernel(const _
       const A* part = static_cast<const A*>(a.part) + int64_t(join.y) * 2 * a.heads;
       each_head(a, [&](const HeadLanes& l) {
         A top = lowest<A>();
+#pragma unroll 8
         for (int i = l.slot; i < join.z; i += l.slots) top = larger(top, part[int64_t(i) * 2 * a.heads + l.h]);
         top = all_max(l, top);
         const A shift = top == lowest<A>() ? A(0) : top;
         A sum = 0;
+#pragma unroll 4
         for (int i = l.slot; i < join.z; i += l.slots) {
           const A* p = part + int64_t(i) * 2 * a.heads + l.h;
           sum += expo(p[0] - shift) * p[a.heads];
@@ -867,7 +873,7 @@ __global__ void __launch_bounds__(256) attn_scale_rows_kernel(const __grid_const
       for (int u = 0; u < U; ++u) {
         if (e[u] >= a.n_edges) continue;
 #pragma unroll
-        for (int k = 0; k < V; ++k) y[u].e[k] = to<S>(f[u] == 0 ? A(0) : f[u] * wide(y[u].e[k]));
+        for (int k = 0; k < V; ++k) y[u].e[k] = to<S>(f[u] == 0 ? A(0) : f[u] * y[u].number(k));
         y[u].store(out + e[u] * a.out.ld + p[u] * V);
       }
     }
@@ -919,7 +925,7 @@ __global__ void __launch_bounds__(256) attn_edge_rows_backward_kernel(const __gr
 #pragma unroll
             for (int k = 0; k < V; ++k) {
               const A d = y[u].e[k];
-              sum += d * wide(x[u].e[k]);
+              sum += d * x[u].number(k);
               y[u].e[k] = f == 0 ? A(0) : f * d;
             }
             y[u].store(gw + at[u]);
@@ -1018,6 +1024,7 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const _
       const Int4 join = a.joins[a.items[it.index].w];
       each_head(a, [&](const HeadLanes& l) {
         A sum = 0;
+#pragma unroll 8
         for (int i = l.slot; i < join.z; i += l.slots) sum += static_cast<const A*>(a.part_sum)[int64_t(join.y + i) * a.heads + l.h];
         sum = all_sum(l, sum);
         if (l.on) sm.stat[l.h] = sum;
@@ -1068,7 +1075,9 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const _
   }
 }
 
-// The sources' kernel, over the transpose: gk, and gv where VALUES.
+// The sources' kernel, over the transpose: gk, and gv where VALUES.  A warp takes a.batch rows side by side, whose lists
+// and weights it reads together where they fit (200,000 sources of 8 edges: the latencies of a row's lists and weights are
+// a third of its time).
 template <typename S, typename R, typename A, int V, int CB, bool VALUES>
 __global__ void __launch_bounds__(256, kResident<1>) attn_send_kernel(const __grid_constant__ AtArgs a) {
   chain_enter();
@@ -1076,74 +1085,135 @@ __global__ void __launch_bounds__(256, kResident<1>) attn_send_kernel(const __gr
   const Smem<A> sm(a, threadIdx.x / 32);
   const A scale = static_cast<A>(a.scale);
   const int wk = (a.kv * a.dk + 3) & ~3, stride = wk + (VALUES ? a.kv * a.dv : 0);   // (aligned for vectors)
-  const Item it = item_of(a, t);
-  if (!it.some) return;
-  {
-    const bool part = it.index >= 0;
-    A* to_part = static_cast<A*>(a.part) + int64_t(it.index) * a.part_ld;
-    const auto finish = [&](int at, A x) {   // element `at` of (gk, gv)
-      if (part) to_part[at] = x;
-      else if (at < a.kv * a.dk) (reinterpret_cast<R*>(a.gk.p) + int64_t(it.row) * a.gk.ld)[at] = to<R>(x);
-      else if (at >= wk) (reinterpret_cast<R*>(a.gv.p) + int64_t(it.row) * a.gv.ld)[at - wk] = to<R>(x);
+  const A* none = nullptr;
+  // weights of the places [0, places) of the lists; a bucket below zero is no edge
+  const auto fetch = [&](int places) {
+    each_pair(a, places, [&](int to_, int i, int h, int) {
+      const int e = sm.bucket[i];
+      const int64_t at = int64_t(e) * a.heads + h;
+      if (VALUES) {
+        Pair<A> x = {0, 0};
+        if (e >= 0) x = static_cast<const Pair<A>*>(a.pairs)[at];
+        sm.z[to_] = x.ds * scale;
+        sm.p[to_] = x.p;
+      } else {
+        sm.z[to_] = e >= 0 ? static_cast<const A*>(a.ds)[at] * scale : A(0);
+      }
+    });
+    __syncwarp();
+  };
+  // sums over cnt places from `from`, for the row (or the item, where it is a piece of a row)
+  const auto add = [&](int row, int item, int from, int cnt, bool first, bool last) {
+    const bool part = item >= 0;
+    A* to_part = static_cast<A*>(a.part) + int64_t(item) * a.part_ld;
+    const auto store = [&](R* to, int at0) {
+      return [=](int, int at, const A* r) {
+        if (part) {
+          store_as<V>(to_part + at0 + at, r);
+        } else {
+          Pack<R, V> y;
+#pragma unroll
+          for (int k = 0; k < V; ++k) y.e[k] = cgtp::to<R>(r[k]);
+          y.store(to + at);
+        }
+      };
     };
+    const auto to_k = store(reinterpret_cast<R*>(a.gk.p) + int64_t(row) * a.gk.ld, 0);
+    const auto to_v = store(reinterpret_cast<R*>(a.gv.p) + int64_t(row) * a.gv.ld, wk);
+    A *zk = sm.z + from, *zv = sm.p + from;
+    const int* idx = sm.idx + from;
+    if (a.group == 1) {
+      short_sums<V, 1, true, false, S>(a, a.qk, cnt, zk, a.q, idx, sm.acc, none, first, last, to_k);
+      if (VALUES) sums<V, CB, 1, true, false, S>(a, a.vv, cnt, zv, a.gout, idx, sm.acc + wk, none, first, last, to_v);
+    } else {
+      short_sums<V, 1, true, true, S>(a, a.qk, cnt, zk, a.q, idx, sm.acc, none, first, last, to_k);
+      if (VALUES) sums<V, CB, 1, true, true, S>(a, a.vv, cnt, zv, a.gout, idx, sm.acc + wk, none, first, last, to_v);
+    }
+  };
+
+  int64_t at = t.one ? int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+  int rows = 1;
+  if (at >= a.n_items) {   // (as item_of)
+    at = a.n_items + (at - a.n_items) * a.batch;
+    rows = static_cast<int>(min(int64_t(a.batch), a.n_items + a.n_rows - at));
+    if (rows <= 0) return;
+  }
+  if (rows > 1) {
+    // lane r < rows: its row's edges, and the place of the first of them, a multiple of what the loops take at a time
+    const int r0 = static_cast<int>(at - a.n_items), lane = t.lane, step = max(32 >> a.qk.abreast, VALUES ? 32 >> a.vv.abreast : 0) * kAtQuad;
+    int e0 = 0, len = 0;
+    if (lane < rows) {
+      e0 = a.rowptr[r0 + lane];
+      len = a.rowptr[r0 + lane + 1] - e0;
+      if (a.n_items && len > a.chunk) len = -1;   // done by items
+    }
+    const int padded = (max(len, 0) + step - 1) & -step;
+    int end = padded;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int before = __shfl_up_sync(kAll, end, o);
+      if (lane >= o) end += before;
+    }
+    const int total = __shfl_sync(kAll, end, 31), from = end - padded;
+    if (total <= a.sub) {
+      for (int i0 = 0; i0 < total; i0 += 32) {
+        const int i = i0 + lane;
+        int first = 0, e = 0, n = 0;
+        for (int r = 0; r < rows; ++r) {
+          const int f = __shfl_sync(kAll, from, r), e_ = __shfl_sync(kAll, e0, r), n_ = __shfl_sync(kAll, len, r);
+          if (f <= i && n_ > 0) first = f, e = e_, n = n_;
+        }
+        if (i < total) {
+          const int k = e + min(i - first, n - 1);
+          const int end_ = a.col[k], id = a.eid[k];
+          sm.idx[i] = end_;
+          sm.bucket[i] = i - first < n ? id : -1;
+        }
+      }
+      __syncwarp();
+      fetch(total);
+      for (int r = 0; r < rows; ++r) {
+        const int f = __shfl_sync(kAll, from, r), n = __shfl_sync(kAll, len, r);
+        if (n >= 0) add(r0 + r, -1, f, (n + step - 1) & -step, true, true);
+      }
+      return;
+    }
+  }
+  for (int r = 0; r < rows; ++r) {
+    const Item it = item_at(a, t, at + r);
+    if (!it.some) continue;
     int e = it.e0;
     do {
       const int cnt = min(a.sub, it.e1 - e);
       load_ends(a, sm, e, cnt);
       for (int i = t.lane; i < cnt; i += 32) sm.bucket[i] = a.eid[e + i];
       __syncwarp();
-      each_pair(a, cnt, [&](int to_, int i, int h, int) {
-        const int64_t at = int64_t(sm.bucket[i]) * a.heads + h;
-        if (VALUES) {
-          const Pair<A> x = static_cast<const Pair<A>*>(a.pairs)[at];
-          sm.z[to_] = x.ds * scale;
-          sm.p[to_] = x.p;
-        } else {
-          sm.z[to_] = static_cast<const A*>(a.ds)[at] * scale;
-        }
-      });
-      __syncwarp();
-      const bool first = e == it.e0, last = t.one && e + cnt >= it.e1;
-      const auto store = [&](R* row, int from) {
-        return [=](int, int at, const A* r) {
-          if (part) {
-            store_as<V>(to_part + from + at, r);
-          } else {
-            Pack<R, V> y;
-#pragma unroll
-            for (int k = 0; k < V; ++k) y.e[k] = to<R>(r[k]);
-            y.store(row + at);
-          }
-        };
-      };
-      const A* none = nullptr;
-      const auto to_k = store(reinterpret_cast<R*>(a.gk.p) + int64_t(it.row) * a.gk.ld, 0);
-      const auto to_v = store(reinterpret_cast<R*>(a.gv.p) + int64_t(it.row) * a.gv.ld, wk);
-      if (a.group == 1) {
-        short_sums<V, 1, true, false, S>(a, a.qk, cnt, sm.z, a.q, sm.idx, sm.acc, none, first, last, to_k);
-        if (VALUES) sums<V, CB, 1, true, false, S>(a, a.vv, cnt, sm.p, a.gout, sm.idx, sm.acc + wk, none, first, last, to_v);
-      } else {
-        short_sums<V, 1, true, true, S>(a, a.qk, cnt, sm.z, a.q, sm.idx, sm.acc, none, first, last, to_k);
-        if (VALUES) sums<V, CB, 1, true, true, S>(a, a.vv, cnt, sm.p, a.gout, sm.idx, sm.acc + wk, none, first, last, to_v);
-      }
-      __syncwarp();
+      fetch(cnt);
+      add(it.row, it.index, 0, cnt, e == it.e0, t.one && e + cnt >= it.e1);
       e += cnt;
     } while (e < it.e1);
     if (!t.one) {
+      const auto finish = [&](int c, A x) {   // element c of (gk, gv)
+        if (it.index >= 0) (static_cast<A*>(a.part) + int64_t(it.index) * a.part_ld)[c] = x;
+        else if (c < a.kv * a.dk) (reinterpret_cast<R*>(a.gk.p) + int64_t(it.row) * a.gk.ld)[c] = to<R>(x);
+        else if (c >= wk) (reinterpret_cast<R*>(a.gv.p) + int64_t(it.row) * a.gv.ld)[c - wk] = to<R>(x);
+      };
       __syncthreads();
       for (int c = t.thread(); c < stride; c += t.threads()) {
-        A r = 0;
-        for (int w = 0; w < t.warps; ++w) r += Smem<A>(a, w).acc[c];
-        finish(c, r);
+        A x = 0;
+        for (int w = 0; w < t.warps; ++w) x += Smem<A>(a, w).acc[c];
+        finish(c, x);
       }
     }
   }
 }
 
 // Gradient of the bias table: sums of ds by bucket.  A lane always adds to the same head's column of its warp's
-// histogram, one column a lane, so that nothing collides and the order is fixed.  ds lies ds_step values apart.
+// histogram, one column a lane, so that nothing collides and the order is fixed.  ds lies hist_step values apart.  A CTA
+// joins its columns in the arithmetic's type (a cell's sum has few terms there, and FP64 additions are slow), the
+// CTAs' parts are joined in FP64.
 template <typename A>
-__global__ void attn_table_kernel(const __grid_constant__ AtArgs a) {
+__global__ void __launch_bounds__(512) attn_table_kernel(const __grid_constant__ AtArgs a) {
   chain_enter();
   extern __shared__ __align__(16) char at_smem[];
   const int buckets = a.n_borders + 1, cols = a.hist_cols, lane = threadIdx.x & 31, w = threadIdx.x / 32, warps_here = blockDim.x / 32;
@@ -1181,30 +1251,42 @@ __global__ void attn_table_kernel(const __grid_constant__ AtArgs a) {
       }
     }
   __syncthreads();
-  // columns of a head: lanes h, h + heads, ... of each block of 32, over all warps
+  // columns of a head: lanes h, h + heads, ... of each block of 32, over all warps (buckets start at different ones, so
+  // that they read different banks)
   for (int i = threadIdx.x; i < buckets * a.heads; i += blockDim.x) {
-    const int b = i / a.heads, h = i - b * a.heads;
-    double sum = 0;
-    for (int q = 0; q < warps_here; ++q)
-      for (int k = 0; k < slots; ++k) sum += all[(q * buckets + b) * cols + h + k * a.heads];
-    if (gridDim.x == 1) static_cast<A*>(a.gtable)[i] = static_cast<A>(sum);
-    else static_cast<double*>(a.hist)[int64_t(blockIdx.x) * buckets * a.heads + i] = sum;
+    const int b = i / a.heads, h = i - b * a.heads, turn = b % slots;
+    A sum = 0;
+#pragma unroll 4
+    for (int q = 0; q < warps_here; ++q) {
+      const A* col = all + (q * buckets + b) * cols + h;
+      A part = 0;
+#pragma unroll 4
+      for (int k = 0; k < slots; ++k) part += col[(k + turn < slots ? k + turn : k + turn - slots) * a.heads];
+      sum += part;
+    }
+    if (gridDim.x == 1) static_cast<A*>(a.gtable)[i] = sum;
+    else static_cast<A*>(a.hist)[int64_t(blockIdx.x) * buckets * a.heads + i] = sum;
   }
 }
 
+// Joins the parts: block (8 columns, 64 streams of parts)
 template <typename A>
-__global__ void attn_table_sum_kernel(const AtArgs a, int parts) {
+__global__ void attn_table_sum_kernel(const __grid_constant__ AtArgs a, int parts) {
   chain_enter();
-  __shared__ double red[8][33];
-  const int c = blockIdx.x * 32 + threadIdx.x, s = threadIdx.y, width = (a.n_borders + 1) * a.heads;
+  __shared__ double red[64][9];
+  const int c = blockIdx.x * 8 + threadIdx.x, s = threadIdx.y, width = (a.n_borders + 1) * a.heads;
   double sum = 0;
-  if (c < width)
-    for (int i = s; i < parts; i += 8) sum += static_cast<const double*>(a.hist)[int64_t(i) * width + c];
+  if (c < width) {
+#pragma unroll 8
+    for (int i = s; i < parts; i += 64) sum += static_cast<const A*>(a.hist)[int64_t(i) * width + c];
+  }
   red[s][threadIdx.x] = sum;
-  __syncthreads();
-  if (s || c >= width) return;
-  for (int i = 1; i < 8; ++i) sum += red[i][threadIdx.x];
-  static_cast<A*>(a.gtable)[c] = static_cast<A>(sum);
+#pragma unroll 1
+  for (int o = 32; o > 0; o /= 2) {
+    __syncthreads();
+    if (s < o) red[s][threadIdx.x] += red[s + o][threadIdx.x];
+  }
+  if (s == 0 && c < width) static_cast<A*>(a.gtable)[c] = static_cast<A>(red[0][threadIdx.x]);
 }
 
 // ---------------------------------------------------------------------------
@@ -1300,7 +1382,7 @@ auto at_variant(const AtArgs& a, int turn, F&& f) {
     cudaError_t e = at_launch(attn_table_kernel<A>, dim3(a.hist_ctas), dim3(32 * a.hist_warps),                              \
                               (size_t(a.hist_warps) * buckets * a.hist_cols + a.n_borders) * sizeof(A), st, a);              \
     if (e != cudaSuccess || a.hist_ctas == 1) return e;                                                                      \
-    return at_launch(attn_table_sum_kernel<A>, dim3((width + 31) / 32), dim3(32, 8), 0, st, a, a.hist_ctas);                 \
+    return at_launch(attn_table_sum_kernel<A>, dim3((width + 7) / 8), dim3(8, 64), 0, st, a, a.hist_ctas);                    \
   }
 
 }  // namespace cgtp
