@@ -268,8 +268,8 @@ cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* 
                         : k == kSendAll                       ? send_ld(p, true)
                                                               : 0;
   // (edge rows have a kernel of their own)
-  const bool values = k == kForward || k == kReceive;
-  a->four = !send && a->group % 4 == 0 && a->qk.vec > 1 && (!values || a->vv.vec > 1);
+  const bool values = k == kForward || k == kReceive || k == kSendAll;
+  a->four = a->group % 4 == 0 && a->qk.vec > 1 && (!values || a->vv.vec > 1);
   a->head_lanes = log2_up(std::min(a->heads, 32));
   const int units = send ? a->kv : a->four ? a->heads / 4 : a->heads;
   const auto most = [&](int vec, int plain) { return vec == 1 ? 4 : a->four ? (vec == 8 ? 1 : 2) : plain; };
@@ -284,12 +284,13 @@ cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* 
       return static_cast<int>(place);
     };
     int64_t run = (longest + warps - 1) / warps;
-    if (send && warps == 1) run = std::max<int64_t>(run, 64);   // (several rows)
+    if (send && warps == 1) run = std::max<int64_t>(run, 48);   // (several rows)
     a->sub = static_cast<int>(std::max<int64_t>(8, std::min<int64_t>((run + 7) / 8 * 8, 4096 / (int64_t(a->heads) * es * pairs) / 8 * 8)));
     // weights of a head: a multiple of 32 and the edges abreast where a lane takes a head's edges, so that heads lie
     // in different banks; whole quads
-    const int64_t held = align16(a->sub + a->pad);
-    a->stride = static_cast<int>((held + 31) / 32 * 32 + std::max(4, 32 >> a->head_lanes) % 32);
+    const int64_t held = (a->sub + a->pad + 3) / 4 * 4;
+    const int64_t shift = std::max(4, 32 >> a->head_lanes) % 32;
+    a->stride = static_cast<int>(std::max<int64_t>(0, held - shift + 31) / 32 * 32 + shift);
     region(int64_t(a->stride) * a->heads * es);
     a->at_p = region(pairs == 2 ? int64_t(a->stride) * a->heads * es : 0);
     a->at_idx = region((held + a->sub) * int64_t(sizeof(int)));
@@ -303,6 +304,7 @@ cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* 
     lay_out();
   }
   a->one = warps == 1;
+  a->whole = a->one && a->n_items == 0 && longest <= a->sub;
   if (a->one) {
     warps = 4;
     while (warps > 1 && warps * at > p->smem_cap) warps /= 2;
@@ -322,13 +324,11 @@ cgtp_status deal(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* 
   return CGTP_OK;
 }
 
-// the launch of a kernel's second phase: items of split rows only
-AtArgs second_phase(const AtArgs& a) {
-  AtArgs b = a;
-  const unsigned teams = a.one ? a.block / 32 : 1;
-  b.phase = kAtSecond;
-  b.grid = (a.n_items + teams - 1) / teams;
-  return b;
+// arguments of a kernel's second phase: items of split rows only
+cgtp_status second_phase(const cgtp_attn_s* p, const cgtp_graph_s* g, Kernel k, AtArgs* a) {
+  a->phase = kAtSecond;
+  a->n_rows = 0;
+  return deal(p, g, k, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -446,7 +446,8 @@ cgtp_status receive(const cgtp_attn_s* p, const cgtp_graph_s* g, AtArgs* a, bool
   a->phase = a->n_items ? kAtFirst : kAtWhole;
   if ((s = done(CGTP_AT_PICK(p, receive)(*a, edges, st)))) return s;
   if (a->n_items) {
-    if ((s = done(CGTP_AT_PICK(p, receive)(second_phase(*a), edges, st)))) return s;
+    AtArgs b = *a;
+    if ((s = second_phase(p, g, edges ? kEdgesReceive : kReceive, &b)) || (s = done(CGTP_AT_PICK(p, receive)(b, edges, st)))) return s;
     if ((s = done(CGTP_AT_PICK(p, join_sum)(*a, a->gq, p->heads * p->dk, 0, a->part_ld, st)))) return s;
   }
   a->phase = kAtWhole;
@@ -614,7 +615,10 @@ cgtp_status cgtp_attn_edges_forward(cgtp_attn p, cgtp_graph g, const void* q, in
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   a.phase = a.n_items ? kAtFirst : kAtWhole;
   if ((s = done(CGTP_AT_PICK(p, weights)(a, st)))) return s;
-  if (a.n_items && (s = done(CGTP_AT_PICK(p, weights)(second_phase(a), st)))) return s;
+  if (a.n_items) {
+    AtArgs b = a;
+    if ((s = second_phase(p, g, kWeights, &b)) || (s = done(CGTP_AT_PICK(p, weights)(b, st)))) return s;
+  }
   const int64_t pieces = int64_t(a.heads) * a.vv.pieces;
   a.pieces_magic = static_cast<uint32_t>(((uint64_t(1) << 32) + pieces - 1) / pieces);
   a.grid = static_cast<unsigned>(std::min<int64_t>((g->E * pieces + 1023) / 1024, int64_t(p->num_sms) * 8));

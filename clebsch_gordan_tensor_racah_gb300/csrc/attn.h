@@ -78,9 +78,10 @@ struct AtArgs {
   int stride = 0;                  // weights of a head
   int batch = 1;                   // sources' kernel: rows that a warp takes side by side
   int pad = 0;                     // places behind a list of edges that the loops may read
-  int four = 0;                    // four heads that share keys and values are taken together
+  int four = 0;                    // four heads of a group, which share keys and values, are taken together
   int head_lanes = 0;              // logarithm of the heads abreast where a lane takes a head's edges
   int one = 1;                     // a warp a row; otherwise a CTA a row
+  int whole = 0;                   // every row is one run of one warp
   int warp_smem = 0, at_p = 0, at_idx = 0, at_stat = 0, at_acc = 0;   // a warp's shared memory and its regions, in bytes
   uint32_t pieces_magic = 0;       // ceil(2^32 / vectors of an edge's row)
   unsigned grid = 0, block = 0;

@@ -200,16 +200,14 @@ __device__ __forceinline__ void with_width(int v, F&& f) {
 
 constexpr unsigned kAll = 0xffffffffu;
 
-// One warp a row, or all warps of the CTA.
+// One warp a row, or all warps of the CTA.  Kernels with WHOLE are those of launches in which every row is one run of one
+// warp (AtArgs::whole): what joins runs, warps and pieces of rows drops out of them, which is a third of a row's
+// fixed cost.
 struct Team {
   bool one;
   int w, warps, lane;   // this warp among the row's
-  __device__ __forceinline__ Team(const AtArgs& a)
-      : one(a.one), w(a.one ? 0 : threadIdx.x / 32), warps(a.one ? 1 : blockDim.x / 32), lane(threadIdx.x & 31) {}
-  __device__ __forceinline__ void sync() const {
-    if (one) __syncwarp();
-    else __syncthreads();
-  }
+  __device__ __forceinline__ Team(const AtArgs& a, bool whole)
+      : one(whole || a.one), w(one ? 0 : threadIdx.x / 32), warps(one ? 1 : blockDim.x / 32), lane(threadIdx.x & 31) {}
   __device__ __forceinline__ int thread() const { return w * 32 + lane; }
   __device__ __forceinline__ int threads() const { return warps * 32; }
 };
@@ -222,8 +220,18 @@ struct Item {
 };
 
 // Piece i of the work.  First come the items of split rows, the longest work.
+template <bool WHOLE>
 __device__ __forceinline__ Item item_at(const AtArgs& a, const Team& t, int64_t i) {
   Item it;
+  if (WHOLE) {
+    if (i < a.n_rows) {
+      it.row = static_cast<int>(i);
+      it.e0 = a.rowptr[it.row];
+      it.e1 = a.rowptr[it.row + 1];
+      it.some = true;
+    }
+    return it;
+  }
   if (i < a.n_items) {
     const Int4 v = a.items[i];
     it.row = v.x, it.e0 = v.y, it.e1 = v.z;
@@ -243,8 +251,9 @@ __device__ __forceinline__ Item item_at(const AtArgs& a, const Team& t, int64_t 
   return it;
 }
 
+template <bool WHOLE>
 __device__ __forceinline__ Item item_of(const AtArgs& a, const Team& t) {
-  return item_at(a, t, t.one ? int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x);
+  return item_at<WHOLE>(a, t, t.one ? int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x);
 }
 
 // pair / heads for pairs below 2^24 (heads <= 64: the error of the multiplier is below 2^-32 a unit)
@@ -284,14 +293,14 @@ struct Smem {
 template <int V, int G>
 constexpr int kShort = G == 4 && V == 8 ? 1 : 2;
 
-// Edges in flight of `elements` elements a lane: as many, up to `most`, as leave them and G sets of results or queries
-// about 48 of the 80 registers (72 of 128 where G = 4).
-template <typename S, typename A, int elements, int G, int most>
-constexpr int kFlight = most > 1 && most * elements * int(sizeof(S)) / 4 + G * elements * int(sizeof(A)) / 4 > (G == 1 ? 48 : 72)
-                            ? kFlight<S, A, elements, G, most / 2>
+// Edges in flight of `elements` elements a lane: as many, up to four, as leave them and `held` results or queries about 48
+// of the 80 registers (72 of 128 where G = 4).
+template <typename S, typename A, int elements, int held, int G, int most = kAtQuad>
+constexpr int kFlight = most > 1 && (most * elements * int(sizeof(S)) + held * int(sizeof(A))) / 4 > (G == 1 ? 48 : 72)
+                            ? kFlight<S, A, elements, held, G, most / 2>
                             : most;
-template <typename S, typename A, int elements, int G>
-constexpr int kFlight<S, A, elements, G, 1> = 1;
+template <typename S, typename A, int elements, int held, int G>
+constexpr int kFlight<S, A, elements, held, G, 1> = 1;
 
 // Sums of v[u] (u < 4) over the 2^width lanes side by side, which share them out as they halve them: in the end lane x holds
 // those of v[first], v[first + 1], ... in v[0..] (4, 2 or 1 of them for width 0, 1 and more).  Returns `first`.
@@ -317,7 +326,7 @@ __device__ __forceinline__ int lane_sums(A (&v)[4], int width, int x) {
 // added to the product times the scale; -infinity stays.
 template <int V, int CB, int G, bool LOGITS, typename S, typename A>
 __device__ __forceinline__ void dots(const AtArgs& a, const AtTab& tab, int cnt, const S* x, const AtRows& rows, const int* idx, A* z) {
-  constexpr int U = kFlight<S, A, V * CB, G, 4>;
+  constexpr int U = kFlight<S, A, V * CB, G * V * CB, G>;
   const AtLanes& l = tab.lanes;
   const Place at(l);
   const int units = a.heads / G, pieces = tab.pieces, slots = 32 >> (l.width + l.units);
@@ -405,7 +414,7 @@ __device__ __forceinline__ void dots(const AtArgs& a, const AtTab& tab, int cnt,
 // part.  The vectors of a row of the shared heads are dealt out to the lanes in the order of memory, so that a row is
 // read in whole lines, and a lane takes four edges at a time: their ends in one load, their weights, which lie side by
 // side, in one or two, and one address a row.  SEND: results are rows of the shared heads, which sum over the heads of
-// their group; otherwise rows of all heads, G that share a vector at a time.  APART: rows of all heads, in which the
+// their group, G at a time; otherwise rows of all heads, G that share a vector at a time.  APART: rows of all heads, in which the
 // vectors of a shared head's group lie apart.
 template <int V, int CB, int G, bool SEND, bool APART, typename S, typename A, typename F>
 __device__ __forceinline__ void sums(const AtArgs& a, const AtTab& tab, int cnt, A* coef, const AtRows& rows, const int* idx, A* keep,
@@ -413,6 +422,7 @@ __device__ __forceinline__ void sums(const AtArgs& a, const AtTab& tab, int cnt,
   const int lane = threadIdx.x & 31, x = lane & ((1 << tab.abreast) - 1), s = lane >> tab.abreast;
   const int step = (32 >> tab.abreast) * kAtQuad, end = (cnt + step - 1) & -step, total = a.kv * tab.pieces;
   constexpr int kOffset = (1 << kAtHeadShift) - 1;
+  constexpr int QA = SEND ? 1 : G, QL = SEND ? G : 1;   // sets of results; of vectors, one a head of the group
   // weights of the places behind the last edge
 #pragma unroll 1
   for (int k = lane; k < (end - cnt) * a.heads; k += 32) {
@@ -424,58 +434,65 @@ __device__ __forceinline__ void sums(const AtArgs& a, const AtTab& tab, int cnt,
   for (int c0 = 0; c0 < total; c0 += CB << tab.abreast) {
 #pragma unroll 1
     for (int g0 = 0; g0 < (SEND ? 1 : a.group); g0 += G) {
-      A acc[G][CB][V];
+      A acc[QA][CB][V];
 #pragma unroll
-      for (int q = 0; q < G; ++q)
+      for (int q = 0; q < QA; ++q)
 #pragma unroll
         for (int j = 0; j < CB; ++j)
 #pragma unroll
           for (int k = 0; k < V; ++k) acc[q][j][k] = 0;
 #pragma unroll 1
-      for (int g = 0; g < (SEND ? a.group : 1); ++g) {
-        const char* base[CB];
-        const A* fp[CB];
+      for (int g = 0; g < (SEND ? a.group : 1); g += QL) {
+        const char* base[QL][CB];
+        const A* fp[QL][CB];
 #pragma unroll
-        for (int j = 0; j < CB; ++j) {
-          // (lanes beyond the last vector take it too, for nothing)
-          const int c = min(c0 + (j << tab.abreast) + x, total - 1), entry = tab.rows[c * a.group + g0 + g];
-          fp[j] = coef + (entry >> kAtHeadShift) * a.stride + s * kAtQuad;
-          base[j] = rows.p + (APART ? entry & kOffset : c * V) * sizeof(S);
-        }
+        for (int q = 0; q < QL; ++q)
+#pragma unroll
+          for (int j = 0; j < CB; ++j) {
+            // (lanes beyond the last vector take it too, for nothing)
+            const int c = min(c0 + (j << tab.abreast) + x, total - 1), entry = tab.rows[c * a.group + g0 + g + q];
+            fp[q][j] = coef + (entry >> kAtHeadShift) * a.stride + s * kAtQuad;
+            base[q][j] = rows.p + (APART ? entry & kOffset : c * V) * sizeof(S);
+          }
         const int* ip = idx + s * kAtQuad;
 #pragma unroll 1
         for (int b = 0; b < end; b += step) {
           Pack<int, 4> ends;
           ends.load(ip + b);
-          constexpr int U = kFlight<S, A, V * CB, G, kAtQuad>;
+          constexpr int U = kFlight<S, A, V * CB * QL, V * CB * QA, G>;
 #pragma unroll
           for (int part = 0; part < kAtQuad; part += U) {
-            Pack<S, V> y[U][CB];
+            Pack<S, V> y[U][QL][CB];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               const unsigned end_ = ends.e[part + u];
 #pragma unroll
-              for (int j = 0; j < CB; ++j) y[u][j].load(reinterpret_cast<const S*>(base[j] + uint64_t(end_) * rows.ld_bytes));
+              for (int q = 0; q < QL; ++q)
+#pragma unroll
+                for (int j = 0; j < CB; ++j) y[u][q][j].load(reinterpret_cast<const S*>(base[q][j] + uint64_t(end_) * rows.ld_bytes));
             }
 #pragma unroll
             for (int j = 0; j < CB; ++j) {
               Pack<A, U> f[G];
 #pragma unroll
-              for (int q = 0; q < G; ++q) f[q].load(fp[j] + q * a.stride + b + part);
+              for (int q = 0; q < G; ++q) f[q].load((SEND ? fp[q][j] : fp[0][j] + q * a.stride) + b + part);
 #pragma unroll
               for (int u = 0; u < U; ++u) {
                 A w[V];
 #pragma unroll
-                for (int k = 0; k < V; ++k) w[k] = y[u][j].number(k);
+                for (int q = 0; q < G; ++q) {
+                  if (SEND || q == 0)
 #pragma unroll
-                for (int q = 0; q < G; ++q) add_weighed<V>(acc[q][j], f[q].e[u], w);
+                    for (int k = 0; k < V; ++k) w[k] = y[u][SEND ? q : 0][j].number(k);
+                  add_weighed<V>(acc[SEND ? 0 : q][j], f[q].e[u], w);
+                }
               }
             }
           }
         }
       }
 #pragma unroll
-      for (int q = 0; q < G; ++q)
+      for (int q = 0; q < QA; ++q)
 #pragma unroll
         for (int j = 0; j < CB; ++j) {
           A* r = acc[q][j];
@@ -660,13 +677,13 @@ __device__ __forceinline__ void join_warps(const AtArgs& a, const Team& t) {
   __syncthreads();
 }
 
-template <typename S, typename R, typename A, int V, int G, int CB>
+template <typename S, typename R, typename A, int V, int G, int CB, bool WHOLE>
 __global__ void __launch_bounds__(256, kResident<G>) attn_forward_kernel(const __grid_constant__ AtArgs a) {
   chain_enter();
-  const Team t(a);
+  const Team t(a, WHOLE);
   const Smem<A> sm(a, threadIdx.x / 32);
   const int width = a.heads * a.dv;
-  const Item it = item_of(a, t);
+  const Item it = item_of<WHOLE>(a, t);
   if (!it.some) return;
   {
     const bool part = it.index >= 0;
@@ -674,11 +691,11 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_forward_kernel(const _
     R* out = reinterpret_cast<R*>(a.out.p) + int64_t(it.row) * a.out.ld;
     int e = it.e0;
     do {
-      const int cnt = min(a.sub, it.e1 - e);
+      const int cnt = WHOLE ? it.e1 - e : min(a.sub, it.e1 - e);
+      const bool first = WHOLE || e == it.e0, last = WHOLE || e + cnt >= it.e1;
       logits<V, G, S>(a, sm, it.row, e, cnt);
-      softmax_step(a, sm, cnt, e == it.e0, false);
-      const bool last = e + cnt >= it.e1;
-      sums<V, CB, G, false, false, S>(a, a.vv, cnt, sm.z, a.v, sm.idx, sm.acc, sm.stat + 2 * a.heads, e == it.e0, t.one && last,
+      softmax_step(a, sm, cnt, first, false);
+      sums<V, CB, G, false, false, S>(a, a.vv, cnt, sm.z, a.v, sm.idx, sm.acc, sm.stat + 2 * a.heads, first, t.one && last,
                   [&](int h, int at, const A* r) {
                     if (part) {
                       store_as<V>(to_part + at, r);
@@ -691,7 +708,7 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_forward_kernel(const _
                     }
                   });
       e += cnt;
-    } while (e < it.e1);
+    } while (!WHOLE && e < it.e1);
     const Smem<A> one(a, t.one ? threadIdx.x / 32 : 0);
     if (!t.one) {
       join_warps<A>(a, t);
@@ -778,10 +795,10 @@ __global__ void attn_join_sum_kernel(const AtArgs a, const AtRows out, int width
 template <typename S, typename A, int V, int G>
 __global__ void __launch_bounds__(256, kResident<G>) attn_weights_kernel(const __grid_constant__ AtArgs a) {
   chain_enter();
-  const Team t(a);
+  const Team t(a, false);
   const Smem<A> sm(a, threadIdx.x / 32), one(a, t.one ? threadIdx.x / 32 : 0);
   A* alpha = static_cast<A*>(a.alpha);
-  const Item it = item_of(a, t);
+  const Item it = item_of<false>(a, t);
   if (!it.some) return;
   {
     const bool held = t.one && it.index < 0 && it.e1 - it.e0 <= a.sub;
@@ -946,15 +963,15 @@ struct alignas(2 * sizeof(A)) Pair {
 
 // The receivers' kernel: ds of every edge, and gq.  EDGES: dp comes in ds and a in alpha; otherwise both are
 // computed here.
-template <typename S, typename R, typename A, int V, int G, int CB, bool EDGES>
+template <typename S, typename R, typename A, int V, int G, int CB, bool EDGES, bool WHOLE>
 __global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const __grid_constant__ AtArgs a) {
   chain_enter();
-  const Team t(a);
+  const Team t(a, WHOLE);
   const Smem<A> sm(a, threadIdx.x / 32);
   const A scale = static_cast<A>(a.scale);
   Pair<A>* pairs = static_cast<Pair<A>*>(a.pairs);
   const int width = a.heads * a.dk;
-  const Item it = item_of(a, t);
+  const Item it = item_of<WHOLE>(a, t);
   if (!it.some) return;
   // dp and a of the edges [e, e + cnt) into z and p: from memory where they are there
   const auto fetch = [&](int e, int cnt) {
@@ -972,11 +989,12 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const _
     __syncwarp();
   };
   {
-    const bool held = it.e1 - it.e0 <= a.sub && a.phase != kAtSecond;   // z, p and idx hold the whole run
-    if (a.phase != kAtSecond) {
+    const int phase = WHOLE ? int(kAtWhole) : a.phase;
+    const bool held = WHOLE || (it.e1 - it.e0 <= a.sub && phase != kAtSecond);   // z, p and idx hold the whole run
+    if (phase != kAtSecond) {
       int e = it.e0;
       do {
-        const int cnt = min(a.sub, it.e1 - e);
+        const int cnt = WHOLE ? it.e1 - e : min(a.sub, it.e1 - e);
         if (EDGES) {
           fetch(e, cnt);
         } else {
@@ -998,11 +1016,11 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const _
             if (p != 0) sum += p * sm.z[l.h * a.stride + i];
           }
           sum = all_sum(l, sum);
-          if (l.on) sm.stat[l.h] = (e == it.e0 ? A(0) : sm.stat[l.h]) + sum;
+          if (l.on) sm.stat[l.h] = (WHOLE || e == it.e0 ? A(0) : sm.stat[l.h]) + sum;
         });
         __syncwarp();
         e += cnt;
-      } while (e < it.e1);
+      } while (!WHOLE && e < it.e1);
       if (!t.one) {
         __syncthreads();
         A total[2] = {0, 0};   // heads <= 64, at least 32 threads
@@ -1037,7 +1055,8 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const _
     };
     int e = it.e0;
     do {
-      const int cnt = min(a.sub, it.e1 - e);
+      const int cnt = WHOLE ? it.e1 - e : min(a.sub, it.e1 - e);
+      const bool first = WHOLE || e == it.e0, last = WHOLE || e + cnt >= it.e1;
       if (!held) fetch(e, cnt);
       each_pair(a, cnt, [&](int at, int, int h, int k) {
         const A p = sm.p[at], d = p == 0 ? A(0) : p * (sm.z[at] - sm.stat[h]);
@@ -1046,8 +1065,7 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const _
         if (a.ds) static_cast<A*>(a.ds)[int64_t(e) * a.heads + k] = d;
       });
       __syncwarp();
-      const bool last = e + cnt >= it.e1;
-      short_sums<V, G, false, false, S>(a, a.qk, cnt, sm.z, a.k, sm.idx, sm.acc, static_cast<const A*>(nullptr), e == it.e0, t.one && last,
+      short_sums<V, G, false, false, S>(a, a.qk, cnt, sm.z, a.k, sm.idx, sm.acc, static_cast<const A*>(nullptr), first, t.one && last,
                   [&](int, int at, const A* r) {
                     if (it.index >= 0) {
                       A x[V];
@@ -1063,7 +1081,7 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const _
                   });
       __syncwarp();
       e += cnt;
-    } while (e < it.e1);
+    } while (!WHOLE && e < it.e1);
     if (!t.one) {
       __syncthreads();
       for (int c = t.thread(); c < width; c += t.threads()) {
@@ -1078,10 +1096,10 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const _
 // The sources' kernel, over the transpose: gk, and gv where VALUES.  A warp takes a.batch rows side by side, whose lists
 // and weights it reads together where they fit (200,000 sources of 8 edges: the latencies of a row's lists and weights are
 // a third of its time).
-template <typename S, typename R, typename A, int V, int CB, bool VALUES>
-__global__ void __launch_bounds__(256, kResident<1>) attn_send_kernel(const __grid_constant__ AtArgs a) {
+template <typename S, typename R, typename A, int V, int G, int CB, bool VALUES, bool WHOLE>
+__global__ void __launch_bounds__(256, kResident<G>) attn_send_kernel(const __grid_constant__ AtArgs a) {
   chain_enter();
-  const Team t(a);
+  const Team t(a, WHOLE);
   const Smem<A> sm(a, threadIdx.x / 32);
   const A scale = static_cast<A>(a.scale);
   const int wk = (a.kv * a.dk + 3) & ~3, stride = wk + (VALUES ? a.kv * a.dv : 0);   // (aligned for vectors)
@@ -1104,7 +1122,7 @@ __global__ void __launch_bounds__(256, kResident<1>) attn_send_kernel(const __gr
   };
   // sums over cnt places from `from`, for the row (or the item, where it is a piece of a row)
   const auto add = [&](int row, int item, int from, int cnt, bool first, bool last) {
-    const bool part = item >= 0;
+    const bool part = !WHOLE && item >= 0;
     A* to_part = static_cast<A*>(a.part) + int64_t(item) * a.part_ld;
     const auto store = [&](R* to, int at0) {
       return [=](int, int at, const A* r) {
@@ -1122,18 +1140,18 @@ __global__ void __launch_bounds__(256, kResident<1>) attn_send_kernel(const __gr
     const auto to_v = store(reinterpret_cast<R*>(a.gv.p) + int64_t(row) * a.gv.ld, wk);
     A *zk = sm.z + from, *zv = sm.p + from;
     const int* idx = sm.idx + from;
-    if (a.group == 1) {
+    if (G == 1 && a.group == 1) {
       short_sums<V, 1, true, false, S>(a, a.qk, cnt, zk, a.q, idx, sm.acc, none, first, last, to_k);
       if (VALUES) sums<V, CB, 1, true, false, S>(a, a.vv, cnt, zv, a.gout, idx, sm.acc + wk, none, first, last, to_v);
     } else {
-      short_sums<V, 1, true, true, S>(a, a.qk, cnt, zk, a.q, idx, sm.acc, none, first, last, to_k);
-      if (VALUES) sums<V, CB, 1, true, true, S>(a, a.vv, cnt, zv, a.gout, idx, sm.acc + wk, none, first, last, to_v);
+      short_sums<V, G, true, true, S>(a, a.qk, cnt, zk, a.q, idx, sm.acc, none, first, last, to_k);
+      if (VALUES) sums<V, CB, G, true, true, S>(a, a.vv, cnt, zv, a.gout, idx, sm.acc + wk, none, first, last, to_v);
     }
   };
 
   int64_t at = t.one ? int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
   int rows = 1;
-  if (at >= a.n_items) {   // (as item_of)
+  if (WHOLE || at >= a.n_items) {   // (as item_of)
     at = a.n_items + (at - a.n_items) * a.batch;
     rows = static_cast<int>(min(int64_t(a.batch), a.n_items + a.n_rows - at));
     if (rows <= 0) return;
@@ -1145,7 +1163,7 @@ __global__ void __launch_bounds__(256, kResident<1>) attn_send_kernel(const __gr
     if (lane < rows) {
       e0 = a.rowptr[r0 + lane];
       len = a.rowptr[r0 + lane + 1] - e0;
-      if (a.n_items && len > a.chunk) len = -1;   // done by items
+      if (!WHOLE && a.n_items && len > a.chunk) len = -1;   // done by items
     }
     const int padded = (max(len, 0) + step - 1) & -step;
     int end = padded;
@@ -1174,24 +1192,24 @@ __global__ void __launch_bounds__(256, kResident<1>) attn_send_kernel(const __gr
       fetch(total);
       for (int r = 0; r < rows; ++r) {
         const int f = __shfl_sync(kAll, from, r), n = __shfl_sync(kAll, len, r);
-        if (n >= 0) add(r0 + r, -1, f, (n + step - 1) & -step, true, true);
+        if (n >= 0) add(r0 + r, -1, f, n, true, true);
       }
       return;
     }
   }
   for (int r = 0; r < rows; ++r) {
-    const Item it = item_at(a, t, at + r);
+    const Item it = item_at<WHOLE>(a, t, at + r);
     if (!it.some) continue;
     int e = it.e0;
     do {
-      const int cnt = min(a.sub, it.e1 - e);
+      const int cnt = WHOLE ? it.e1 - e : min(a.sub, it.e1 - e);
       load_ends(a, sm, e, cnt);
       for (int i = t.lane; i < cnt; i += 32) sm.bucket[i] = a.eid[e + i];
       __syncwarp();
       fetch(cnt);
-      add(it.row, it.index, 0, cnt, e == it.e0, t.one && e + cnt >= it.e1);
+      add(it.row, it.index, 0, cnt, WHOLE || e == it.e0, WHOLE || (t.one && e + cnt >= it.e1));
       e += cnt;
-    } while (e < it.e1);
+    } while (!WHOLE && e < it.e1);
     if (!t.one) {
       const auto finish = [&](int c, A x) {   // element c of (gk, gv)
         if (it.index >= 0) (static_cast<A*>(a.part) + int64_t(it.index) * a.part_ld)[c] = x;
@@ -1315,23 +1333,32 @@ cudaError_t at_run(void (*kernel)(P...), const AtArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// kernel(V, G, CB) for the call's vectors; turn: those of values that a lane holds at once
+// kernel(V, G, CB, WHOLE) for the call's vectors; turn: those of values that a lane holds at once.  Kernels for whole rows
+// are built where most calls go: wide vectors, heads with keys of their own, no FP64.
 template <typename S, typename F>
 auto at_variant(const AtArgs& a, int turn, F&& f) {
   const std::integral_constant<int, 1> one{};
   const std::integral_constant<int, 2> two{};
   const std::integral_constant<int, 3> three{};
   const std::integral_constant<int, 4> four{};
-  const auto with = [&](auto v) {
-    if (a.four) {
-      if constexpr (kShort<decltype(v)::value, 4> == 2) {
-        if (turn == 2) return f(v, four, two);
-      }
-      return f(v, four, one);
-    }
-    return turn == 1 ? f(v, one, one) : turn == 2 ? f(v, one, two) : turn == 3 ? f(v, one, three) : f(v, one, four);
+  const std::false_type any{};
+  const auto turns = [&](auto v, auto w) {
+    return turn == 1 ? f(v, one, one, w) : turn == 2 ? f(v, one, two, w) : turn == 3 ? f(v, one, three, w) : f(v, one, four, w);
   };
-  if (a.qk.vec == 1) return f(one, one, four);
+  const auto with = [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    if (a.four) {
+      if constexpr (kShort<V, 4> == 2) {
+        if (turn == 2) return f(v, four, two, any);
+      }
+      return f(v, four, one, any);
+    }
+    if constexpr (V == kWide<S> && sizeof(S) < 8) {
+      if (a.whole) return turns(v, std::true_type());
+    }
+    return turns(v, any);
+  };
+  if (a.qk.vec == 1) return f(one, one, four, any);
   if constexpr (kWide<S> == 8) {
     if (a.qk.vec == 4) return with(four);
   }
@@ -1340,12 +1367,12 @@ auto at_variant(const AtArgs& a, int turn, F&& f) {
 
 #define CGTP_AT_FORWARD(suffix, S, R, A)                                                                                     \
   cudaError_t at_forward_##suffix(const AtArgs& a, cudaStream_t st) {                                                        \
-    return at_variant<S>(a, a.vv.turn, [&](auto v, auto g, auto cb) {                                                        \
-      return at_run(attn_forward_kernel<S, R, A, decltype(v)::value, decltype(g)::value, decltype(cb)::value>, a, st);       \
+    return at_variant<S>(a, a.vv.turn, [&](auto v, auto g, auto cb, auto w) {                                                \
+      return at_run(attn_forward_kernel<S, R, A, decltype(v)::value, decltype(g)::value, decltype(cb)::value, decltype(w)::value>, a, st); \
     });                                                                                                                      \
   }                                                                                                                          \
   cudaError_t at_weights_##suffix(const AtArgs& a, cudaStream_t st) {                                                        \
-    return at_variant<S>(a, 1, [&](auto v, auto g, auto) {                                                                   \
+    return at_variant<S>(a, 1, [&](auto v, auto g, auto, auto) {                                                             \
       return at_run(attn_weights_kernel<S, A, decltype(v)::value, decltype(g)::value>, a, st);                               \
     });                                                                                                                      \
   }                                                                                                                          \
@@ -1362,15 +1389,17 @@ auto at_variant(const AtArgs& a, int turn, F&& f) {
     return at_launch(attn_edge_rows_backward_kernel<S, A>, dim3(a.grid), dim3(256), 0, st, a);                               \
   }                                                                                                                          \
   cudaError_t at_receive_##suffix(const AtArgs& a, bool edges, cudaStream_t st) {                                            \
-    return at_variant<S>(a, edges ? 1 : a.vv.dot_turn, [&](auto v, auto g, auto cb) {                                        \
+    return at_variant<S>(a, edges ? 1 : a.vv.dot_turn, [&](auto v, auto g, auto cb, auto w) {                                \
       constexpr int V = decltype(v)::value, G = decltype(g)::value, CB = decltype(cb)::value;                                \
-      return at_run(edges ? attn_receive_kernel<S, R, A, V, G, 1, true> : attn_receive_kernel<S, R, A, V, G, CB, false>, a, st); \
+      constexpr bool W = decltype(w)::value;                                                                                 \
+      return at_run(edges ? attn_receive_kernel<S, R, A, V, G, 1, true, false> : attn_receive_kernel<S, R, A, V, G, CB, false, W>, a, st); \
     });                                                                                                                      \
   }                                                                                                                          \
   cudaError_t at_send_##suffix(const AtArgs& a, bool values, cudaStream_t st) {                                              \
-    return at_variant<S>(a, values ? a.vv.turn : 1, [&](auto v, auto, auto cb) {                                             \
-      constexpr int V = decltype(v)::value, CB = decltype(cb)::value;                                                        \
-      return at_run(values ? attn_send_kernel<S, R, A, V, CB, true> : attn_send_kernel<S, R, A, V, 1, false>, a, st);        \
+    return at_variant<S>(a, values ? a.vv.turn : 1, [&](auto v, auto g, auto cb, auto w) {                                   \
+      constexpr int V = decltype(v)::value, G = decltype(g)::value, CB = decltype(cb)::value;                                \
+      constexpr bool W = decltype(w)::value;                                                                                 \
+      return at_run(values ? attn_send_kernel<S, R, A, V, G, CB, true, W> : attn_send_kernel<S, R, A, V, G, 1, false, false>, a, st); \
     });                                                                                                                      \
   }                                                                                                                          \
   cudaError_t at_join_sum_##suffix(const AtArgs& a, const AtRows& out, int width, int at, int stride, cudaStream_t st) {     \
