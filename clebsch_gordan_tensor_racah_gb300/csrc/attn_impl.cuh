@@ -1242,32 +1242,37 @@ __global__ void __launch_bounds__(512) attn_table_kernel(const __grid_constant__
   for (int i = threadIdx.x; i < a.n_borders; i += blockDim.x) borders[i] = static_cast<const A*>(a.borders)[i];
   __syncthreads();
   const int slots = a.heads < 32 ? 32 / a.heads : 1;
-  const int h0 = a.heads < 32 ? lane % a.heads : lane, s = a.heads < 32 ? lane / a.heads : 0;
-  const int64_t step = int64_t(gridDim.x) * warps_here * slots, first = (int64_t(blockIdx.x) * warps_here + w) * slots + s;
+  const int h0 = a.heads < 32 ? lane % a.heads : lane, s = a.heads < 32 ? lane / a.heads : 32;
+  const int steps = (32 + slots - 1) / slots;
   const A *lengths = static_cast<const A*>(a.lengths), *ds = static_cast<const A*>(a.hist_from);
-  constexpr int U = 4;
-  if (s < slots)
-    for (int64_t e = first; e < a.n_edges; e += U * step) {
-      A r[U], d[U][2];
+  // a warp takes 32 edges at a time, finds a bucket a lane, and then adds `slots` edges a step
+  for (int64_t e0 = (int64_t(blockIdx.x) * warps_here + w) * 32; e0 < a.n_edges; e0 += int64_t(gridDim.x) * warps_here * 32) {
+    const int n = static_cast<int>(min(int64_t(32), a.n_edges - e0));
+    const int mine = lane < n ? bucket_of(borders, a.n_borders, lengths[e0 + lane]) * cols : 0;
+    const A* from = ds + e0 * a.heads * a.hist_step;
+    constexpr int U = 4;
+#pragma unroll 1
+    for (int k = 0; k < steps; k += U) {
+      A d[U][2];
+      int at[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t at = e + u * step;
-        r[u] = 0;
+        // (lanes beyond the last whole edge of a step have none; with 32 heads or more every lane has the step's edge)
+        const int i = a.heads < 32 ? (k + u) * slots + s : k + u;
+        const bool on = i < n && (a.heads >= 32 || s < slots);
+        at[u] = __shfl_sync(kAll, mine, i & 31);
         d[u][0] = d[u][1] = 0;
-        if (at < a.n_edges) {
-          r[u] = lengths[at];
-          if (h0 < a.heads) d[u][0] = ds[(at * a.heads + h0) * a.hist_step];
-          if (h0 + 32 < a.heads) d[u][1] = ds[(at * a.heads + h0 + 32) * a.hist_step];
-        }
+        if (on && h0 < a.heads) d[u][0] = from[(i * a.heads + h0) * a.hist_step];
+        if (on && h0 + 32 < a.heads) d[u][1] = from[(i * a.heads + h0 + 32) * a.hist_step];
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (e + u * step >= a.n_edges) continue;
-        A* at = hist + bucket_of(borders, a.n_borders, r[u]) * cols + lane;
-        at[0] += d[u][0];
-        if (cols > 32) at[32] += d[u][1];
+        A* to = hist + at[u] + lane;
+        to[0] += d[u][0];
+        if (cols > 32) to[32] += d[u][1];
       }
     }
+  }
   __syncthreads();
   // columns of a head: lanes h, h + heads, ... of each block of 32, over all warps (buckets start at different ones, so
   // that they read different banks)
@@ -1335,7 +1340,8 @@ cudaError_t at_run(void (*kernel)(P...), const AtArgs& a, cudaStream_t st) {
 
 // kernel(V, G, CB, WHOLE) for the call's vectors; turn: those of values that a lane holds at once.  Kernels for whole rows
 // are built where most calls go: wide vectors, heads with keys of their own, no FP64.
-template <typename S, typename F>
+// (FOUR: also where four heads share keys, for the sources, whose rows are short there.)
+template <typename S, bool FOUR, typename F>
 auto at_variant(const AtArgs& a, int turn, F&& f) {
   const std::integral_constant<int, 1> one{};
   const std::integral_constant<int, 2> two{};
@@ -1347,12 +1353,16 @@ auto at_variant(const AtArgs& a, int turn, F&& f) {
   };
   const auto with = [&](auto v) {
     constexpr int V = decltype(v)::value;
-    if (a.four) {
+    const auto shared = [&](auto w) {
       if constexpr (kShort<V, 4> == 2) {
-        if (turn == 2) return f(v, four, two, any);
+        if (turn == 2) return f(v, four, two, w);
       }
-      return f(v, four, one, any);
+      return f(v, four, one, w);
+    };
+    if constexpr (FOUR && V == kWide<S> && sizeof(S) < 8) {
+      if (a.four && a.whole) return shared(std::true_type());
     }
+    if (a.four) return shared(any);
     if constexpr (V == kWide<S> && sizeof(S) < 8) {
       if (a.whole) return turns(v, std::true_type());
     }
@@ -1367,12 +1377,12 @@ auto at_variant(const AtArgs& a, int turn, F&& f) {
 
 #define CGTP_AT_FORWARD(suffix, S, R, A)                                                                                     \
   cudaError_t at_forward_##suffix(const AtArgs& a, cudaStream_t st) {                                                        \
-    return at_variant<S>(a, a.vv.turn, [&](auto v, auto g, auto cb, auto w) {                                                \
+    return at_variant<S, false>(a, a.vv.turn, [&](auto v, auto g, auto cb, auto w) {                                                \
       return at_run(attn_forward_kernel<S, R, A, decltype(v)::value, decltype(g)::value, decltype(cb)::value, decltype(w)::value>, a, st); \
     });                                                                                                                      \
   }                                                                                                                          \
   cudaError_t at_weights_##suffix(const AtArgs& a, cudaStream_t st) {                                                        \
-    return at_variant<S>(a, 1, [&](auto v, auto g, auto, auto) {                                                             \
+    return at_variant<S, false>(a, 1, [&](auto v, auto g, auto, auto) {                                                             \
       return at_run(attn_weights_kernel<S, A, decltype(v)::value, decltype(g)::value>, a, st);                               \
     });                                                                                                                      \
   }                                                                                                                          \
@@ -1389,14 +1399,14 @@ auto at_variant(const AtArgs& a, int turn, F&& f) {
     return at_launch(attn_edge_rows_backward_kernel<S, A>, dim3(a.grid), dim3(256), 0, st, a);                               \
   }                                                                                                                          \
   cudaError_t at_receive_##suffix(const AtArgs& a, bool edges, cudaStream_t st) {                                            \
-    return at_variant<S>(a, edges ? 1 : a.vv.dot_turn, [&](auto v, auto g, auto cb, auto w) {                                \
+    return at_variant<S, false>(a, edges ? 1 : a.vv.dot_turn, [&](auto v, auto g, auto cb, auto w) {                                \
       constexpr int V = decltype(v)::value, G = decltype(g)::value, CB = decltype(cb)::value;                                \
       constexpr bool W = decltype(w)::value;                                                                                 \
       return at_run(edges ? attn_receive_kernel<S, R, A, V, G, 1, true, false> : attn_receive_kernel<S, R, A, V, G, CB, false, W>, a, st); \
     });                                                                                                                      \
   }                                                                                                                          \
   cudaError_t at_send_##suffix(const AtArgs& a, bool values, cudaStream_t st) {                                              \
-    return at_variant<S>(a, values ? a.vv.turn : 1, [&](auto v, auto g, auto cb, auto w) {                                   \
+    return at_variant<S, true>(a, values ? a.vv.turn : 1, [&](auto v, auto g, auto cb, auto w) {                                   \
       constexpr int V = decltype(v)::value, G = decltype(g)::value, CB = decltype(cb)::value;                                \
       constexpr bool W = decltype(w)::value;                                                                                 \
       return at_run(values ? attn_send_kernel<S, R, A, V, G, CB, true, W> : attn_send_kernel<S, R, A, V, G, 1, false, false>, a, st); \
