@@ -10,12 +10,23 @@
 // A logit of -infinity leaves its edge out: a weight of zero takes nothing from its edge's rows, whatever they hold.
 //
 // Split.  A warp takes a row (or a run of its edges; several warps of a CTA share a row where rows are few) and holds
-// `sub` edges at once, so that no barrier stands between the steps of a row.  Its lanes are (edge, head, lane of the
-// head): the vectors of a head's queries or results stay in registers while the edges pass, a dot product needs
-// the shuffles of one head's lanes only, and every gathered row is read in whole sectors.  The receivers' kernel of
-// the backward writes ds and a (edges x heads); the sources' kernel, over the transpose, only gathers and adds.  Rows
-// longer than the graph's chunk are cut into items whose partial results another launch joins in a fixed order.
-// Edge rows, which are most of their bytes, pass through kernels of their own that know nothing of the graph.
+// `sub` edges at once, so that no barrier stands between the steps of a row.  For dot products its lanes are (edge, head,
+// lane of the head): the vectors of a head's queries stay in registers while the edges pass, four edges a lane share the
+// exchanges that sum over a head's lanes.  For sums over edges its lanes are the vectors of a row in the order of memory,
+// so that a row is read in whole lines and no lane talks to another.  The receivers' kernel of the backward writes ds and
+// a (edges x heads); the sources' kernel, over the transpose, only gathers and adds.  Rows longer than the graph's chunk
+// are cut into items whose partial results another launch joins in a fixed order.  Edge rows, which are most of
+// their bytes, pass through kernels of their own that know nothing of the graph.
+//
+// What bounds them.  An edge's rows of k and v have no reuse within a row of the graph, so each comes from L2 (or HBM)
+// to the SM once an edge: 10,000 x 32 edges of 2.3 KB are 737 MB, 40 us at the 64 bytes a clock that an SM takes in, and
+// the forward takes 51 us (14.3 TB/s).  bfloat16 rows halve the bytes and not the arithmetic (an element costs one
+// instruction to widen and one to add), so those are bound by instructions: 105 warp instructions an edge of 832
+// elements and 1,400 a row, 1.6 M edges in 396 us.  With 24 warps an SM (80 registers a thread, three CTAs of 256)
+// and two to four edges in flight a lane both ends are balanced: 32 warps with half the edges in flight
+// take 55 us and 430 us, 16 warps with twice as many 57 us and 435 us.  Tried and dropped: rows by bulk copies into
+// shared memory (101 us; a copy costs a warp 18 instructions, and every byte passes shared memory twice), by cp.async (92
+// us), rows fetched ahead into L2 (520 us of 397 us where the sources are 333 MB).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -597,10 +608,18 @@ __device__ __forceinline__ void each_pair(const AtArgs& a, int cnt, F&& f) {
   }
 }
 
+// A row that a warp will read soon, on its way to its SM.
+template <typename S>
+__device__ __forceinline__ void ahead(const S* row, int elements) {
+  for (int i = (threadIdx.x & 31) * (128 / int(sizeof(S))); i < elements; i += 32 * (128 / int(sizeof(S))))
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(row + i));
+}
+
 // Logits of the edges [e, e + cnt) of `row` into z.
 template <int V, int G, typename S, typename A>
 __device__ __forceinline__ void logits(const AtArgs& a, const Smem<A>& sm, int row, int e, int cnt) {
-  // (the biases of the run are on their way while the ends and lengths arrive)
+  // (the row's queries and the biases of the run are on their way while the ends and lengths arrive)
+  ahead(reinterpret_cast<const S*>(a.q.p) + int64_t(row) * a.q.ld, a.heads * a.dk);
   const int far = (threadIdx.x & 31) * (128 / int(sizeof(A)));
   if (a.bias && far < cnt * a.heads)
     asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const A*>(a.bias) + int64_t(e) * a.heads + far));
@@ -998,6 +1017,7 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const _
         if (EDGES) {
           fetch(e, cnt);
         } else {
+          ahead(reinterpret_cast<const S*>(a.gout.p) + int64_t(it.row) * a.gout.ld, a.heads * a.dv);
           logits<V, G, S>(a, sm, it.row, e, cnt);
           const A* lse = static_cast<const A*>(a.lse) + int64_t(it.row) * a.heads;
           each_pair(a, cnt, [&](int at, int, int h, int) {
