@@ -501,3 +501,25 @@ def test_attention_on_the_weights_of_a_convolution(dtype):
                 ds, oat.buckets(lengths.cpu().numpy(), np.float32(c.attention_borders(8, 1.0, 5.0))), 8))
     for got, ref in zip((gq, gk, gw, gtable), want):
         assert np.abs(_num(got) - ref).max() <= 1e-4 * np.abs(ref).max()
+
+
+@pytest.mark.parametrize("hubs", [False, True])
+@pytest.mark.parametrize("shape,kind", [(("16x0e", "4x0e+4x1o", 4, 4), "f32"), (("8x0e", "8x0e+8x1o", 4, 4), "bf16s"),
+                                        (("8x0e+8x1o", "8x0e+8x1o+8x2e", 2, 2), "bf16"), (("4x0e", "4x0e", 8, 2), "f32"),
+                                        (("3x0e", "1x1o", 2, 1), "f32"), (("4x0e", "2x0e", 3, 3), "f64")], ids=str)
+def test_many_sources_of_few_edges(shape, kind, hubs):
+    """Enough rows of both sides for one warp each, sources side by side; with hubs, whose rows are cut, and rows of more
+    edges than a warp holds at once, on both sides."""
+    rng = np.random.default_rng(24)
+    deg = rng.poisson(14, 3000)
+    deg[::50] = 0
+    if hubs:
+        deg[7], deg[8], deg[2999] = 700, 64, 90
+    c = Case(shape, kind, deg, m=60000, seed=24)
+    if hubs:
+        c.col[100:900], c.col[1000:1060], c.col[2000:2050] = 59999, 5, 6
+    c.col[3000:3012] = 7
+    c.graph = cg().Graph(_dev(c.rowptr, torch.int32), _dev(c.col, torch.int32), c.n, n_src=c.m)
+    c.check(["fwd", "bwd"])
+    first = [t.clone() for t in c.run("bwd")]
+    assert all(torch.equal(a, b) for a, b in zip(first, c.run("bwd")))
