@@ -408,6 +408,14 @@ cgtp_status logit_terms(const cgtp_attn_s* p, const cgtp_graph_s* g, const void*
   return CGTP_OK;
 }
 
+// columns of a warp's histogram of the bias table, whose gradient needs one in shared memory
+int hist_cols(const cgtp_attn_s* p) { return p->heads <= 32 ? 32 : 64; }
+cgtp_status check_table(const cgtp_attn_s* p, const void* gtable) {
+  if (gtable && (int64_t(p->n_borders + 1) * hist_cols(p) + p->n_borders) * es_acc(p) > p->smem_cap)
+    return fail(CGTP_EUNSUPPORTED, "gtable: FP64 plans of more than 32 heads have room for 446 borders");
+  return CGTP_OK;
+}
+
 // gradients of keys (and values), and of the table, from a and ds
 cgtp_status finish_backward(const cgtp_attn_s* p, const cgtp_graph_s* g, AtArgs a, bool values, cudaStream_t st) {
   cgtp_status s;
@@ -427,9 +435,8 @@ cgtp_status finish_backward(const cgtp_attn_s* p, const cgtp_graph_s* g, AtArgs 
   }
   // Two CTAs an SM, of up to sixteen warps where their histograms fit twice; a CTA for each 2048 values, one where that
   // saves the second launch.
-  a.hist_cols = p->heads <= 32 ? 32 : 64;
-  const int64_t one = int64_t(p->n_borders + 1) * a.hist_cols * es_acc(p), room = p->smem_cap - p->n_borders * es_acc(p);
-  if (one > room) return fail(CGTP_EUNSUPPORTED, "bias table too large for shared memory");
+  a.hist_cols = hist_cols(p);
+  const int64_t one = int64_t(p->n_borders + 1) * a.hist_cols * es_acc(p);
   a.hist_warps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, (p->smem_cap / 2 - 1024 - p->n_borders * es_acc(p)) / one)));
   a.hist_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(hist_ctas(p), g->E * p->heads / 2048)));
   a.hist_from = values ? a.pairs : a.ds;
@@ -570,7 +577,7 @@ cgtp_status cgtp_attn_backward(cgtp_attn p, cgtp_graph g, const void* gout, int6
   if ((s = check(&tq, &a.q)) || (s = check(&tk, &a.k)) || (s = check(&tv, &a.v)) || (s = check(&tg, &a.gout)) || (s = check(&tgq, &a.gq)) ||
       (s = check(&tgk, &a.gk)) || (s = check(&tgv, &a.gv)) || (s = check_vector(lse, ea, true, "lse")) ||
       (s = check_vector(gtable, ea, false, "gtable")) || (s = check_vector(gbias, ea, false, "gbias")) ||
-      (s = logit_terms(p, g, lengths, table, bias, &a)))
+      (s = logit_terms(p, g, lengths, table, bias, &a)) || (s = check_table(p, gtable)))
     return s;
   if (gtable && !table) return fail(CGTP_EINVAL, "gtable needs table");
   const Space sp = space(p, g, CGTP_ATTN_BACKWARD);
@@ -642,7 +649,7 @@ cgtp_status cgtp_attn_edges_backward(cgtp_attn p, cgtp_graph g, const void* gout
   if ((s = check(&tq, &a.q)) || (s = check(&tk, &a.k)) || (s = check(&tw, &a.v)) || (s = check(&tg, &a.gout)) || (s = check(&tgq, &a.gq)) ||
       (s = check(&tgk, &a.gk)) || (s = check(&tgw, &a.gv)) || (s = check_vector(alpha, ea, g->E > 0, "alpha")) ||
       (s = check_vector(lengths, ea, gtable && g->E > 0, "lengths")) || (s = check_vector(gtable, ea, false, "gtable")) ||
-      (s = check_vector(gbias, ea, false, "gbias")))
+      (s = check_vector(gbias, ea, false, "gbias")) || (s = check_table(p, gtable)))
     return s;
   if (gtable && p->n_borders == 0) return fail(CGTP_EINVAL, "gtable needs a plan with borders");
   const Space sp = space(p, g, CGTP_ATTN_EDGES_BACKWARD);

@@ -81,7 +81,8 @@ cgtp_status cgtp_attn_forward(cgtp_attn plan, cgtp_graph graph, const void* q, i
 /*
  * cgtp_attn_backward -- adjoint for gout [N, heads*dim_v], from the inputs and lse of the forward.
  *  gq, gk, gv as q, k, v (every row is written: zeros for nodes without edges).
- *  gtable [n_borders+1, heads] : NULL, or wanted (needs table).  gbias [E, heads] : NULL, or wanted (bias need not
+ *  gtable [n_borders+1, heads] : NULL, or wanted (needs table; CGTP_F64 plans of more than 32 heads: at most 446
+ *      borders).  gbias [E, heads] : NULL, or wanted (bias need not
  *      be given: it is the gradient of the logits).
  *  Lengths have no gradient: the table is constant within a bucket.  All sums are taken in a fixed order.
  */

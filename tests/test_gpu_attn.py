@@ -9,8 +9,8 @@ Tolerances.  u = 2^-24 (FP32) or 2^-53 (FP64), all in units of the sums of magni
   dp: (dv + 2) u G, G = sum |gout v|; D = sum a dp: relative to Gm = sum a G.  ds = a (dp - D):
      Kd = Kp + dv + deg + 12 times u a (G + Gm), and |ds| <= a (G + Gm).
   gq, gk: (Kd + deg + 6) u scale sum a (G + Gm) |k| or |q|, deg the longest row of either side times the heads of
-     a group; gv: (Kp + deg + 4) u sum a |gout|; table: at most 128 values a lane are added in the arithmetic's type,
-     the rest in FP64: (Kd + 128) u sum a (G + Gm).
+     a group; gv: (Kp + deg + 4) u sum a |gout|; table: at most 80 values of a lane and 48 columns of its CTA are added in
+     the arithmetic's type, the CTAs in FP64: (Kd + 128) u sum a (G + Gm).
 Results stored in bfloat16 add half a step, 2^-8 of the value.
 """
 
@@ -523,3 +523,14 @@ def test_many_sources_of_few_edges(shape, kind, hubs):
     c.check(["fwd", "bwd"])
     first = [t.clone() for t in c.run("bwd")]
     assert all(torch.equal(a, b) for a, b in zip(first, c.run("bwd")))
+
+
+@pytest.mark.parametrize("edges", [False, True])
+def test_the_largest_tables(edges):
+    ops = ["efwd", "ebwd"] if edges else ["fwd", "bwd"]
+    for heads, borders, kind in ((33, 446, "f64"), (64, 511, "f32"), (32, 511, "f64")):
+        Case(("2x0e", "2x0e", heads, heads), kind, "mixed", n=12, borders=borders, seed=25, edges=edges).check(ops)
+    c = Case(("2x0e", "2x0e", 33, 33), "f64", "mixed", n=12, borders=447, seed=25, edges=edges)
+    c.check(ops[:1])
+    with pytest.raises(cg().CgtpError, match="446 borders"):
+        c.run(ops[1])
