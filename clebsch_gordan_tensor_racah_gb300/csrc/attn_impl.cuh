@@ -1143,6 +1143,14 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_send_kernel(const __gr
   // sums over cnt places from `from`, for the row (or the item, where it is a piece of a row)
   const auto add = [&](int row, int item, int from, int cnt, bool first, bool last) {
     const bool part = !WHOLE && item >= 0;
+    if (cnt == 0 && first && last && !part) {   // a source without edges
+      Pack<R, V> zeros;
+      zeros.clear();
+      for (int c = t.lane * V; c < a.kv * a.dk; c += 32 * V) zeros.store(reinterpret_cast<R*>(a.gk.p) + int64_t(row) * a.gk.ld + c);
+      if (VALUES)
+        for (int c = t.lane * V; c < a.kv * a.dv; c += 32 * V) zeros.store(reinterpret_cast<R*>(a.gv.p) + int64_t(row) * a.gv.ld + c);
+      return;
+    }
     A* to_part = static_cast<A*>(a.part) + int64_t(item) * a.part_ld;
     const auto store = [&](R* to, int at0) {
       return [=](int, int at, const A* r) {
