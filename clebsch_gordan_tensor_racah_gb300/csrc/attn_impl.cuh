@@ -20,13 +20,13 @@
 //
 // What bounds them.  An edge's rows of k and v have no reuse within a row of the graph, so each comes from L2 (or HBM)
 // to the SM once an edge: 10,000 x 32 edges of 2.3 KB are 737 MB, 40 us at the 64 bytes a clock that an SM takes in, and
-// the forward takes 51 us (14.3 TB/s).  bfloat16 rows halve the bytes and not the arithmetic (an element costs one
+// the forward takes 51 us (14.5 TB/s).  bfloat16 rows halve the bytes and not the arithmetic (an element costs one
 // instruction to widen and one to add), so those are bound by instructions: 105 warp instructions an edge of 832
-// elements and 1,400 a row, 1.6 M edges in 396 us.  With 24 warps an SM (80 registers a thread, three CTAs of 256)
+// elements and 1,400 a row, 1.6 M edges in 391 us.  With 24 warps an SM (80 registers a thread)
 // and two to four edges in flight a lane both ends are balanced: 32 warps with half the edges in flight
-// take 55 us and 430 us, 16 warps with twice as many 57 us and 435 us.  Tried and dropped: rows by bulk copies into
+// take 55 us and 430 us, 16 warps with twice as many 57 us and 435 us (of 51 and 396).  Tried and dropped: rows by bulk copies into
 // shared memory (101 us; a copy costs a warp 18 instructions, and every byte passes shared memory twice), by cp.async (92
-// us), rows fetched ahead into L2 (520 us of 397 us where the sources are 333 MB).
+// us), rows fetched ahead into L2 (520 us of 452 us then, where the sources are 333 MB).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -543,7 +543,7 @@ __device__ __forceinline__ void short_sums(const AtArgs& a, const AtTab& tab, P&
   else sums<V, kShort<V, G>, G, SEND, APART, S>(a, tab, x...);
 }
 
-// CTAs of 256 threads that an SM is to hold: registers bound the edges in flight.
+// Groups of 256 threads that an SM is to hold (24 or 16 warps): registers bound the edges in flight.
 template <int G>
 constexpr int kResident = G == 1 ? 3 : 2;
 
