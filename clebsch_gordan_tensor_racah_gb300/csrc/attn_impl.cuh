@@ -56,7 +56,6 @@ template <>
 __device__ __forceinline__ float narrow<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ bf16 narrow<bf16>(float x) { return __float2bfloat16_rn(x); }
-__device__ __forceinline__ double narrow_d(double x) { return x; }
 
 template <int BYTES>
 struct Raw;
@@ -212,8 +211,8 @@ __device__ __forceinline__ void with_width(int v, F&& f) {
 constexpr unsigned kAll = 0xffffffffu;
 
 // One warp a row, or all warps of the CTA.  Kernels with WHOLE are those of launches in which every row is one run of one
-// warp (AtArgs::whole): what joins runs, warps and pieces of rows drops out of them, which is a third of a row's
-// fixed cost.
+// warp (AtArgs::whole): what joins runs, warps and pieces of rows drops out of them (10,000 x 32
+// edges forward 54 -> 51 us, 50,001 x 32 in bfloat16 452 -> 397 us).
 struct Team {
   bool one;
   int w, warps, lane;   // this warp among the row's
@@ -289,7 +288,7 @@ struct Smem {
   A *z, *p, *stat, *acc;
   int *idx, *bucket;
   __device__ __forceinline__ Smem(const AtArgs& a, int warp) {
-    extern __shared__ __align__(128) char at_smem[];
+    extern __shared__ __align__(16) char at_smem[];
     char* s = at_smem + warp * a.warp_smem;
     z = reinterpret_cast<A*>(s);
     p = reinterpret_cast<A*>(s + a.at_p);
@@ -704,54 +703,52 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_forward_kernel(const _
   const int width = a.heads * a.dv;
   const Item it = item_of<WHOLE>(a, t);
   if (!it.some) return;
-  {
-    const bool part = it.index >= 0;
-    A* to_part = static_cast<A*>(a.part) + int64_t(it.index) * a.part_ld;
-    R* out = reinterpret_cast<R*>(a.out.p) + int64_t(it.row) * a.out.ld;
-    int e = it.e0;
-    do {
-      const int cnt = WHOLE ? it.e1 - e : min(a.sub, it.e1 - e);
-      const bool first = WHOLE || e == it.e0, last = WHOLE || e + cnt >= it.e1;
-      logits<V, G, S>(a, sm, it.row, e, cnt);
-      softmax_step(a, sm, cnt, first, false);
-      sums<V, CB, G, false, false, S>(a, a.vv, cnt, sm.z, a.v, sm.idx, sm.acc, sm.stat + 2 * a.heads, first, t.one && last,
-                  [&](int h, int at, const A* r) {
-                    if (part) {
-                      store_as<V>(to_part + at, r);
-                    } else {
-                      const A l = sm.stat[a.heads + h], f = l == 0 ? A(0) : A(1) / l;
-                      Pack<R, V> y;
+  const bool part = it.index >= 0;
+  A* to_part = static_cast<A*>(a.part) + int64_t(it.index) * a.part_ld;
+  R* out = reinterpret_cast<R*>(a.out.p) + int64_t(it.row) * a.out.ld;
+  int e = it.e0;
+  do {
+    const int cnt = WHOLE ? it.e1 - e : min(a.sub, it.e1 - e);
+    const bool first = WHOLE || e == it.e0, last = WHOLE || e + cnt >= it.e1;
+    logits<V, G, S>(a, sm, it.row, e, cnt);
+    softmax_step(a, sm, cnt, first, false);
+    sums<V, CB, G, false, false, S>(a, a.vv, cnt, sm.z, a.v, sm.idx, sm.acc, sm.stat + 2 * a.heads, first, t.one && last,
+                [&](int h, int at, const A* r) {
+                  if (part) {
+                    store_as<V>(to_part + at, r);
+                  } else {
+                    const A l = sm.stat[a.heads + h], f = l == 0 ? A(0) : A(1) / l;
+                    Pack<R, V> y;
 #pragma unroll
-                      for (int k = 0; k < V; ++k) y.e[k] = to<R>(r[k] * f);
-                      y.store(out + at);
-                    }
-                  });
-      e += cnt;
-    } while (!WHOLE && e < it.e1);
-    const Smem<A> one(a, t.one ? threadIdx.x / 32 : 0);
-    if (!t.one) {
-      join_warps<A>(a, t);
-      for (int c = t.thread(); c < width; c += t.threads()) {
-        const int h = a.vv.acc[c / a.vv.vec] >> kAtHeadShift;
-        A r = 0;
-        for (int w = 0; w < t.warps; ++w) {
-          const Smem<A> other(a, w);
-          const A f = other.stat[2 * a.heads + h];
-          if (f != 0) r += f * other.acc[c];
-        }
-        const A l = one.stat[a.heads + h];
-        if (part) to_part[c] = r;
-        else out[c] = to<R>(l == 0 ? A(0) : r / l);
+                    for (int k = 0; k < V; ++k) y.e[k] = to<R>(r[k] * f);
+                    y.store(out + at);
+                  }
+                });
+    e += cnt;
+  } while (!WHOLE && e < it.e1);
+  const Smem<A> one(a, t.one ? threadIdx.x / 32 : 0);
+  if (!t.one) {
+    join_warps<A>(a, t);
+    for (int c = t.thread(); c < width; c += t.threads()) {
+      const int h = a.vv.acc[c / a.vv.vec] >> kAtHeadShift;
+      A r = 0;
+      for (int w = 0; w < t.warps; ++w) {
+        const Smem<A> other(a, w);
+        const A f = other.stat[2 * a.heads + h];
+        if (f != 0) r += f * other.acc[c];
       }
+      const A l = one.stat[a.heads + h];
+      if (part) to_part[c] = r;
+      else out[c] = to<R>(l == 0 ? A(0) : r / l);
     }
-    for (int h = t.thread(); h < a.heads; h += t.threads()) {
-      const A top = one.stat[h], l = one.stat[a.heads + h];
-      if (part) {
-        to_part[width + h] = top;
-        to_part[width + a.heads + h] = l;
-      } else {
-        static_cast<A*>(a.lse)[int64_t(it.row) * a.heads + h] = loga(l) + (top == lowest<A>() ? A(0) : top);
-      }
+  }
+  for (int h = t.thread(); h < a.heads; h += t.threads()) {
+    const A top = one.stat[h], l = one.stat[a.heads + h];
+    if (part) {
+      to_part[width + h] = top;
+      to_part[width + a.heads + h] = l;
+    } else {
+      static_cast<A*>(a.lse)[int64_t(it.row) * a.heads + h] = loga(l) + (top == lowest<A>() ? A(0) : top);
     }
   }
 }
@@ -819,58 +816,56 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_weights_kernel(const _
   A* alpha = static_cast<A*>(a.alpha);
   const Item it = item_of<false>(a, t);
   if (!it.some) return;
-  {
-    const bool held = t.one && it.index < 0 && it.e1 - it.e0 <= a.sub;
-    if (a.phase != kAtSecond) {
-      int e = it.e0;
-      do {
-        const int cnt = min(a.sub, it.e1 - e);
-        logits<V, G, S>(a, sm, it.row, e, cnt);
-        softmax_step(a, sm, cnt, e == it.e0, !held);
-        if (!held)
-          each_pair(a, cnt, [&](int at, int, int, int k) { alpha[int64_t(e) * a.heads + k] = sm.z[at]; });
-        __syncwarp();
-        e += cnt;
-      } while (e < it.e1);
-      if (!t.one) join_warps<A>(a, t);
-      if (it.index >= 0) {
-        A* part = static_cast<A*>(a.part) + int64_t(it.index) * 2 * a.heads;
-        for (int h = t.thread(); h < 2 * a.heads; h += t.threads()) part[h] = one.stat[h];
-        return;
-      }
-    } else {
-      // statistics of the row from those of its items, by every warp for itself
-      const Int4 join = a.joins[a.items[it.index].w];
-      const A* part = static_cast<const A*>(a.part) + int64_t(join.y) * 2 * a.heads;
-      each_head(a, [&](const HeadLanes& l) {
-        A top = lowest<A>();
-#pragma unroll 8
-        for (int i = l.slot; i < join.z; i += l.slots) top = larger(top, part[int64_t(i) * 2 * a.heads + l.h]);
-        top = all_max(l, top);
-        const A shift = top == lowest<A>() ? A(0) : top;
-        A sum = 0;
-#pragma unroll 4
-        for (int i = l.slot; i < join.z; i += l.slots) {
-          const A* p = part + int64_t(i) * 2 * a.heads + l.h;
-          sum += expo(p[0] - shift) * p[a.heads];
-        }
-        sum = all_sum(l, sum);
-        if (l.on) {
-          sm.stat[l.h] = top;
-          sm.stat[a.heads + l.h] = sum;
-        }
-      });
+  const bool held = t.one && it.index < 0 && it.e1 - it.e0 <= a.sub;
+  if (a.phase != kAtSecond) {
+    int e = it.e0;
+    do {
+      const int cnt = min(a.sub, it.e1 - e);
+      logits<V, G, S>(a, sm, it.row, e, cnt);
+      softmax_step(a, sm, cnt, e == it.e0, !held);
+      if (!held)
+        each_pair(a, cnt, [&](int at, int, int, int k) { alpha[int64_t(e) * a.heads + k] = sm.z[at]; });
       __syncwarp();
+      e += cnt;
+    } while (e < it.e1);
+    if (!t.one) join_warps<A>(a, t);
+    if (it.index >= 0) {
+      A* part = static_cast<A*>(a.part) + int64_t(it.index) * 2 * a.heads;
+      for (int h = t.thread(); h < 2 * a.heads; h += t.threads()) part[h] = one.stat[h];
+      return;
     }
-    const A* stat = a.phase == kAtSecond ? sm.stat : one.stat;
-    const int64_t base = int64_t(it.e0) * a.heads;
-    const int count = it.e1 - it.e0;   // no run is longer than the graph's chunk
-    each_pair(a, count, [&](int at, int, int h, int k) {
-      const A l = stat[a.heads + h], top = stat[h];
-      const A p = held ? sm.z[at] : expo(alpha[base + k] - (top == lowest<A>() ? A(0) : top));
-      alpha[base + k] = p == 0 ? A(0) : p / l;
+  } else {
+    // statistics of the row from those of its items, by every warp for itself
+    const Int4 join = a.joins[a.items[it.index].w];
+    const A* part = static_cast<const A*>(a.part) + int64_t(join.y) * 2 * a.heads;
+    each_head(a, [&](const HeadLanes& l) {
+      A top = lowest<A>();
+#pragma unroll 8
+      for (int i = l.slot; i < join.z; i += l.slots) top = larger(top, part[int64_t(i) * 2 * a.heads + l.h]);
+      top = all_max(l, top);
+      const A shift = top == lowest<A>() ? A(0) : top;
+      A sum = 0;
+#pragma unroll 4
+      for (int i = l.slot; i < join.z; i += l.slots) {
+        const A* p = part + int64_t(i) * 2 * a.heads + l.h;
+        sum += expo(p[0] - shift) * p[a.heads];
+      }
+      sum = all_sum(l, sum);
+      if (l.on) {
+        sm.stat[l.h] = top;
+        sm.stat[a.heads + l.h] = sum;
+      }
     });
+    __syncwarp();
   }
+  const A* stat = a.phase == kAtSecond ? sm.stat : one.stat;
+  const int64_t base = int64_t(it.e0) * a.heads;
+  const int count = it.e1 - it.e0;   // no run is longer than the graph's chunk
+  each_pair(a, count, [&](int at, int, int h, int k) {
+    const A l = stat[a.heads + h], top = stat[h];
+    const A p = held ? sm.z[at] : expo(alpha[base + k] - (top == lowest<A>() ? A(0) : top));
+    alpha[base + k] = p == 0 ? A(0) : p / l;
+  });
 }
 
 // w' = a w: vectors of all rows in the order of memory, four a thread and turn.
@@ -1007,108 +1002,106 @@ __global__ void __launch_bounds__(256, kResident<G>) attn_receive_kernel(const _
     });
     __syncwarp();
   };
-  {
-    const int phase = WHOLE ? int(kAtWhole) : a.phase;
-    const bool held = WHOLE || (it.e1 - it.e0 <= a.sub && phase != kAtSecond);   // z, p and idx hold the whole run
-    if (phase != kAtSecond) {
-      int e = it.e0;
-      do {
-        const int cnt = WHOLE ? it.e1 - e : min(a.sub, it.e1 - e);
-        if (EDGES) {
-          fetch(e, cnt);
-        } else {
-          ahead(reinterpret_cast<const S*>(a.gout.p) + int64_t(it.row) * a.gout.ld, a.heads * a.dv);
-          logits<V, G, S>(a, sm, it.row, e, cnt);
-          const A* lse = static_cast<const A*>(a.lse) + int64_t(it.row) * a.heads;
-          each_pair(a, cnt, [&](int at, int, int h, int) {
-            const A z = sm.z[at];
-            sm.p[at] = z == lowest<A>() ? A(0) : expo(z - lse[h]);
-          });
-          __syncwarp();
-          dots<V, CB, G, false>(a, a.vv, cnt, reinterpret_cast<const S*>(a.gout.p) + int64_t(it.row) * a.gout.ld, a.v, sm.idx, sm.z);
-          if (!held || it.index >= 0)
-            each_pair(a, cnt, [&](int at, int, int, int k) { pairs[int64_t(e) * a.heads + k] = {sm.z[at], sm.p[at]}; });
-        }
-        each_head(a, [&](const HeadLanes& l) {
-          A sum = 0;
-          for (int i = l.slot; i < cnt; i += l.slots) {
-            const A p = sm.p[l.h * a.stride + i];
-            if (p != 0) sum += p * sm.z[l.h * a.stride + i];
-          }
-          sum = all_sum(l, sum);
-          if (l.on) sm.stat[l.h] = (WHOLE || e == it.e0 ? A(0) : sm.stat[l.h]) + sum;
-        });
-        __syncwarp();
-        e += cnt;
-      } while (!WHOLE && e < it.e1);
-      if (!t.one) {
-        __syncthreads();
-        A total[2] = {0, 0};   // heads <= 64, at least 32 threads
-        for (int j = 0; j < 2; ++j)
-          if (t.thread() + j * t.threads() < a.heads)
-            for (int w = 0; w < t.warps; ++w) total[j] += Smem<A>(a, w).stat[t.thread() + j * t.threads()];
-        __syncthreads();
-        for (int j = 0; j < 2; ++j)
-          if (t.thread() + j * t.threads() < a.heads)
-            for (int w = 0; w < t.warps; ++w) Smem<A>(a, w).stat[t.thread() + j * t.threads()] = total[j];
-        __syncthreads();
-      }
-      if (it.index >= 0) {
-        A* part = static_cast<A*>(a.part_sum) + int64_t(it.index) * a.heads;
-        for (int h = t.thread(); h < a.heads; h += t.threads()) part[h] = sm.stat[h];
-        return;
-      }
-    } else {
-      const Int4 join = a.joins[a.items[it.index].w];
-      each_head(a, [&](const HeadLanes& l) {
-        A sum = 0;
-#pragma unroll 8
-        for (int i = l.slot; i < join.z; i += l.slots) sum += static_cast<const A*>(a.part_sum)[int64_t(join.y + i) * a.heads + l.h];
-        sum = all_sum(l, sum);
-        if (l.on) sm.stat[l.h] = sum;
-      });
-      __syncwarp();
-    }
-    const auto finish = [&](int at, A x) {   // one element of gq
-      if (it.index >= 0) static_cast<A*>(a.part)[int64_t(it.index) * a.part_ld + at] = x * scale;
-      else (reinterpret_cast<R*>(a.gq.p) + int64_t(it.row) * a.gq.ld)[at] = to<R>(x * scale);
-    };
+  const int phase = WHOLE ? int(kAtWhole) : a.phase;
+  const bool held = WHOLE || (it.e1 - it.e0 <= a.sub && phase != kAtSecond);   // z, p and idx hold the whole run
+  if (phase != kAtSecond) {
     int e = it.e0;
     do {
       const int cnt = WHOLE ? it.e1 - e : min(a.sub, it.e1 - e);
-      const bool first = WHOLE || e == it.e0, last = WHOLE || e + cnt >= it.e1;
-      if (!held) fetch(e, cnt);
-      each_pair(a, cnt, [&](int at, int, int h, int k) {
-        const A p = sm.p[at], d = p == 0 ? A(0) : p * (sm.z[at] - sm.stat[h]);
-        sm.z[at] = d;
-        if (!EDGES) pairs[int64_t(e) * a.heads + k] = {d, p};
-        if (a.ds) static_cast<A*>(a.ds)[int64_t(e) * a.heads + k] = d;
+      if (EDGES) {
+        fetch(e, cnt);
+      } else {
+        ahead(reinterpret_cast<const S*>(a.gout.p) + int64_t(it.row) * a.gout.ld, a.heads * a.dv);
+        logits<V, G, S>(a, sm, it.row, e, cnt);
+        const A* lse = static_cast<const A*>(a.lse) + int64_t(it.row) * a.heads;
+        each_pair(a, cnt, [&](int at, int, int h, int) {
+          const A z = sm.z[at];
+          sm.p[at] = z == lowest<A>() ? A(0) : expo(z - lse[h]);
+        });
+        __syncwarp();
+        dots<V, CB, G, false>(a, a.vv, cnt, reinterpret_cast<const S*>(a.gout.p) + int64_t(it.row) * a.gout.ld, a.v, sm.idx, sm.z);
+        if (!held || it.index >= 0)
+          each_pair(a, cnt, [&](int at, int, int, int k) { pairs[int64_t(e) * a.heads + k] = {sm.z[at], sm.p[at]}; });
+      }
+      each_head(a, [&](const HeadLanes& l) {
+        A sum = 0;
+        for (int i = l.slot; i < cnt; i += l.slots) {
+          const A p = sm.p[l.h * a.stride + i];
+          if (p != 0) sum += p * sm.z[l.h * a.stride + i];
+        }
+        sum = all_sum(l, sum);
+        if (l.on) sm.stat[l.h] = (WHOLE || e == it.e0 ? A(0) : sm.stat[l.h]) + sum;
       });
-      __syncwarp();
-      short_sums<V, G, false, false, S>(a, a.qk, cnt, sm.z, a.k, sm.idx, sm.acc, static_cast<const A*>(nullptr), first, t.one && last,
-                  [&](int, int at, const A* r) {
-                    if (it.index >= 0) {
-                      A x[V];
-#pragma unroll
-                      for (int k = 0; k < V; ++k) x[k] = r[k] * scale;
-                      store_as<V>(static_cast<A*>(a.part) + int64_t(it.index) * a.part_ld + at, x);
-                    } else {
-                      Pack<R, V> y;
-#pragma unroll
-                      for (int k = 0; k < V; ++k) y.e[k] = to<R>(r[k] * scale);
-                      y.store(reinterpret_cast<R*>(a.gq.p) + int64_t(it.row) * a.gq.ld + at);
-                    }
-                  });
       __syncwarp();
       e += cnt;
     } while (!WHOLE && e < it.e1);
     if (!t.one) {
       __syncthreads();
-      for (int c = t.thread(); c < width; c += t.threads()) {
-        A r = 0;
-        for (int w = 0; w < t.warps; ++w) r += Smem<A>(a, w).acc[c];
-        finish(c, r);
-      }
+      A total[2] = {0, 0};   // heads <= 64, at least 32 threads
+      for (int j = 0; j < 2; ++j)
+        if (t.thread() + j * t.threads() < a.heads)
+          for (int w = 0; w < t.warps; ++w) total[j] += Smem<A>(a, w).stat[t.thread() + j * t.threads()];
+      __syncthreads();
+      for (int j = 0; j < 2; ++j)
+        if (t.thread() + j * t.threads() < a.heads)
+          for (int w = 0; w < t.warps; ++w) Smem<A>(a, w).stat[t.thread() + j * t.threads()] = total[j];
+      __syncthreads();
+    }
+    if (it.index >= 0) {
+      A* part = static_cast<A*>(a.part_sum) + int64_t(it.index) * a.heads;
+      for (int h = t.thread(); h < a.heads; h += t.threads()) part[h] = sm.stat[h];
+      return;
+    }
+  } else {
+    const Int4 join = a.joins[a.items[it.index].w];
+    each_head(a, [&](const HeadLanes& l) {
+      A sum = 0;
+#pragma unroll 8
+      for (int i = l.slot; i < join.z; i += l.slots) sum += static_cast<const A*>(a.part_sum)[int64_t(join.y + i) * a.heads + l.h];
+      sum = all_sum(l, sum);
+      if (l.on) sm.stat[l.h] = sum;
+    });
+    __syncwarp();
+  }
+  const auto finish = [&](int at, A x) {   // one element of gq
+    if (it.index >= 0) static_cast<A*>(a.part)[int64_t(it.index) * a.part_ld + at] = x * scale;
+    else (reinterpret_cast<R*>(a.gq.p) + int64_t(it.row) * a.gq.ld)[at] = to<R>(x * scale);
+  };
+  int e = it.e0;
+  do {
+    const int cnt = WHOLE ? it.e1 - e : min(a.sub, it.e1 - e);
+    const bool first = WHOLE || e == it.e0, last = WHOLE || e + cnt >= it.e1;
+    if (!held) fetch(e, cnt);
+    each_pair(a, cnt, [&](int at, int, int h, int k) {
+      const A p = sm.p[at], d = p == 0 ? A(0) : p * (sm.z[at] - sm.stat[h]);
+      sm.z[at] = d;
+      if (!EDGES) pairs[int64_t(e) * a.heads + k] = {d, p};
+      if (a.ds) static_cast<A*>(a.ds)[int64_t(e) * a.heads + k] = d;
+    });
+    __syncwarp();
+    short_sums<V, G, false, false, S>(a, a.qk, cnt, sm.z, a.k, sm.idx, sm.acc, static_cast<const A*>(nullptr), first, t.one && last,
+                [&](int, int at, const A* r) {
+                  if (it.index >= 0) {
+                    A x[V];
+#pragma unroll
+                    for (int k = 0; k < V; ++k) x[k] = r[k] * scale;
+                    store_as<V>(static_cast<A*>(a.part) + int64_t(it.index) * a.part_ld + at, x);
+                  } else {
+                    Pack<R, V> y;
+#pragma unroll
+                    for (int k = 0; k < V; ++k) y.e[k] = to<R>(r[k] * scale);
+                    y.store(reinterpret_cast<R*>(a.gq.p) + int64_t(it.row) * a.gq.ld + at);
+                  }
+                });
+    __syncwarp();
+    e += cnt;
+  } while (!WHOLE && e < it.e1);
+  if (!t.one) {
+    __syncthreads();
+    for (int c = t.thread(); c < width; c += t.threads()) {
+      A r = 0;
+      for (int w = 0; w < t.warps; ++w) r += Smem<A>(a, w).acc[c];
+      finish(c, r);
     }
   }
 }
