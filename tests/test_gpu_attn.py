@@ -534,3 +534,49 @@ def test_the_largest_tables(edges):
     c.check(ops[:1])
     with pytest.raises(cg().CgtpError, match="446 borders"):
         c.run(ops[1])
+
+
+def test_rows_behind_the_first_four_gigabytes():
+    """Sources at the end of tables of 5 GB give what the same sources give in tables of their own."""
+    rng = np.random.default_rng(26)
+    n, m, near = 40, 300000, 700
+    deg = rng.poisson(20, n)
+    col = rng.integers(m - near, m, deg.sum())
+    c = Case(("16x0e", "1024x0e", 4, 4), "f32", deg, m=near, borders=0, seed=26)
+    big = lambda t: torch.cat([torch.full((m - near, t.shape[1]), float("nan"), device="cuda"), t])  # noqa: E731
+    rowptr = _dev(c.rowptr, torch.int32)
+    small = cg().Graph(rowptr, _dev(col - (m - near), torch.int32), n, n_src=near)
+    large = cg().Graph(rowptr, _dev(col, torch.int32), n, n_src=m)
+    k, v = big(c.k), big(c.x)
+    assert v.numel() * 4 > 2 ** 32
+    out, lse = cg().cgtp_attn_forward(c.plan, large, c.q, k, v)
+    want, wlse = cg().cgtp_attn_forward(c.plan, small, c.q, c.k, c.x)
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+    got = cg().cgtp_attn_backward(c.plan, large, c.gout, c.q, k, v, lse)
+    ref = cg().cgtp_attn_backward(c.plan, small, c.gout, c.q, c.k, c.x, wlse)
+    assert torch.equal(got[0], ref[0])
+    for a, b in zip(got[1:3], ref[1:3]):
+        # sums over a source's edges, at most a dozen, whose order may differ
+        assert (a[:m - near] == 0).all() and torch.allclose(a[m - near:], b, rtol=0, atol=16 * 2.0 ** -24 * float(b.abs().max()))
+
+
+def test_edge_rows_behind_the_first_two_billion_elements():
+    n, deg, dv = 4096, 130, 1024
+    c = Case(("4x0e", f"{dv}x0e", 4, 4), "f32", [2], m=64, borders=0, seed=27, edges=True)
+    col = torch.randint(0, 64, (n * deg,), dtype=torch.int32, device="cuda")
+    g = cg().Graph(torch.arange(0, n * deg + 1, deg, dtype=torch.int32, device="cuda"), col, n, n_src=64)
+    q = torch.randn(n, 16, device="cuda")
+    w = torch.randn(n * deg, 4 * dv, device="cuda")
+    assert w.numel() > 2 ** 31
+    out, alpha = cg().cgtp_attn_edges_forward(c.plan, g, q, c.k, w)
+    tail = slice(-500, None)
+    wide = lambda a: a[tail].repeat_interleave(dv, dim=1)  # noqa: E731
+    assert torch.allclose(alpha.view(n, deg, 4).sum(1), torch.ones(n, 4, device="cuda"), rtol=0, atol=deg * 2.0 ** -24)
+    assert torch.equal(out[tail], wide(alpha) * w[tail])
+    gq, gk, gw, _, ds = cg().cgtp_attn_edges_backward(c.plan, g, out, q, c.k, w, alpha, need_gbias=True)
+    assert torch.equal(gw[tail], wide(alpha) * out[tail])
+    # the last receiver's gradient, from the formula in 64 bits: dv + deg + 12 roundings of sums of magnitudes
+    a, dp = alpha[-deg:].double(), (out[-deg:].double() * w[-deg:].double()).view(deg, 4, dv).sum(2)
+    mag = (out[-deg:].double() * w[-deg:].double()).abs().view(deg, 4, dv).sum(2)
+    want = a * (dp - (a * dp).sum(0))
+    assert ((ds[-deg:] - want).abs() <= (dv + deg + 12) * 2.0 ** -24 * a * (mag + (a * mag).sum(0))).all()
